@@ -13,6 +13,11 @@
  *                             resample (or greedy / tree-greedy acceptance)
  *   sv_kv_rollback            truncate every sequence at its accepted length
  *
+ * For models with head norms and rotary positions sv_kv_append_rope takes the
+ * place of sv_kv_append (sv_qk_norm_rope does the same to rows outside the
+ * cache), and for models with capped scores, a distance bias or a sliding
+ * window sv_spec_verify_attn_scored that of sv_spec_verify_attn.
+ *
  * Between steps, on the host, sv_adaptive_k_update turns the accept counts
  * into each sequence's draft length for the next step. sv_kv_fork lets new
  * sequences share a parent's blocks (copy-on-write, with kv->ref_count) and
@@ -241,6 +246,114 @@ sv_status sv_spec_verify_attn_no_alloc(const sv_paged_kv *kv, const void *q, voi
                                        int32_t num_q_heads, int32_t total_q, int32_t max_q_per_seq,
                                        int32_t max_seq_len, float scale, int32_t mask_kind,
                                        const uint64_t *tree_mask, int32_t *status_dev, void *stream);
+
+/*
+ * What a layer does to its query and key heads before attention: a norm per
+ * head, then the rotation of pairs of its values by the row's position.
+ *   y_e = x_e * rsqrt(mean(x^2) + eps) * (w_e + weight_offset)
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
+ * over the pairs i < rotary_dim / 2 of the head's first rotary_dim values:
+ * (y_i, y_{i + rotary_dim/2}), or (y_2i, y_{2i+1}) when interleaved is 1. The
+ * arithmetic is fp32, the angle fp64 up to its reduction to a fraction of a
+ * turn, and the result is rounded once, to the output's type.
+ *   inv_freq       float [rotary_dim / 2], device; NULL with rotary_dim 0 (no
+ *                  rotation). rotary_dim is even, at most head_dim
+ *   q_weight, k_weight  [head_dim] of the rows' type, device, 16-byte aligned;
+ *                  NULL: no norm of that kind of head
+ *   eps            finite, >= 0; weight_offset: finite (1 for weights stored as w - 1)
+ */
+typedef struct sv_head_transform {
+  const float *inv_freq;
+  const void *q_weight;
+  const void *k_weight;
+  float eps;
+  float weight_offset;
+  int32_t rotary_dim;
+  int32_t interleaved;
+} sv_head_transform;
+
+/*
+ * sv_qk_norm_rope -- head norms and rotation of query and key rows, one pass.
+ *
+ * Row r's heads lie side by side from q + r * q_row_stride (k likewise), so the
+ * rows may be parts of one projection's output.
+ *   q, q_out   [total_q, num_q_heads, head_dim] of dtype (SV_DTYPE_BF16 or
+ *              SV_DTYPE_F32), rows *_row_stride elements apart; 16-byte aligned,
+ *              strides at least num_heads * head_dim and multiples of 16 bytes.
+ *              q_out may be q itself (same stride); other overlaps are undefined
+ *   k, k_out   the same with num_kv_heads. num_q_heads or num_kv_heads may be 0
+ *              (no such rows; the pointers are not read)
+ *   positions  int32 [total_q], any values; may be NULL with rotary_dim 0
+ * head_dim: a multiple of 8 in [8, 256]. Every row is written.
+ */
+sv_status sv_qk_norm_rope(const sv_head_transform *transform, const void *q, int64_t q_row_stride, void *q_out,
+                          int64_t q_out_row_stride, int32_t num_q_heads, const void *k, int64_t k_row_stride,
+                          void *k_out, int64_t k_out_row_stride, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                          int32_t total_q, const int32_t *positions, void *stream);
+
+/*
+ * sv_kv_append_rope -- sv_kv_append with the keys normalised and rotated on the
+ * way into the cache, and the queries beside them.
+ *
+ * Block allocation, copy-on-write, order, errors and the status word are those
+ * of sv_kv_append. The stored key is the transformed one, rounded once to the
+ * pool's type (for SV_DTYPE_E4M3 from fp32: nearest code to y / k_scale);
+ * values are stored as sv_kv_append stores them. With num_q_heads > 0 the
+ * transformed queries go to q_out in the same pass.
+ *   new_k, new_v, q, q_out  rows as in sv_qk_norm_rope, of kv->dtype (bf16 for an
+ *              E4M3 pool); new_k and new_v with kv->num_kv_heads heads
+ *   positions  int32 [total_q], or NULL: c_b + i for row i of sequence b (chains)
+ * Rows past cu_q[batch] and every row of a call that fails are not written, in
+ * the cache or in q_out.
+ */
+sv_status sv_kv_append_rope(const sv_paged_kv *kv, const sv_head_transform *transform, const void *new_k,
+                            int64_t k_row_stride, const void *new_v, int64_t v_row_stride, const void *q,
+                            int64_t q_row_stride, void *q_out, int64_t q_out_row_stride, int32_t num_q_heads,
+                            const int32_t *cu_q, int32_t total_q, const int32_t *positions, int32_t *status_dev,
+                            void *stream);
+
+/*
+ * How sv_spec_verify_attn_scored changes the scores.
+ *   softcap  > 0: a score x becomes softcap * tanh(x / softcap); 0: unchanged
+ *   slopes   float [num_q_heads], device, or NULL: head h's score of a key at
+ *            distance d loses slopes[h] * d
+ *   window   > 0: a key at distance >= window is not visible; 0: no limit
+ */
+typedef struct sv_score_mod {
+  const float *slopes;
+  float softcap;
+  int32_t window;
+} sv_score_mod;
+
+/*
+ * sv_spec_verify_attn_scored -- sv_spec_verify_attn with capped scores, a bias
+ * that falls with distance, and a window of visible distances.
+ *
+ * For query row i of sequence b at position p_i, head h and key t at position
+ * p_t, the distance is p_i - p_t and the score
+ *   cap(scale * <q, k_t>) - slopes[h] * (p_i - p_t).
+ * Committed keys are at p_t = t, new row j at p_j = positions[cu_q[b] + j], or
+ * c_b + j with positions NULL. A key is visible if sv_spec_verify_attn's mask
+ * shows it and its distance is below the window. Softmax and accumulation are
+ * fp32; a row that sees no key gets zeros; what a key that no row sees holds
+ * (NaN and infinities too) does not reach the output.
+ *   positions  int32 [total_q] or NULL; each at least c_b, the first position
+ *              after the committed keys (a smaller one sets SV_ERR_BAD_LENGTH
+ *              and leaves that sequence's rows undefined)
+ *   workspace  device scratch of at least
+ *              sv_spec_verify_attn_scored_workspace_bytes, 256-byte aligned; its
+ *              contents need no initialisation. Calls that may overlap on the
+ *              GPU need workspaces of their own
+ * The other arguments, types, sizes and errors are those of
+ * sv_spec_verify_attn. SV_OPT_ATTN_PATH has no say here.
+ */
+size_t sv_spec_verify_attn_scored_workspace_bytes(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q,
+                                                  int32_t max_q_per_seq, int32_t max_seq_len);
+sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void *out, const int32_t *cu_q,
+                                     int32_t num_q_heads, int32_t total_q, int32_t max_q_per_seq, int32_t max_seq_len,
+                                     float scale, const sv_score_mod *mod, const int32_t *positions, int32_t mask_kind,
+                                     const uint64_t *tree_mask, void *workspace, size_t workspace_bytes,
+                                     int32_t *status_dev, void *stream);
 
 /*
  * sv_spec_rejection_sample -- lossless verification of chain drafts.

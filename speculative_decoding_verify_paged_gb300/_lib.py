@@ -31,7 +31,8 @@ STATUS_NAMES = {
     8: "SV_ERR_BAD_TOKEN", 9: "SV_ERR_NONFINITE", 10: "SV_ERR_WORKSPACE",
 }
 
-EXPORTS = ("sv_kv_append", "sv_spec_verify_attn_workspace_bytes", "sv_spec_verify_attn",
+EXPORTS = ("sv_kv_append", "sv_kv_append_rope", "sv_qk_norm_rope", "sv_spec_verify_attn_scored_workspace_bytes",
+           "sv_spec_verify_attn_scored", "sv_spec_verify_attn_workspace_bytes", "sv_spec_verify_attn",
            "sv_spec_verify_attn_no_alloc", "sv_spec_rejection_sample_workspace_bytes", "sv_spec_rejection_sample",
            "sv_tree_greedy_accept", "sv_tree_rejection_sample", "sv_kv_rollback", "sv_kv_fork", "sv_kv_release", "sv_adaptive_k_state_bytes", "sv_adaptive_k_init",
            "sv_adaptive_k_update", "sv_adaptive_k_reset", "sv_adaptive_k_current",
@@ -66,6 +67,18 @@ class sv_paged_kv(ctypes.Structure):
     ]
 
 
+class sv_head_transform(ctypes.Structure):
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+    ]
+
+
+class sv_score_mod(ctypes.Structure):
+    _fields_ = [("slopes", ctypes.c_void_p), ("softcap", ctypes.c_float), ("window", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -85,8 +98,13 @@ def load(path: Optional[str] = None, build_if_missing: bool = True) -> ctypes.CD
         lib = ctypes.CDLL(p)
         P, I, F, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
         KVP = ctypes.POINTER(sv_paged_kv)
+        HTP, SMP, I64 = ctypes.POINTER(sv_head_transform), ctypes.POINTER(sv_score_mod), ctypes.c_int64
         sig = {
             "sv_kv_append": (I, [KVP, P, P, P, I, P, P]),
+            "sv_kv_append_rope": (I, [KVP, HTP, P, I64, P, I64, P, I64, P, I64, I, P, I, P, P, P]),
+            "sv_qk_norm_rope": (I, [HTP, P, I64, P, I64, I, P, I64, P, I64, I, I, I, I, P, P]),
+            "sv_spec_verify_attn_scored_workspace_bytes": (S, [KVP, I, I, I, I]),
+            "sv_spec_verify_attn_scored": (I, [KVP, P, P, P, I, I, I, I, F, SMP, P, I, P, P, S, P, P]),
             "sv_spec_verify_attn_workspace_bytes": (S, [KVP, I, I, I, I]),
             "sv_spec_verify_attn": (I, [KVP, P, P, P, I, I, I, I, F, I, P, P, S, P, P]),
             "sv_spec_verify_attn_no_alloc": (I, [KVP, P, P, P, I, I, I, I, F, I, P, P, P]),
@@ -244,6 +262,154 @@ def spec_verify_attn_no_alloc(kv: PagedKV, q: torch.Tensor, out: torch.Tensor, c
                                                int(q.shape[0]), int(max_q), int(max_seq_len), float(scale),
                                                int(mask_kind), _ptr(tree_mask), _ptr(status), _stream(stream)),
            "sv_spec_verify_attn_no_alloc")
+
+
+@dataclass
+class HeadTransform:
+    """What a layer does to its query and key heads before attention (see
+    sv_head_transform): a norm per head (where a weight is given), then the
+    rotation of the first 2 * len(inv_freq) values by the row's position."""
+
+    inv_freq: Optional[torch.Tensor] = None  # float32 [rotary_dim / 2]; None: no rotation
+    q_weight: Optional[torch.Tensor] = None  # [head_dim] of the rows' type; None: no norm
+    k_weight: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    weight_offset: float = 0.0  # 1 for weights stored as w - 1
+    interleaved: bool = False  # pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2)
+
+    def struct(self, rows: torch.Tensor) -> sv_head_transform:
+        d = rows.shape[2]
+        for w in (self.q_weight, self.k_weight):
+            if w is not None and (w.dtype != rows.dtype or w.numel() != d):
+                raise ValueError(f"a norm weight holds {d} values of {rows.dtype}")
+        rot = 0
+        if self.inv_freq is not None:
+            if self.inv_freq.dtype != torch.float32:
+                raise TypeError("inv_freq is float32")
+            rot = 2 * self.inv_freq.numel()
+        return sv_head_transform(_ptr(self.inv_freq) if rot else None, _ptr(self.q_weight), _ptr(self.k_weight), self.eps,
+                                 self.weight_offset, rot, int(self.interleaved))
+
+
+@dataclass
+class ScoreMod:
+    """How spec_verify_attn_scored changes the scores (see sv_score_mod)."""
+
+    softcap: float = 0.0  # 0: not capped
+    slopes: Optional[torch.Tensor] = None  # float32 [num_q_heads]
+    window: int = 0  # 0: no limit
+
+    def struct(self, num_q_heads: int) -> sv_score_mod:
+        if self.slopes is not None and (self.slopes.dtype != torch.float32 or self.slopes.numel() != num_q_heads):
+            raise ValueError(f"slopes holds {num_q_heads} float32 values")
+        return sv_score_mod(_ptr(self.slopes), self.softcap, self.window)
+
+
+def _rows(t: torch.Tensor, like: Optional[torch.Tensor] = None) -> tuple:
+    """Pointer and row stride (elements) of rows of heads [n, heads, head_dim]; the
+    heads of a row are contiguous, the rows may be parts of wider ones."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("libspecverify takes CUDA tensors only")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise ValueError("the heads of a row are contiguous")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"expected rows {tuple(like.shape)} of {like.dtype}, got {tuple(t.shape)} of {t.dtype}")
+    return t.data_ptr(), (sn if n > 1 else h * d)
+
+
+def _i32(t: Optional[torch.Tensor], n: int, what: str) -> Optional[int]:
+    """Pointer of a contiguous int32 tensor of n values."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != n:
+        raise ValueError(f"{what} holds {n} int32 values")
+    return _ptr(t)
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """The stream to launch on: the caller's, or the current one. The library launches on the
+    current device, which has to be the tensors'."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, the current device is {torch.cuda.current_device()}")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def qk_norm_rope(transform: HeadTransform, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                 positions: Optional[torch.Tensor], q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor],
+                 stream=None) -> None:
+    """Head norms and rotation of query rows [n, heads, head_dim] and key rows (either may be
+    None) into q_out and k_out, which may be the inputs themselves. positions: int32 [n]."""
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("no rows: q and k are both None")
+    n, _, d = some.shape
+    qp, qs, qo, qos, hq, kp, ks, ko, kos, hkv = None, 0, None, 0, 0, None, 0, None, 0, 0
+    if q is not None:
+        (qp, qs), (qo, qos), hq = _rows(q), _rows(q_out, q), q.shape[1]
+    if k is not None:
+        (kp, ks), (ko, kos), hkv = _rows(k), _rows(k_out, k), k.shape[1]
+        if k.shape[0] != n or k.shape[2] != d or k.dtype != some.dtype:
+            raise ValueError("q and k have the same rows, head_dim and type")
+    _check(load().sv_qk_norm_rope(ctypes.byref(transform.struct(some)), qp, qs, qo, qos, hq, kp, ks, ko, kos, hkv, d,
+                                  _dtype_code(some), n, _i32(positions, n, "positions"), _stream_of(some, stream)),
+           "sv_qk_norm_rope")
+
+
+def kv_append_rope(kv: PagedKV, transform: HeadTransform, new_k: torch.Tensor, new_v: torch.Tensor, cu_q: torch.Tensor,
+                   status: torch.Tensor, *, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                   positions: Optional[torch.Tensor] = None, stream=None) -> None:
+    """kv_append with the keys normalised and rotated on the way into the cache; with q, the
+    queries too, into q_out (which may be q). positions: int32 [n], or None for chains."""
+    s = kv.struct()
+    n, hkv, d = new_k.shape
+    rows = torch.float32 if kv.k_pool.dtype == torch.float32 else torch.bfloat16
+    if new_k.dtype != rows or hkv != s.num_kv_heads or d != s.head_dim:
+        raise ValueError(f"expected rows [n, {s.num_kv_heads}, {s.head_dim}] of {rows}")
+    (kp, ks), (vp, vs) = _rows(new_k), _rows(new_v, new_k)
+    qp, qs, qo, qos, hq = None, 0, None, 0, 0
+    if q is not None:
+        if q.shape[0] != n or q.shape[2] != d or q.dtype != rows:
+            raise ValueError(f"expected queries [{n}, heads, {d}] of {rows}")
+        (qp, qs), (qo, qos), hq = _rows(q), _rows(q_out, q), q.shape[1]
+    _check(load().sv_kv_append_rope(ctypes.byref(s), ctypes.byref(transform.struct(new_k)), kp, ks, vp, vs, qp, qs, qo,
+                                    qos, hq, _i32(cu_q, s.batch + 1, "cu_q"), n, _i32(positions, n, "positions"),
+                                    _i32(status, 1, "status"), _stream_of(new_k, stream)), "sv_kv_append_rope")
+
+
+def spec_verify_attn_scored_workspace_bytes(kv: PagedKV, num_q_heads: int, total_q: int, max_q: int,
+                                            max_seq_len: int) -> int:
+    s = kv.struct()
+    return load().sv_spec_verify_attn_scored_workspace_bytes(ctypes.byref(s), num_q_heads, total_q, max_q, max_seq_len)
+
+
+def spec_verify_attn_scored(kv: PagedKV, q: torch.Tensor, out: torch.Tensor, cu_q: torch.Tensor, *, max_q: int,
+                            max_seq_len: int, scale: float, mod: ScoreMod, positions: Optional[torch.Tensor] = None,
+                            mask_kind: int = SV_MASK_CAUSAL, tree_mask: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """spec_verify_attn with capped scores, a distance bias and a window (mod). Without a
+    workspace a new one of the size the library asks for is taken."""
+    s = kv.struct()
+    n, hq, d = q.shape
+    rows = torch.float32 if kv.k_pool.dtype == torch.float32 else torch.bfloat16
+    if q.dtype != rows or d != s.head_dim or out.shape != q.shape or out.dtype != rows:
+        raise ValueError(f"expected queries and outputs [n, heads, {s.head_dim}] of {rows}")
+    if tree_mask is not None and (tree_mask.element_size() != 8 or tree_mask.numel() != n):
+        raise ValueError(f"tree_mask holds {n} 64-bit values")
+    lib, kvp, st = load(), ctypes.byref(s), _stream_of(q, stream)
+    if workspace is None:
+        need = lib.sv_spec_verify_attn_scored_workspace_bytes(kvp, hq, n, max_q, max_seq_len)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        if stream is not None and st != torch.cuda.current_stream().cuda_stream:
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(st))
+    _check(lib.sv_spec_verify_attn_scored(
+        kvp, _ptr(q), _ptr(out), _i32(cu_q, s.batch + 1, "cu_q"), hq, n, max_q, max_seq_len, scale,
+        ctypes.byref(mod.struct(hq)), _i32(positions, n, "positions"), mask_kind, _ptr(tree_mask), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _i32(status, 1, "status"), st), "sv_spec_verify_attn_scored")
 
 
 def spec_rejection_sample_workspace_bytes(logits_dtype: torch.dtype, vocab: int, batch: int, total_q: int,

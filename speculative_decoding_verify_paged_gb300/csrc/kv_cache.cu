@@ -17,7 +17,7 @@
 // scatter and the tree-path compaction run one CTA per row / per sequence.
 #include <cuda_fp8.h>
 
-#include "sv_internal.cuh"
+#include "kv_rows.cuh"
 
 namespace sv {
 namespace {
@@ -294,29 +294,8 @@ __global__ void __launch_bounds__(kScatterThreads) kv_scatter_kernel(KV kv, cons
     return;
   }
   const int slot = pos % kv.block_size;
-  if (i == 0 && slot > 0 && kv.ref_count != nullptr) {
-    // the sequence's first row lands in its private copy of a shared block (see
-    // kv_alloc_kernel): bring over the rows written before, every head, K and V
-    const int m = kv.ref_count[blk];
-    if (m < 0) {
-      const int src = -m - 1;
-      const int per_head = slot * vec_per_row;  // the rows before `slot` are contiguous in a (block, head)
-      const size_t head_bytes = (size_t)kv.block_size * row_bytes;
-      if (src >= 0 && src < kv.num_blocks) {
-        for (int x = threadIdx.x; x < kv.num_kv_heads * per_head; x += blockDim.x) {
-          const int h = x / per_head, v = x - h * per_head;
-          const size_t so = ((size_t)src * kv.num_kv_heads + h) * head_bytes + (size_t)v * 16;
-          const size_t d_o = ((size_t)blk * kv.num_kv_heads + h) * head_bytes + (size_t)v * 16;
-          *reinterpret_cast<uint4 *>((uint8_t *)kv.k_pool + d_o) = *reinterpret_cast<const uint4 *>((const uint8_t *)kv.k_pool + so);
-          *reinterpret_cast<uint4 *>((uint8_t *)kv.v_pool + d_o) = *reinterpret_cast<const uint4 *>((const uint8_t *)kv.v_pool + so);
-        }
-      } else if (threadIdx.x == 0) {
-        record(status, SV_ERR_BAD_BLOCK_ID);
-      }
-      __syncthreads();  // every thread has read the marker
-      if (threadIdx.x == 0) kv.ref_count[blk] = 1;
-    }
-  }
+  // the sequence's first row lands in its private copy of a shared block (see kv_alloc_kernel)
+  if (i == 0 && slot > 0 && kv.ref_count != nullptr) copy_shared_block(kv, blk, slot, row_bytes, status);
   for (int x = threadIdx.x; x < total; x += blockDim.x) {
     const int h = x / vec_per_row, v = x % vec_per_row;
     uint4 kk = kk0, vv = vv0, kb = kk1, vb = vv1;
@@ -697,9 +676,13 @@ __global__ void __launch_bounds__(kBookThreads) kv_release_kernel(KV kv, const i
 
 }  // namespace
 
+cudaError_t launch_kv_alloc(const KV &kv, const int32_t *cu_q, int32_t *status, cudaStream_t st) {
+  return launch_pdl(kv_alloc_kernel, dim3(1), dim3(kBookThreads), 0, st, kv, cu_q, status);
+}
+
 cudaError_t launch_kv_append(const KV &kv, const void *new_k, const void *new_v, const int32_t *cu_q,
                              int total_q, int32_t *status, cudaStream_t st) {
-  cudaError_t e = launch_pdl(kv_alloc_kernel, dim3(1), dim3(kBookThreads), 0, st, kv, cu_q, status);
+  cudaError_t e = launch_kv_alloc(kv, cu_q, status, st);
   if (e != cudaSuccess || total_q == 0) return e;
   return launch_pdl(kv_scatter_kernel, dim3((unsigned)total_q), dim3(kScatterThreads), 0, st, kv, (const uint8_t *)new_k,
                     (const uint8_t *)new_v, cu_q, status);

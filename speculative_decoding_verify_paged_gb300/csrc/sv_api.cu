@@ -55,6 +55,7 @@ namespace {
 
 constexpr int kMaxQ = 64;
 constexpr int kGranule = 64;
+constexpr float kLog2e = 1.4426950408889634f;
 int g_attn_path = SV_ATTN_AUTO;
 unsigned long long g_wait_ns = kDefaultWaitNs;  // budget of the kernels' pipeline waits
 int g_stall = SV_STALL_NONE;                    // failure-path test hook
@@ -94,16 +95,53 @@ bool keys_usable(const sv_paged_kv *kv, int32_t num_q_heads, int32_t max_q, int3
          attn_keys_fits(make_kv(*kv), num_q_heads, max_q, max_seq_len);
 }
 
+// Split-KV partials of the kernels that take one CTA per key split.
+size_t split_workspace(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q, int32_t max_seq_len) {
+  const SplitPlan p = plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kGranule);
+  if (p.max_splits <= 1) return 0;
+  const size_t rows = (size_t)p.max_splits * total_q * num_q_heads;
+  return rows * (size_t)kv->head_dim * sizeof(float) + rows * sizeof(float) + 256;
+}
+
+// Checks a head transform and puts it into the kernels' arguments.
+sv_status head_args(HeadArgs *a, const sv_head_transform *t, int head_dim, int dtype) {
+  if (t == nullptr || head_dim < 8 || head_dim > 256 || head_dim % 8 != 0) return SV_ERR_INVALID_ARG;
+  if (t->rotary_dim < 0 || t->rotary_dim > head_dim || t->rotary_dim % 2 != 0) return SV_ERR_INVALID_ARG;
+  if (t->rotary_dim > 0 && t->inv_freq == nullptr) return SV_ERR_INVALID_ARG;
+  if (t->interleaved != 0 && t->interleaved != 1) return SV_ERR_INVALID_ARG;
+  if (!aligned16(t->q_weight) || !aligned16(t->k_weight)) return SV_ERR_INVALID_ARG;
+  if ((t->q_weight != nullptr || t->k_weight != nullptr) && (!(t->eps >= 0.f) || !std::isfinite(t->eps) || !std::isfinite(t->weight_offset)))
+    return SV_ERR_INVALID_ARG;
+  std::memset(a, 0, sizeof *a);
+  a->inv_freq = t->inv_freq;
+  a->q_weight = (const uint8_t *)t->q_weight;
+  a->k_weight = (const uint8_t *)t->k_weight;
+  a->head_dim = head_dim;
+  a->rot = t->rotary_dim;
+  a->interleaved = t->interleaved != 0;
+  a->eps = t->eps;
+  a->offset = t->weight_offset;
+  a->inv_dim = 1.f / (float)head_dim;
+  return SV_OK;
+}
+
+// Rows of `heads` heads, `stride` elements apart: present, 16-byte aligned and not overlapping.
+template <typename P>
+bool head_rows(P *at, long long *bytes, const void *p, int64_t stride, int heads, int head_dim, int dtype) {
+  const int64_t esz = dtype == SV_DTYPE_F32 ? 4 : 2;
+  if (heads == 0) return true;
+  if (p == nullptr || !aligned16(p) || stride < (int64_t)heads * head_dim || stride > (INT64_MAX >> 36) || stride * esz % 16 != 0)
+    return false;
+  *at = (P)const_cast<void *>(p);
+  *bytes = stride * esz;
+  return true;
+}
+
 // Workspace of whichever kernel a call may select: the split-KV partials of the
 // CUDA-core and mma.sync kernels, or the tcgen05 kernel's slots and tile prefix.
 size_t attn_workspace(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q, int32_t max_q,
                       int32_t max_seq_len) {
-  const SplitPlan p = plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kGranule);
-  size_t need = 0;
-  if (p.max_splits > 1) {
-    const size_t rows = (size_t)p.max_splits * total_q * num_q_heads;
-    need = rows * (size_t)kv->head_dim * sizeof(float) + rows * sizeof(float) + 256;
-  }
+  size_t need = split_workspace(kv, num_q_heads, total_q, max_seq_len);
   if (kv->batch > 0 && umma_usable(kv, num_q_heads, max_q, max_seq_len))
     need = std::max(need, attn_umma_workspace_bytes(make_kv(*kv), num_q_heads, max_q, max_seq_len));
   if (kv->batch > 0 && keys_usable(kv, num_q_heads, max_q, max_seq_len))
@@ -141,7 +179,7 @@ const char *sv_status_string(int32_t status) {
   }
 }
 
-int32_t sv_version(void) { return 30100; }
+int32_t sv_version(void) { return 30200; }
 
 sv_status sv_set_option(int32_t option, int32_t value) {
   if (option == SV_OPT_ATTN_PATH && value >= SV_ATTN_AUTO && value <= SV_ATTN_KEYS_MAJOR) {
@@ -243,6 +281,117 @@ sv_status sv_spec_verify_attn(const sv_paged_kv *kv, const void *q, void *out, c
   }
   if (e != cudaSuccess) return SV_ERR_CUDA;
   return cuda_status(launch_attn_combine(a, kv->dtype, st));
+}
+
+sv_status sv_qk_norm_rope(const sv_head_transform *transform, const void *q, int64_t q_row_stride, void *q_out,
+                          int64_t q_out_row_stride, int32_t num_q_heads, const void *k, int64_t k_row_stride,
+                          void *k_out, int64_t k_out_row_stride, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                          int32_t total_q, const int32_t *positions, void *stream) {
+  if (dtype != SV_DTYPE_BF16 && dtype != SV_DTYPE_F32) return SV_ERR_INVALID_ARG;
+  if (num_q_heads < 0 || num_kv_heads < 0 || total_q < 0) return SV_ERR_INVALID_ARG;
+  HeadArgs a;
+  const sv_status s = head_args(&a, transform, head_dim, dtype);
+  if (s != SV_OK) return s;
+  if (total_q == 0 || (num_q_heads == 0 && num_kv_heads == 0)) return SV_OK;
+  if (transform->rotary_dim > 0 && positions == nullptr) return SV_ERR_INVALID_ARG;
+  if (!head_rows(&a.q, &a.q_stride, q, q_row_stride, num_q_heads, head_dim, dtype) ||
+      !head_rows(&a.q_out, &a.q_out_stride, q_out, q_out_row_stride, num_q_heads, head_dim, dtype) ||
+      !head_rows(&a.k, &a.k_stride, k, k_row_stride, num_kv_heads, head_dim, dtype) ||
+      !head_rows(&a.k_out, &a.k_out_stride, k_out, k_out_row_stride, num_kv_heads, head_dim, dtype))
+    return SV_ERR_INVALID_ARG;
+  a.hq = num_q_heads;
+  a.hkv = num_kv_heads;
+  a.positions = positions;
+  return cuda_status(launch_head_rows(a, dtype, total_q, false, (cudaStream_t)stream));
+}
+
+sv_status sv_kv_append_rope(const sv_paged_kv *kv, const sv_head_transform *transform, const void *new_k,
+                            int64_t k_row_stride, const void *new_v, int64_t v_row_stride, const void *q,
+                            int64_t q_row_stride, void *q_out, int64_t q_out_row_stride, int32_t num_q_heads,
+                            const int32_t *cu_q, int32_t total_q, const int32_t *positions, int32_t *status_dev,
+                            void *stream) {
+  sv_status s = check_kv(kv, true);
+  if (s != SV_OK) return s;
+  if (status_dev == nullptr || total_q < 0 || num_q_heads < 0 || (kv->batch > 0 && cu_q == nullptr))
+    return SV_ERR_INVALID_ARG;
+  const int dtype = kv->dtype == SV_DTYPE_F32 ? SV_DTYPE_F32 : SV_DTYPE_BF16;  // of the rows
+  HeadArgs a;
+  s = head_args(&a, transform, kv->head_dim, dtype);
+  if (s != SV_OK) return s;
+  if (total_q > 0 && (!head_rows(&a.k, &a.k_stride, new_k, k_row_stride, kv->num_kv_heads, kv->head_dim, dtype) ||
+                      !head_rows(&a.v, &a.v_stride, new_v, v_row_stride, kv->num_kv_heads, kv->head_dim, dtype) ||
+                      !head_rows(&a.q, &a.q_stride, q, q_row_stride, num_q_heads, kv->head_dim, dtype) ||
+                      !head_rows(&a.q_out, &a.q_out_stride, q_out, q_out_row_stride, num_q_heads, kv->head_dim, dtype)))
+    return SV_ERR_INVALID_ARG;
+  if (kv->batch == 0) return SV_OK;
+  if (kv->ref_count != nullptr && kv->batch > kv_cow_max_batch()) return SV_ERR_UNSUPPORTED;
+  a.hq = num_q_heads;
+  a.hkv = kv->num_kv_heads;
+  a.positions = positions;
+  a.kv = make_kv(*kv);
+  a.cu_q = cu_q;
+  a.status = status_dev;
+  const cudaError_t e = launch_kv_alloc(a.kv, cu_q, status_dev, (cudaStream_t)stream);
+  if (e != cudaSuccess || total_q == 0) return cuda_status(e);
+  return cuda_status(launch_head_rows(a, dtype, total_q, true, (cudaStream_t)stream));
+}
+
+size_t sv_spec_verify_attn_scored_workspace_bytes(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q,
+                                                  int32_t max_q_per_seq, int32_t max_seq_len) {
+  if (kv == nullptr || num_q_heads <= 0 || kv->num_kv_heads <= 0 || num_q_heads % kv->num_kv_heads != 0 ||
+      total_q < 0 || max_q_per_seq < 1 || max_q_per_seq > kMaxQ || max_seq_len <= 0)
+    return 0;
+  return split_workspace(kv, num_q_heads, total_q, max_seq_len);
+}
+
+sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void *out, const int32_t *cu_q,
+                                     int32_t num_q_heads, int32_t total_q, int32_t max_q_per_seq, int32_t max_seq_len,
+                                     float scale, const sv_score_mod *mod, const int32_t *positions, int32_t mask_kind,
+                                     const uint64_t *tree_mask, void *workspace, size_t workspace_bytes,
+                                     int32_t *status_dev, void *stream) {
+  sv_status s = check_kv(kv, false);
+  if (s != SV_OK) return s;
+  if (num_q_heads <= 0 || num_q_heads % kv->num_kv_heads != 0) return SV_ERR_INVALID_ARG;
+  if (total_q < 0 || max_q_per_seq < 1 || max_q_per_seq > kMaxQ || max_seq_len < 1) return SV_ERR_INVALID_ARG;
+  if (mask_kind != SV_MASK_CAUSAL && mask_kind != SV_MASK_TREE) return SV_ERR_INVALID_ARG;
+  if (mask_kind == SV_MASK_TREE && tree_mask == nullptr && total_q > 0) return SV_ERR_INVALID_ARG;
+  if (!(scale == scale) || mod == nullptr || !(mod->softcap >= 0.f) || mod->softcap == INFINITY || mod->window < 0)
+    return SV_ERR_INVALID_ARG;
+  if (kv->batch == 0 || total_q == 0) return SV_OK;
+  if (q == nullptr || out == nullptr || cu_q == nullptr || !aligned16(q) || !aligned16(out)) return SV_ERR_INVALID_ARG;
+  if (kv->head_dim % 32 != 0) return SV_ERR_UNSUPPORTED;
+  const size_t need =
+      sv_spec_verify_attn_scored_workspace_bytes(kv, num_q_heads, total_q, max_q_per_seq, max_seq_len);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || ((uintptr_t)workspace & 255u) != 0))
+    return SV_ERR_WORKSPACE;
+  const SplitPlan p = plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kGranule);
+  const size_t rows = (size_t)p.max_splits * total_q * num_q_heads;
+  ScoredArgs sa;
+  AttnArgs &a = sa.a;
+  a.kv = make_kv(*kv);
+  a.q = q;
+  a.out = out;
+  a.cu_q = cu_q;
+  a.tree_mask = tree_mask;
+  a.ws_o = p.max_splits > 1 ? (float *)workspace : nullptr;
+  a.ws_lse = p.max_splits > 1 ? (float *)workspace + rows * (size_t)kv->head_dim : nullptr;
+  a.status = status_dev;
+  a.num_q_heads = num_q_heads;
+  a.total_q = total_q;
+  a.max_q = max_q_per_seq;
+  a.max_seq_len = max_seq_len;
+  a.chunk = p.chunk;
+  a.max_splits = p.max_splits;
+  a.mask_kind = mask_kind;
+  a.scale_log2 = scale * kLog2e;
+  a.wait_ns = g_wait_ns;
+  a.stall = g_stall;
+  sa.cap = mod->softcap * kLog2e;
+  sa.window = mod->window;
+  sa.slopes = mod->slopes;
+  sa.positions = positions;
+  cudaStream_t st = (cudaStream_t)stream;
+  return cuda_status(launch_attn_scored_simt(sa, kv->dtype, st));
 }
 
 size_t sv_spec_rejection_sample_workspace_bytes(int32_t logits_dtype, int32_t vocab, int32_t batch, int32_t total_q,

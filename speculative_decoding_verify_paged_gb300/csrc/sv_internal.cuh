@@ -170,6 +170,31 @@ struct AttnArgs {
   int stall;                   // failure-path test: SV_STALL_ATTENTION makes the producer wait on nothing
 };
 
+// Attention with modified scores. scale_log2 of `a` carries log2(e), and so does cap.
+struct ScoredArgs {
+  AttnArgs a;
+  float cap;                 // softcap * log2(e); 0: none
+  int window;                // keys at a distance >= window are not visible; 0: no limit
+  const float *slopes;       // [num_q_heads] or null
+  const int32_t *positions;  // [total_q] or null: c_b + i
+};
+
+// Rows of heads to normalise and rotate (head_rows.cu). Strides are in bytes.
+struct HeadArgs {
+  const uint8_t *q, *k, *v;
+  uint8_t *q_out, *k_out;
+  long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  const float *inv_freq;
+  const uint8_t *q_weight, *k_weight;  // of the rows' type, or null: no norm
+  const int32_t *positions;            // [rows] or null (append only): c_b + i
+  int hq, hkv, head_dim, rot;
+  bool interleaved;
+  float eps, offset, inv_dim;
+  KV kv;  // append only, with cu_q and status
+  const int32_t *cu_q;
+  int32_t *status;
+};
+
 // How the key range of every sequence is split across CTAs.
 struct SplitPlan {
   int chunk;       // tokens per split, a multiple of `granule`
@@ -178,6 +203,7 @@ struct SplitPlan {
 SplitPlan plan_splits(int batch, int num_kv_heads, int max_seq_len, int granule);
 
 // kernels' host-side launchers (return a cudaError_t from the launch)
+cudaError_t launch_kv_alloc(const KV &kv, const int32_t *cu_q, int32_t *status, cudaStream_t st);
 cudaError_t launch_kv_append(const KV &kv, const void *new_k, const void *new_v, const int32_t *cu_q,
                              int total_q, int32_t *status, cudaStream_t st);
 cudaError_t launch_kv_rollback(const KV &kv, const int32_t *cu_q, const int32_t *accept, const int32_t *path,
@@ -187,6 +213,9 @@ cudaError_t launch_kv_fork(const KV &kv, const int32_t *parents, const int32_t *
 cudaError_t launch_kv_release(const KV &kv, const int32_t *seqs, int n, int32_t *status, cudaStream_t st);
 int kv_cow_max_batch();  // batch limit of append and rollback with reference counts
 int kv_max_seq_bits();   // batch limit of fork and release
+// Head rows: the append's second half after launch_kv_alloc (append), or into q_out and k_out.
+cudaError_t launch_head_rows(const HeadArgs &a, int dtype, int total_q, bool append, cudaStream_t st);
+cudaError_t launch_attn_scored_simt(const ScoredArgs &sa, int dtype, cudaStream_t st);
 cudaError_t launch_attn_simt(const AttnArgs &a, int dtype, cudaStream_t st);
 cudaError_t launch_attn_combine(const AttnArgs &a, int dtype, cudaStream_t st);
 bool attn_tc_supported(const KV &kv, int num_q_heads, int max_q);

@@ -6,6 +6,11 @@ and scratch, and `run_step` issues the four library calls on one stream:
     kv_append -> spec_verify_attn -> spec_rejection_sample (or
     tree_greedy_accept) -> kv_rollback
 
+A step of a model with head norms and rotary positions (`DeviceStep.transform`)
+appends with kv_append_rope and attends with the queries it wrote; one with
+capped scores, a distance bias or a window (`DeviceStep.mod`) attends with
+spec_verify_attn_scored.
+
 Host arrays come in the layout of `workloads` (bf16 as uint16 bit patterns).
 This module only moves data and orders calls; the arithmetic is in the CUDA
 library.
@@ -74,6 +79,9 @@ class DeviceStep:
     max_q: int
     scale: float
     num_q_heads: int
+    transform: Optional[L.HeadTransform] = None  # head norms and rotation of new_k and q
+    mod: Optional[L.ScoreMod] = None  # modified attention scores
+    positions: Optional[torch.Tensor] = None  # int32 [total_q] of the rows (trees); None: c_b + i
 
     @property
     def batch(self) -> int:
@@ -114,10 +122,11 @@ class StepBuffers:
     path: torch.Tensor
     status: torch.Tensor
     margin: torch.Tensor  # per sequence: the decisions' smallest distance to a threshold (near-ties < 1e-4)
+    q_rot: Optional[torch.Tensor] = None  # the transformed queries (steps with a head transform)
 
     @classmethod
     def make(cls, kv: L.PagedKV, dstep: DeviceStep, max_seq_len: int, device="cuda") -> "StepBuffers":
-        ws = L.spec_verify_attn_workspace_bytes(kv, dstep.num_q_heads, dstep.total_q, dstep.max_q, max_seq_len)
+        ws = attn_workspace_bytes(kv, dstep, max_seq_len)
         B = dstep.batch
         temp = 0.0 if dstep.mask_kind == L.SV_MASK_TREE else dstep.temperature
         sws = L.spec_rejection_sample_workspace_bytes(dstep.target_logits.dtype, int(dstep.target_logits.shape[1]),
@@ -131,15 +140,32 @@ class StepBuffers:
             num_out=torch.empty(B, dtype=torch.int32, device=device),
             path=torch.empty((B, dstep.max_q), dtype=torch.int32, device=device),
             status=torch.zeros(1, dtype=torch.int32, device=device),
-            margin=torch.empty(B, dtype=torch.float32, device=device))
+            margin=torch.empty(B, dtype=torch.float32, device=device),
+            q_rot=torch.empty(dstep.q.shape, dtype=dstep.q.dtype, device=device) if dstep.transform is not None else None)
+
+
+def attn_workspace_bytes(kv, d: DeviceStep, max_seq_len: int) -> int:
+    """Workspace of the attention call that the step makes."""
+    need = L.spec_verify_attn_workspace_bytes if d.mod is None else L.spec_verify_attn_scored_workspace_bytes
+    return need(kv, d.num_q_heads, d.total_q, d.max_q, max_seq_len)
 
 
 def append(kv, d: DeviceStep, buf: StepBuffers, stream=None):
+    if d.transform is not None:
+        L.kv_append_rope(kv, d.transform, d.new_k, d.new_v, d.cu_q, buf.status, q=d.q, q_out=buf.q_rot,
+                         positions=d.positions, stream=stream)
+        return
     L.kv_append(kv, d.new_k, d.new_v, d.cu_q, buf.status, stream=stream)
 
 
 def attention(kv, d: DeviceStep, buf: StepBuffers, max_seq_len: int, stream=None):
-    L.spec_verify_attn(kv, d.q, buf.attn_out, d.cu_q, max_q=d.max_q, max_seq_len=max_seq_len, scale=d.scale,
+    q = d.q if d.transform is None else buf.q_rot
+    if d.mod is not None:
+        L.spec_verify_attn_scored(kv, q, buf.attn_out, d.cu_q, max_q=d.max_q, max_seq_len=max_seq_len, scale=d.scale,
+                                  mod=d.mod, positions=d.positions, mask_kind=d.mask_kind, tree_mask=d.tree_mask,
+                                  workspace=buf.workspace, status=buf.status, stream=stream)
+        return
+    L.spec_verify_attn(kv, q, buf.attn_out, d.cu_q, max_q=d.max_q, max_seq_len=max_seq_len, scale=d.scale,
                        mask_kind=d.mask_kind, tree_mask=d.tree_mask, workspace=buf.workspace, status=buf.status,
                        stream=stream)
 
@@ -176,6 +202,6 @@ def run_step(kv: L.PagedKV, d: DeviceStep, buf: StepBuffers, max_seq_len: int, s
 def launches_per_step(d: DeviceStep, max_seq_len: int, kv: L.PagedKV) -> int:
     """Kernels the library launches for one run_step (append 2, attention 1 or
     2, sampler 2: statistics and decisions, rollback 1 or 2)."""
-    ws = L.spec_verify_attn_workspace_bytes(kv, d.num_q_heads, d.total_q, d.max_q, max_seq_len)
+    ws = attn_workspace_bytes(kv, d, max_seq_len)
     n = 2 + (2 if ws > 0 else 1) + 2 + (2 if d.mask_kind == L.SV_MASK_TREE else 1)
     return n
