@@ -1,0 +1,32 @@
+// Which kernel takes a call of sv_spec_verify_attn_scored.
+#include <algorithm>
+
+#include "sv_internal.cuh"
+
+namespace sv {
+namespace scored {
+template <int D, bool F8>
+cudaError_t pick(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);
+}
+
+// bf16 and E4M3 caches with heads of 64, 128 or 256 values (attn_scored.cuh).
+bool attn_scored_mma_fits(const ScoredArgs &sa) {
+  const KV &kv = sa.a.kv;
+  if (kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return false;
+  // positions of the work order (at most one tile and two lead-in positions more per 64 keys and unit of 8
+  // rows) and the combine's grid stay in range
+  const long long rows = (long long)(sa.a.num_q_heads / kv.num_kv_heads) * sa.a.max_q;
+  const long long units = (long long)kv.batch * kv.num_kv_heads * ((rows + 63) / 64);
+  return units * (sa.a.max_seq_len / 64 + 3) < (1LL << 30) && kv.num_kv_heads * ((rows + 63) / 64) <= 65535;
+}
+
+cudaError_t launch_attn_scored_mma(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {
+  const bool f8 = sa.a.kv.fp8;
+  switch (sa.a.kv.head_dim) {
+    case 64: return f8 ? scored::pick<64, true>(sa, workspace, bytes, st, go) : scored::pick<64, false>(sa, workspace, bytes, st, go);
+    case 128: return f8 ? scored::pick<128, true>(sa, workspace, bytes, st, go) : scored::pick<128, false>(sa, workspace, bytes, st, go);
+    default: return f8 ? scored::pick<256, true>(sa, workspace, bytes, st, go) : scored::pick<256, false>(sa, workspace, bytes, st, go);
+  }
+}
+
+}  // namespace sv

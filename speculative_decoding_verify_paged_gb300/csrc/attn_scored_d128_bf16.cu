@@ -1,0 +1,8 @@
+// Attention with modified scores: heads of 128 values, bf16 caches (attn_scored.cuh).
+#include <algorithm>
+
+#include "attn_scored.cuh"
+
+namespace sv {
+template cudaError_t scored::pick<128, false>(const ScoredArgs &, void *, size_t *, cudaStream_t, bool);
+}

@@ -1,0 +1,8 @@
+// Attention with modified scores: heads of 256 values, e4m3 caches (attn_scored.cuh).
+#include <algorithm>
+
+#include "attn_scored.cuh"
+
+namespace sv {
+template cudaError_t scored::pick<256, true>(const ScoredArgs &, void *, size_t *, cudaStream_t, bool);
+}

@@ -341,7 +341,16 @@ size_t sv_spec_verify_attn_scored_workspace_bytes(const sv_paged_kv *kv, int32_t
   if (kv == nullptr || num_q_heads <= 0 || kv->num_kv_heads <= 0 || num_q_heads % kv->num_kv_heads != 0 ||
       total_q < 0 || max_q_per_seq < 1 || max_q_per_seq > kMaxQ || max_seq_len <= 0)
     return 0;
-  return split_workspace(kv, num_q_heads, total_q, max_seq_len);
+  ScoredArgs sa;
+  std::memset(&sa, 0, sizeof sa);
+  sa.a.kv = make_kv(*kv);
+  sa.a.num_q_heads = num_q_heads;
+  sa.a.max_q = max_q_per_seq;
+  sa.a.max_seq_len = max_seq_len;
+  if (!attn_scored_mma_fits(sa)) return split_workspace(kv, num_q_heads, total_q, max_seq_len);
+  size_t need = 0;
+  launch_attn_scored_mma(sa, nullptr, &need, nullptr, false);
+  return need;
 }
 
 sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void *out, const int32_t *cu_q,
@@ -359,8 +368,8 @@ sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void 
     return SV_ERR_INVALID_ARG;
   if (kv->batch == 0 || total_q == 0) return SV_OK;
   if (q == nullptr || out == nullptr || cu_q == nullptr || !aligned16(q) || !aligned16(out)) return SV_ERR_INVALID_ARG;
-  if (kv->head_dim % 32 != 0) return SV_ERR_UNSUPPORTED;
-  const size_t need =
+  if (kv->head_dim % 32 != 0 || kv->batch > 65535) return SV_ERR_UNSUPPORTED;
+  size_t need =
       sv_spec_verify_attn_scored_workspace_bytes(kv, num_q_heads, total_q, max_q_per_seq, max_seq_len);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || ((uintptr_t)workspace & 255u) != 0))
     return SV_ERR_WORKSPACE;
@@ -391,6 +400,7 @@ sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void 
   sa.slopes = mod->slopes;
   sa.positions = positions;
   cudaStream_t st = (cudaStream_t)stream;
+  if (attn_scored_mma_fits(sa)) return cuda_status(launch_attn_scored_mma(sa, workspace, &need, st, true));
   return cuda_status(launch_attn_scored_simt(sa, kv->dtype, st));
 }
 
