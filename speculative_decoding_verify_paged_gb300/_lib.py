@@ -210,10 +210,10 @@ class PagedKV:
     def struct(self) -> sv_paged_kv:
         nb, hkv, bs, d = self.k_pool.shape
         return sv_paged_kv(
-            _ptr(self.k_pool), _ptr(self.v_pool), _ptr(self.block_table), _ptr(self.seq_lens),
-            _ptr(self.free_list), _ptr(self.free_top), nb, bs, self.block_table.shape[1], hkv, d,
+            _at(self.k_pool), _at(self.v_pool), _at(self.block_table), _at(self.seq_lens),
+            _at(self.free_list), _at(self.free_top), nb, bs, self.block_table.shape[1], hkv, d,
             self.seq_lens.shape[0], SV_DTYPE_E4M3 if self.k_pool.dtype == torch.uint8 else _dtype_code(self.k_pool),
-            _ptr(self.ref_count), float(self.k_scale), float(self.v_scale))
+            _at(self.ref_count), self.k_scale, self.v_scale)
 
     @property
     def batch(self) -> int:
@@ -282,13 +282,13 @@ class HeadTransform:
         for w in (self.q_weight, self.k_weight):
             if w is not None and (w.dtype != rows.dtype or w.numel() != d):
                 raise ValueError(f"a norm weight holds {d} values of {rows.dtype}")
-        rot = 0
-        if self.inv_freq is not None:
-            if self.inv_freq.dtype != torch.float32:
+        rot, freq = 0, self.inv_freq
+        if freq is not None:
+            if freq.dtype != torch.float32:
                 raise TypeError("inv_freq is float32")
-            rot = 2 * self.inv_freq.numel()
-        return sv_head_transform(_ptr(self.inv_freq) if rot else None, _ptr(self.q_weight), _ptr(self.k_weight), self.eps,
-                                 self.weight_offset, rot, int(self.interleaved))
+            rot = 2 * freq.numel()
+        return sv_head_transform(_at(freq) if rot else None, _at(self.q_weight), _at(self.k_weight), self.eps,
+                                 self.weight_offset, rot, self.interleaved)
 
 
 @dataclass
@@ -302,7 +302,18 @@ class ScoreMod:
     def struct(self, num_q_heads: int) -> sv_score_mod:
         if self.slopes is not None and (self.slopes.dtype != torch.float32 or self.slopes.numel() != num_q_heads):
             raise ValueError(f"slopes holds {num_q_heads} float32 values")
-        return sv_score_mod(_ptr(self.slopes), self.softcap, self.window)
+        return sv_score_mod(_at(self.slopes), self.softcap, self.window)
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    """_ptr as a plain number (a pointer argument takes it without an object of its own)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("libspecverify takes CUDA tensors only")
+    if not t.is_contiguous():
+        raise ValueError("libspecverify takes contiguous tensors only")
+    return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, like: Optional[torch.Tensor] = None) -> tuple:
@@ -325,16 +336,17 @@ def _i32(t: Optional[torch.Tensor], n: int, what: str) -> Optional[int]:
         return None
     if t.dtype != torch.int32 or t.numel() != n:
         raise ValueError(f"{what} holds {n} int32 values")
-    return _ptr(t)
+    return _at(t)
 
 
 def _stream_of(t: torch.Tensor, stream) -> int:
     """The stream to launch on: the caller's, or the current one. The library launches on the
     current device, which has to be the tensors'."""
-    if t.device.index != torch.cuda.current_device():
+    device = t.get_device()
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {t.device}, the current device is {torch.cuda.current_device()}")
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -354,7 +366,7 @@ def qk_norm_rope(transform: HeadTransform, q: Optional[torch.Tensor], k: Optiona
         (kp, ks), (ko, kos), hkv = _rows(k), _rows(k_out, k), k.shape[1]
         if k.shape[0] != n or k.shape[2] != d or k.dtype != some.dtype:
             raise ValueError("q and k have the same rows, head_dim and type")
-    _check(load().sv_qk_norm_rope(ctypes.byref(transform.struct(some)), qp, qs, qo, qos, hq, kp, ks, ko, kos, hkv, d,
+    _check((_lib or load()).sv_qk_norm_rope(ctypes.byref(transform.struct(some)), qp, qs, qo, qos, hq, kp, ks, ko, kos, hkv, d,
                                   _dtype_code(some), n, _i32(positions, n, "positions"), _stream_of(some, stream)),
            "sv_qk_norm_rope")
 
@@ -375,7 +387,7 @@ def kv_append_rope(kv: PagedKV, transform: HeadTransform, new_k: torch.Tensor, n
         if q.shape[0] != n or q.shape[2] != d or q.dtype != rows:
             raise ValueError(f"expected queries [{n}, heads, {d}] of {rows}")
         (qp, qs), (qo, qos), hq = _rows(q), _rows(q_out, q), q.shape[1]
-    _check(load().sv_kv_append_rope(ctypes.byref(s), ctypes.byref(transform.struct(new_k)), kp, ks, vp, vs, qp, qs, qo,
+    _check((_lib or load()).sv_kv_append_rope(ctypes.byref(s), ctypes.byref(transform.struct(new_k)), kp, ks, vp, vs, qp, qs, qo,
                                     qos, hq, _i32(cu_q, s.batch + 1, "cu_q"), n, _i32(positions, n, "positions"),
                                     _i32(status, 1, "status"), _stream_of(new_k, stream)), "sv_kv_append_rope")
 
@@ -400,15 +412,15 @@ def spec_verify_attn_scored(kv: PagedKV, q: torch.Tensor, out: torch.Tensor, cu_
         raise ValueError(f"expected queries and outputs [n, heads, {s.head_dim}] of {rows}")
     if tree_mask is not None and (tree_mask.element_size() != 8 or tree_mask.numel() != n):
         raise ValueError(f"tree_mask holds {n} 64-bit values")
-    lib, kvp, st = load(), ctypes.byref(s), _stream_of(q, stream)
+    lib, kvp, st = _lib or load(), ctypes.byref(s), _stream_of(q, stream)
     if workspace is None:
         need = lib.sv_spec_verify_attn_scored_workspace_bytes(kvp, hq, n, max_q, max_seq_len)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        if stream is not None and st != torch.cuda.current_stream().cuda_stream:
+        workspace = q.new_empty(max(need, 1), dtype=torch.uint8)
+        if stream is not None and st != torch._C._cuda_getCurrentRawStream(q.get_device()):
             workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(st))
     _check(lib.sv_spec_verify_attn_scored(
-        kvp, _ptr(q), _ptr(out), _i32(cu_q, s.batch + 1, "cu_q"), hq, n, max_q, max_seq_len, scale,
-        ctypes.byref(mod.struct(hq)), _i32(positions, n, "positions"), mask_kind, _ptr(tree_mask), _ptr(workspace),
+        kvp, _at(q), _at(out), _i32(cu_q, s.batch + 1, "cu_q"), hq, n, max_q, max_seq_len, scale,
+        ctypes.byref(mod.struct(hq)), _i32(positions, n, "positions"), mask_kind, _at(tree_mask), _at(workspace),
         workspace.numel() * workspace.element_size(), _i32(status, 1, "status"), st), "sv_spec_verify_attn_scored")
 
 

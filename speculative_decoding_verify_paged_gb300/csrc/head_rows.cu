@@ -10,22 +10,27 @@
 // angle is the exact product of the position and the fp32 frequency up to one rounding in fp64,
 // reduced to a fraction of a turn there: in fp32 the angle of position 10^5 would be off by 4e-3.
 //
-// A CTA takes one row. A lane holds 8 consecutive values of a head, a group of pow2ceil(D / 8)
-// lanes a head, so a row's heads are slots of a group each, spread over the CTA's warps. A
-// thread's place in its head is the same in all its slots, so its 8 weights (query and key) and
-// its 8 (cos, sin) are loaded once. The sum of squares is a butterfly over the group; the
-// rotation's partners are a shuffle away (rot a multiple of 16), in the same lane (interleaved),
-// or exchanged through shared memory.
+// A lane holds 8 consecutive values of a head, a group of pow2ceil(D / 8) lanes a head, a warp
+// 32 / group heads at a time (an iteration). A warp's item is a chunk of one row's iterations, queries,
+// keys and values in turn, and needs no other warp: it makes a (cos, sin) table of the row and folds it
+// with the norm's weights into two factors per value, once per kind of head, so that a head costs
+//   out_j = r (x_j A_j + x'_j B_j),  A = cos * w,  B = +-sin * w',  r = rsqrt(mean x^2 + eps)
+// with x' the pair's other value and w' its weight: a shuffle of the row's packed words away (rot a
+// multiple of 16), in the same lane (interleaved, rot a multiple of 8), or exchanged through
+// shared memory (the kernel for other sizes of heads and rotations).
 //
-// The work is bound by memory: every value is read once and written once.
+// Bound: memory, every value read once and written once; next to it the issue of instructions (some
+// 80 an iteration of 512 bytes), which is why the head size is a template parameter where it is 64,
+// 128 or 256 and nothing but shuffles, products and conversions is left in the loop. Long
+// batches take whole rows as items; short ones are cut until every resident warp has a chunk.
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "kv_rows.cuh"
 
 namespace sv {
 namespace {
-
-constexpr int kSlotsAhead = 4;  // slots of a thread whose loads are in flight together
 
 template <typename T> struct Vec8;  // 8 values of a row as loaded
 template <> struct Vec8<__nv_bfloat16> {
@@ -71,27 +76,39 @@ template <> struct Vec8<float> {
   }
 };
 
-// 8 fp32 values -> E4M3 codes of x / scale (fp32 division; nearest, ties to even; saturating)
-__device__ __forceinline__ uint2 quantize8(const float (&x)[8], float scale) {
+// 8 fp32 values -> E4M3 codes of x / scale (fp32 division; nearest, ties to even; saturating). inv: 1 / scale
+// where that is exact (a power of two, the division's result bit for bit), else 0.
+__device__ __forceinline__ uint2 quantize8(const float (&x)[8], float scale, float inv) {
   uint32_t w[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     w[q] = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float2 v = make_float2(__fdiv_rn(x[4 * q + 2 * h], scale), __fdiv_rn(x[4 * q + 2 * h + 1], scale));
+      const float x0 = x[4 * q + 2 * h], x1 = x[4 * q + 2 * h + 1];
+      const float2 v = inv != 0.f ? make_float2(x0 * inv, x1 * inv) : make_float2(__fdiv_rn(x0, scale), __fdiv_rn(x1, scale));
       w[q] |= (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3) << (16 * h);
     }
   }
   return make_uint2(w[0], w[1]);
 }
 
-// cos and sin of position * freq
+// cos and sin of position * freq. A turn is 2^64: freq = M 2^E turns by M 2^E / (2 pi) per position, the
+// product of M with the first 64 bits of 2^66 / (2 pi), shifted; times the position it wraps exactly.
+// Off by under |position freq| 2^-64 turns; the upper 32 bits, rounded to fp32, go to sincospif.
 __device__ __forceinline__ float2 turn(int position, float freq) {
-  const double turns = (double)position * (double)freq * 0.15915494309189535;  // radians / (2 pi)
-  float s, c;
-  sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-  return make_float2(c, s);
+  const uint32_t bits = __float_as_uint(freq);
+  const int e = (bits >> 23) & 255;
+  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u), k = 0xa2f9836e4e44152aull;
+  const unsigned long long hi = __umul64hi(m, k), lo = m * k;
+  const int s = 152 - (e ? e : 1);  // 2 - E
+  unsigned long long per = s >= 64 ? (s < 128 ? hi >> (s - 64) : 0ull)
+                                   : s > 0 ? (hi << (64 - s)) | (lo >> s) : (s > -64 ? lo << -s : 0ull);
+  if (bits >> 31) per = 0ull - per;
+  const unsigned long long f = (unsigned long long)(long long)position * per;
+  float sn, cs;
+  sincospif((float)(int)(f >> 32) * 4.656612873077393e-10f /* 2^-31 */, &sn, &cs);
+  return make_float2(cs, sn);
 }
 
 // The last b < n with cu[b] <= row (0 if none), by the whole warp: 32 probes at a time.
@@ -108,46 +125,78 @@ __device__ __forceinline__ int owner_of(const int32_t *cu, int n, int row) {
   return lo;
 }
 
-// APPEND: keys and values go to the cache (kv, cu_q, status); else keys go to k_out.
-template <typename T, bool APPEND>
-__global__ void __launch_bounds__(256) head_rows_kernel(const HeadArgs a) {
-  __shared__ float2 s_turn[128];     // (cos, sin) of the row's angles
-  __shared__ float s_swap[8][32 * 8];  // partners that neither a shuffle nor the lane itself holds
+constexpr int kThreads = 128;
+constexpr int kCtasPerSm = 5;
+
+// The pair's other values x' of a lane's 8.
+template <typename T> __device__ __forceinline__ void from_lane(const Vec8<T> &x, int lane, float (&p)[8]);
+template <> __device__ __forceinline__ void from_lane(const Vec8<__nv_bfloat16> &x, int lane, float (&p)[8]) {
+  Vec8<__nv_bfloat16> y;
+  y.r.x = __shfl_sync(0xffffffffu, x.r.x, lane);
+  y.r.y = __shfl_sync(0xffffffffu, x.r.y, lane);
+  y.r.z = __shfl_sync(0xffffffffu, x.r.z, lane);
+  y.r.w = __shfl_sync(0xffffffffu, x.r.w, lane);
+  y.get(p);
+}
+template <> __device__ __forceinline__ void from_lane(const Vec8<float> &x, int lane, float (&p)[8]) {
+  float v[8];
+  x.get(v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) p[j] = __shfl_sync(0xffffffffu, v[j], lane);
+}
+
+enum Pairs { kShuffle, kInLane, kExchange };  // where a value's pair is
+
+// APPEND: keys and values go to the cache (kv, cu_q, status); else keys go to k_out. DIM: the head
+// size, or 0: any (with PAIRS == kExchange). A warp takes chunk x % chunks of row x / chunks.
+template <typename T, bool APPEND, int PAIRS, int DIM>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const HeadArgs a, int chunks, int per_chunk,
+                                                                         long long items) {
+  constexpr int kAhead = sizeof(T) == 2 ? 5 : 3;  // iterations whose loads are in flight together
+  constexpr int kEsz = sizeof(T);
+  __shared__ float2 s_turn[kThreads / 32][128];
+  __shared__ float s_swap[PAIRS == kExchange ? kThreads / 32 : 1][32 * 8];
   if (!APPEND) {
     // what follows on the stream may read the rows before its own dependency wait: this kernel
     // lets it start only when it is complete (no grid_dependents_launch)
     grid_dependency_wait();
   }
-  const int row = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_head = a.head_dim >> 3;  // lanes that hold a head
-  const int gsh = 31 - __clz(2 * per_head - 1), gl = 1 << gsh;  // lanes of a head's group
-  const int place = lane & (gl - 1);     // this thread's 8 values of a head
-  const bool holds = place < per_head;
-  const int heads = a.hq + a.hkv * (APPEND ? 2 : 1);  // queries, keys, values
-  const int groups = blockDim.x >> gsh;
-  const int group = threadIdx.x >> gsh;
-  const size_t esz = sizeof(T);
-  const uint8_t *qrow = a.q + (size_t)row * a.q_stride;
-  const uint8_t *krow = a.k + (size_t)row * a.k_stride;
-  const uint8_t *vrow = a.v + (size_t)row * a.v_stride;
-  auto src = [&](int h) -> const uint8_t * {
-    const uint8_t *base = h < a.hq ? qrow + (size_t)h * a.head_dim * esz
-                          : h < a.hq + a.hkv ? krow + (size_t)(h - a.hq) * a.head_dim * esz
-                                             : vrow + (size_t)(h - a.hq - a.hkv) * a.head_dim * esz;
-    return base + (size_t)place * 8 * esz;
-  };
-  // The rows, weights, frequencies, positions, cu_q and (append) lengths are complete before this
-  // kernel starts: kv_alloc_kernel, the one ahead of it, writes none of them and let it launch
-  // only after its own dependency wait. What that kernel writes is read after the wait below.
-  Vec8<T> x[kSlotsAhead];
-#pragma unroll
-  for (int u = 0; u < kSlotsAhead; ++u) {
-    const int h = group + u * groups;
-    if (h < heads && holds) x[u].load(src(h));
-    else x[u].zero();
+  const int dim = DIM ? DIM : a.head_dim, per_head = dim >> 3;  // lanes that hold a head
+  const int gsh = DIM == 64 ? 3 : DIM == 128 ? 4 : DIM == 256 ? 5 : 31 - __clz(2 * per_head - 1);
+  const int gl = 1 << gsh, hpw = 32 >> gsh;  // lanes of a head's group, heads of an iteration
+  const int place = lane & (gl - 1), sub = lane >> gsh;
+  const bool holds = DIM != 0 || place < per_head;
+  const int nq = (a.hq + hpw - 1) / hpw, nk = (a.hkv + hpw - 1) / hpw;
+  const int all = nq + nk + (APPEND ? nk : 0);  // iterations of a row
+  const int half = a.rot >> 1, hl = half >> 3;
+  const long long item = (long long)blockIdx.x * (kThreads / 32) + warp;
+  const int row = (int)(item / chunks), i0 = (int)(item - (long long)row * chunks) * per_chunk, i1 = min(all, i0 + per_chunk);
+  if (item >= items || i0 >= i1) {
+    if (APPEND) grid_dependency_wait();  // completion stays transitive along the stream
+    return;
   }
-  int b = 0, i = 0, n = 1, c = 0, pos = 0;
+  // The rows, weights, frequencies, positions, cu_q and lengths are complete before this kernel
+  // starts: the append's kernel ahead of it writes none of them and let it launch only after its own
+  // dependency wait. What that kernel writes is read after the wait below.
+  const size_t in_head = (size_t)sub * dim + place * 8;  // this lane's values of an iteration
+  const uint8_t *in_q = a.q + (size_t)row * a.q_stride + in_head * kEsz;
+  const uint8_t *in_k = a.k + (size_t)row * a.k_stride + in_head * kEsz;
+  const uint8_t *in_v = APPEND ? a.v + (size_t)row * a.v_stride + in_head * kEsz : nullptr;
+  const int step = hpw * dim;  // values of an iteration
+  Vec8<T> x[kAhead];
+  // iterations [it, it + kAhead) of a kind that begins at iteration `first` and ends before `end`
+  auto load = [&](const uint8_t *in, int count, int it, int end, int first) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = it + u - first;
+      if (it + u < end && holds && k * hpw + sub < count) x[u].load(in + (size_t)k * step * kEsz);
+      else x[u].zero();
+    }
+  };
+  const int kind0 = i0 < nq ? 0 : i0 < nq + nk ? 1 : 2;
+  load(kind0 == 0 ? in_q : kind0 == 1 ? in_k : in_v, kind0 == 0 ? a.hq : a.hkv, i0, min(i1, kind0 == 0 ? nq : kind0 == 1 ? nq + nk : all), kind0 == 0 ? 0 : kind0 == 1 ? nq : nq + nk);
+  int b = 0, i = 0, n = 1, c = 0;
   if (APPEND) {
     b = owner_of(a.cu_q, a.kv.batch, row);
     const int row0 = a.cu_q[b];
@@ -155,129 +204,138 @@ __global__ void __launch_bounds__(256) head_rows_kernel(const HeadArgs a) {
     n = a.cu_q[b + 1] - row0;
     c = a.kv.seq_lens[b];
   }
-  if (a.positions != nullptr) pos = a.positions[row];
-  else pos = c + i;
-  const int half = a.rot >> 1;
-  for (int e = threadIdx.x; e < half; e += blockDim.x) s_turn[e] = turn(pos, a.inv_freq[e]);
-  Vec8<T> qw, kw;
-  qw.zero();
-  kw.zero();
-  if (holds && a.q_weight != nullptr) qw.load(a.q_weight + (size_t)place * 8 * esz);
-  if (holds && a.k_weight != nullptr) kw.load(a.k_weight + (size_t)place * 8 * esz);
-  __syncthreads();
-  // this thread's values of a head: value j turns by (cs[j], sn[j]), sn with the sign its partner takes
-  float cs[8], sn[8];
-  uint32_t turns = 0;  // bit j: value j is rotated
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int e = place * 8 + j;
-    cs[j] = 1.f;
-    sn[j] = 0.f;
-    if (e < a.rot) {
-      const bool first = a.interleaved ? (e & 1) == 0 : e < half;
-      const float2 t = s_turn[a.interleaved ? e >> 1 : (first ? e : e - half)];
-      cs[j] = t.x;
-      sn[j] = first ? -t.y : t.y;
-      turns |= 1u << j;
-    }
+  if (kind0 < 2 && half > 0) {
+    const int pos = a.positions != nullptr ? a.positions[row] : c + i;
+    for (int e = lane; e < half; e += 32) s_turn[warp][e] = turn(pos, a.inv_freq[e]);
+    __syncwarp();
   }
-  const bool by_shuffle = !a.interleaved && (half & 7) == 0;
-  const int hl = half >> 3;
-  const int partner = (lane & ~(gl - 1)) + (place < hl ? place + hl : place < 2 * hl ? place - hl : place);
-
-  int blk = 0, slot = 0;
-  bool write = true;
+  uint8_t *out[3] = {a.q_out + (size_t)row * a.q_out_stride + in_head * kEsz,
+                     APPEND ? nullptr : a.k_out + (size_t)row * a.k_out_stride + in_head * kEsz, nullptr};
+  size_t out_step[2] = {(size_t)step * kEsz, (size_t)step * kEsz};  // of an iteration: queries; keys and values
   if (APPEND) {
     grid_dependency_wait();
     grid_dependents_launch();
     if (status_set(a.status)) return;
     if (i < 0 || i >= n) return;  // rows past cu_q[batch]: nothing to write
-    const int at = c + i;
-    blk = a.kv.block_table[(size_t)b * a.kv.max_blocks + at / a.kv.block_size];
+    const int at = c + i, bsh = __ffs(a.kv.block_size) - 1;
+    const int blk = a.kv.block_table[(size_t)b * a.kv.max_blocks + (at >> bsh)];
     if (blk < 0 || blk >= a.kv.num_blocks) {
-      if (threadIdx.x == 0) record(a.status, SV_ERR_BAD_BLOCK_ID);
+      if (lane == 0) record(a.status, SV_ERR_BAD_BLOCK_ID);
       return;
     }
-    slot = at % a.kv.block_size;
-    if (i == 0 && slot > 0 && a.kv.ref_count != nullptr)
-      copy_shared_block(a.kv, blk, slot, a.kv.head_dim * a.kv.elem_bytes, a.status);
+    const int eb = a.kv.elem_bytes;
+    const size_t off =
+        (((((size_t)blk * a.hkv + sub) << bsh) + (at & (a.kv.block_size - 1))) * dim + place * 8) * eb;
+    out[1] = reinterpret_cast<uint8_t *>(a.kv.k_pool) + off;
+    out[2] = reinterpret_cast<uint8_t *>(a.kv.v_pool) + off;
+    out_step[1] = ((size_t)hpw * dim << bsh) * eb;
   }
 
-  for (int base = 0; base < heads; base += kSlotsAhead * groups) {
-    if (base > 0) {
+  const int other = place < hl ? place + hl : place < 2 * hl ? place - hl : place;  // the pair's place (kShuffle)
+  const bool turned = PAIRS == kExchange || place * 8 < a.rot;                      // this lane's values are rotated
 #pragma unroll
-      for (int u = 0; u < kSlotsAhead; ++u) {
-        const int h = base + group + u * groups;
-        if (h < heads && holds) x[u].load(src(h));
-        else x[u].zero();
-      }
-    }
+  for (int kind = 0; kind < (APPEND ? 3 : 2); ++kind) {
+    const int first = kind == 0 ? 0 : kind == 1 ? nq : nq + nk;
+    const int lo = max(i0, first), end = min(i1, kind == 0 ? nq : kind == 1 ? nq + nk : all);
+    if (lo >= end) continue;  // uniform
+    const int count = kind == 0 ? a.hq : a.hkv;
+    const uint8_t *weight = kind == 0 ? a.q_weight : a.k_weight;
+    float A[8], Bf[8];   // the kind's factors
+    uint32_t turns = 0;  // kExchange: bit j: value j is rotated
+    if (kind < 2) {
+      float w[8], wo[8];
 #pragma unroll
-    for (int u = 0; u < kSlotsAhead; ++u) {
-      const int h = base + group + u * groups;
-      if (base + u * groups >= heads) break;  // uniform: no thread has this slot
-      write = h < heads && holds;
-      const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
-      float y[8];
-      x[u].get(y);
-      // the norm
-      const bool norm = is_q ? a.q_weight != nullptr : (!is_v && a.k_weight != nullptr);
-      float ss = 0.f;
+      for (int j = 0; j < 8; ++j) w[j] = wo[j] = 1.f;
+      if (weight != nullptr && holds) {
+        Vec8<T> v;
+        v.load(weight + place * 8 * kEsz);
+        v.get(w);
+        if (PAIRS == kShuffle) {
+          v.load(weight + other * 8 * kEsz);
+          v.get(wo);
+        } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
-      for (int o = gl >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (norm) {
-        const float r = rsqrtf(ss * a.inv_dim + a.eps);
-        float w[8];
-        if (is_q) qw.get(w);
-        else kw.get(w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = y[j] * r * (w[j] + a.offset);
-      }
-      // the rotation
-      float p[8];
-      if (by_shuffle) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = __shfl_sync(0xffffffffu, y[j], partner);
-      } else if (a.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = y[j ^ 1];
-      } else {
-        float *sw = s_swap[warp];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sw[lane * 8 + j] = y[j];
-        __syncwarp();
+          for (int j = 0; j < 8; ++j) {
+            const int e = place * 8 + j, o = a.interleaved ? e ^ 1 : e < half ? e + half : e - half;
+            if (PAIRS == kInLane) wo[j] = w[j ^ 1];
+            else if (e < a.rot) wo[j] = to_f32(reinterpret_cast<const T *>(weight)[o]);
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int e = place * 8 + j;
-          const int q = e < half ? e + half : e < a.rot ? e - half : e;
-          p[j] = sw[(lane & ~(gl - 1)) * 8 + q];
+          w[j] += a.offset;
+          wo[j] += a.offset;
         }
-        __syncwarp();
       }
-      if (!is_v) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if ((turns >> j) & 1u) y[j] = fmaf(y[j], cs[j], p[j] * sn[j]);
+      for (int j = 0; j < 8; ++j) {
+        const int e = place * 8 + j;
+        A[j] = w[j];
+        Bf[j] = 0.f;
+        if (e < a.rot) {
+          const bool lower = PAIRS == kInLane || (PAIRS == kExchange && a.interleaved) ? (j & 1) == 0 : e < half;
+          const bool pairs2 = PAIRS == kInLane || (PAIRS == kExchange && a.interleaved);
+          const float2 t = s_turn[warp][pairs2 ? e >> 1 : (lower ? e : e - half)];
+          A[j] = t.x * w[j];
+          Bf[j] = lower ? -t.y * wo[j] : t.y * wo[j];
+          turns |= 1u << j;
+        }
       }
-      if (!write) continue;
-      // the output, rounded once
-      if (is_q) {
-        x[u].set(y);
-        x[u].store(a.q_out + (size_t)row * a.q_out_stride + ((size_t)h * a.head_dim + place * 8) * esz);
-      } else if (!APPEND) {
-        x[u].set(y);
-        x[u].store(a.k_out + (size_t)row * a.k_out_stride + ((size_t)(h - a.hq) * a.head_dim + place * 8) * esz);
-      } else {
-        const int kvh = is_v ? h - a.hq - a.hkv : h - a.hq;
-        const size_t at =
-            (((size_t)blk * a.hkv + kvh) * a.kv.block_size + slot) * a.head_dim + (size_t)place * 8;  // value in the pool
-        uint8_t *pool = reinterpret_cast<uint8_t *>(is_v ? a.kv.v_pool : a.kv.k_pool);
-        if (a.kv.fp8) {
-          *reinterpret_cast<uint2 *>(pool + at) = quantize8(y, is_v ? a.kv.v_scale : a.kv.k_scale);
+    }
+    for (int it = lo; it < end; it += kAhead) {
+      if (it > i0) load(kind == 0 ? in_q : kind == 1 ? in_k : in_v, count, it, end, first);  // the item's first loads are on their way since its start
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (it + u >= end) break;  // uniform
+        const int k = it + u - first;
+        float y[8];
+        if (kind < 2 || a.kv.fp8) x[u].get(y);
+        if (kind < 2) {
+          float r = 1.f;
+          if (weight != nullptr) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
+            if (DIM) {
+#pragma unroll
+              for (int o = 1; o < DIM / 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            } else {
+              for (int o = 1; o < gl; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            }
+            r = rsqrtf(ss * a.inv_dim + a.eps);
+          }
+          float p[8];
+          if (PAIRS == kShuffle) {
+            from_lane(x[u], (lane & ~(gl - 1)) + other, p);
+          } else if (PAIRS == kInLane) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = y[j ^ 1];
+          } else {
+            float *sw = s_swap[warp];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sw[lane * 8 + j] = y[j];
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int e = place * 8 + j, o = a.interleaved ? e ^ 1 : e < half ? e + half : e - half;
+              p[j] = sw[(lane & ~(gl - 1)) * 8 + ((turns >> j) & 1u ? o : e)];
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const bool rotate = PAIRS == kExchange ? ((turns >> j) & 1u) != 0 : turned;
+            y[j] = r * (rotate ? fmaf(p[j], Bf[j], y[j] * A[j]) : y[j] * A[j]);
+          }
+        }
+        if (!holds || k * hpw + sub >= count) continue;
+        // the output, rounded once
+        uint8_t *dst = out[kind] + (size_t)k * out_step[kind > 0];
+        if (APPEND && kind > 0 && a.kv.fp8) {
+          *reinterpret_cast<uint2 *>(dst) = quantize8(y, kind == 2 ? a.kv.v_scale : a.kv.k_scale, kind == 2 ? a.v_inv : a.k_inv);
         } else {
-          if (!is_v) x[u].set(y);  // values are copied as they are
-          x[u].store(pool + at * esz);
+          if (kind < 2) x[u].set(y);  // values are copied as they are
+          x[u].store(dst);
         }
       }
     }
@@ -288,15 +346,46 @@ template <typename T, bool APPEND>
 cudaError_t launch_rows(const HeadArgs &a, int total_q, cudaStream_t st) {
   int gl = 1;
   while (gl < a.head_dim / 8) gl *= 2;
-  const int lanes = (a.hq + a.hkv * (APPEND ? 2 : 1)) * gl;
-  int threads = 64;
-  while (threads < 256 && threads * (kSlotsAhead - 1) < lanes) threads *= 2;
-  return launch_pdl(head_rows_kernel<T, APPEND>, dim3((unsigned)total_q), dim3(threads), 0, st, a);
+  const int hpw = 32 / gl, nk = ceil_div(a.hkv, hpw);
+  const int all = ceil_div(a.hq, hpw) + nk * (APPEND ? 2 : 1);
+  // as many iterations an item as give every resident warp one, whole rows at most
+  const long long warps = (long long)num_sms() * kCtasPerSm * (kThreads / 32);
+  const int per_chunk = (int)std::min<long long>(all, ((long long)all * total_q + warps - 1) / warps);
+  const int chunks = ceil_div(all, per_chunk);
+  const long long items = (long long)total_q * chunks;
+  const unsigned ctas = (unsigned)((items + kThreads / 32 - 1) / (kThreads / 32));
+  auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(ctas), dim3(kThreads), 0, st, a, chunks, per_chunk, items); };
+  const int d = a.head_dim;
+  if (d == 64 || d == 128 || d == 256) {
+    if (!a.interleaved && a.rot % 16 == 0)
+      return d == 64 ? go(head_rows_kernel<T, APPEND, kShuffle, 64>) : d == 128 ? go(head_rows_kernel<T, APPEND, kShuffle, 128>)
+                                                                               : go(head_rows_kernel<T, APPEND, kShuffle, 256>);
+    if (a.interleaved && a.rot % 8 == 0)
+      return d == 64 ? go(head_rows_kernel<T, APPEND, kInLane, 64>) : d == 128 ? go(head_rows_kernel<T, APPEND, kInLane, 128>)
+                                                                              : go(head_rows_kernel<T, APPEND, kInLane, 256>);
+  }
+  return go(head_rows_kernel<T, APPEND, kExchange, 0>);
+}
+
+// One CTA per sequence whose first new row lands in a private copy of a shared block.
+__global__ void __launch_bounds__(256) kv_private_copy_kernel(KV kv, const int32_t *cu_q, int32_t *status) {
+  grid_dependency_wait();  // the allocation is complete and visible
+  grid_dependents_launch();
+  if (status_set(status)) return;
+  const int b = blockIdx.x, c = kv.seq_lens[b], slot = c % kv.block_size;
+  if (cu_q[b + 1] - cu_q[b] < 1 || slot == 0) return;
+  const int blk = kv.block_table[(size_t)b * kv.max_blocks + c / kv.block_size];
+  if (blk < 0 || blk >= kv.num_blocks) return;  // the rows' kernel reports it
+  copy_shared_block(kv, blk, slot, kv.head_dim * kv.elem_bytes, status);
 }
 
 }  // namespace
 
 cudaError_t launch_head_rows(const HeadArgs &a, int dtype, int total_q, bool append, cudaStream_t st) {
+  if (append && a.kv.ref_count != nullptr) {
+    const cudaError_t e = launch_pdl(kv_private_copy_kernel, dim3(a.kv.batch), dim3(256), 0, st, a.kv, a.cu_q, a.status);
+    if (e != cudaSuccess) return e;
+  }
   if (dtype == SV_DTYPE_F32) return append ? launch_rows<float, true>(a, total_q, st) : launch_rows<float, false>(a, total_q, st);
   return append ? launch_rows<__nv_bfloat16, true>(a, total_q, st) : launch_rows<__nv_bfloat16, false>(a, total_q, st);
 }

@@ -1,4 +1,4 @@
-// Shared by the kernels that write a step's rows into the cache.
+// Shared by the kernels that write a step's rows into the cache: copy-on-write's second half.
 #pragma once
 
 #include "sv_internal.cuh"

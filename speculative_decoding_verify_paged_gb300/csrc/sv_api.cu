@@ -125,6 +125,12 @@ sv_status head_args(HeadArgs *a, const sv_head_transform *t, int head_dim, int d
   return SV_OK;
 }
 
+// 1 / x of a power of two whose inverse is a normal number, else 0.
+float exact_inverse(float x) {
+  int e;
+  return x > 0.f && std::isfinite(x) && std::frexp(x, &e) == 0.5f && e > -120 && e < 120 ? 1.f / x : 0.f;
+}
+
 // Rows of `heads` heads, `stride` elements apart: present, 16-byte aligned and not overlapping.
 template <typename P>
 bool head_rows(P *at, long long *bytes, const void *p, int64_t stride, int heads, int head_dim, int dtype) {
@@ -331,6 +337,8 @@ sv_status sv_kv_append_rope(const sv_paged_kv *kv, const sv_head_transform *tran
   a.kv = make_kv(*kv);
   a.cu_q = cu_q;
   a.status = status_dev;
+  a.k_inv = exact_inverse(kv->k_scale);
+  a.v_inv = exact_inverse(kv->v_scale);
   const cudaError_t e = launch_kv_alloc(a.kv, cu_q, status_dev, (cudaStream_t)stream);
   if (e != cudaSuccess || total_q == 0) return cuda_status(e);
   return cuda_status(launch_head_rows(a, dtype, total_q, true, (cudaStream_t)stream));

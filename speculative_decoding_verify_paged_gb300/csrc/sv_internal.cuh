@@ -190,6 +190,7 @@ struct HeadArgs {
   int hq, hkv, head_dim, rot;
   bool interleaved;
   float eps, offset, inv_dim;
+  float k_inv, v_inv;  // 1 / scale of an E4M3 pool where that is exact, else 0
   KV kv;  // append only, with cu_q and status
   const int32_t *cu_q;
   int32_t *status;
