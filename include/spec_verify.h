@@ -591,7 +591,8 @@ sv_status sv_adaptive_k_current(const void *state, int32_t *k);
  *   SV_OPT_WAIT_BUDGET_US (value in microseconds, 1000 .. 2000000; default
  *     500000): how long a pipeline wait (a consumer waiting for the data its
  *     producer brings, a producer waiting for a free stage) of the tcgen05
- *     attention kernels and of the sampler's statistics kernel may take before
+ *     attention kernels, of the warp-matrix kernels of sv_spec_verify_attn_scored
+ *     and of the sampler's statistics kernel may take before
  *     the kernel gives up, records SV_ERR_TIMEOUT in the status word and ends.
  *     A kernel that gives up still waits for the copies and matrix operations
  *     it has issued (at most 0.5 s each, whatever this option says) before it
@@ -602,7 +603,8 @@ sv_status sv_adaptive_k_current(const void *state, int32_t *k);
  *     fail, hence the 1 ms floor.
  *   SV_OPT_STALL_FOR_TEST (SV_STALL_NONE, the default; SV_STALL_ATTENTION;
  *     SV_STALL_SAMPLER): for tests of the failure path only. The producer warp
- *     of the tensor-core attention kernel, or of the sampler's statistics
+ *     of the tensor-core attention kernel (every warp of
+ *     sv_spec_verify_attn_scored's), or of the sampler's statistics
  *     kernel, first waits on a barrier that nothing ever completes, as a
  *     producer whose data never arrives would; that wait runs out after the
  *     wait budget, the producer issues nothing, and every pipeline wait of its

@@ -1,18 +1,38 @@
 // Which kernel takes a call of sv_spec_verify_attn_scored.
 #include <algorithm>
 
+#include <cuda.h>
+
 #include "sv_internal.cuh"
 
 namespace sv {
 namespace scored {
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encoder() {
+  static const EncodeTiledFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
 template <int D, bool F8>
 cudaError_t pick(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);
 }
 
-// bf16 and E4M3 caches with heads of 64, 128 or 256 values (attn_scored.cuh).
+// bf16 and E4M3 caches with heads of 64, 128 or 256 values in blocks of 8 tokens and more
+// (attn_scored.cuh); a TMA row coordinate is a 32-bit number.
 bool attn_scored_mma_fits(const ScoredArgs &sa) {
   const KV &kv = sa.a.kv;
   if (kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return false;
+  if (kv.block_size < 8 || (long long)kv.num_blocks * kv.num_kv_heads * kv.block_size >= (1LL << 31)) return false;
   // positions of the work order (at most one tile and two lead-in positions more per 64 keys and unit of 8
   // rows) and the combine's grid stay in range
   const long long rows = (long long)(sa.a.num_q_heads / kv.num_kv_heads) * sa.a.max_q;

@@ -22,22 +22,29 @@
 // With a window a unit's tiles start at its first visible one: keys out of sight are not read.
 //
 // A CTA's four warps are WK key groups x WR row groups. Every tile of TK keys goes into a ring of
-// kStages shared-memory stages by 16-byte asynchronous copies, all threads taking part, rows
-// swizzled so that ldmatrix reads without bank conflicts; the pool row of each of a tile's keys is
-// looked up one tile before its copy is issued. A warp takes 16 keys at a time:
+// kStages shared-memory stages by TMA, a box per block (or per tile, where blocks are larger), the pool
+// seen as (128 bytes, 8 rows, 128-byte parts of a row, groups of 8 rows) and swizzled so that
+// ldmatrix reads without bank conflicts. The warps take turns in issuing a tile, each a turn after it has
+// read the block ids; a stage is refilled when all four have arrived on its barrier, so that no
+// barrier of the whole CTA is left in the loop. A warp takes 16 keys at a time:
 //   S^T (keys x rows) = K Q^T, A = K (ldmatrix), B = Q held in registers, accumulators fp32;
-//   the running maximum of a row moves only when a score passes it by 2^8 (one vote per 16 keys);
+//   the running maximum of a row moves only when a score passes it by 2^8 (one vote per 16 keys), and
+//   not at all where the cap bounds the scores well enough (kBoundedCap);
 //   P^T = 2^(S^T - m) in bf16 (fp16 for E4M3 pools) turned into a B operand by movmatrix;
 //   O^T (dims x rows) += V^T P^T, A = V^T (ldmatrix.trans), accumulators fp32 in registers.
 // Query rows sit on the n dimension, so that 24 rows (4 heads x 6) cost 24 and not 32. At the end
 // of a piece the WK key groups' (m, l, O) are merged through shared memory.
 //
-// E4M3 codes become fp16 operands in registers, exactly, as the code's value times 2^-8 (the
-// exponent field's place; 2^8 joins the score scale and the output's normalisation). ldmatrix moves
-// pairs of codes; which dimension lands at which place of the operand differs from the bf16 form, and
-// Q's registers and O's columns follow it.
+// A cap's constant term is dropped like the bias's: -2 cap / (1 + 2^(2 y log2 e)) is what is left.
+// E4M3 codes become fp16 operands in registers (exactly). ldmatrix moves pairs of codes; which
+// dimension lands at which place of the operand differs from the bf16 form, and Q's registers and O's
+// columns follow it.
+//
+// All mbarrier waits are bounded: after one that gives up, a warp goes through the rest of its work
+// without waiting (on whatever the stages hold) and the call records SV_ERR_TIMEOUT.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "sv_internal.cuh"
@@ -48,12 +55,17 @@ namespace scored {
 constexpr int kThreads = 128;
 constexpr float kMoveAt = 8.f;     // the running maximum moves when a score passes it by this (log2)
 constexpr float kFastCap = 200.f;  // caps up to this take the two-instruction tanh
+// Capped scores lie within [-2 cap, 0] (the constant dropped): up to this cap (log2 units) weights of
+// 2^-120 and more keep their precision in bf16 and fp32, and no maximum is needed.
+constexpr float kBoundedCap = 60.f;
+constexpr float kNone = -3.3e38f;  // a running maximum before the first visible key
 
 struct Params {
   ScoredArgs s;
   float cap_in;  // what a product is multiplied with to give 2 y log2(e)
   int G;         // query heads per KV head
   int ctas, alpha, rows_cap, rb_max;
+  int box;       // rows of a TMA box: min(block_size, TK)
   float *part_o;    // [ctas][2][rows_cap][D]
   float *part_lse;  // [ctas][2][rows_cap], log2
   int *prefix;      // [batch + 1]: first position of each sequence's units, then all positions
@@ -74,8 +86,8 @@ struct Cfg {
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kPad = D + 4;  // floats of a row in the merge buffer
   static_assert(WK * RB * kPad * 4 <= kRing, "the merge buffer fits the ring");
-  static_assert(TK <= kThreads && TK % (16 * WK) == 0 && RB <= kThreads, "one key and one row per thread");
-  static constexpr size_t kSmem = kRing;
+  static_assert(TK % (16 * WK) == 0 && RB <= kThreads && 2 * (TK / 8) <= 32, "a row per thread, a box per lane");
+  static constexpr size_t kSmem = kRing + 1024;  // the ring starts on a 1 KB boundary
 };
 
 struct Seq {
@@ -117,11 +129,30 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool take) {  // zeros if !take
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// A box of rows from row y (a multiple of 8) on: groups of [part 0: 8 rows x 128 B][part 1: ...]..., or
+// (rows of 64 bytes) as they are.
+template <int ROWB> __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int y, uint32_t bar) {
+  if (ROWB >= 128)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y >> 3), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -158,28 +189,33 @@ template <bool F16> __device__ __forceinline__ uint32_t pack2(float lo, float hi
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
-// Two E4M3 codes of a word as fp16 pairs of their values times 2^-8, exactly: sign on top, then the
-// exponent and mantissa bits one place down (both formats' exponents read with their own bias: 7
-// and 15). SEL puts the two bytes into the upper bytes of the two halves.
-template <int SEL> __device__ __forceinline__ uint32_t widen(uint32_t w) {
-  const uint32_t y = __byte_perm(w, 0u, SEL);
-  return (y & 0x80008000u) | ((y >> 1) & 0x3f803f80u);
+// The E4M3 codes in the lower half of a word as an fp16 pair (exact).
+__device__ __forceinline__ uint32_t widen(uint32_t w) {
+  uint32_t y;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(y) : "r"(w));
+  return y;
 }
-constexpr float kCodeScale = 256.f;  // 2^8: what the operands above lack
+__device__ __forceinline__ uint32_t without_nan(uint32_t x) {  // an fp16 pair, NaN halves set to zero
+  if ((x & 0x7c00u) == 0x7c00u) x &= 0xffff0000u;
+  if ((x & 0x7c000000u) == 0x7c000000u) x &= 0xffffu;
+  return x;
+}
 
 __device__ __forceinline__ bool nonfinite2(uint32_t x) {  // a bf16 pair
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(const Params P) {
+__global__ void __launch_bounds__(kThreads, C::kCtasPerSm)
+    attn_scored_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params P) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
   constexpr int D = C::D, NT = C::NT, TK = C::TK, CH = C::CH, RB = C::RB, WK = C::WK, ST = C::kStages;
   constexpr int KT = D / 16;  // 16-value steps of a head
   constexpr bool F8 = C::F8;
-  extern __shared__ __align__(1024) uint8_t ring[];
-  __shared__ long long s_off[ST][TK];  // byte offset of a key's row in the pools, or -1: zeros
+  extern __shared__ uint8_t smem[];
+  __shared__ __align__(8) uint64_t s_full[ST], s_free[ST];  // a stage's copies have landed; all warps have read it
+  __shared__ int s_dead;                                    // a wait gave up
   __shared__ uint64_t s_mask[RB];      // tree mask of a row
   __shared__ int s_pos[RB], s_row[RB];  // position, and row of the sequence (-1: padding)
   __shared__ float s_slope[RB];
@@ -193,7 +229,16 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
   const int g = lane >> 2, t = lane & 3;
   const int wk = warp % WK, wr = warp / WK;
   const int B = kv.batch;
-  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring_at = smem_at(ring);
+  if (tid == 0) {
+    for (int k = 0; k < ST; ++k) {
+      bar_init(smem_at(&s_full[k]), 1);
+      bar_init(smem_at(&s_free[k]), 4);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_dead = 0;
+  }
 
   // ---- this CTA's range [g0, g1) of the launch's W positions ----
   auto scan = [&](int v, int *total) {  // inclusive sum over the CTA's threads
@@ -246,13 +291,38 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
   bool bad_seq;
   Seq s = load_seq(P, b, TK, RB, &bad_seq);
 
-  const int bs_shift = __ffs(kv.block_size) - 1;
-  const float sl2 = F8 ? a.scale_log2 * (kv.k_scale * kCodeScale) : a.scale_log2;
-  const float cap = P.s.cap, cap_in = F8 ? P.cap_in * (kv.k_scale * kCodeScale) : P.cap_in;
+  const int bs_shift = __ffs(kv.block_size) - 1, box = P.box;
+  const float sl2 = F8 ? a.scale_log2 * kv.k_scale : a.scale_log2;
+  const float cap = P.s.cap, cap_in = F8 ? P.cap_in * kv.k_scale : P.cap_in;
   const bool fast_cap = cap <= kFastCap * 1.4426950408889634f;
   const int window = P.s.window;
   const bool biased = P.s.slopes != nullptr;
+  const bool bounded = !F8 && cap > 0.f && cap <= kBoundedCap && !biased;
   bool first_piece = true;
+  int issued[2] = {-1, -1};  // this warp's last tiles
+  static_assert(ST <= 8, "a warp has two tiles in flight at most");
+  uint32_t tile0 = 0;  // tiles of the CTA's earlier pieces: tile x of the launch goes to stage x % ST
+  bool dead = false;
+  auto wait = [&](uint64_t &bar, uint32_t parity) {
+    if (dead) return;
+    const bool landed = mbar_wait_bounded(smem_at(&bar), parity, a.wait_ns);
+    dead = __any_sync(0xffffffffu, !landed || *(volatile int *)&s_dead != 0);
+    if (dead) s_dead = 1;
+  };
+  // what ldmatrix adds to a row's place for 16-value step q (mod 4) of its head: chunk 2 q + (0 or 1), swizzled
+  const int lr = lane & 7, lm = lane >> 3;
+  const int k_row = lm & 1, k_hi = lm >> 1, v_row = F8 ? lm & 1 : lm >> 1, v_hi = F8 ? lm >> 1 : lm & 1;
+  uint32_t k_off[4], v_off[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    k_off[x] = CH >= 8 ? ((x * 2 + k_hi) ^ lr) << 4 : (((x * 2 + k_hi) & (CH - 1)) ^ ((lr >> 1) & 3)) << 4;
+    v_off[x] = CH >= 8 ? ((x * 2 + v_hi) ^ lr) << 4 : (((x * 2 + v_hi) & (CH - 1)) ^ ((lr >> 1) & 3)) << 4;
+  }
+  constexpr int kRow = C::ROWB >= 128 ? 128 : 64;  // bytes between a group's rows
+  const uint32_t k_lane = k_row * 8 * C::ROWB + lr * kRow, v_lane = v_row * 8 * C::ROWB + lr * kRow;
+
+  // failure-path test: a wait that nothing ends (no tile has been read yet), as for copies that never come
+  if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);
 
   while (pos < end) {
     // ---- the next piece: tiles [kt0, kt1) of a unit ----
@@ -293,47 +363,45 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) s_top[warp] = top;
     const int32_t *bt = kv.block_table + (size_t)b * kv.max_blocks;
-    auto block_of = [&](int kt) -> int {  // physical block of this thread's key of tile kt; -2: no key
-      const int key = kt * TK + tid;
-      return tid < TK && key >= lo && key < ke ? bt[key >> bs_shift] : -2;
+    // This warp issues tiles k = turn, turn + 4, ... of the piece: lane 2 j (2 j + 1) the keys' (values') box
+    // of rows j box ... of the tile, skipping boxes without a visible key.
+    const int ntiles = kt1 - kt0;
+    int turn = (int)((warp - tile0) & 3u);
+    const int box_row = (lane >> 1) * box;
+    auto block_of = [&](int k) -> int {  // physical block of this lane's box of tile k; -2: none
+      const int tok = (kt0 + k) * TK + box_row;
+      return k < ntiles && box_row < TK && tok < ke && tok + box > lo ? bt[tok >> bs_shift] : -2;
     };
-    auto put_row = [&](int kt, int id) {
-      if (tid >= TK) return;
-      long long at = -1;
-      if (id != -2) {
-        if (id < 0 || id >= kv.num_blocks) record(a.status, SV_ERR_BAD_BLOCK_ID);
-        else
-          at = ((((long long)id * kv.num_kv_heads + kvh) << bs_shift) + ((kt * TK + tid) & (kv.block_size - 1))) * C::ROWB;
+    int id = block_of(turn);
+    auto issue_until = [&](int limit) {  // this warp's tiles below limit
+      while (turn < min(limit, ntiles)) {
+        const uint32_t x = tile0 + turn, st = x % ST;
+        if (turn >= ST) wait(s_free[st], (x / ST - 1) & 1u);
+        if (dead) {  // nothing more is issued
+          turn += 4;
+          continue;
+        }
+        const bool want = id != -2, bad = want && (id < 0 || id >= kv.num_blocks), go = want && !bad;
+        if (bad) record(a.status, SV_ERR_BAD_BLOCK_ID);
+        const uint32_t bar = smem_at(&s_full[st]);
+        const int boxes = __popc(__ballot_sync(0xffffffffu, go));
+        if (lane == 0) bar_expect(bar, boxes * box * C::ROWB);
+        __syncwarp();
+        if (go) {
+          const int tok = (kt0 + turn) * TK + box_row;
+          const int y = ((id * kv.num_kv_heads + kvh) << bs_shift) + (tok & (kv.block_size - 1));
+          const uint32_t dst = ring_at + st * C::kStageBytes + (lane & 1) * TK * C::ROWB + box_row * C::ROWB;
+          load_box<C::ROWB>(dst, (lane & 1) ? &map_v : &map_k, y, bar);
+        }
+        __syncwarp();
+        issued[1] = issued[0];
+        issued[0] = (int)x;
+        turn += 4;
+        id = block_of(turn);
       }
-      s_off[kt % ST][tid] = at;
     };
-    {
-      int id[ST];
-#pragma unroll
-      for (int k = 0; k < ST; ++k) id[k] = block_of(kt0 + k);
-#pragma unroll
-      for (int k = 0; k < ST; ++k) put_row(kt0 + k, id[k]);
-    }
+    issue_until(ST - 1);  // the stages are free: the previous piece is done with them
     __syncthreads();
-    auto issue = [&](int kt) {
-      const uint32_t at = ring_at + (kt % ST) * C::kStageBytes;
-      const int ch = tid % CH;
-#pragma unroll
-      for (int k = 0; k < TK / (kThreads / CH); ++k) {
-        const int r = tid / CH + k * (kThreads / CH);
-        const long long o = s_off[kt % ST][r];
-        const uint32_t dst = at + r * C::ROWB + ((CH >= 8 ? ch ^ (r & 7) : ch ^ ((r >> 1) & (CH - 1))) << 4);
-        const long long src = (o < 0 ? 0 : o) + ch * 16;
-        copy16(dst, (const uint8_t *)kv.k_pool + src, o >= 0);
-        copy16(dst + TK * C::ROWB, (const uint8_t *)kv.v_pool + src, o >= 0);
-      }
-    };
-#pragma unroll
-    for (int k = 0; k < ST - 1; ++k) {
-      if (kt0 + k < kt1) issue(kt0 + k);
-      copies_commit();
-    }
-    int next_id = block_of(kt0 + ST);
     const int row_top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
     const int all_see = window > 0 ? row_top - window + 1 : 0;  // keys from here to c are visible to every row
 
@@ -368,20 +436,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
     float o[KT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = bounded ? 0.f : kNone;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
     }
 
     for (int kt = kt0; kt < kt1; ++kt) {
-      copies_wait<ST - 2>();
-      __syncthreads();  // tile kt has landed, and every warp is done with tile kt - 1
-      if (kt + ST - 1 < kt1) issue(kt + ST - 1);
-      copies_commit();
-      put_row(kt + ST, next_id);
-      next_id = block_of(kt + ST + 1);
-      const uint32_t k_at = ring_at + (kt % ST) * C::kStageBytes, v_at = k_at + TK * C::ROWB;
+      const uint32_t x = tile0 + (kt - kt0), st = x % ST;
+      issue_until(kt - kt0 + ST);
+      wait(s_full[st], (x / ST) & 1u);
+      const uint32_t k_at = ring_at + st * C::kStageBytes + k_lane, v_at = ring_at + st * C::kStageBytes + TK * C::ROWB + v_lane;
 #pragma unroll 1
       for (int k16 = wk * 16; k16 < TK; k16 += WK * 16) {
         const int key0 = kt * TK + k16;
@@ -390,15 +455,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
         float sc[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-        const int lr = lane & 7, lm = lane >> 3;
-        const int krow = k16 + lr + (lm & 1) * 8;
-        const uint32_t kaddr = k_at + krow * C::ROWB;
-        const int ksw = CH >= 8 ? krow & 7 : (krow >> 1) & (CH - 1);
+        const uint32_t kaddr = k_at + k16 * C::ROWB;
         if (!F8) {
 #pragma unroll
           for (int kk = 0; kk < KT; ++kk) {
             uint32_t f[4];
-            ldm4(f, kaddr + (((kk * 2 + (lm >> 1)) ^ ksw) << 4));
+            ldm4(f, kaddr + k_off[kk & 3] + (kk >> 2) * 1024);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], f, q[nt][kk][0], q[nt][kk][1]);
           }
@@ -406,11 +468,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
 #pragma unroll
           for (int k2 = 0; k2 < KT / 2; ++k2) {
             uint32_t f[4];
-            ldm4(f, kaddr + (((k2 * 2 + (lm >> 1)) ^ ksw) << 4));
+            ldm4(f, kaddr + k_off[k2 & 3] + (k2 >> 2) * 1024);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t e[4] = {widen<0x1404>(f[2 * h]), widen<0x1404>(f[2 * h + 1]), widen<0x3424>(f[2 * h]),
-                                     widen<0x3424>(f[2 * h + 1])};
+              const uint32_t e[4] = {widen(f[2 * h]), widen(f[2 * h + 1]), widen(f[2 * h] >> 16), widen(f[2 * h + 1] >> 16)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma<true>(sc[nt], e, q[nt][2 * k2 + h][0], q[nt][2 * k2 + h][1]);
             }
@@ -426,12 +487,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = fmaf(-2.f * cap, rcp(1.f + ex2(sc[nt][e] * cap_in)), cap);
+            for (int e = 0; e < 4; ++e) sc[nt][e] = -2.f * cap * rcp(1.f + ex2(sc[nt][e] * cap_in));
         } else {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = cap * tanhf(sc[nt][e] * sl2 / cap);
+            for (int e = 0; e < 4; ++e) sc[nt][e] = cap * tanhf(sc[nt][e] * sl2 / cap) - cap;
         }
         const bool edge = key0 + 16 > min(c, ke) || key0 < all_see;  // warp-uniform: some row may not see some key
         if (biased && !edge) {
@@ -463,39 +524,44 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
           }
         }
         // ---- the running maximum ----
-        bool move = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) move |= sc[nt][e] > m[nt][e & 1] + kMoveAt;
-        if (__any_sync(0xffffffffu, move)) {
+        if (!bounded) {
+          bool move = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(sc[nt][e], sc[nt][e + 2]);
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-              const float mn = fmaxf(m[nt][e], mx);
-              const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
-              m[nt][e] = mn;
-              l[nt][e] *= f;
-#pragma unroll
-              for (int mt = 0; mt < KT; ++mt) {
-                o[mt][nt][e] *= f;
-                o[mt][nt][e + 2] *= f;
-              }
+            for (int e = 0; e < 4; ++e) {
+              move |= sc[nt][e] > m[nt][e & 1] + kMoveAt;
             }
+          if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(sc[nt][e], sc[nt][e + 2]);
+#pragma unroll
+                for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+                const float mn = fmaxf(m[nt][e], mx);
+                const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
+                m[nt][e] = mn;
+                l[nt][e] *= f;
+#pragma unroll
+                for (int mt = 0; mt < KT; ++mt) {
+                  o[mt][nt][e] *= f;
+                  o[mt][nt][e + 2] *= f;
+                }
+              }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[nt][e] -= m[nt][e & 1];
         }
         // ---- P^T ----
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-          sc[nt][0] = ex2(sc[nt][0] - r0);
-          sc[nt][1] = ex2(sc[nt][1] - r1);
-          sc[nt][2] = ex2(sc[nt][2] - r0);
-          sc[nt][3] = ex2(sc[nt][3] - r1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][e] = ex2(sc[nt][e]);
           l[nt][0] += sc[nt][0] + sc[nt][2];
           l[nt][1] += sc[nt][1] + sc[nt][3];
           pb[nt][0] = turn8x8(pack2<F8>(sc[nt][0], sc[nt][1]));
@@ -503,13 +569,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
         }
         // ---- O^T += V^T P^T ----
         if (!F8) {
-          const int vrow = k16 + lr + (lm >> 1) * 8;
-          const uint32_t vaddr = v_at + vrow * C::ROWB;
+          const uint32_t vaddr = v_at + k16 * C::ROWB;
           bool odd = false;  // an infinity or NaN among this step's values
 #pragma unroll
           for (int mt = 0; mt < KT; ++mt) {
             uint32_t f[4];
-            ldm4t(f, vaddr + (((mt * 2 + (lm & 1)) ^ (vrow & 7)) << 4));
+            ldm4t(f, vaddr + v_off[mt & 3] + (mt >> 2) * 1024);
             if (edge) {  // 0 * infinity must not reach a row that does not see the key
 #pragma unroll
               for (int x = 0; x < 4; ++x)
@@ -524,10 +589,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
           }
           if (edge && __any_sync(0xffffffffu, odd)) {
             // the values set to zero above, for the rows that see their keys
-            const uint8_t *vs = ring + (v_at - ring_at);
+            const uint8_t *vs = ring + st * C::kStageBytes + TK * C::ROWB + k16 * C::ROWB;
 #pragma unroll 1
             for (int key = 0; key < 16; ++key) {
-              const int r = k16 + key;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const float e0 = key < 8 ? sc[nt][0] : sc[nt][2], e1 = key < 8 ? sc[nt][1] : sc[nt][3];
@@ -538,7 +602,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
 #pragma unroll
                   for (int h = 0; h < 2; ++h) {
                     const uint32_t x =
-                        *reinterpret_cast<const uint16_t *>(vs + r * C::ROWB + (((mt * 2 + h) ^ (r & 7)) << 4) + g * 2);
+                        *reinterpret_cast<const uint16_t *>(vs + (key >> 3) * 8 * C::ROWB + (key & 7) * 128 + (mt >> 2) * 1024 +
+                                                            ((((mt & 3) * 2 + h) ^ (key & 7)) << 4) + g * 2);
                     if ((x & 0x7f80u) != 0x7f80u) continue;
                     const float v = __uint_as_float(x << 16);
                     if (p0 > 0.f) o[mt][nt][2 * h] += p0 * v;
@@ -548,27 +613,32 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
             }
           }
         } else {
-          const int vrow = k16 + lr + (lm & 1) * 8;
-          const uint32_t vaddr = v_at + vrow * C::ROWB;
-          const int vsw = CH >= 8 ? vrow & 7 : (vrow >> 1) & (CH - 1);
+          const uint32_t vaddr = v_at + k16 * C::ROWB;
 #pragma unroll
           for (int m2 = 0; m2 < KT / 2; ++m2) {
             uint32_t f[4];
-            ldm4t(f, vaddr + (((m2 * 2 + (lm >> 1)) ^ vsw) << 4));
+            ldm4t(f, vaddr + v_off[m2 & 3] + (m2 >> 2) * 1024);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t e[4] = {widen<0x2404>(f[2 * h]), widen<0x3414>(f[2 * h]), widen<0x2404>(f[2 * h + 1]),
-                                     widen<0x3414>(f[2 * h + 1])};
+              // a word: two dimensions of one key below, of the next key above; pairs of keys are wanted
+              const uint32_t w0 = __byte_perm(f[2 * h], 0u, 0x3120), w1 = __byte_perm(f[2 * h + 1], 0u, 0x3120);
+              uint32_t e[4] = {widen(w0), widen(w0 >> 16), widen(w1), widen(w1 >> 16)};
+              if (edge) {  // slots that no row sees may hold anything
+#pragma unroll
+                for (int y = 0; y < 4; ++y) e[y] = without_nan(e[y]);
+              }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma<true>(o[m2 * 2 + h][nt], e, pb[nt][0], pb[nt][1]);
             }
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_at(&s_free[st]));
     }
     // ---- the key groups' results, merged ----
-    copies_wait<0>();
     __syncthreads();  // every warp is done with the ring
+    tile0 += ntiles;
     float *buf = reinterpret_cast<float *>(ring);  // [WK][RB][kPad]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -595,10 +665,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
       float M = s_m[0][tid], tot = 0.f;
 #pragma unroll
       for (int w = 1; w < WK; ++w) M = fmaxf(M, s_m[w][tid]);
-      const float ref = M == -INFINITY ? 0.f : M;
+      const float ref = M;  // finite: kNone at the least
 #pragma unroll
       for (int w = 0; w < WK; ++w) tot += s_l[w][tid] * ex2(s_m[w][tid] - ref);
-      const float inv = tot == 0.f ? 0.f : (F8 ? kv.v_scale * kCodeScale : 1.f) / tot;
+      const float inv = tot == 0.f ? 0.f : (F8 ? kv.v_scale : 1.f) / tot;
       if (!whole) P.part_lse[slot + tid] = tot == 0.f ? -INFINITY : M + log2f(tot);
 #pragma unroll
       for (int w = 0; w < WK; ++w) s_l[w][tid] = ex2(s_m[w][tid] - ref) * inv;
@@ -629,7 +699,16 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_scored_kernel(co
       }
     }
     first_piece = false;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the merge's accesses, before the next piece's copies
   }
+  if (dead) {
+    if (lane == 0) record(a.status, SV_ERR_TIMEOUT);
+    // the copies this warp has in flight land before the CTA's shared memory is released
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (issued[k] >= 0) mbar_wait_bounded(smem_at(&s_full[issued[k] % ST]), (issued[k] / ST) & 1, kDrainBudgetNs);
+  }
+  __syncthreads();
 }
 
 // Merges the partials of every unit that two or more CTAs shared: o = sum_p 2^lse_p o_p / sum_p 2^lse_p,
@@ -719,6 +798,28 @@ Layout layout_of(const KV &kv, int G, int max_q, int max_seq_len) {
 
 constexpr int kAlpha = 2;  // positions of a unit's lead-in
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encoder();  // null without a driver that has it
+
+template <class C> bool make_map(CUtensorMap *map, void *pool, const KV &kv, int box) {
+  const cuuint64_t rows = (cuuint64_t)kv.num_blocks * kv.num_kv_heads * kv.block_size;
+  const EncodeTiledFn fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  if (C::ROWB >= 128) {
+    const cuuint64_t dim[4] = {128, 8, C::ROWB / 128, rows / 8}, stride[3] = {C::ROWB, 128, 8 * C::ROWB};
+    const cuuint32_t b[4] = {128, 8, C::ROWB / 128, (cuuint32_t)box / 8};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pool, dim, stride, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  const cuuint64_t dim[2] = {64, rows}, stride[1] = {64};
+  const cuuint32_t b[2] = {64, (cuuint32_t)box};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pool, dim, stride, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Launches (st != null via `go`) or sizes one instance.
 template <class C>
 cudaError_t run(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {
@@ -737,9 +838,12 @@ cudaError_t run(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream
   p.part_o = reinterpret_cast<float *>(workspace);
   p.part_lse = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + l.lse_offset);
   p.prefix = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(workspace) + l.prefix_offset);
+  p.box = std::min(kv.block_size, C::TK);
+  CUtensorMap mk, mv;
+  if (!make_map<C>(&mk, kv.k_pool, kv, p.box) || !make_map<C>(&mv, kv.v_pool, kv, p.box)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attn_scored_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_scored_kernel<C>, dim3(p.ctas), dim3(kThreads), C::kSmem, st, p);
+  e = launch_pdl(attn_scored_kernel<C>, dim3(p.ctas), dim3(kThreads), C::kSmem, st, mk, mv, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_scored_combine<C>, dim3(kv.batch, kv.num_kv_heads * p.rb_max), dim3(128), 0, st, p);
 }

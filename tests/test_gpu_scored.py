@@ -9,6 +9,8 @@ over sqrt(sum p^2 |v|^2), the size of an average of independent values, and |wan
  * bf16 and E4M3 caches: each weight p is rounded to bf16 (2^-8, fp16 2^-11 for E4M3) and the
    output to bf16 (2^-8); fp16 queries add 2^-11 to each product: at most 2^-7 in all, compared
    against the row's norm plus that of the weighted values' root sum of squares."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -102,6 +104,8 @@ SMALL = {
     "bf16-g8-ragged": (13, [16, 900, 255, 129, 1], [3, 9, 2, 5, 1], 64, 8, 128, 128, "bf16"),
     "bf16-d64": (14, [333, 47], [5, 3], 8, 2, 64, 16, "bf16"),
     "bf16-d64-bs1": (15, [33, 70], [5, 2], 4, 1, 64, 1, "bf16"),
+    "bf16-bs8": (27, [75, 8, 140], [6, 1, 3], 8, 2, 128, 8, "bf16"),
+    "e4m3-d64-bs8": (28, [300, 9], [2, 1], 8, 2, 64, 8, "e4m3"),
     "bf16-d256": (16, [290, 31], [2, 4], 8, 2, 256, 32, "bf16"),
     "bf16-d96": (17, [130, 31], [2, 4], 6, 2, 96, 8, "bf16"),
     "bf16-wide": (18, [200, 90], [64, 33], 8, 1, 128, 64, "bf16"),
@@ -290,6 +294,31 @@ def test_repeatable_on_two_streams_and_in_graphs():
         torch.cuda.synchronize()
         assert torch.equal(outs[2], first)
     assert torch.equal(outs[0], first) and torch.equal(outs[1], first)
+
+
+def test_wait_that_runs_out_then_recovers():
+    """The failure-path hook: nothing is issued, every wait runs out, the call records SV_ERR_TIMEOUT and
+    the next one on the stream is right."""
+    case = W.custom(51, batch=4, ctx_lens=[700, 65, 1, 300], n_q=[6, 6, 6, 6], num_q_heads=32, num_kv_heads=8, head_dim=128, block_size=16, vocab=16,
+                    use_bank=False)
+    mod = ScoreMod(softcap=20.0)
+    kv, d, buf = run(case, mod)
+    first = buf.attn_out.clone()
+    L.set_wait_budget_us(2000)
+    L.set_stall_for_test("attention")
+    try:
+        t0 = time.perf_counter()
+        S.attention(kv, d, buf, 706)
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 1.0
+    finally:
+        L.set_stall_for_test("none")
+        L.set_wait_budget_us(L.DEFAULT_WAIT_BUDGET_US)
+    assert status_of(buf) == L.SV_ERR_TIMEOUT
+    buf.status.zero_()
+    S.attention(kv, d, buf, 706)
+    torch.cuda.synchronize()
+    assert status_of(buf) == 0 and torch.equal(buf.attn_out, first)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "e4m3"])
