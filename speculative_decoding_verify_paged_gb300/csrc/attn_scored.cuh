@@ -21,19 +21,23 @@
 // attn_scored_combine merges the partials in the order of the CTAs (so results repeat bit for bit).
 // With a window a unit's tiles start at its first visible one: keys out of sight are not read.
 //
-// A CTA's four warps are WK key groups x WR row groups. Every tile of TK keys goes into a ring of
-// kStages shared-memory stages by TMA, a box per block (or per tile, where blocks are larger), the pool
-// seen as (128 bytes, 8 rows, 128-byte parts of a row, groups of 8 rows) and swizzled so that
-// ldmatrix reads without bank conflicts. The warps take turns in issuing a tile, each a turn after it has
-// read the block ids; a stage is refilled when all four have arrived on its barrier, so that no
-// barrier of the whole CTA is left in the loop. A warp takes 16 keys at a time:
+// A CTA's warps are one producer and WK key groups x WR row groups of consumers, each with NT x 8 rows
+// (Cfg; `pick` says which). The producer walks the CTA's pieces and brings tiles of TK keys (16 KB of K and
+// V) into a ring of kStages stages by TMA, a box per block (or per tile, where blocks are larger), the
+// pool seen as (128 bytes, 8 rows, 128-byte parts of a row, groups of 8 rows) and swizzled so that
+// ldmatrix reads without bank conflicts; it runs on into the next piece while the consumers finish one. A
+// consumer takes every WK-th 16 keys of a piece:
 //   S^T (keys x rows) = K Q^T, A = K (ldmatrix), B = Q held in registers, accumulators fp32;
-//   the running maximum of a row moves only when a score passes it by 2^8 (one vote per 16 keys), and
+//   the running maximum of a row moves only when a score passes it by far (kMoveAt; one vote a step), and
 //   not at all where the cap bounds the scores well enough (kBoundedCap);
 //   P^T = 2^(S^T - m) in bf16 (fp16 for E4M3 pools) turned into a B operand by movmatrix;
 //   O^T (dims x rows) += V^T P^T, A = V^T (ldmatrix.trans), accumulators fp32 in registers.
 // Query rows sit on the n dimension, so that 24 rows (4 heads x 6) cost 24 and not 32. At the end
-// of a piece the WK key groups' (m, l, O) are merged through shared memory.
+// of a piece the WK key groups' (m, l, O) are merged through shared memory, 8 rows of each warp at a time.
+//
+// What decides the speed is the number of warps: a warp's 16 keys are a chain of products, special
+// functions and products again, some 1000 cycles of latency for 300 instructions. Few rows a warp (and
+// K and V read from shared memory once per row group) leave registers for 16 to 18 of them on an SM.
 //
 // A cap's constant term is dropped like the bias's: -2 cap / (1 + 2^(2 y log2 e)) is what is left.
 // E4M3 codes become fp16 operands in registers (exactly). ldmatrix moves pairs of codes; which
@@ -47,17 +51,24 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include <climits>
+#include <type_traits>
+
 #include "sv_internal.cuh"
 
 namespace sv {
 namespace scored {
 
-constexpr int kThreads = 128;
-constexpr float kMoveAt = 8.f;     // the running maximum moves when a score passes it by this (log2)
+// The running maximum moves when a score passes it by this (log2): weights in bf16 and sums in fp32 have
+// room for 2^60, weights in fp16 for 2^8 and their sums over the row group's products.
+template <bool F16> constexpr float kMoveAt = F16 ? 8.f : 60.f;
 constexpr float kFastCap = 200.f;  // caps up to this take the two-instruction tanh
 // Capped scores lie within [-2 cap, 0] (the constant dropped): up to this cap (log2 units) weights of
 // 2^-120 and more keep their precision in bf16 and fp32, and no maximum is needed.
 constexpr float kBoundedCap = 60.f;
+// Registers of a thread: as launched (256 threads, two CTAs an SM), and after the split.
+constexpr int kLaunchRegs = 128, kProducerRegs = 40, kConsumerRegs = 216;
+static_assert(kProducerRegs + kConsumerRegs == 2 * kLaunchRegs, "a split above the launch's share would wait forever");
 constexpr float kNone = -3.3e38f;  // a running maximum before the first visible key
 
 struct Params {
@@ -71,23 +82,35 @@ struct Params {
   int *prefix;      // [batch + 1]: first position of each sequence's units, then all positions
 };
 
-template <int D_, int NT_, int WR_, bool F8_>
+template <int D_, int NT_, int WR_, int WK_, bool F8_>
 struct Cfg {
-  static constexpr int D = D_, NT = NT_, WR = WR_, WK = 4 / WR_, RB = WR_ * NT_ * 8;  // RB: rows of a unit
+  static constexpr int D = D_, NT = NT_, WR = WR_, WK = WK_, RB = WR_ * NT_ * 8;  // RB: rows of a unit
   static constexpr bool F8 = F8_;
+  // four consumer warps, then four of which the first produces: register shares go by four warps
+  static constexpr int kConsumers = 4, kThreads = 256, kCtasPerSm = 2;
+  static_assert(WK * WR == kConsumers, "a consumer on each quarter of the SM");
   static constexpr int ROWB = D * (F8 ? 1 : 2);  // bytes of a key's row
-  static constexpr int CH = ROWB / 16;           // 16-byte chunks of it
-  // 32 KB of K and V per stage where that is 64 or 128 keys; three stages of it let two CTAs share
-  // an SM (bf16 rows of 256 values: one CTA with three stages of 64 KB)
-  static constexpr int TK = ROWB <= 128 ? 128 : 64;
+  static constexpr int TK = 8192 / ROWB;         // keys of a tile: 16 KB of K and V
+  // a step: M x 16 keys; two where registers allow, so that a chain of products hides another
+  static constexpr int M = TK >= 32 && D_ * NT_ <= (WR_ == 4 ? 384 : 256) && (WK_ < 4 || TK >= 64) ? 2 : 1;
+  static constexpr int S = TK / (16 * M);        // steps of a tile
   static constexpr int kStageBytes = 2 * TK * ROWB;
-  static constexpr int kCtasPerSm = kStageBytes > 32768 ? 1 : 2;
-  static constexpr int kStages = kStageBytes > 32768 ? 3 : 98304 / kStageBytes;
+  // Values of a row that are merged at a time: all, or 64 where the shared memory is better spent on
+  // stages (four key groups of few rows hold two stages; 6 of them against 4: 70.7 and 74.5 us for one
+  // token of 32 sequences of 2 to 4 K, 86 % and 81 % of the memory rate).
+  static constexpr bool kNarrow = D == 128 && NT_ <= 2 && WK_ == 4;
+  static constexpr int kChunk = D == 128 && !kNarrow ? 128 : 64, kStages = kNarrow ? 6 : 4;
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kPad = D + 4;  // floats of a row in the merge buffer
-  static_assert(WK * RB * kPad * 4 <= kRing, "the merge buffer fits the ring");
-  static_assert(TK % (16 * WK) == 0 && RB <= kThreads && 2 * (TK / 8) <= 32, "a row per thread, a box per lane");
-  static constexpr size_t kSmem = kRing + 1024;  // the ring starts on a 1 KB boundary
+  static constexpr int kPad = kChunk + 4;                   // floats of a row in the merge buffer
+  static constexpr int kMerge = kConsumers * 8 * kPad * 4;  // 8 rows of every consumer
+  static constexpr size_t kSmem = 1024 + kRing + kMerge;  // the ring starts on a 1 KB boundary
+  static_assert(kCtasPerSm * (kSmem + 4608) <= 228 * 1024, "shared memory of an SM");
+  // A parity wait for a stage's phase n returns at once while phase n - 1 has not completed, so a consumer has
+  // to have seen phase n - 1: it visits every tile, or every ST-th of the stages that it uses. (At the
+  // start of a piece all phases of the earlier pieces' tiles have been seen by some consumer, and the
+  // consumers have met at a barrier since.)
+  static constexpr int gcd(int x, int y) { return y == 0 ? x : gcd(y, x % y); }
+  static_assert(kStages % (WK / gcd(WK, S)) == 0, "a consumer sees each phase of its stages");
 };
 
 struct Seq {
@@ -201,46 +224,88 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t x) {  // an fp16 pair, 
   return x;
 }
 
+__device__ __forceinline__ bool nan_code4(uint32_t x) {  // four E4M3 codes
+  return (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
+}
 __device__ __forceinline__ bool nonfinite2(uint32_t x) {  // a bf16 pair
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 
+// A CTA's position in the work order: the sequence that holds it and where that one's positions begin.
+struct Place {
+  int b, base, pos, end;
+  Seq s;
+};
+// The part of a unit that comes next: tiles [kt0, kt1) (kt1 <= kt0: only lead-in positions).
+struct Piece {
+  int kt0, kt1, kvh, rb, lo, ke;
+  bool whole;
+};
+
+template <class C> __device__ __forceinline__ bool next_piece(const Params &P, Place &at, Piece &p) {
+  while (at.pos < at.end) {
+    bool bad;
+    int work = seq_work(P, at.s);
+    while (at.pos - at.base >= work && at.b + 1 < P.s.a.kv.batch) {
+      at.base += work;
+      at.s = load_seq(P, ++at.b, C::TK, C::RB, &bad);
+      work = seq_work(P, at.s);
+    }
+    if (at.pos - at.base >= work) break;  // cannot happen while the lengths stay put
+    const Seq &s = at.s;
+    const int U = s.tiles + P.alpha, unit = (at.pos - at.base) / U, off = (at.pos - at.base) - unit * U;
+    const int npos = min(U - off, at.end - at.pos);
+    at.pos += npos;
+    p.kt0 = s.t0 + max(0, off - P.alpha);
+    p.kt1 = s.t0 + off + npos - P.alpha;
+    if (p.kt1 <= p.kt0) continue;  // only the unit's lead-in lies in this range
+    p.kvh = unit / s.rbs;
+    p.rb = unit - p.kvh * s.rbs;
+    p.whole = p.kt0 == s.t0 && p.kt1 == s.t0 + s.tiles;
+    p.ke = min(s.L, p.kt1 * C::TK);
+    p.lo = P.s.window > 0 ? max(0, s.c - P.s.window + 1) : 0;
+    return true;
+  }
+  at.pos = at.end;
+  return false;
+}
+
 template <class C>
-__global__ void __launch_bounds__(kThreads, C::kCtasPerSm)
+__global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     attn_scored_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params P) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
-  constexpr int D = C::D, NT = C::NT, TK = C::TK, CH = C::CH, RB = C::RB, WK = C::WK, ST = C::kStages;
+  constexpr int D = C::D, NT = C::NT, TK = C::TK, RB = C::RB, WK = C::WK, WR = C::WR, ST = C::kStages, S = C::S, M = C::M;
   constexpr int KT = D / 16;  // 16-value steps of a head
+  constexpr int kThreads = C::kThreads, kWarps = kThreads / 32, kC = C::kConsumers * 32;
   constexpr bool F8 = C::F8;
   extern __shared__ uint8_t smem[];
-  __shared__ __align__(8) uint64_t s_full[ST], s_free[ST];  // a stage's copies have landed; all warps have read it
+  __shared__ __align__(8) uint64_t s_full[ST], s_free[ST];  // a stage's copies have landed; its steps are done
   __shared__ int s_dead;                                    // a wait gave up
-  __shared__ uint64_t s_mask[RB];      // tree mask of a row
-  __shared__ int s_pos[RB], s_row[RB];  // position, and row of the sequence (-1: padding)
+  __shared__ uint64_t s_mask[RB];         // new keys that a row sees
+  __shared__ int s_reach[RB], s_row[RB];  // last place out of the window, and row of the sequence (-1: padding)
   __shared__ float s_slope[RB];
   __shared__ int s_place[64];  // position of a new row minus c
   __shared__ float s_m[WK][RB], s_l[WK][RB];
-  __shared__ int s_scan[4], s_first_b, s_first_base, s_top[4];
+  __shared__ int s_scan[kWarps], s_first_b, s_first_base, s_top[kWarps];
 
   const AttnArgs &a = P.s.a;
   const KV &kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const int wk = warp % WK, wr = warp / WK;
   const int B = kv.batch;
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
   const uint32_t ring_at = smem_at(ring);
   if (tid == 0) {
     for (int k = 0; k < ST; ++k) {
       bar_init(smem_at(&s_full[k]), 1);
-      bar_init(smem_at(&s_free[k]), 4);
+      bar_init(smem_at(&s_free[k]), S * WR);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_dead = 0;
+    s_first_b = s_first_base = 0;
   }
 
-  // ---- this CTA's range [g0, g1) of the launch's W positions ----
+  // ---- this CTA's range [pos, end) of the launch's W positions ----
   auto scan = [&](int v, int *total) {  // inclusive sum over the CTA's threads
     int x = v;
 #pragma unroll
@@ -252,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm)
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       before += w < warp ? s_scan[w] : 0;
       all += s_scan[w];
     }
@@ -260,461 +325,558 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm)
     *total = all;
     return x + before;
   };
-  int mine = 0, W, run = 0;
-  if (tid == 0) s_first_b = s_first_base = 0;
-  for (int b = tid; b < B; b += kThreads) {
-    bool bad;
-    const Seq s = load_seq(P, b, TK, RB, &bad);
-    if (bad && blockIdx.x == 0) record(a.status, SV_ERR_BAD_LENGTH);
-    mine += seq_work(P, s);
+  auto work_of = [&](int b, bool report) {
+    bool bad = false;
+    const int v = b < B ? seq_work(P, load_seq(P, b, TK, RB, &bad)) : 0;
+    if (bad && report && blockIdx.x == 0) record(a.status, SV_ERR_BAD_LENGTH);
+    return v;
+  };
+  int v = work_of(tid, true), W, incl = scan(v, &W), run = 0;  // the first kThreads sequences: most batches whole
+  if (B > kThreads) {
+    int more = 0, rest;
+    for (int b = tid + kThreads; b < B; b += kThreads) more += work_of(b, true);
+    run = W;
+    scan(more, &rest);
+    W += rest;
   }
-  scan(mine, &W);
-  int pos = range_start(blockIdx.x, W, P.ctas);
-  const int end = range_start(blockIdx.x + 1, W, P.ctas);
+  Place at;
+  at.pos = range_start(blockIdx.x, W, P.ctas);
+  at.end = range_start(blockIdx.x + 1, W, P.ctas);
   for (int b0 = 0; b0 < B; b0 += kThreads) {  // the sequence that holds the first position; CTA 0 stores the prefix
     const int b = b0 + tid;
-    int v = 0, tot;
-    bool bad;
-    if (b < B) v = seq_work(P, load_seq(P, b, TK, RB, &bad));
-    const int excl = run + scan(v, &tot) - v;
+    if (b0 > 0) {
+      int tot;
+      v = work_of(b, false);
+      incl = run + scan(v, &tot);
+      run += tot;
+    }
+    const int excl = incl - v;
     if (blockIdx.x == 0 && b < B) P.prefix[b] = excl;
-    if (v > 0 && excl <= pos && pos < excl + v) {
+    if (v > 0 && excl <= at.pos && at.pos < incl) {
       s_first_b = b;
       s_first_base = excl;
     }
-    run += tot;
-    if (blockIdx.x != 0 && run > pos) break;  // uniform
+    if (blockIdx.x != 0 && b0 > 0 && run > at.pos) break;  // uniform
   }
   if (blockIdx.x == 0 && tid == 0) P.prefix[B] = W;
   __syncthreads();
-  int b = s_first_b, base = s_first_base;
-  bool bad_seq;
-  Seq s = load_seq(P, b, TK, RB, &bad_seq);
-
-  const int bs_shift = __ffs(kv.block_size) - 1, box = P.box;
-  const float sl2 = F8 ? a.scale_log2 * kv.k_scale : a.scale_log2;
-  const float cap = P.s.cap, cap_in = F8 ? P.cap_in * kv.k_scale : P.cap_in;
-  const bool fast_cap = cap <= kFastCap * 1.4426950408889634f;
-  const int window = P.s.window;
-  const bool biased = P.s.slopes != nullptr;
-  const bool bounded = !F8 && cap > 0.f && cap <= kBoundedCap && !biased;
-  bool first_piece = true;
-  int issued[2] = {-1, -1};  // this warp's last tiles
-  static_assert(ST <= 8, "a warp has two tiles in flight at most");
+  at.b = s_first_b;
+  at.base = s_first_base;
+  {
+    bool bad;
+    at.s = load_seq(P, at.b, TK, RB, &bad);
+  }
+  Piece p;
   uint32_t tile0 = 0;  // tiles of the CTA's earlier pieces: tile x of the launch goes to stage x % ST
   bool dead = false;
   auto wait = [&](uint64_t &bar, uint32_t parity) {
-    if (dead) return;
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done)
+                 : "r"(smem_at(&bar)), "r"(parity)
+                 : "memory");
+    if (__all_sync(0xffffffffu, done != 0) || dead) return;
     const bool landed = mbar_wait_bounded(smem_at(&bar), parity, a.wait_ns);
     dead = __any_sync(0xffffffffu, !landed || *(volatile int *)&s_dead != 0);
     if (dead) s_dead = 1;
   };
-  // what ldmatrix adds to a row's place for 16-value step q (mod 4) of its head: chunk 2 q + (0 or 1), swizzled
-  const int lr = lane & 7, lm = lane >> 3;
-  const int k_row = lm & 1, k_hi = lm >> 1, v_row = F8 ? lm & 1 : lm >> 1, v_hi = F8 ? lm >> 1 : lm & 1;
-  uint32_t k_off[4], v_off[4];
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    k_off[x] = CH >= 8 ? ((x * 2 + k_hi) ^ lr) << 4 : (((x * 2 + k_hi) & (CH - 1)) ^ ((lr >> 1) & 3)) << 4;
-    v_off[x] = CH >= 8 ? ((x * 2 + v_hi) ^ lr) << 4 : (((x * 2 + v_hi) & (CH - 1)) ^ ((lr >> 1) & 3)) << 4;
-  }
-  constexpr int kRow = C::ROWB >= 128 ? 128 : 64;  // bytes between a group's rows
-  const uint32_t k_lane = k_row * 8 * C::ROWB + lr * kRow, v_lane = v_row * 8 * C::ROWB + lr * kRow;
+  const int bs_shift = __ffs(kv.block_size) - 1;
 
-  // failure-path test: a wait that nothing ends (no tile has been read yet), as for copies that never come
-  if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);
-
-  while (pos < end) {
-    // ---- the next piece: tiles [kt0, kt1) of a unit ----
-    int work = seq_work(P, s);
-    while (pos - base >= work && b + 1 < B) {
-      base += work;
-      s = load_seq(P, ++b, TK, RB, &bad_seq);
-      work = seq_work(P, s);
-    }
-    if (pos - base >= work) break;  // cannot happen while the lengths stay put
-    const int U = s.tiles + P.alpha;
-    const int unit = (pos - base) / U, off = (pos - base) - unit * U;
-    const int npos = min(U - off, end - pos);
-    pos += npos;
-    const int kt0 = s.t0 + max(0, off - P.alpha), kt1 = s.t0 + off + npos - P.alpha;
-    if (kt1 <= kt0) continue;  // only the unit's lead-in lies in this range
-    const int kvh = unit / s.rbs, rb = unit - kvh * s.rbs;
-    const bool whole = kt0 == s.t0 && kt1 == s.t0 + s.tiles;
-    const int c = s.c, ke = min(s.L, kt1 * TK);
-    const int lo = window > 0 ? max(0, c - window + 1) : 0;
-    const int rows = min(RB, P.G * s.n - rb * RB);  // live rows of the block
-
-    __syncthreads();  // the previous piece's shared memory is free
-    // ---- rows of the block, new keys' places, the first tiles' pool rows ----
-    int top = c;
-    if (tid < RB) {
-      const bool live = tid < rows;
-      const int r = rb * RB + tid, i = live ? r / P.G : 0, head = kvh * P.G + (live ? r - i * P.G : 0);
-      const int p = P.s.positions != nullptr ? P.s.positions[s.row0 + i] : c + i;
-      if (p < c) record(a.status, SV_ERR_BAD_LENGTH);
-      s_pos[tid] = p;
-      s_row[tid] = live ? i : -1;
-      s_mask[tid] = live && a.mask_kind == SV_MASK_TREE ? a.tree_mask[s.row0 + i] : 0ull;
-      s_slope[tid] = biased ? P.s.slopes[head] * 1.4426950408889634f : 0.f;
-      top = live ? p : c;
-    }
-    if (tid < 64 && tid < s.n) s_place[tid] = P.s.positions != nullptr ? P.s.positions[s.row0 + tid] - c : tid;
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) s_top[warp] = top;
-    const int32_t *bt = kv.block_table + (size_t)b * kv.max_blocks;
-    // This warp issues tiles k = turn, turn + 4, ... of the piece: lane 2 j (2 j + 1) the keys' (values') box
-    // of rows j box ... of the tile, skipping boxes without a visible key.
-    const int ntiles = kt1 - kt0;
-    int turn = (int)((warp - tile0) & 3u);
-    const int box_row = (lane >> 1) * box;
-    auto block_of = [&](int k) -> int {  // physical block of this lane's box of tile k; -2: none
-      const int tok = (kt0 + k) * TK + box_row;
-      return k < ntiles && box_row < TK && tok < ke && tok + box > lo ? bt[tok >> bs_shift] : -2;
-    };
-    int id = block_of(turn);
-    auto issue_until = [&](int limit) {  // this warp's tiles below limit
-      while (turn < min(limit, ntiles)) {
-        const uint32_t x = tile0 + turn, st = x % ST;
-        if (turn >= ST) wait(s_free[st], (x / ST - 1) & 1u);
-        if (dead) {  // nothing more is issued
-          turn += 4;
-          continue;
+  // The registers that the launch gives every thread alike (kLaunchRegs) are shared out again. (Each
+  // setmaxnreg stands in its own branch: the compiler then allocates each branch by its share.)
+  if (warp >= C::kConsumers) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    if (warp == C::kConsumers) {
+    // ================= producer =================
+    // Lane 2 j (2 j + 1) takes the keys' (values') box of rows j box ... of a tile. Block ids come from a
+    // 64-block window of the block table, two entries per lane, loaded one window before they are used.
+    const int box = P.box, box_row = (lane >> 1) * box;
+    if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);  // failure-path test: a wait that nothing ends
+    while (next_piece<C>(P, at, p)) {
+      const int32_t *bt = kv.block_table + (size_t)at.b * kv.max_blocks;
+      const int last = (p.ke - 1) >> bs_shift;
+      auto load_id = [&](int blk) { return blk <= last ? bt[blk] : -1; };
+      int wbase = max(p.kt0 * TK, p.lo) >> bs_shift;
+      int cur = load_id(wbase + lane), nxt = load_id(wbase + 32 + lane);
+      {  // the piece's query rows on their way to L2
+        const int R = min(RB, P.G * at.s.n - p.rb * RB);
+        for (int x = lane; x < R * (D / 64); x += 32) {
+          const int r = p.rb * RB + x / (D / 64), i = r / P.G, head = p.kvh * P.G + r - i * P.G;
+          const char *q = reinterpret_cast<const char *>(a.q) + (((size_t)(at.s.row0 + i) * a.num_q_heads + head) * D + x % (D / 64) * 64) * 2;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
         }
-        const bool want = id != -2, bad = want && (id < 0 || id >= kv.num_blocks), go = want && !bad;
+      }
+      for (int kt = p.kt0; kt < p.kt1; ++kt, ++tile0) {
+        const uint32_t st = tile0 % ST;
+        const int tok = kt * TK + box_row, first = max(kt * TK, p.lo) >> bs_shift;
+        while (first >= wbase + 32) {  // uniform
+          wbase += 32;
+          cur = nxt;
+          nxt = load_id(wbase + 32 + lane);
+        }
+        // boxes without a key that some row may see are not read
+        const bool want = box_row < TK && tok < p.ke && tok + box > p.lo;
+        const int src = want ? (tok >> bs_shift) - wbase : 0;
+        const int id0 = __shfl_sync(0xffffffffu, cur, src & 31), id1 = __shfl_sync(0xffffffffu, nxt, src & 31);
+        const int id = src < 32 ? id0 : id1;
+        const bool bad = want && (id < 0 || id >= kv.num_blocks), go = want && !bad;
         if (bad) record(a.status, SV_ERR_BAD_BLOCK_ID);
+        if (tile0 >= ST) wait(s_free[st], (tile0 / ST - 1) & 1u);
+        if (dead) break;  // nothing more is issued
         const uint32_t bar = smem_at(&s_full[st]);
         const int boxes = __popc(__ballot_sync(0xffffffffu, go));
         if (lane == 0) bar_expect(bar, boxes * box * C::ROWB);
         __syncwarp();
         if (go) {
-          const int tok = (kt0 + turn) * TK + box_row;
-          const int y = ((id * kv.num_kv_heads + kvh) << bs_shift) + (tok & (kv.block_size - 1));
-          const uint32_t dst = ring_at + st * C::kStageBytes + (lane & 1) * TK * C::ROWB + box_row * C::ROWB;
-          load_box<C::ROWB>(dst, (lane & 1) ? &map_v : &map_k, y, bar);
+          const int y = ((id * kv.num_kv_heads + p.kvh) << bs_shift) + (tok & (kv.block_size - 1));
+          load_box<C::ROWB>(ring_at + st * C::kStageBytes + (lane & 1) * TK * C::ROWB + box_row * C::ROWB,
+                            (lane & 1) ? &map_v : &map_k, y, bar);
         }
         __syncwarp();
-        issued[1] = issued[0];
-        issued[0] = (int)x;
-        turn += 4;
-        id = block_of(turn);
       }
-    };
-    issue_until(ST - 1);  // the stages are free: the previous piece is done with them
-    __syncthreads();
-    const int row_top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
-    const int all_see = window > 0 ? row_top - window + 1 : 0;  // keys from here to c are visible to every row
-
-    // ---- Q into registers ----
-    uint32_t q[NT][KT][2];
-    {
-      const uint32_t *src = reinterpret_cast<const uint32_t *>(a.q);
-      bool over = false;
+      if (dead) break;
+    }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+    // ================= consumers =================
+    const int g = lane >> 2, t = lane & 3;
+    const int wk = warp % WK, wr = warp / WK;
+    float *merge = reinterpret_cast<float *>(ring + C::kRing);  // [consumer][8][kPad]
+    auto together = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory"); };
+    const float sl2 = F8 ? a.scale_log2 * kv.k_scale : a.scale_log2;
+    const float cap = P.s.cap, cap_in = F8 ? P.cap_in * kv.k_scale : P.cap_in;
+    const bool fast_cap = cap <= kFastCap * 1.4426950408889634f;
+    const int window = P.s.window;
+    const bool biased = P.s.slopes != nullptr;
+    const bool bounded = !F8 && cap > 0.f && cap <= kBoundedCap && !biased;
+    bool first_piece = true;
+    // what ldmatrix adds to a row's place for 16-value step q (mod 4) of its head: chunk 2 q + (0 or 1), swizzled
+    const int lr = lane & 7, lm = lane >> 3;
+    const int k_row = lm & 1, k_hi = lm >> 1, v_row = F8 ? lm & 1 : lm >> 1, v_hi = F8 ? lm >> 1 : lm & 1;
+    constexpr int CH = C::ROWB / 16, kRow = C::ROWB >= 128 ? 128 : 64;  // chunks of a row; bytes between a group's rows
+    uint32_t k_off[4], v_off[4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int rl = (wr * NT + nt) * 8 + g, i = s_row[rl];
-        const int r = rb * RB + rl;
-        const size_t at = i < 0 ? 0 : ((size_t)(s.row0 + i) * a.num_q_heads + kvh * P.G + (r - i * P.G)) * (D / 2);
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-          if (F8) {
-            const uint2 x = i < 0 ? make_uint2(0, 0) : *reinterpret_cast<const uint2 *>(src + at + kk * 8 + 2 * t);
-            q[nt][kk][0] = pack2<true>(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
-            q[nt][kk][1] = pack2<true>(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              over |= (q[nt][kk][h] & 0x7c00u) == 0x7c00u || (q[nt][kk][h] & 0x7c000000u) == 0x7c000000u;
-          } else {
-            q[nt][kk][0] = i < 0 ? 0u : src[at + kk * 8 + t];
-            q[nt][kk][1] = i < 0 ? 0u : src[at + kk * 8 + t + 4];
-          }
-        }
-      }
-      if (F8 && over) record(a.status, SV_ERR_NONFINITE);  // a query element beyond the fp16 range
+    for (int x = 0; x < 4; ++x) {
+      k_off[x] = k_row * 8 * C::ROWB + lr * kRow + (CH >= 8 ? ((x * 2 + k_hi) ^ lr) << 4 : (((x * 2 + k_hi) & 3) ^ ((lr >> 1) & 3)) << 4);
+      v_off[x] = TK * C::ROWB + v_row * 8 * C::ROWB + lr * kRow +
+                 (CH >= 8 ? ((x * 2 + v_hi) ^ lr) << 4 : (((x * 2 + v_hi) & 3) ^ ((lr >> 1) & 3)) << 4);
     }
 
-    float o[KT][NT][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = bounded ? 0.f : kNone;
-      l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-      for (int mt = 0; mt < KT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
-    }
+    while (next_piece<C>(P, at, p)) {
+      const Seq &s = at.s;
+      const int c = s.c, ke = p.ke, lo = p.lo, kvh = p.kvh, rb = p.rb;
+      const int rows = min(RB, P.G * s.n - rb * RB);  // live rows of the block
+      // ---- rows of the block and the new keys' places (every consumer is done with the previous piece's) ----
+      int top = c;
+      for (int x = tid; x < RB; x += kC) {
+        const bool live = x < rows;
+        const int r = rb * RB + x, i = live ? r / P.G : 0, head = kvh * P.G + (live ? r - i * P.G : 0);
+        const int pos = P.s.positions != nullptr ? P.s.positions[s.row0 + i] : c + i;
+        if (pos < c) record(a.status, SV_ERR_BAD_LENGTH);
+        s_row[x] = live ? i : -1;
+        // places (positions minus c) from reach + 1 on are within the window; new keys are bits of the mask
+        s_reach[x] = !live ? 1 << 30 : window > 0 ? pos - c - window : -(1 << 30);
+        uint64_t mask = 0ull;
+        if (live) {
+          mask = a.mask_kind == SV_MASK_TREE ? a.tree_mask[s.row0 + i] : (2ull << i) - 1ull;
+          if (s.n < 64) mask &= (1ull << s.n) - 1ull;
+          if (window > 0 && pos - c >= window)
+            for (int j = 0; j < s.n; ++j) {
+              const int place = P.s.positions != nullptr ? P.s.positions[s.row0 + j] - c : j;
+              if (place <= pos - c - window) mask &= ~(1ull << j);
+            }
+        }
+        s_mask[x] = mask;
+        s_slope[x] = biased ? P.s.slopes[head] * 1.4426950408889634f : 0.f;
+        top = max(top, live ? pos : c);
+      }
+      for (int x = tid; x < s.n; x += kC) s_place[x] = P.s.positions != nullptr ? P.s.positions[s.row0 + x] - c : x;
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) s_top[warp] = top;
 
-    for (int kt = kt0; kt < kt1; ++kt) {
-      const uint32_t x = tile0 + (kt - kt0), st = x % ST;
-      issue_until(kt - kt0 + ST);
-      wait(s_full[st], (x / ST) & 1u);
-      const uint32_t k_at = ring_at + st * C::kStageBytes + k_lane, v_at = ring_at + st * C::kStageBytes + TK * C::ROWB + v_lane;
-#pragma unroll 1
-      for (int k16 = wk * 16; k16 < TK; k16 += WK * 16) {
-        const int key0 = kt * TK + k16;
-        if (key0 >= ke || key0 + 16 <= lo) continue;  // warp-uniform: nothing to see here
-        // ---- S^T = K Q^T ----
-        float sc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-        const uint32_t kaddr = k_at + k16 * C::ROWB;
-        if (!F8) {
-#pragma unroll
-          for (int kk = 0; kk < KT; ++kk) {
-            uint32_t f[4];
-            ldm4(f, kaddr + k_off[kk & 3] + (kk >> 2) * 1024);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], f, q[nt][kk][0], q[nt][kk][1]);
-          }
-        } else {
-#pragma unroll
-          for (int k2 = 0; k2 < KT / 2; ++k2) {
-            uint32_t f[4];
-            ldm4(f, kaddr + k_off[k2 & 3] + (k2 >> 2) * 1024);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t e[4] = {widen(f[2 * h]), widen(f[2 * h + 1]), widen(f[2 * h] >> 16), widen(f[2 * h + 1] >> 16)};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<true>(sc[nt], e, q[nt][2 * k2 + h][0], q[nt][2 * k2 + h][1]);
-            }
-          }
-        }
-        // ---- scores ----
-        if (cap == 0.f) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] *= sl2;
-        } else if (fast_cap) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = -2.f * cap * rcp(1.f + ex2(sc[nt][e] * cap_in));
-        } else {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = cap * tanhf(sc[nt][e] * sl2 / cap) - cap;
-        }
-        const bool edge = key0 + 16 > min(c, ke) || key0 < all_see;  // warp-uniform: some row may not see some key
-        if (biased && !edge) {
-          const float d0 = (float)(key0 + g - c), d1 = d0 + 8.f;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float2 sl = *reinterpret_cast<const float2 *>(&s_slope[(wr * NT + nt) * 8 + 2 * t]);
-            sc[nt][0] = fmaf(sl.x, d0, sc[nt][0]);
-            sc[nt][1] = fmaf(sl.y, d0, sc[nt][1]);
-            sc[nt][2] = fmaf(sl.x, d1, sc[nt][2]);
-            sc[nt][3] = fmaf(sl.y, d1, sc[nt][3]);
-          }
-        }
-        if (edge) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = key0 + g + 8 * h, j = key - c;
-            const int place = j >= 0 && key < ke ? s_place[j] : j;  // position of the key minus c
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int rl = (wr * NT + nt) * 8 + 2 * t + e, i = s_row[rl];
-                bool vis = key < ke && i >= 0;
-                if (vis && j >= 0) vis = a.mask_kind == SV_MASK_CAUSAL ? j <= i : ((s_mask[rl] >> j) & 1ull) != 0;
-                if (vis && window > 0) vis = s_pos[rl] - c - place < window;
-                sc[nt][2 * h + e] = vis ? fmaf(s_slope[rl], (float)place, sc[nt][2 * h + e]) : -INFINITY;
-              }
-          }
-        }
-        // ---- the running maximum ----
-        if (!bounded) {
-          bool move = false;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              move |= sc[nt][e] > m[nt][e & 1] + kMoveAt;
-            }
-          if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(sc[nt][e], sc[nt][e + 2]);
-#pragma unroll
-                for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
-                const float mn = fmaxf(m[nt][e], mx);
-                const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
-                m[nt][e] = mn;
-                l[nt][e] *= f;
-#pragma unroll
-                for (int mt = 0; mt < KT; ++mt) {
-                  o[mt][nt][e] *= f;
-                  o[mt][nt][e + 2] *= f;
-                }
-              }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] -= m[nt][e & 1];
-        }
-        // ---- P^T ----
-        uint32_t pb[NT][2];
+      // ---- Q into registers ----
+      uint32_t q[NT][KT][2];
+      {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(a.q);
+        bool over = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          const int rl = (wr * NT + nt) * 8 + g, r = rb * RB + rl, i = r / P.G;
+          const bool live = rl < rows;
+          const size_t from = live ? ((size_t)(s.row0 + i) * a.num_q_heads + kvh * P.G + (r - i * P.G)) * (D / 2) : 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[nt][e] = ex2(sc[nt][e]);
-          l[nt][0] += sc[nt][0] + sc[nt][2];
-          l[nt][1] += sc[nt][1] + sc[nt][3];
-          pb[nt][0] = turn8x8(pack2<F8>(sc[nt][0], sc[nt][1]));
-          pb[nt][1] = turn8x8(pack2<F8>(sc[nt][2], sc[nt][3]));
+          for (int kk = 0; kk < KT; ++kk) {
+            if (F8) {
+              const uint2 x = live ? *reinterpret_cast<const uint2 *>(src + from + kk * 8 + 2 * t) : make_uint2(0, 0);
+              q[nt][kk][0] = pack2<true>(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
+              q[nt][kk][1] = pack2<true>(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                over |= (q[nt][kk][h] & 0x7c00u) == 0x7c00u || (q[nt][kk][h] & 0x7c000000u) == 0x7c000000u;
+            } else {
+              q[nt][kk][0] = live ? src[from + kk * 8 + t] : 0u;
+              q[nt][kk][1] = live ? src[from + kk * 8 + t + 4] : 0u;
+            }
+          }
         }
-        // ---- O^T += V^T P^T ----
-        if (!F8) {
-          const uint32_t vaddr = v_at + k16 * C::ROWB;
-          bool odd = false;  // an infinity or NaN among this step's values
+        if (F8 && over) record(a.status, SV_ERR_NONFINITE);  // a query element beyond the fp16 range
+      }
+      together();
+      int row_top = s_top[0];
 #pragma unroll
-          for (int mt = 0; mt < KT; ++mt) {
-            uint32_t f[4];
-            ldm4t(f, vaddr + v_off[mt & 3] + (mt >> 2) * 1024);
-            if (edge) {  // 0 * infinity must not reach a row that does not see the key
+      for (int w = 1; w < C::kConsumers; ++w) row_top = max(row_top, s_top[w]);
+      const int all_see = window > 0 ? row_top - window + 1 : 0;  // keys from here to c are visible to every row
+
+      float o[KT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (nonfinite2(f[x])) {
-                  odd = true;
-                  if ((f[x] & 0x7f80u) == 0x7f80u) f[x] &= 0xffff0000u;
-                  if ((f[x] & 0x7f800000u) == 0x7f800000u) f[x] &= 0xffffu;
+      for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = bounded ? 0.f : kNone;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < KT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
+      }
+
+      const int steps = (p.kt1 - p.kt0) * S;
+      for (int step = wk; step < steps; step += WK) {
+        const uint32_t x = tile0 + step / S, st = x % ST;
+        wait(s_full[st], (x / ST) & 1u);
+        const int key0 = p.kt0 * TK + step * 16 * M;
+        if (key0 < ke && key0 + 16 * M > lo) {  // warp-uniform: else nothing to see here
+          const uint32_t tile = ring_at + st * C::kStageBytes + (step % S) * 16 * M * C::ROWB;
+          // ---- S^T = K Q^T ----
+          float sc[M][NT][4];
+#pragma unroll
+          for (int u = 0; u < M; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) sc[u][nt][0] = sc[u][nt][1] = sc[u][nt][2] = sc[u][nt][3] = 0.f;
+          // ldmatrix results in flight: a read takes as long as five products, and one feeds this many
+          constexpr int kFeedK = M * NT * (F8 ? 2 : 1), kFeedV = NT * (F8 ? 2 : 1);
+          constexpr int PB = 1 + (4 + kFeedK) / kFeedK, PV = 1 + (4 + kFeedV) / kFeedV;
+          constexpr int KL = F8 ? KT / 2 : KT, VL = KL;  // reads of 16 keys, K and V
+          auto k_at = [&](int x, int u) { return tile + u * 16 * C::ROWB + k_off[x & 3] + (x >> 2) * 1024; };
+          auto v_at = [&](int x) { return tile + x / VL * 16 * C::ROWB + v_off[x % VL & 3] + (x % VL >> 2) * 1024; };
+          {
+            uint32_t f[PB][M][4];
+#pragma unroll
+            for (int kk = 0; kk < PB - 1 && kk < KL; ++kk)
+#pragma unroll
+              for (int u = 0; u < M; ++u) ldm4(f[kk][u], k_at(kk, u));
+#pragma unroll
+            for (int kk = 0; kk < KL; ++kk) {
+              if (kk + PB - 1 < KL) {
+#pragma unroll
+                for (int u = 0; u < M; ++u) ldm4(f[(kk + PB - 1) % PB][u], k_at(kk + PB - 1, u));
+              }
+              if (!F8) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int u = 0; u < M; ++u) mma<false>(sc[u][nt], f[kk % PB][u], q[nt][kk][0], q[nt][kk][1]);
+              } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t e[M][4];
+#pragma unroll
+                  for (int u = 0; u < M; ++u) {
+                    const uint32_t c0 = f[kk % PB][u][2 * h], c1 = f[kk % PB][u][2 * h + 1];
+                    e[u][0] = widen(c0), e[u][1] = widen(c1), e[u][2] = widen(c0 >> 16), e[u][3] = widen(c1 >> 16);
+                  }
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < M; ++u) mma<true>(sc[u][nt], e[u], q[nt][2 * kk + h][0], q[nt][2 * kk + h][1]);
+                }
+              }
+            }
+          }
+          uint32_t vf[PV][4];  // the first values are on their way during the softmax
+#pragma unroll
+          for (int y = 0; y < PV - 1; ++y) ldm4t(vf[y], v_at(y));
+          // ---- scores ----
+          float *const sv = &sc[0][0][0];
+          constexpr int kE = M * NT * 4;  // of them; element x: key half (x >> 1) & 1, row x & 1 of its n tile
+          if (cap == 0.f) {
+#pragma unroll
+            for (int y = 0; y < kE; ++y) sv[y] *= sl2;
+          } else if (fast_cap) {
+#pragma unroll
+            for (int y = 0; y < kE; ++y) sv[y] = -2.f * cap * rcp(1.f + ex2(sv[y] * cap_in));
+          } else {
+#pragma unroll
+            for (int y = 0; y < kE; ++y) sv[y] = cap * tanhf(sv[y] * sl2 / cap) - cap;
+          }
+          const bool edge = key0 + 16 * M > min(c, ke) || key0 < all_see;  // warp-uniform: some row may not see some key
+          if (biased && !edge) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float2 sl = *reinterpret_cast<const float2 *>(&s_slope[(wr * NT + nt) * 8 + 2 * t]);
+#pragma unroll
+              for (int u = 0; u < M; ++u) {
+                const float d0 = (float)(key0 + 16 * u + g - c), d1 = d0 + 8.f;
+                sc[u][nt][0] = fmaf(sl.x, d0, sc[u][nt][0]);
+                sc[u][nt][1] = fmaf(sl.y, d0, sc[u][nt][1]);
+                sc[u][nt][2] = fmaf(sl.x, d1, sc[u][nt][2]);
+                sc[u][nt][3] = fmaf(sl.y, d1, sc[u][nt][3]);
+              }
+            }
+          }
+          bool odd = false;  // an edge step whose values hold an infinity or NaN
+          if (edge) {
+            const int base = key0 - c;  // place of the step's first key
+            if (biased) {
+#pragma unroll
+              for (int h = 0; h < 2 * M; ++h) {
+                const int j = base + g + 8 * h;
+                const float place = (float)(j >= 0 && j < s.n ? s_place[j] : j);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    float &v = sc[h >> 1][nt][2 * (h & 1) + e];
+                    v = fmaf(s_slope[(wr * NT + nt) * 8 + 2 * t + e], place, v);
+                  }
+              }
+            }
+            // A row's view of the step's keys as bits: committed keys beyond its reach, and its mask of new ones.
+            const uint32_t old = base >= 0 ? 0u : base <= -32 ? ~0u : (1u << -base) - 1u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int rl = (wr * NT + nt) * 8 + 2 * t + e, first = s_reach[rl] + 1 - base;
+                const uint64_t mask = s_mask[rl];
+                const uint32_t near = first <= 0 ? ~0u : first >= 32 ? 0u : ~0u << first;
+                const uint32_t fresh =
+                    base >= 0 ? (base < 64 ? (uint32_t)(mask >> base) : 0u) : (base > -32 ? (uint32_t)mask << -base : 0u);
+                const uint32_t seen = ((old & near) | fresh) >> g;
+#pragma unroll
+                for (int h = 0; h < 2 * M; ++h) {
+                  float &v = sc[h >> 1][nt][2 * (h & 1) + e];
+                  v = (seen >> (8 * h)) & 1u ? v : -INFINITY;
+                }
+              }
+            // Do the step's values hold what must not meet a weight of zero? (E4M3: NaN codes of unused slots.)
+            constexpr int kChunks = 16 * M * C::ROWB / 16;
+            const uint8_t *vs = ring + st * C::kStageBytes + (TK + (step % S) * 16 * M) * C::ROWB;
+#pragma unroll 4
+            for (int y = lane; y < kChunks; y += 32) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(vs + y * 16);
+              odd |= F8 ? nan_code4(w.x) | nan_code4(w.y) | nan_code4(w.z) | nan_code4(w.w)
+                        : nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w);
+            }
+            odd = __any_sync(0xffffffffu, odd);
+          }
+          // ---- the running maximum ----
+          if (!bounded) {
+            bool move = false;
+#pragma unroll
+            for (int u = 0; u < M; ++u)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  move |= sc[u][nt][e] > m[nt][e & 1] + kMoveAt<F8>;
+                }
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float mx = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+#pragma unroll
+                  for (int u = 1; u < M; ++u) mx = fmaxf(mx, fmaxf(sc[u][nt][e], sc[u][nt][e + 2]));
+#pragma unroll
+                  for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+                  const float mn = fmaxf(m[nt][e], mx);
+                  const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
+                  m[nt][e] = mn;
+                  l[nt][e] *= f;
+#pragma unroll
+                  for (int mt = 0; mt < KT; ++mt) {
+                    o[mt][nt][e] *= f;
+                    o[mt][nt][e + 2] *= f;
+                  }
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<false>(o[mt][nt], f, pb[nt][0], pb[nt][1]);
+            for (int u = 0; u < M; ++u)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[u][nt][e] -= m[nt][e & 1];
           }
-          if (edge && __any_sync(0xffffffffu, odd)) {
+          // ---- P^T ----
+          uint32_t pb[M][NT][2];
+#pragma unroll
+          for (int u = 0; u < M; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[u][nt][e] = ex2(sc[u][nt][e]);
+              l[nt][0] += sc[u][nt][0] + sc[u][nt][2];
+              l[nt][1] += sc[u][nt][1] + sc[u][nt][3];
+              pb[u][nt][0] = turn8x8(pack2<F8>(sc[u][nt][0], sc[u][nt][1]));
+              pb[u][nt][1] = turn8x8(pack2<F8>(sc[u][nt][2], sc[u][nt][3]));
+            }
+          // ---- O^T += V^T P^T ----
+          auto pv = [&](auto checked) {  // checked: without infinities and NaN
+            constexpr bool kCheck = decltype(checked)::value;
+#pragma unroll
+            for (int x = 0; x < M * VL; ++x) {
+              if (x + PV - 1 < M * VL) ldm4t(vf[(x + PV - 1) % PV], v_at(x + PV - 1));
+              uint32_t(&w)[4] = vf[x % PV];
+              const int u = x / VL, mt = x % VL;
+              if (!F8) {
+                if (kCheck) {  // 0 * infinity must not reach a row that does not see the key
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) {
+                    if ((w[y] & 0x7f80u) == 0x7f80u) w[y] &= 0xffff0000u;
+                    if ((w[y] & 0x7f800000u) == 0x7f800000u) w[y] &= 0xffffu;
+                  }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma<false>(o[mt][nt], w, pb[u][nt][0], pb[u][nt][1]);
+              } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  // a word: two dimensions of one key below, of the next key above; pairs of keys are wanted
+                  const uint32_t w0 = __byte_perm(w[2 * h], 0u, 0x3120), w1 = __byte_perm(w[2 * h + 1], 0u, 0x3120);
+                  uint32_t e[4] = {widen(w0), widen(w0 >> 16), widen(w1), widen(w1 >> 16)};
+                  if (kCheck) {  // slots that no row sees may hold anything
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) e[y] = without_nan(e[y]);
+                  }
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma<true>(o[mt * 2 + h][nt], e, pb[u][nt][0], pb[u][nt][1]);
+                }
+              }
+            }
+          };
+          if (!odd) pv(std::false_type());
+          else pv(std::true_type());
+          if (!F8 && odd) {
             // the values set to zero above, for the rows that see their keys
-            const uint8_t *vs = ring + st * C::kStageBytes + TK * C::ROWB + k16 * C::ROWB;
+            const uint8_t *vs = ring + st * C::kStageBytes + (TK + (step % S) * 16 * M) * C::ROWB;
 #pragma unroll 1
-            for (int key = 0; key < 16; ++key) {
+            for (int key = 0; key < 16 * M; ++key) {
+              const int h = key >> 3;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const float e0 = key < 8 ? sc[nt][0] : sc[nt][2], e1 = key < 8 ? sc[nt][1] : sc[nt][3];
+                float e0 = sc[0][nt][0], e1 = sc[0][nt][1];
+#pragma unroll
+                for (int y = 1; y < 2 * M; ++y)
+                  if (h == y) {
+                    e0 = sc[y >> 1][nt][2 * (y & 1)];
+                    e1 = sc[y >> 1][nt][2 * (y & 1) + 1];
+                  }
                 const float p0 = __shfl_sync(0xffffffffu, e0, (key & 7) * 4 + t);
                 const float p1 = __shfl_sync(0xffffffffu, e1, (key & 7) * 4 + t);
 #pragma unroll
                 for (int mt = 0; mt < KT; ++mt)
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const uint32_t x =
-                        *reinterpret_cast<const uint16_t *>(vs + (key >> 3) * 8 * C::ROWB + (key & 7) * 128 + (mt >> 2) * 1024 +
-                                                            ((((mt & 3) * 2 + h) ^ (key & 7)) << 4) + g * 2);
-                    if ((x & 0x7f80u) != 0x7f80u) continue;
-                    const float v = __uint_as_float(x << 16);
-                    if (p0 > 0.f) o[mt][nt][2 * h] += p0 * v;
-                    if (p1 > 0.f) o[mt][nt][2 * h + 1] += p1 * v;
+                  for (int y = 0; y < 2; ++y) {
+                    const uint32_t w =
+                        *reinterpret_cast<const uint16_t *>(vs + h * 8 * C::ROWB + (key & 7) * 128 + (mt >> 2) * 1024 +
+                                                            ((((mt & 3) * 2 + y) ^ (key & 7)) << 4) + g * 2);
+                    if ((w & 0x7f80u) != 0x7f80u) continue;
+                    const float v = __uint_as_float(w << 16);
+                    if (p0 > 0.f) o[mt][nt][2 * y] += p0 * v;
+                    if (p1 > 0.f) o[mt][nt][2 * y + 1] += p1 * v;
                   }
               }
             }
           }
-        } else {
-          const uint32_t vaddr = v_at + k16 * C::ROWB;
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_at(&s_free[st]));
+      }
+      tile0 += p.kt1 - p.kt0;
+
+      // ---- the key groups' results, merged, 8 rows of each row group at a time ----
 #pragma unroll
-          for (int m2 = 0; m2 < KT / 2; ++m2) {
-            uint32_t f[4];
-            ldm4t(f, vaddr + v_off[m2 & 3] + (m2 >> 2) * 1024);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // a word: two dimensions of one key below, of the next key above; pairs of keys are wanted
-              const uint32_t w0 = __byte_perm(f[2 * h], 0u, 0x3120), w1 = __byte_perm(f[2 * h + 1], 0u, 0x3120);
-              uint32_t e[4] = {widen(w0), widen(w0 >> 16), widen(w1), widen(w1 >> 16)};
-              if (edge) {  // slots that no row sees may hold anything
+        for (int e = 0; e < 2; ++e) {
+          float sum = l[nt][e];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) e[y] = without_nan(e[y]);
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<true>(o[m2 * 2 + h][nt], e, pb[nt][0], pb[nt][1]);
-            }
+          for (int y = 4; y < 32; y <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+          if (g == 0) {
+            s_m[wk][(wr * NT + nt) * 8 + 2 * t + e] = m[nt][e];
+            s_l[wk][(wr * NT + nt) * 8 + 2 * t + e] = sum;
           }
         }
-      }
-      __syncwarp();
-      if (lane == 0) bar_arrive(smem_at(&s_free[st]));
-    }
-    // ---- the key groups' results, merged ----
-    __syncthreads();  // every warp is done with the ring
-    tile0 += ntiles;
-    float *buf = reinterpret_cast<float *>(ring);  // [WK][RB][kPad]
+      const size_t slot = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * P.rows_cap;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rl = (wr * NT + nt) * 8 + 2 * t + e;
-        float sum = l[nt][e];
+        for (int d0 = 0; d0 < D; d0 += C::kChunk) {
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        if (g == 0) {
-          s_m[wk][rl] = m[nt][e];
-          s_l[wk][rl] = sum;
+          for (int e = 0; e < 2; ++e) {
+            float *dst = merge + ((wr * WK + wk) * 8 + 2 * t + e) * C::kPad;
+#pragma unroll
+            for (int mt = 0; mt < C::kChunk / 16; ++mt) {
+              dst[mt * 16 + (F8 ? 2 * g : g)] = o[d0 / 16 + mt][nt][e];
+              dst[mt * 16 + (F8 ? 2 * g + 1 : g + 8)] = o[d0 / 16 + mt][nt][e + 2];
+            }
+          }
+          together();
+          if (nt == 0 && d0 == 0) {  // every group's weight in a row, over the rows' total
+            for (int rl = tid; rl < rows; rl += kC) {
+              float mx = s_m[0][rl], tot = 0.f;
+#pragma unroll
+              for (int w = 1; w < WK; ++w) mx = fmaxf(mx, s_m[w][rl]);  // finite: kNone at the least
+#pragma unroll
+              for (int w = 0; w < WK; ++w) tot += s_l[w][rl] * ex2(s_m[w][rl] - mx);
+              const float inv = tot == 0.f ? 0.f : (F8 ? kv.v_scale : 1.f) / tot;
+              if (!p.whole) P.part_lse[slot + rl] = tot == 0.f ? -INFINITY : mx + log2f(tot);
+#pragma unroll
+              for (int w = 0; w < WK; ++w) s_l[w][rl] = ex2(s_m[w][rl] - mx) * inv;
+            }
+            together();
+          }
+          for (int x = tid; x < WR * C::kChunk; x += kC) {  // 8 values of a row
+            const int r8 = x / (C::kChunk / 8), d8 = x % (C::kChunk / 8) * 8, rl = ((r8 >> 3) * NT + nt) * 8 + (r8 & 7);
+            if (rl >= rows) continue;
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < WK; ++w) {
+              const float f = s_l[w][rl];
+              const float4 *src = reinterpret_cast<const float4 *>(merge + (((r8 >> 3) * WK + w) * 8 + (r8 & 7)) * C::kPad + d8);
+              const float4 x0 = src[0], x1 = src[1];
+              v[0] = fmaf(f, x0.x, v[0]), v[1] = fmaf(f, x0.y, v[1]), v[2] = fmaf(f, x0.z, v[2]), v[3] = fmaf(f, x0.w, v[3]);
+              v[4] = fmaf(f, x1.x, v[4]), v[5] = fmaf(f, x1.y, v[5]), v[6] = fmaf(f, x1.z, v[6]), v[7] = fmaf(f, x1.w, v[7]);
+            }
+            if (p.whole) {
+              const int i = s_row[rl], head = kvh * P.G + (rb * RB + rl) - i * P.G;
+              *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
+                                         ((size_t)(s.row0 + i) * a.num_q_heads + head) * D + d0 + d8) =
+                  make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
+            } else {
+              float4 *dst = reinterpret_cast<float4 *>(P.part_o + (slot + rl) * D + d0 + d8);
+              dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+              dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+          }
+          together();
         }
-        float *dst = buf + (wk * RB + rl) * C::kPad;
-#pragma unroll
-        for (int mt = 0; mt < KT; ++mt) {
-          dst[mt * 16 + (F8 ? 2 * g : g)] = o[mt][nt][e];
-          dst[mt * 16 + (F8 ? 2 * g + 1 : g + 8)] = o[mt][nt][e + 2];
-        }
-      }
-    __syncthreads();
-    const size_t slot = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * P.rows_cap;
-    if (tid < rows) {
-      float M = s_m[0][tid], tot = 0.f;
-#pragma unroll
-      for (int w = 1; w < WK; ++w) M = fmaxf(M, s_m[w][tid]);
-      const float ref = M;  // finite: kNone at the least
-#pragma unroll
-      for (int w = 0; w < WK; ++w) tot += s_l[w][tid] * ex2(s_m[w][tid] - ref);
-      const float inv = tot == 0.f ? 0.f : (F8 ? kv.v_scale : 1.f) / tot;
-      if (!whole) P.part_lse[slot + tid] = tot == 0.f ? -INFINITY : M + log2f(tot);
-#pragma unroll
-      for (int w = 0; w < WK; ++w) s_l[w][tid] = ex2(s_m[w][tid] - ref) * inv;
+      first_piece = false;
     }
-    __syncthreads();
-    for (int x = tid; x < rows * (D / 8); x += kThreads) {
-      const int rl = x / (D / 8), d8 = (x % (D / 8)) * 8;
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = 0.f;
-#pragma unroll
-      for (int w = 0; w < WK; ++w) {
-        const float f = s_l[w][rl];
-        const float4 *src = reinterpret_cast<const float4 *>(buf + (w * RB + rl) * C::kPad + d8);
-        const float4 x0 = src[0], x1 = src[1];
-        v[0] = fmaf(f, x0.x, v[0]), v[1] = fmaf(f, x0.y, v[1]), v[2] = fmaf(f, x0.z, v[2]), v[3] = fmaf(f, x0.w, v[3]);
-        v[4] = fmaf(f, x1.x, v[4]), v[5] = fmaf(f, x1.y, v[5]), v[6] = fmaf(f, x1.z, v[6]), v[7] = fmaf(f, x1.w, v[7]);
-      }
-      if (whole) {
-        const int i = s_row[rl], head = kvh * P.G + (rb * RB + rl) - i * P.G;
-        *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
-                                   ((size_t)(s.row0 + i) * a.num_q_heads + head) * D + d8) =
-            make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
-      } else {
-        float4 *dst = reinterpret_cast<float4 *>(P.part_o + (slot + rl) * D + d8);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-      }
-    }
-    first_piece = false;
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the merge's accesses, before the next piece's copies
   }
-  if (dead) {
-    if (lane == 0) record(a.status, SV_ERR_TIMEOUT);
-    // the copies this warp has in flight land before the CTA's shared memory is released
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (issued[k] >= 0) mbar_wait_bounded(smem_at(&s_full[issued[k] % ST]), (issued[k] / ST) & 1, kDrainBudgetNs);
-  }
+  if (dead && lane == 0) record(a.status, SV_ERR_TIMEOUT);
   __syncthreads();
+  // after a wait that gave up: the copies in flight land before the CTA's shared memory is released
+  if (s_dead && warp == C::kConsumers)
+    for (uint32_t x = tile0 > ST ? tile0 - ST : 0; x < tile0; ++x)
+      mbar_wait_bounded(smem_at(&s_full[x % ST]), (x / ST) & 1u, kDrainBudgetNs);
 }
 
 // Merges the partials of every unit that two or more CTAs shared: o = sum_p 2^lse_p o_p / sum_p 2^lse_p,
 // in the order of the CTAs. A thread takes 8 values of a row, four pieces' loads in flight.
 template <class C>
-__global__ void __launch_bounds__(128) attn_scored_combine(const Params P) {
+__global__ void __launch_bounds__(512) attn_scored_combine(const Params P) {
   grid_dependents_launch();
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   constexpr int D = C::D;
@@ -796,7 +958,7 @@ Layout layout_of(const KV &kv, int G, int max_q, int max_seq_len) {
   return l;
 }
 
-constexpr int kAlpha = 2;  // positions of a unit's lead-in
+constexpr int kAlpha = 4;  // positions of a unit's lead-in
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -841,28 +1003,42 @@ cudaError_t run(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream
   p.box = std::min(kv.block_size, C::TK);
   CUtensorMap mk, mv;
   if (!make_map<C>(&mk, kv.k_pool, kv, p.box) || !make_map<C>(&mv, kv.v_pool, kv, p.box)) return cudaErrorInvalidValue;
+  static const bool split_fits = [] {  // the kernel was compiled for the registers that its split shares out
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, attn_scored_kernel<C>) == cudaSuccess && fa.numRegs == kLaunchRegs;
+  }();
+  if (!split_fits) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(attn_scored_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_scored_kernel<C>, dim3(p.ctas), dim3(kThreads), C::kSmem, st, mk, mv, p);
+  e = launch_pdl(attn_scored_kernel<C>, dim3(p.ctas), dim3(C::kThreads), C::kSmem, st, mk, mv, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_scored_combine<C>, dim3(kv.batch, kv.num_kv_heads * p.rb_max), dim3(128), 0, st, p);
+  const int items = std::min(512, (l.rows_cap * (C::D / 8) + 31) / 32 * 32);  // threads: one item each, if they fit
+  return launch_pdl(attn_scored_combine<C>, dim3(kv.batch, kv.num_kv_heads * p.rb_max), dim3(items), 0, st, p);
 }
 
 // The smallest block of query rows that holds a unit's, else blocks of the largest.
 template <int D, bool F8>
 cudaError_t pick(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {
   const int rows = sa.a.num_q_heads / sa.a.kv.num_kv_heads * sa.a.max_q;
-  if (rows <= 8) return run<Cfg<D, 1, 1, F8>>(sa, workspace, bytes, st, go);
-  if (rows <= 16) return run<Cfg<D, 2, 1, F8>>(sa, workspace, bytes, st, go);
-  if constexpr (D <= 128) {
-    if (rows <= 24) return run<Cfg<D, 3, 1, F8>>(sa, workspace, bytes, st, go);
-    if (rows <= 32) return run<Cfg<D, 4, 1, F8>>(sa, workspace, bytes, st, go);
-    if (rows <= 48) return run<Cfg<D, 3, 2, F8>>(sa, workspace, bytes, st, go);
-    if (rows <= 64) return run<Cfg<D, 4, 2, F8>>(sa, workspace, bytes, st, go);
-    return run<Cfg<D, 4, 4, F8>>(sa, workspace, bytes, st, go);
+  auto on = [&](auto cfg) { return run<decltype(cfg)>(sa, workspace, bytes, st, go); };
+  if constexpr (D == 64) {
+    if (rows <= 8) return on(Cfg<D, 1, 1, 4, F8>());
+    if (rows <= 16) return on(Cfg<D, 2, 1, 4, F8>());
+    if (rows <= 32) return on(Cfg<D, 4, 1, 4, F8>());
+    if (rows <= 48) return on(Cfg<D, 3, 2, 2, F8>());
+    if (rows <= 64) return on(Cfg<D, 4, 2, 2, F8>());
+    return on(Cfg<D, 4, 4, 1, F8>());
+  } else if constexpr (D == 128) {
+    if (rows <= 8) return on(Cfg<D, 1, 1, 4, F8>());
+    if (rows <= 16) return on(Cfg<D, 2, 1, 4, F8>());
+    if (rows <= 24) return on(Cfg<D, 3, 1, 4, F8>());
+    if (rows <= 32) return on(Cfg<D, 2, 2, 2, F8>());
+    if (rows <= 48) return on(Cfg<D, 3, 2, 2, F8>());
+    if (rows <= 64) return on(Cfg<D, 2, 4, 1, F8>());
+    return on(Cfg<D, 3, 4, 1, F8>());
   } else {
-    if (rows <= 32) return run<Cfg<D, 2, 2, F8>>(sa, workspace, bytes, st, go);
-    return run<Cfg<D, 2, 4, F8>>(sa, workspace, bytes, st, go);
+    if (rows <= 16) return on(Cfg<D, 1, 2, 2, F8>());
+    return on(Cfg<D, 1, 4, 1, F8>());
   }
 }
 

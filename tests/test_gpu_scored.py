@@ -203,7 +203,7 @@ def test_nonfinite_where_nothing_is_seen(dt, d):
                 pool[int(kv.block_table[b, x // 16]), :, x % 16] = bad
         # draft row 4 of sequence 0 (bit 4: only row 4 sees it)
         pool[int(kv.block_table[0, 204 // 16]), :, 204 % 16] = bad
-    S.attention(kv, dd, buf, 243)
+    S.attention(kv, dd, buf, max_seq_len(case.state, case.step))
     torch.cuda.synchronize()
     keep = [0, 1, 2, 3, 5, 6, 7, 8, 9, 10]
     assert torch.equal(buf.attn_out[keep], clean[keep])
