@@ -1,8 +1,8 @@
 """ctypes binding of libspecverify (include/spec_verify.h).
 
-Argument marshalling only: every function takes torch CUDA tensors, passes
-their device pointers and the current CUDA stream to the C ABI, and raises
-SVError on a non-OK return. Nothing here computes any part of the verify
+Argument marshalling only (the calls of the module _calls do theirs in C++):
+every function takes torch CUDA tensors, passes their device pointers and the
+current CUDA stream to the C ABI, and raises SVError on a non-OK return. Nothing here computes any part of the verify
 step, and nothing falls back to the CPU: a missing library or a CPU tensor is
 an error.
 """
@@ -277,19 +277,6 @@ class HeadTransform:
     weight_offset: float = 0.0  # 1 for weights stored as w - 1
     interleaved: bool = False  # pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2)
 
-    def struct(self, rows: torch.Tensor) -> sv_head_transform:
-        d = rows.shape[2]
-        for w in (self.q_weight, self.k_weight):
-            if w is not None and (w.dtype != rows.dtype or w.numel() != d):
-                raise ValueError(f"a norm weight holds {d} values of {rows.dtype}")
-        rot, freq = 0, self.inv_freq
-        if freq is not None:
-            if freq.dtype != torch.float32:
-                raise TypeError("inv_freq is float32")
-            rot = 2 * freq.numel()
-        return sv_head_transform(_at(freq) if rot else None, _at(self.q_weight), _at(self.k_weight), self.eps,
-                                 self.weight_offset, rot, self.interleaved)
-
 
 @dataclass
 class ScoreMod:
@@ -298,11 +285,6 @@ class ScoreMod:
     softcap: float = 0.0  # 0: not capped
     slopes: Optional[torch.Tensor] = None  # float32 [num_q_heads]
     window: int = 0  # 0: no limit
-
-    def struct(self, num_q_heads: int) -> sv_score_mod:
-        if self.slopes is not None and (self.slopes.dtype != torch.float32 or self.slopes.numel() != num_q_heads):
-            raise ValueError(f"slopes holds {num_q_heads} float32 values")
-        return sv_score_mod(_at(self.slopes), self.softcap, self.window)
 
 
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -316,32 +298,27 @@ def _at(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, like: Optional[torch.Tensor] = None) -> tuple:
-    """Pointer and row stride (elements) of rows of heads [n, heads, head_dim]; the
-    heads of a row are contiguous, the rows may be parts of wider ones."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("libspecverify takes CUDA tensors only")
-    n, h, d = t.shape
-    sn, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and h > 1):
-        raise ValueError("the heads of a row are contiguous")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"expected rows {tuple(like.shape)} of {like.dtype}, got {tuple(t.shape)} of {t.dtype}")
-    return t.data_ptr(), (sn if n > 1 else h * d)
+_calls = None
 
 
-def _i32(t: Optional[torch.Tensor], n: int, what: str) -> Optional[int]:
-    """Pointer of a contiguous int32 tensor of n values."""
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.numel() != n:
-        raise ValueError(f"{what} holds {n} int32 values")
-    return _at(t)
+def _bound():
+    """The extension module with the library's entry points."""
+    global _calls
+    lib = load()
+    from . import _calls as module
+    at = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+          for n in ("sv_qk_norm_rope", "sv_kv_append_rope", "sv_spec_verify_attn_scored",
+                    "sv_spec_verify_attn_scored_workspace_bytes")]
+    module.bind(*at)
+    _calls = module
+    return module
 
 
 def _stream_of(t: torch.Tensor, stream) -> int:
     """The stream to launch on: the caller's, or the current one. The library launches on the
     current device, which has to be the tensors'."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("libspecverify takes CUDA tensors only")
     device = t.get_device()
     if device != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {t.device}, the current device is {torch.cuda.current_device()}")
@@ -358,17 +335,9 @@ def qk_norm_rope(transform: HeadTransform, q: Optional[torch.Tensor], k: Optiona
     some = q if q is not None else k
     if some is None:
         raise ValueError("no rows: q and k are both None")
-    n, _, d = some.shape
-    qp, qs, qo, qos, hq, kp, ks, ko, kos, hkv = None, 0, None, 0, 0, None, 0, None, 0, 0
-    if q is not None:
-        (qp, qs), (qo, qos), hq = _rows(q), _rows(q_out, q), q.shape[1]
-    if k is not None:
-        (kp, ks), (ko, kos), hkv = _rows(k), _rows(k_out, k), k.shape[1]
-        if k.shape[0] != n or k.shape[2] != d or k.dtype != some.dtype:
-            raise ValueError("q and k have the same rows, head_dim and type")
-    _check((_lib or load()).sv_qk_norm_rope(ctypes.byref(transform.struct(some)), qp, qs, qo, qos, hq, kp, ks, ko, kos, hkv, d,
-                                  _dtype_code(some), n, _i32(positions, n, "positions"), _stream_of(some, stream)),
-           "sv_qk_norm_rope")
+    rc = (_calls or _bound()).qk_norm_rope(transform, q, k, positions, q_out, k_out, _stream_of(some, stream))
+    if rc:
+        raise SVError(rc, "sv_qk_norm_rope")
 
 
 def kv_append_rope(kv: PagedKV, transform: HeadTransform, new_k: torch.Tensor, new_v: torch.Tensor, cu_q: torch.Tensor,
@@ -376,20 +345,10 @@ def kv_append_rope(kv: PagedKV, transform: HeadTransform, new_k: torch.Tensor, n
                    positions: Optional[torch.Tensor] = None, stream=None) -> None:
     """kv_append with the keys normalised and rotated on the way into the cache; with q, the
     queries too, into q_out (which may be q). positions: int32 [n], or None for chains."""
-    s = kv.struct()
-    n, hkv, d = new_k.shape
-    rows = torch.float32 if kv.k_pool.dtype == torch.float32 else torch.bfloat16
-    if new_k.dtype != rows or hkv != s.num_kv_heads or d != s.head_dim:
-        raise ValueError(f"expected rows [n, {s.num_kv_heads}, {s.head_dim}] of {rows}")
-    (kp, ks), (vp, vs) = _rows(new_k), _rows(new_v, new_k)
-    qp, qs, qo, qos, hq = None, 0, None, 0, 0
-    if q is not None:
-        if q.shape[0] != n or q.shape[2] != d or q.dtype != rows:
-            raise ValueError(f"expected queries [{n}, heads, {d}] of {rows}")
-        (qp, qs), (qo, qos), hq = _rows(q), _rows(q_out, q), q.shape[1]
-    _check((_lib or load()).sv_kv_append_rope(ctypes.byref(s), ctypes.byref(transform.struct(new_k)), kp, ks, vp, vs, qp, qs, qo,
-                                    qos, hq, _i32(cu_q, s.batch + 1, "cu_q"), n, _i32(positions, n, "positions"),
-                                    _i32(status, 1, "status"), _stream_of(new_k, stream)), "sv_kv_append_rope")
+    rc = (_calls or _bound()).kv_append_rope(kv, transform, new_k, new_v, cu_q, status, q, q_out, positions,
+                                             _stream_of(new_k, stream))
+    if rc:
+        raise SVError(rc, "sv_kv_append_rope")
 
 
 def spec_verify_attn_scored_workspace_bytes(kv: PagedKV, num_q_heads: int, total_q: int, max_q: int,
@@ -405,23 +364,17 @@ def spec_verify_attn_scored(kv: PagedKV, q: torch.Tensor, out: torch.Tensor, cu_
                             stream=None) -> None:
     """spec_verify_attn with capped scores, a distance bias and a window (mod). Without a
     workspace a new one of the size the library asks for is taken."""
-    s = kv.struct()
-    n, hq, d = q.shape
-    rows = torch.float32 if kv.k_pool.dtype == torch.float32 else torch.bfloat16
-    if q.dtype != rows or d != s.head_dim or out.shape != q.shape or out.dtype != rows:
-        raise ValueError(f"expected queries and outputs [n, heads, {s.head_dim}] of {rows}")
-    if tree_mask is not None and (tree_mask.element_size() != 8 or tree_mask.numel() != n):
-        raise ValueError(f"tree_mask holds {n} 64-bit values")
-    lib, kvp, st = _lib or load(), ctypes.byref(s), _stream_of(q, stream)
-    if workspace is None:
-        need = lib.sv_spec_verify_attn_scored_workspace_bytes(kvp, hq, n, max_q, max_seq_len)
-        workspace = q.new_empty(max(need, 1), dtype=torch.uint8)
-        if stream is not None and st != torch._C._cuda_getCurrentRawStream(q.get_device()):
+    st = _stream_of(q, stream)
+    if workspace is None and stream is not None:
+        workspace = torch.empty(max(1, spec_verify_attn_scored_workspace_bytes(kv, q.shape[1], q.shape[0], max_q, max_seq_len)),
+                                dtype=torch.uint8, device=q.device)
+        if st != torch._C._cuda_getCurrentRawStream(q.get_device()):
             workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(st))
-    _check(lib.sv_spec_verify_attn_scored(
-        kvp, _at(q), _at(out), _i32(cu_q, s.batch + 1, "cu_q"), hq, n, max_q, max_seq_len, scale,
-        ctypes.byref(mod.struct(hq)), _i32(positions, n, "positions"), mask_kind, _at(tree_mask), _at(workspace),
-        workspace.numel() * workspace.element_size(), _i32(status, 1, "status"), st), "sv_spec_verify_attn_scored")
+    rc = (_calls or _bound()).spec_verify_attn_scored(
+        kv, q, out, cu_q, max_q, max_seq_len, scale, mod.softcap, mod.slopes, mod.window, positions, mask_kind, tree_mask,
+        workspace, status, st)
+    if rc:
+        raise SVError(rc, "sv_spec_verify_attn_scored")
 
 
 def spec_rejection_sample_workspace_bytes(logits_dtype: torch.dtype, vocab: int, batch: int, total_q: int,

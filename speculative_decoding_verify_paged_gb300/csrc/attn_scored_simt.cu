@@ -8,10 +8,13 @@
 // p_i - p_t < window. A key that a row does not see never enters its sums, whatever it holds.
 //
 // A CTA owns (key split, KV head, sequence) and all G n_b query rows of the KV head, 16 at a time;
-// keys go through shared memory 32 at a time; a warp keeps four rows' running maximum and sum and
-// their accumulators, a lane per key for the scores and a lane per column for the weighted sum.
+// keys go through shared memory as fp32, 32 at a time, in 16-byte reads; a warp keeps four rows' running
+// maximum and sum and their accumulators, a lane per key for the scores (four rows' products on
+// each 16-byte read of its key) and a lane per column for the weighted sum (four keys' weights a read).
+// Bound: latency for the short splits it is cut into (four CTAs an SM), the products for wide units.
 // Splits that the window leaves no key in write an empty partial (log-sum-exp -inf). A visible
 // NaN makes its row's sum and log-sum-exp NaN, and the merge of the splits carries it on.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "sv_internal.cuh"
@@ -34,11 +37,26 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-__device__ __forceinline__ float pool_f32(__nv_bfloat16 x, float) { return __bfloat162float(x); }
-__device__ __forceinline__ float pool_f32(float x, float) { return x; }
-__device__ __forceinline__ float pool_f32(uint8_t x, float scale) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(x, __NV_E4M3);
-  return __half2float(__half(h)) * scale;
+// 16 bytes of a row as fp32 into shared memory
+__device__ __forceinline__ void widen16(float *dst, uint4 w, float, const float *) {
+  *reinterpret_cast<uint4 *>(dst) = w;
+}
+__device__ __forceinline__ void widen16(float *dst, uint4 w, float, const __nv_bfloat16 *) {
+  reinterpret_cast<float4 *>(dst)[0] = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                                                   __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  reinterpret_cast<float4 *>(dst)[1] = make_float4(__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u),
+                                                   __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u));
+}
+__device__ __forceinline__ void widen16(float *dst, uint4 w, float scale, const uint8_t *) {
+  const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      v[h] = __half2float(__half(__nv_cvt_fp8_to_halfraw((uint8_t)(word[q] >> (8 * h)), __NV_E4M3))) * scale;
+    reinterpret_cast<float4 *>(dst)[q] = make_float4(v[0], v[1], v[2], v[3]);
+  }
 }
 
 template <typename T, typename KT /* pool element */, int NK /* head_dim / 32 */>
@@ -46,9 +64,11 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
   constexpr int D = NK * 32;
-  __shared__ float q_s[kRowsPerPass][D];
-  __shared__ float k_s[kKeys][D + 1];
-  __shared__ float v_s[kKeys][D];
+  constexpr int kVec = 16 / sizeof(KT), kChunks = D / kVec;  // values in 16 bytes of a pool row; reads of a row
+  __shared__ __align__(16) float q_s[kRowsPerPass][D];
+  __shared__ __align__(16) float k_s[kKeys][D + 4];
+  __shared__ __align__(16) float v_s[kKeys][D];
+  __shared__ __align__(16) float p_s[kRowsPerPass][kKeys];
   __shared__ int s_bad;
 
   const AttnArgs &a = sa.a;
@@ -89,6 +109,7 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
       q_s[rr][d] = val;
     }
     float m[4], l[4], acc[4][NK], slope[4];
+    unsigned hide[4];  // keys of the tile that a row does not see
     int pos[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -103,60 +124,95 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
     }
     for (int kt = kb; kt < ke; kt += kKeys) {
       __syncthreads();
-      for (int x = tid; x < kKeys * D; x += kThreads) {
-        const int j = x / D, d = x % D, t = kt + j;
-        float kk = 0.f, vv = 0.f;
+#pragma unroll 4
+      for (int x = tid; x < kKeys * kChunks; x += kThreads) {
+        const int j = x / kChunks, d = x % kChunks * kVec, t = kt + j;
+        uint4 kk = make_uint4(0, 0, 0, 0), vv = kk;
         if (t < ke) {
           const int blk = kv.block_table[(size_t)b * kv.max_blocks + t / kv.block_size];
           if (blk >= 0 && blk < kv.num_blocks) {
             const size_t off = (((size_t)blk * kv.num_kv_heads + kvh) * kv.block_size + t % kv.block_size) * D + d;
-            kk = pool_f32(kp[off], kv.k_scale);
-            vv = pool_f32(vp[off], kv.v_scale);
+            kk = *reinterpret_cast<const uint4 *>(kp + off);
+            vv = *reinterpret_cast<const uint4 *>(vp + off);
           } else {
             s_bad = 1;
           }
         }
-        k_s[j][d] = kk;
-        v_s[j][d] = vv;
+        widen16(&k_s[j][d], kk, kv.k_scale, (const KT *)nullptr);
+        widen16(&v_s[j][d], vv, kv.v_scale, (const KT *)nullptr);
       }
       __syncthreads();
       const int t = kt + lane, j = t - c;
       int pt = t;
       if (j >= 0 && j < n && sa.positions != nullptr) pt = sa.positions[row0 + j];
+      if (rg + warp * 4 >= R) continue;  // none of this warp's rows
+      float dot[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+      for (int d = 0; d < D; d += 4) {
+        const float4 kk = *reinterpret_cast<const float4 *>(&k_s[lane][d]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 qq = *reinterpret_cast<const float4 *>(&q_s[warp * 4 + w][d]);
+          dot[w] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, dot[w]))));
+        }
+      }
+      unsigned any = 0u;  // keys that some row of the warp sees
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const int rr = warp * 4 + w, r = rg + rr;
-        if (r >= R) continue;
-        const int i = r / G;
-        bool vis = t < ke && (sa.window <= 0 || pos[w] - pt < sa.window);
+        const int r = rg + warp * 4 + w, i = r < R ? r / G : 0;
+        bool vis = r < R && t < ke && (sa.window <= 0 || pos[w] - pt < sa.window);
         if (vis && j >= 0)
           vis = a.mask_kind == SV_MASK_CAUSAL ? j <= i : (j < 64 && ((a.tree_mask[row0 + i] >> j) & 1ull));
         float s = -INFINITY;
         if (vis) {
-          float dot = 0.f;
-#pragma unroll 8
-          for (int d = 0; d < D; ++d) dot = fmaf(q_s[rr][d], k_s[lane][d], dot);
-          s = dot * a.scale_log2;
+          s = dot[w] * a.scale_log2;
           if (sa.cap > 0.f) s = sa.cap * tanhf(s / sa.cap);  // both in units of log2
           s -= slope[w] * (float)(pos[w] - pt);
         }
         const unsigned seen = __ballot_sync(0xffffffffu, vis);
-        const float mn = fmaxf(m[w], warp_max(s));
-        if (seen == 0u) continue;
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float p = vis ? exp2f(s - ref) : 0.f;
-        const float alpha = exp2f(m[w] - ref);
-        l[w] = l[w] * alpha + warp_sum(p);
+        float p = 0.f;
+        if (seen != 0u) {
+          const float mn = fmaxf(m[w], warp_max(s)), ref = mn == -INFINITY ? 0.f : mn;
+          p = vis ? exp2f(s - ref) : 0.f;
+          const float alpha = exp2f(m[w] - ref);
+          l[w] = l[w] * alpha + warp_sum(p);
 #pragma unroll
-        for (int k = 0; k < NK; ++k) acc[w][k] *= alpha;
-        for (unsigned left = seen; left != 0u; left &= left - 1u) {
-          const int key = __ffs(left) - 1;
-          const float pj = __shfl_sync(0xffffffffu, p, key);
-#pragma unroll
-          for (int k = 0; k < NK; ++k) acc[w][k] = fmaf(pj, v_s[key][lane + 32 * k], acc[w][k]);
+          for (int k = 0; k < NK; ++k) acc[w][k] *= alpha;
+          m[w] = mn;
         }
-        m[w] = mn;
+        p_s[warp * 4 + w][lane] = p;
+        any |= seen;
+        hide[w] = r < R ? ~seen : 0u;
       }
+      __syncwarp();
+      // a row takes nothing of a key that it does not see, whatever the key's values are
+      bool odd = false;
+      if ((any & hide[0]) | (any & hide[1]) | (any & hide[2]) | (any & hide[3]))
+        for (int d = 0; d < D; d += 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(&v_s[lane][d]);
+          odd |= !(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) < INFINITY);
+        }
+      odd = __any_sync(0xffffffffu, odd && ((any >> lane) & 1u));
+      for (int x = 0; x < kKeys; x += 4) {
+        if (((any >> x) & 15u) == 0u) continue;
+        float4 pw[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) pw[w] = *reinterpret_cast<const float4 *>(&p_s[warp * 4 + w][x]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          if (!((any >> (x + y)) & 1u)) continue;
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            const float v = v_s[x + y][lane + 32 * k];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float pj = y == 0 ? pw[w].x : y == 1 ? pw[w].y : y == 2 ? pw[w].z : pw[w].w;
+              if (!odd || !((hide[w] >> (x + y)) & 1u)) acc[w][k] = fmaf(pj, v, acc[w][k]);
+            }
+          }
+        }
+      }
+      __syncwarp();
     }
     // write this pass's rows
 #pragma unroll
@@ -201,18 +257,28 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_combine(ScoredArgs 
   const int D = a.kv.head_dim;
   const size_t idx = (size_t)row0 * a.num_q_heads + x, stride = (size_t)a.total_q * a.num_q_heads;
   float M = -INFINITY;
-  for (int s = 0; s < nsplit; ++s) M = fmaxf(M, a.ws_lse[s * stride + idx]);
+  for (int s = lane; s < nsplit; s += 32) M = fmaxf(M, a.ws_lse[s * stride + idx]);
+  M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
-  T *op = reinterpret_cast<T *>(a.out);
-  for (int d = lane; d < D; d += 32) {
-    float num = 0.f, den = 0.f;
-    for (int s = 0; s < nsplit; ++s) {
-      const float w = exp2f(a.ws_lse[s * stride + idx] - ref);
-      den += w;
-      num = fmaf(w, a.ws_o[(s * stride + idx) * D + d], num);
+  float num[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, den = 0.f;  // columns lane + 32 k
+  for (int s0 = 0; s0 < nsplit; s0 += 32) {
+    const float w = s0 + lane < nsplit ? exp2f(a.ws_lse[(s0 + lane) * stride + idx] - ref) : 0.f;
+    den += w;
+    const int n_s = min(32, nsplit - s0);
+#pragma unroll 4
+    for (int s = 0; s < n_s; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      const float *o = a.ws_o + ((s0 + s) * stride + idx) * D + lane;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k * 32 < D) num[k] = fmaf(ws, o[32 * k], num[k]);
     }
-    op[idx * D + d] = from_f32<T>(den == 0.f ? 0.f : num / den);
   }
+  den = warp_sum(den);
+  T *op = reinterpret_cast<T *>(a.out);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k * 32 < D) op[idx * D + lane + 32 * k] = from_f32<T>(den == 0.f ? 0.f : num[k] / den);
 }
 
 template <typename T, typename KT>

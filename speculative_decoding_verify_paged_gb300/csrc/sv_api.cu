@@ -55,6 +55,7 @@ namespace {
 
 constexpr int kMaxQ = 64;
 constexpr int kGranule = 64;
+constexpr int kScoredGranule = 32;  // one tile of the CUDA-core kernel: short caches are all latency
 constexpr float kLog2e = 1.4426950408889634f;
 int g_attn_path = SV_ATTN_AUTO;
 unsigned long long g_wait_ns = kDefaultWaitNs;  // budget of the kernels' pipeline waits
@@ -96,8 +97,9 @@ bool keys_usable(const sv_paged_kv *kv, int32_t num_q_heads, int32_t max_q, int3
 }
 
 // Split-KV partials of the kernels that take one CTA per key split.
-size_t split_workspace(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q, int32_t max_seq_len) {
-  const SplitPlan p = plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kGranule);
+size_t split_workspace(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q, int32_t max_seq_len,
+                       int granule = kGranule) {
+  const SplitPlan p = plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, granule);
   if (p.max_splits <= 1) return 0;
   const size_t rows = (size_t)p.max_splits * total_q * num_q_heads;
   return rows * (size_t)kv->head_dim * sizeof(float) + rows * sizeof(float) + 256;
@@ -355,7 +357,7 @@ size_t sv_spec_verify_attn_scored_workspace_bytes(const sv_paged_kv *kv, int32_t
   sa.a.num_q_heads = num_q_heads;
   sa.a.max_q = max_q_per_seq;
   sa.a.max_seq_len = max_seq_len;
-  if (!attn_scored_mma_fits(sa)) return split_workspace(kv, num_q_heads, total_q, max_seq_len);
+  if (!attn_scored_mma_fits(sa)) return split_workspace(kv, num_q_heads, total_q, max_seq_len, kScoredGranule);
   size_t need = 0;
   launch_attn_scored_mma(sa, nullptr, &need, nullptr, false);
   return need;
@@ -381,7 +383,7 @@ sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void 
       sv_spec_verify_attn_scored_workspace_bytes(kv, num_q_heads, total_q, max_q_per_seq, max_seq_len);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || ((uintptr_t)workspace & 255u) != 0))
     return SV_ERR_WORKSPACE;
-  const SplitPlan p = plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kGranule);
+  const SplitPlan p = plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kScoredGranule);
   const size_t rows = (size_t)p.max_splits * total_q * num_q_heads;
   ScoredArgs sa;
   AttnArgs &a = sa.a;

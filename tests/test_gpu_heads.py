@@ -293,6 +293,16 @@ def test_bindings_refuse_what_does_not_fit():
         L.qk_norm_rope(t, q.transpose(0, 1), None, pos, qo.transpose(0, 1), None)
     with pytest.raises(ValueError):
         L.qk_norm_rope(HeadTransform(q_weight=torch.ones(32, dtype=q.dtype, device="cuda")), q, k, pos, qo, ko)
+    with pytest.raises(TypeError):
+        L.qk_norm_rope(t, q.cpu(), k, pos, qo, ko)
+    with pytest.raises(TypeError):
+        L.qk_norm_rope(t, q, k, pos.cpu(), qo, ko)
+    with pytest.raises(TypeError):
+        L.qk_norm_rope(HeadTransform(), q.half(), None, pos, qo.half(), None)
+    with pytest.raises(ValueError):
+        L.qk_norm_rope(t, q, k, pos, None, ko)
+    with pytest.raises(ValueError):
+        L.qk_norm_rope(t, None, None, pos, None, None)
     with pytest.raises(SVError):
         L.qk_norm_rope(t, q, k, None, qo, ko)  # a rotation without positions
     odd = torch.empty(4 * 6 * 64 + 8, dtype=q.dtype, device="cuda")[1:1 + 4 * 6 * 64].view(4, 6, 64)
