@@ -982,39 +982,56 @@ template <class C> bool make_map(CUtensorMap *map, void *pool, const KV &kv, int
             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launches (st != null via `go`) or sizes one instance.
+// A call's parameters and the size of its workspace.
+template <class C>
+Layout plan(const ScoredArgs &sa, void *workspace, size_t *bytes, Params *p) {
+  const KV &kv = sa.a.kv;
+  p->s = sa;
+  p->G = sa.a.num_q_heads / kv.num_kv_heads;
+  const Layout l = layout_of<C>(kv, p->G, sa.a.max_q, sa.a.max_seq_len);
+  *bytes = l.bytes;
+  p->cap_in = sa.cap > 0.f ? sa.a.scale_log2 * 2.f * 1.4426950408889634f / sa.cap : 0.f;
+  p->ctas = l.ctas;
+  p->alpha = kAlpha;
+  p->rows_cap = l.rows_cap;
+  p->rb_max = l.rb_max;
+  p->box = std::min(kv.block_size, C::TK);
+  p->part_o = reinterpret_cast<float *>(workspace);
+  p->part_lse = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + l.lse_offset);
+  p->prefix = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(workspace) + l.prefix_offset);
+  return l;
+}
+
+template <class C> cudaError_t launch_combine(const Params &p, const Layout &l, cudaStream_t st) {
+  const KV &kv = p.s.a.kv;
+  const int items = std::min(512, (l.rows_cap * (C::D / 8) + 31) / 32 * 32);  // threads: one item each, if they fit
+  return launch_pdl(attn_scored_combine<C>, dim3(kv.batch, kv.num_kv_heads * p.rb_max), dim3(items), 0, st, p);
+}
+
+// Launches (`go`) or sizes one instance.
 template <class C>
 cudaError_t run(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {
   const KV &kv = sa.a.kv;
   Params p;
-  p.s = sa;
-  p.G = sa.a.num_q_heads / kv.num_kv_heads;
-  const Layout l = layout_of<C>(kv, p.G, sa.a.max_q, sa.a.max_seq_len);
-  *bytes = l.bytes;
+  const Layout l = plan<C>(sa, workspace, bytes, &p);
   if (!go) return cudaSuccess;
-  p.cap_in = sa.cap > 0.f ? sa.a.scale_log2 * 2.f * 1.4426950408889634f / sa.cap : 0.f;
-  p.ctas = l.ctas;
-  p.alpha = kAlpha;
-  p.rows_cap = l.rows_cap;
-  p.rb_max = l.rb_max;
-  p.part_o = reinterpret_cast<float *>(workspace);
-  p.part_lse = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + l.lse_offset);
-  p.prefix = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(workspace) + l.prefix_offset);
-  p.box = std::min(kv.block_size, C::TK);
-  CUtensorMap mk, mv;
-  if (!make_map<C>(&mk, kv.k_pool, kv, p.box) || !make_map<C>(&mv, kv.v_pool, kv, p.box)) return cudaErrorInvalidValue;
   static const bool split_fits = [] {  // the kernel was compiled for the registers that its split shares out
     cudaFuncAttributes fa;
     return cudaFuncGetAttributes(&fa, attn_scored_kernel<C>) == cudaSuccess && fa.numRegs == kLaunchRegs;
   }();
   if (!split_fits) return cudaErrorInvalidConfiguration;
+  CUtensorMap mk, mv;
+  if (!make_map<C>(&mk, kv.k_pool, kv, p.box) || !make_map<C>(&mv, kv.v_pool, kv, p.box)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attn_scored_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_scored_kernel<C>, dim3(p.ctas), dim3(C::kThreads), C::kSmem, st, mk, mv, p);
   if (e != cudaSuccess) return e;
-  const int items = std::min(512, (l.rows_cap * (C::D / 8) + 31) / 32 * 32);  // threads: one item each, if they fit
-  return launch_pdl(attn_scored_combine<C>, dim3(kv.batch, kv.num_kv_heads * p.rb_max), dim3(items), 0, st, p);
+  return launch_combine<C>(p, l, st);
 }
+
+constexpr int kWideRows = 96;  // units of more query rows go to attn_scored_wide.cu, where it takes them
+bool wide_fits(const ScoredArgs &sa);
+cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);
 
 // The smallest block of query rows that holds a unit's, else blocks of the largest.
 template <int D, bool F8>
@@ -1035,7 +1052,14 @@ cudaError_t pick(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStrea
     if (rows <= 32) return on(Cfg<D, 2, 2, 2, F8>());
     if (rows <= 48) return on(Cfg<D, 3, 2, 2, F8>());
     if (rows <= 64) return on(Cfg<D, 2, 4, 1, F8>());
-    return on(Cfg<D, 3, 4, 1, F8>());
+    if (!wide_fits(sa)) return on(Cfg<D, 3, 4, 1, F8>());
+    // a cap past the two-instruction tanh stays here; the workspace suits both
+    size_t most = 0;
+    run_wide(sa, nullptr, &most, st, false);
+    if (go && sa.cap <= kFastCap * 1.4426950408889634f) return run_wide(sa, workspace, bytes, st, go);
+    const cudaError_t e = on(Cfg<D, 3, 4, 1, F8>());
+    *bytes = std::max(*bytes, most);
+    return e;
   } else {
     if (rows <= 16) return on(Cfg<D, 1, 2, 2, F8>());
     return on(Cfg<D, 1, 4, 1, F8>());

@@ -1,0 +1,625 @@
+// Attention with modified scores for wide units (more than kWideRows query rows per KV head and sequence:
+// draft trees, long drafts, wide query groups) on the 5th-generation tensor cores: bf16 caches with
+// heads of 128 values. The mathematics, the work order, the partials and their merge are those of
+// attn_scored.cuh.
+//
+// Bound: the special functions and the products. 256 query rows a unit are 256 flops per byte of K and
+// V, past what memory limits; a capped score costs two 2^x and a reciprocal (2048 cycles of an SM per
+// 128 x 128 scores) next to 1024 cycles of tensor core for the two products.
+//
+// A unit is one KV head of one sequence and up to 256 query rows, as two blocks of 128, one row per
+// tensor-memory lane, so that K and V are read once for all of them. One CTA an SM, ten warps:
+//  * softmax A and B, four warps each: a thread keeps one row. It reads its 128 scores from tensor memory,
+//    caps, biases and masks them, moves its running maximum if they pass it by far (then rescales its
+//    row of O), and writes P = 2^(s - m) as bf16 over the scores;
+//  * the producer: K and V tiles of 128 keys (2 x 32 KB) by TMA into two stages;
+//  * the issuer (one lane): S = Q K^T (M 128, N 128, both operands in shared memory), then O += P V (P
+//    in tensor memory, V with its dimensions major). The two blocks alternate, so that one block's
+//    products run while the other block's scores are worked on:
+//      P V_a(t), S_a(t + 1), P V_b(t), S_b(t + 1), ...
+//    Products of one thread finish in the order of their issue, so the S that follows a P V may
+//    overwrite P, and S(t + 1) being there says that P V(t) is done.
+// Tensor memory: S_a, S_b (P over them), O_a, O_b, 128 columns each: all 512. Before a piece its rows
+// zero O, so every P V accumulates.
+//
+// Edge tiles (new rows, the window's start, the end) see keys as bits of a row. Values past the end of
+// the sequence are set to zero in the stage; infinities and NaN of keys that some row does not see are
+// taken out of it too, and added to the rows that see them by hand.
+//
+// All waits are bounded, as in attn_scored.cuh.
+#include <algorithm>
+
+#include "attn_scored.cuh"
+
+namespace sv {
+namespace scored {
+namespace {
+
+struct Wide {  // what the work order and the merge need
+  static constexpr int D = 128, TK = 128, RB = 256, ROWB = 256, kCtasPerSm = 1;
+};
+constexpr int kSoft = 8;                   // softmax warps
+constexpr int kWideThreads = (kSoft + 4) * 32;  // the last two warps do nothing: register shares go by four warps
+// Registers of a thread as launched, of the softmax warps and of the others after the split
+constexpr int kWideRegs = 168, kSoftRegs = 216, kOtherRegs = 72;
+static_assert(8 * kSoftRegs + 4 * kOtherRegs == 12 * kWideRegs, "a split above the launch's share would wait forever");
+constexpr int kBlock = 128;                // rows of a block, keys of a tile
+constexpr int kHalf = kBlock * 256;        // bytes of 128 rows of K, V or Q
+constexpr int kStage = 2 * kHalf;          // K and V of a tile
+constexpr int kWideSmem = 1024 + 2 * kStage + 2 * kHalf;
+constexpr int kColO = 256;                 // S_a 0, S_b 128, O_a 256, O_b 384
+
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lbo, uint32_t sbo) {  // 128-byte swizzle
+  return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 | (uint64_t)((sbo >> 4) & 0x3FFF) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16, fp32 accumulate, bf16 operands, M 128, N 128
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24);
+constexpr uint32_t kIdescV = kIdesc | (1u << 16);  // B with its N dimension major
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int accumulate) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int accumulate) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+#define SV_O8(x, o) "=r"(x[o]), "=r"(x[o + 1]), "=r"(x[o + 2]), "=r"(x[o + 3]), "=r"(x[o + 4]), "=r"(x[o + 5]), "=r"(x[o + 6]), "=r"(x[o + 7])
+#define SV_I8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
+// 32 columns of this thread's lane
+__device__ __forceinline__ void tmem_get(uint32_t at, uint32_t *x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+      "%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : SV_O8(x, 0), SV_O8(x, 8), SV_O8(x, 16), SV_O8(x, 24)
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_put(uint32_t at, const uint32_t *x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      SV_I8(x, 0), SV_I8(x, 8), SV_I8(x, 16), SV_I8(x, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_get_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// byte of (row, 16-byte chunk of its 16) in 128 rows as the TMA lays them
+__device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
+  return (row >> 3) * 2048 + (chunk >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+__global__ void __launch_bounds__(kWideThreads, 1)
+    attn_scored_wide_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params P) {
+  grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
+  grid_dependents_launch();
+  constexpr int kWarps = kWideThreads / 32;
+  extern __shared__ uint8_t smem[];
+  __shared__ __align__(8) uint64_t s_full[2], s_free[2];  // stages
+  __shared__ __align__(8) uint64_t s_q[2], s_s[2], s_p[2], s_o[2];  // blocks: Q written, S there, P written, last P V done
+  __shared__ __align__(8) uint64_t s_done;                // every product issued has finished
+  __shared__ int s_dead, s_scan[kWarps], s_first_b, s_first_base;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_place[64], s_top[kSoft], s_odd;
+
+  const AttnArgs &a = P.s.a;
+  const KV &kv = a.kv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = kv.batch;
+  uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
+  uint8_t *qs = ring + 2 * kStage;  // Q of block a, of block b
+  if (tid == 0) {
+    for (int k = 0; k < 2; ++k) {
+      bar_init(smem_at(&s_full[k]), 1);
+      bar_init(smem_at(&s_free[k]), 1);
+      bar_init(smem_at(&s_q[k]), 4);
+      bar_init(smem_at(&s_s[k]), 1);
+      bar_init(smem_at(&s_p[k]), 4);
+      bar_init(smem_at(&s_o[k]), 1);
+    }
+    bar_init(smem_at(&s_done), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_dead = s_odd = 0;
+    s_first_b = s_first_base = 0;
+  }
+  if (warp == kSoft + 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&s_tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // ---- this CTA's range [pos, end) of the launch's W positions ----
+  auto scan = [&](int v, int *total) {  // inclusive sum over the CTA's threads
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      before += w < warp ? s_scan[w] : 0;
+      all += s_scan[w];
+    }
+    __syncthreads();
+    *total = all;
+    return x + before;
+  };
+  auto work_of = [&](int b, bool report) {
+    bool bad = false;
+    const int v = b < B ? seq_work(P, load_seq(P, b, Wide::TK, Wide::RB, &bad)) : 0;
+    if (bad && report && blockIdx.x == 0) record(a.status, SV_ERR_BAD_LENGTH);
+    return v;
+  };
+  int v0 = work_of(tid, true), W, incl = scan(v0, &W), run = 0;
+  if (B > kWideThreads) {
+    int more = 0, rest;
+    for (int b = tid + kWideThreads; b < B; b += kWideThreads) more += work_of(b, true);
+    run = W;
+    scan(more, &rest);
+    W += rest;
+  }
+  Place at;
+  at.pos = range_start(blockIdx.x, W, P.ctas);
+  at.end = range_start(blockIdx.x + 1, W, P.ctas);
+  for (int b0 = 0; b0 < B; b0 += kWideThreads) {
+    const int b = b0 + tid;
+    if (b0 > 0) {
+      int tot;
+      v0 = work_of(b, false);
+      incl = run + scan(v0, &tot);
+      run += tot;
+    }
+    const int excl = incl - v0;
+    if (blockIdx.x == 0 && b < B) P.prefix[b] = excl;
+    if (v0 > 0 && excl <= at.pos && at.pos < incl) {
+      s_first_b = b;
+      s_first_base = excl;
+    }
+    if (blockIdx.x != 0 && b0 > 0 && run > at.pos) break;  // uniform
+  }
+  if (blockIdx.x == 0 && tid == 0) P.prefix[B] = W;
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  at.b = s_first_b;
+  at.base = s_first_base;
+  {
+    bool bad;
+    at.s = load_seq(P, at.b, Wide::TK, Wide::RB, &bad);
+  }
+  Piece p = {};
+  bool dead = false;
+  auto wait = [&](uint64_t &bar, uint32_t parity) {
+    if (dead) return;
+    const bool landed = mbar_wait_bounded(smem_at(&bar), parity, a.wait_ns);
+    dead = __any_sync(0xffffffffu, !landed || *(volatile int *)&s_dead != 0);
+    if (dead) s_dead = 1;
+  };
+  uint32_t tile0 = 0;  // tiles of the CTA's earlier pieces: tile x of the launch goes to stage x % 2
+  auto two_blocks = [&] { return P.G * at.s.n - p.rb * Wide::RB > kBlock; };
+
+  if (warp >= kSoft) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kSoft) {
+    // ================= producer =================
+    const int bs_shift = __ffs(kv.block_size) - 1, box = P.box, box_row = (lane >> 1) * box;
+    if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);  // failure-path test: a wait that nothing ends
+    while (next_piece<Wide>(P, at, p)) {
+      const int32_t *bt = kv.block_table + (size_t)at.b * kv.max_blocks;
+      const int last = (p.ke - 1) >> bs_shift;
+      auto load_id = [&](int blk) { return blk <= last ? bt[blk] : -1; };
+      int wbase = max(p.kt0 * Wide::TK, p.lo) >> bs_shift;
+      int cur = load_id(wbase + lane), nxt = load_id(wbase + 32 + lane);
+      for (int kt = p.kt0; kt < p.kt1; ++kt, ++tile0) {
+        const uint32_t st = tile0 & 1u;
+        const int tok = kt * Wide::TK + box_row, first = max(kt * Wide::TK, p.lo) >> bs_shift;
+        while (first >= wbase + 32) {  // uniform
+          wbase += 32;
+          cur = nxt;
+          nxt = load_id(wbase + 32 + lane);
+        }
+        const bool want = box_row < Wide::TK && tok < p.ke && tok + box > p.lo;
+        const int src = want ? (tok >> bs_shift) - wbase : 0;
+        const int id0 = __shfl_sync(0xffffffffu, cur, src & 31), id1 = __shfl_sync(0xffffffffu, nxt, src & 31);
+        const int id = src < 32 ? id0 : id1;
+        const bool bad = want && (id < 0 || id >= kv.num_blocks), go = want && !bad;
+        if (bad) record(a.status, SV_ERR_BAD_BLOCK_ID);
+        if (tile0 >= 2) wait(s_free[st], (tile0 / 2 - 1) & 1u);
+        if (dead) break;  // nothing more is issued
+        const uint32_t bar = smem_at(&s_full[st]);
+        const int boxes = __popc(__ballot_sync(0xffffffffu, go));
+        if (lane == 0) bar_expect(bar, boxes * box * Wide::ROWB);
+        __syncwarp();
+        if (go) {
+          const int y = ((id * kv.num_kv_heads + p.kvh) << bs_shift) + (tok & (kv.block_size - 1));
+          load_box<Wide::ROWB>(smem_at(ring) + st * kStage + (lane & 1) * kHalf + box_row * Wide::ROWB, (lane & 1) ? &map_v : &map_k, y, bar);
+        }
+        __syncwarp();
+      }
+      if (dead) break;
+    }
+    } else if (warp == kSoft + 1) {
+    // ================= issuer =================
+    uint32_t cq[2] = {0, 0}, cp[2] = {0, 0};  // phases of s_q and s_p so far
+    auto issue_s = [&](int blk, uint32_t x) {
+      if (lane == 0) {
+        const uint32_t k = smem_at(ring) + (x & 1u) * kStage, q = smem_at(qs) + blk * kHalf;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 32;
+          mma_ss(tmem + blk * 128, operand(q + off, 16, 2048), operand(k + off, 16, 2048), kIdesc, kk > 0);
+        }
+        commit(smem_at(&s_s[blk]));
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int blk, uint32_t x) {
+      if (lane == 0) {
+        const uint32_t v = smem_at(ring) + (x & 1u) * kStage + kHalf;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + kColO + blk * 128, tmem + blk * 128 + kk * 8, operand(v + kk * 4096, 1024, 2048), kIdescV, 1);
+      }
+      __syncwarp();
+    };
+    auto commit_to = [&](uint64_t &bar) {
+      if (lane == 0) commit(smem_at(&bar));
+      __syncwarp();
+    };
+    while (!dead && next_piece<Wide>(P, at, p)) {
+      const int n = p.kt1 - p.kt0, blocks = two_blocks() ? 2 : 1;
+      wait(s_full[tile0 & 1u], (tile0 / 2) & 1u);
+      for (int blk = 0; blk < blocks && !dead; ++blk) {
+        wait(s_q[blk], cq[blk]++ & 1u);
+        if (dead) break;
+        fence_after();
+        issue_s(blk, tile0);
+      }
+      for (int t = 0; t < n && !dead; ++t) {
+        const uint32_t x = tile0 + t;
+        for (int blk = 0; blk < blocks && !dead; ++blk) {
+          wait(s_p[blk], cp[blk]++ & 1u);
+          if (dead) break;
+          fence_after();
+          issue_pv(blk, x);
+          if (blk == blocks - 1) commit_to(s_free[x & 1u]);
+          if (t + 1 < n) {
+            if (blk == 0) wait(s_full[(x + 1) & 1u], ((x + 1) / 2) & 1u);
+            if (dead) break;
+            issue_s(blk, x + 1);
+          } else {
+            commit_to(s_o[blk]);
+          }
+        }
+      }
+      tile0 += n;
+    }
+    // every product issued finishes before tensor memory is released
+    commit_to(s_done);
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_at(&s_done), 0, kDrainBudgetNs))) dead = true;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ================= softmax: one row per thread =================
+    const int blk = warp >> 2, row = (warp & 3) * 32 + lane, rl = blk * kBlock + row;  // row of the block, of the unit
+    const uint32_t lane_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lane_at + blk * 128, to = lane_at + kColO + blk * 128;
+    const float sl2 = a.scale_log2, cap = P.s.cap, cap_in = P.cap_in;
+    const bool biased = P.s.slopes != nullptr;
+    const bool bounded = cap > 0.f && cap <= kBoundedCap && !biased;
+    const int window = P.s.window;
+    auto together = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };  // both blocks
+    auto of_piece = [&](bool two) {                                           // the blocks that have rows
+      if (two) asm volatile("bar.sync 2, 256;" ::: "memory");
+      else asm volatile("bar.sync 2, 128;" ::: "memory");
+    };
+    bool first_piece = true;
+    uint32_t cs = 0, co = 0;  // phases of s_s and s_o so far
+    auto zero_o = [&] {
+      uint32_t z[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) z[k] = 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_put(to + k * 32, z);
+      tmem_put_wait();
+    };
+    auto load_q = [&](const Place &pl, const Piece &pc) {  // this row of a piece's Q into shared memory
+      const int r = pc.rb * Wide::RB + rl, i = r / P.G;
+      const bool live = r < P.G * pl.s.n;
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          reinterpret_cast<const __nv_bfloat16 *>(a.q) +
+          (live ? ((size_t)(pl.s.row0 + i) * a.num_q_heads + pc.kvh * P.G + (r - i * P.G)) * 128 : 0));
+      uint8_t *dst = qs + blk * kHalf;
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        *reinterpret_cast<uint4 *>(dst + chunk_at(row, c)) = live ? src[c] : make_uint4(0, 0, 0, 0);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_at(&s_q[blk]));
+    };
+    bool has = next_piece<Wide>(P, at, p);
+    if (has && (blk == 0 || two_blocks())) load_q(at, p);
+    while (has) {
+      const Seq s = at.s;
+      const Piece pc = p;
+      const bool two = two_blocks(), active = blk == 0 || two;  // the block has rows
+      has = next_piece<Wide>(P, at, p);                          // at and p: the next piece from here on
+      const int c = s.c, ke = pc.ke, r = pc.rb * Wide::RB + rl, n_tiles = pc.kt1 - pc.kt0;
+      const bool live = r < P.G * s.n;
+      const int i = live ? r / P.G : 0, head = pc.kvh * P.G + (live ? r - i * P.G : 0);
+      // ---- this row: position, new keys that it sees, reach (the last place out of its window) ----
+      const int where = P.s.positions != nullptr ? P.s.positions[s.row0 + i] : c + i;
+      if (where < c) record(a.status, SV_ERR_BAD_LENGTH);
+      const int reach = !live ? 1 << 30 : window > 0 ? where - c - window : -(1 << 30);
+      const float slope = biased ? P.s.slopes[head] * 1.4426950408889634f : 0.f;
+      uint64_t mask = 0ull;
+      if (live) {
+        mask = a.mask_kind == SV_MASK_TREE ? a.tree_mask[s.row0 + i] : (2ull << i) - 1ull;
+        if (s.n < 64) mask &= (1ull << s.n) - 1ull;
+        if (window > 0 && where - c >= window)
+          for (int j = 0; j < s.n; ++j) {
+            const int place = P.s.positions != nullptr ? P.s.positions[s.row0 + j] - c : j;
+            if (place <= reach) mask &= ~(1ull << j);
+          }
+      }
+      together();  // both blocks are done with the previous piece's places
+      if (tid < s.n) s_place[tid] = P.s.positions != nullptr ? P.s.positions[s.row0 + tid] - c : tid;
+      const int warp_top = __reduce_max_sync(0xffffffffu, live ? where : c);
+      if (lane == 0) s_top[warp] = warp_top;
+      together();
+      int row_top = s_top[0];
+#pragma unroll
+      for (int w = 1; w < kSoft; ++w) row_top = max(row_top, s_top[w]);
+      const int all_see = window > 0 ? row_top - window + 1 : 0;  // keys from here to c are visible to every row
+      if (!active) {
+        tile0 += n_tiles;
+        first_piece = false;
+        if (has && two_blocks()) load_q(at, p);
+        continue;
+      }
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      zero_o();
+      fence_before();
+      float m = bounded ? 0.f : kNone, l = 0.f;
+      for (int t = 0; t < n_tiles; ++t) {
+        const int key0 = (pc.kt0 + t) * Wide::TK, base = key0 - c;
+        const uint32_t x = tile0 + t;
+        wait(s_s[blk], cs++ & 1u);
+        fence_after();
+        const bool edge = key0 + Wide::TK > min(c, ke) || key0 < all_see;  // the same for the whole CTA
+        uint8_t *vs = ring + (x & 1u) * kStage + kHalf;
+        bool odd = false;
+        if (edge) {
+          // Values that no weight of zero may meet: slots past the end or before the first visible key hold
+          // anything and become zeros; infinities and NaN among the others are looked for.
+          wait(s_full[x & 1u], (x / 2) & 1u);  // (landed: this makes the copies visible here)
+          for (int y = tid; y < kBlock * 16; y += two ? 256 : 128) {
+            const int key = y >> 4;
+            uint4 *w = reinterpret_cast<uint4 *>(vs + chunk_at(key, y & 15));
+            if (key0 + key >= ke || key0 + key < pc.lo) *w = make_uint4(0, 0, 0, 0);
+            else odd |= nonfinite2(w->x) | nonfinite2(w->y) | nonfinite2(w->z) | nonfinite2(w->w);
+          }
+          if (odd) s_odd = 1;
+          fence_async();
+          of_piece(two);
+          odd = *(volatile int *)&s_odd != 0;
+        }
+        if (warp_live || odd) {
+          uint32_t w[128];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_get(ts + k * 32, w + k * 32);
+          tmem_get_wait();
+          // ---- scores ----
+          if (cap == 0.f) {
+#pragma unroll
+            for (int k = 0; k < 128; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * sl2);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              w[k] = __float_as_uint(-2.f * cap * rcp(1.f + ex2(__uint_as_float(w[k]) * cap_in)));
+          }
+          if (biased) {
+            if (!edge) {
+              const float f0 = (float)base;
+#pragma unroll
+              for (int k = 0; k < 128; ++k)
+                w[k] = __float_as_uint(fmaf(slope, f0 + (float)k, __uint_as_float(w[k])));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 128; ++k) {
+                const int j = base + k;
+                const float place = (float)(j >= 0 && j < s.n ? s_place[j] : j);
+                w[k] = __float_as_uint(fmaf(slope, place, __uint_as_float(w[k])));
+              }
+            }
+          }
+          if (edge) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // the row's view of 32 keys as bits
+              const int b0 = base + 32 * q, first = reach + 1 - b0;
+              const uint32_t old = b0 >= 0 ? 0u : b0 <= -32 ? ~0u : (1u << -b0) - 1u;
+              const uint32_t near = first <= 0 ? ~0u : first >= 32 ? 0u : ~0u << first;
+              const uint32_t fresh = b0 >= 0 ? (b0 < 64 ? (uint32_t)(mask >> b0) : 0u) : (b0 > -32 ? (uint32_t)mask << -b0 : 0u);
+              const uint32_t seen = (old & near) | fresh;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((seen >> k) & 1u)) w[q * 32 + k] = 0xff800000u;  // -inf
+            }
+          }
+          // ---- the running maximum ----
+          if (!bounded) {
+            float mx = kNone;
+#pragma unroll
+            for (int k = 0; k < 128; ++k) mx = fmaxf(mx, __uint_as_float(w[k]));
+            const bool move = mx > m + kMoveAt<false>;
+            if (__any_sync(0xffffffffu, move)) {
+              const float f = move ? ex2(m - mx) : 1.f;
+              if (move) m = mx;
+              l *= f;
+              uint32_t o[32];
+#pragma unroll 1
+              for (int k = 0; k < 4; ++k) {  // S(t) is there, so P V(t - 1) is done
+                tmem_get(to + k * 32, o);
+                tmem_get_wait();
+#pragma unroll
+                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                tmem_put(to + k * 32, o);
+              }
+              tmem_put_wait();
+            }
+          }
+          // ---- P ----
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 128; ++k) {
+            const float e = ex2(__uint_as_float(w[k]) - m);
+            part[k & 3] += e;
+            w[k] = __float_as_uint(e);
+          }
+          l += (part[0] + part[1]) + (part[2] + part[3]);
+          if (odd) {
+            // infinities and NaN, for the rows that see their keys; then out of the tile
+            float weight[128];
+#pragma unroll
+            for (int k = 0; k < 128; ++k) weight[k] = __uint_as_float(w[k]);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              uint32_t o[32];
+              tmem_get(to + k * 32, o);
+              tmem_get_wait();
+#pragma unroll 1
+              for (int key = 0; key < kBlock; ++key) {
+                const float e = *(volatile float *)&weight[key];
+                if (!(e > 0.f)) continue;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const uint4 u = *reinterpret_cast<const uint4 *>(vs + chunk_at(key, k * 4 + y));
+                  const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                  for (int z = 0; z < 8; ++z) {
+                    const uint32_t v = (word[z >> 1] >> (16 * (z & 1))) & 0xffffu;
+                    if ((v & 0x7f80u) == 0x7f80u)
+                      o[y * 8 + z] = __float_as_uint(__uint_as_float(o[y * 8 + z]) + e * __uint_as_float(v << 16));
+                  }
+                }
+              }
+              tmem_put(to + k * 32, o);
+            }
+            tmem_put_wait();
+          }
+#pragma unroll
+          for (int k = 0; k < 64; ++k) w[k] = pack2<false>(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+          tmem_put(ts, w);
+          tmem_put(ts + 32, w + 32);
+          tmem_put_wait();
+        }
+        if (odd) {
+          of_piece(two);  // every row has taken its share
+          for (int y = tid; y < kBlock * 16; y += two ? 256 : 128) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(vs + chunk_at(y >> 4, y & 15));
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              if ((w[z] & 0x7f80u) == 0x7f80u) w[z] &= 0xffff0000u;
+              if ((w[z] & 0x7f800000u) == 0x7f800000u) w[z] &= 0xffffu;
+            }
+          }
+          fence_async();
+          of_piece(two);
+          if (tid == 0) s_odd = 0;
+          of_piece(two);
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_at(&s_p[blk]));
+      }
+      tile0 += n_tiles;
+      // the piece's last S is done with Q: the next piece's rows take its place
+      if (has && (blk == 0 || two_blocks())) load_q(at, p);
+      // ---- the piece's rows ----
+      wait(s_o[blk], co++ & 1u);
+      fence_after();
+      if (warp_live) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * P.rows_cap + rl;
+        if (live && !pc.whole) P.part_lse[slot] = l == 0.f ? -INFINITY : m + log2f(l);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[32];
+          tmem_get(to + k * 32, o);
+          tmem_get_wait();
+          if (!live) continue;
+          if (pc.whole) {
+            uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
+                                                   ((size_t)(s.row0 + i) * a.num_q_heads + head) * 128 + k * 32);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t q[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                q[z] = pack2<false>(__uint_as_float(o[8 * y + 2 * z]) * inv, __uint_as_float(o[8 * y + 2 * z + 1]) * inv);
+              dst[y] = make_uint4(q[0], q[1], q[2], q[3]);
+            }
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(P.part_o + slot * 128 + k * 32);
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              dst[y] = make_float4(__uint_as_float(o[4 * y]) * inv, __uint_as_float(o[4 * y + 1]) * inv,
+                                   __uint_as_float(o[4 * y + 2]) * inv, __uint_as_float(o[4 * y + 3]) * inv);
+          }
+        }
+      }
+      first_piece = false;
+    }
+  }
+  if (dead && lane == 0) record(a.status, SV_ERR_TIMEOUT);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  // after a wait that gave up: the copies in flight land before the CTA's shared memory is released
+  if (s_dead && warp == kSoft)
+    for (uint32_t x = tile0 > 2 ? tile0 - 2 : 0; x < tile0; ++x)
+      mbar_wait_bounded(smem_at(&s_full[x & 1u]), (x / 2) & 1u, kDrainBudgetNs);
+  if (warp == kSoft + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+}  // namespace
+
+bool wide_fits(const ScoredArgs &sa) {
+  const KV &kv = sa.a.kv;
+  return !kv.fp8 && kv.elem_bytes == 2 && kv.head_dim == 128 &&
+         sa.a.num_q_heads / kv.num_kv_heads * sa.a.max_q > kWideRows;
+}
+
+cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {
+  const KV &kv = sa.a.kv;
+  Params p;
+  const Layout l = plan<Wide>(sa, workspace, bytes, &p);
+  if (!go) return cudaSuccess;
+  static const bool split_fits = [] {  // the kernel was compiled for the registers that its split shares out
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, attn_scored_wide_kernel) == cudaSuccess && fa.numRegs == kWideRegs;
+  }();
+  if (!split_fits) return cudaErrorInvalidConfiguration;
+  CUtensorMap mk, mv;
+  if (!make_map<Wide>(&mk, kv.k_pool, kv, p.box) || !make_map<Wide>(&mv, kv.v_pool, kv, p.box)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(attn_scored_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_scored_wide_kernel, dim3(p.ctas), dim3(kWideThreads), (size_t)kWideSmem, st, mk, mv, p);
+  if (e != cudaSuccess) return e;
+  return launch_combine<Wide>(p, l, st);
+}
+
+}  // namespace scored
+}  // namespace sv

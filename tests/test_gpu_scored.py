@@ -109,6 +109,8 @@ SMALL = {
     "bf16-d256": (16, [290, 31], [2, 4], 8, 2, 256, 32, "bf16"),
     "bf16-d96": (17, [130, 31], [2, 4], 6, 2, 96, 8, "bf16"),
     "bf16-wide": (18, [200, 90], [64, 33], 8, 1, 128, 64, "bf16"),
+    "bf16-one-block": (29, [300, 129], [26, 25], 8, 2, 128, 16, "bf16"),
+    "bf16-two-blocks-ragged": (30, [1000, 5, 127, 128], [33, 64, 1, 40], 16, 4, 128, 32, "bf16"),
     "bf16-d256-wide": (19, [150], [30], 8, 1, 256, 16, "bf16"),
     "bf16-mha": (20, [400, 20], [7, 1], 3, 3, 128, 256, "bf16"),
     "e4m3-g4": (21, [700, 3, 129], [6, 6, 6], 32, 8, 128, 16, "e4m3"),
@@ -174,6 +176,7 @@ def test_large_scores():
     """Scores far past the cap, far apart without one, and negative ones throughout."""
     case = W.custom(33, batch=2, ctx_lens=[300, 80], n_q=[4, 2], num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=16, vocab=16, use_bank=False)
     run(case, ScoreMod(softcap=30.0), q_scale=64.0)
+    run(case, ScoreMod(softcap=1000.0), q_scale=16.0)
     run(case, ScoreMod(slopes=1000.0 * slopes(8)), q_scale=1.0)
     run(case, ScoreMod(slopes=-0.01 * slopes(8)), q_scale=1.0)  # a bias that grows with distance
 
@@ -185,11 +188,11 @@ def test_long_context_and_loose_bound():
     run(case, ScoreMod(softcap=10.0, window=64))
 
 
-@pytest.mark.parametrize("dt,d", [("bf16", 128), ("bf16", 96), ("f32", 64)])
-def test_nonfinite_where_nothing_is_seen(dt, d):
+@pytest.mark.parametrize("dt,d,hq", [("bf16", 128, 8), ("bf16", 96, 8), ("f32", 64, 8), ("bf16", 128, 48), ("bf16", 64, 32), ("bf16", 256, 8)])
+def test_nonfinite_where_nothing_is_seen(dt, d, hq):
     """NaN and infinities in slots past the end of a sequence, before its window, and in draft rows
     that a row does not see: the rows that do not see them are as if they were not there."""
-    case = W.custom(35, batch=2, ctx_lens=[200, 37], n_q=[5, 6], num_q_heads=8, num_kv_heads=2, head_dim=d, block_size=16, vocab=16, dtype=dt,
+    case = W.custom(35, batch=2, ctx_lens=[200, 37], n_q=[5, 6], num_q_heads=hq, num_kv_heads=2, head_dim=d, block_size=16, vocab=16, dtype=dt,
                     use_bank=False)
     mod = ScoreMod(softcap=20.0, window=50)
     masks = torch.tensor([1, 3, 5, 9, 17] * 1 + [1, 3, 5, 9, 17, 33], dtype=torch.int64, device="cuda")
