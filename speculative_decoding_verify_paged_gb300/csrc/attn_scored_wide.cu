@@ -8,19 +8,21 @@
 // 128 x 128 scores) next to 1024 cycles of tensor core for the two products.
 //
 // A unit is one KV head of one sequence and up to 256 query rows, as two blocks of 128, one row per
-// tensor-memory lane, so that K and V are read once for all of them. One CTA an SM, ten warps:
-//  * softmax A and B, four warps each: a thread keeps one row. It reads its 128 scores from tensor memory,
+// tensor-memory lane, so that K and V are read once for all of them. One CTA an SM, eleven warps:
+//  * softmax a and b, four warps each: a thread keeps one row. It reads its 64 scores from tensor memory,
 //    caps, biases and masks them, moves its running maximum if they pass it by far (then rescales its
 //    row of O), and writes P = 2^(s - m) as bf16 over the scores;
-//  * the producer: K and V tiles of 128 keys (2 x 32 KB) by TMA into two stages;
-//  * the issuer (one lane): S = Q K^T (M 128, N 128, both operands in shared memory), then O += P V (P
-//    in tensor memory, V with its dimensions major). The two blocks alternate, so that one block's
-//    products run while the other block's scores are worked on:
-//      P V_a(t), S_a(t + 1), P V_b(t), S_b(t + 1), ...
-//    Products of one thread finish in the order of their issue, so the S that follows a P V may
-//    overwrite P, and S(t + 1) being there says that P V(t) is done.
-// Tensor memory: S_a, S_b (P over them), O_a, O_b, 128 columns each: all 512. Before a piece its rows
-// zero O, so every P V accumulates.
+//  * the producer: K and V tiles of 64 keys (2 x 16 KB) by TMA into four stages;
+//  * two issuers, a block each (one lane): S = Q K^T (M 128, N 64, both operands in shared memory) into one
+//    of the block's two S buffers, then O += P V (P in tensor memory, V with its dimensions major):
+//      S(t + 1), P V(t), S(t + 2), P V(t + 1), ...
+//    so the next scores are there when a row is done with its last ones. Products of one thread finish
+//    in the order of their issue: S(t + 1) may overwrite P(t - 1), whose product was issued before it.
+// Tensor memory: S_a, S_b (two buffers of 64 columns each, P over them), O_a, O_b (128 each): all 512 columns.
+// Before a piece its rows zero O, so every P V accumulates.
+//
+// (128 keys a tile with one S buffer a block waited a third of its time for the next scores: 278 us on
+// 16 trees of 61 rows over 8192 tokens.) Two scores share a reciprocal: 1/a = b / (ab), 1/b = a / (ab).
 //
 // Edge tiles (new rows, the window's start, the end) see keys as bits of a row. Values past the end of
 // the sequence are set to zero in the stage; infinities and NaN of keys that some row does not see are
@@ -36,26 +38,28 @@ namespace scored {
 namespace {
 
 struct Wide {  // what the work order and the merge need
-  static constexpr int D = 128, TK = 128, RB = 256, ROWB = 256, kCtasPerSm = 1;
+  static constexpr int D = 128, TK = 64, RB = 256, ROWB = 256, kCtasPerSm = 1;
 };
 constexpr int kSoft = 8;                   // softmax warps
-constexpr int kWideThreads = (kSoft + 4) * 32;  // the last two warps do nothing: register shares go by four warps
+constexpr int kWideThreads = (kSoft + 4) * 32;  // the last warp does nothing: register shares go by four warps
 // Registers of a thread as launched, of the softmax warps and of the others after the split
 constexpr int kWideRegs = 168, kSoftRegs = 216, kOtherRegs = 72;
 static_assert(8 * kSoftRegs + 4 * kOtherRegs == 12 * kWideRegs, "a split above the launch's share would wait forever");
-constexpr int kBlock = 128;                // rows of a block, keys of a tile
-constexpr int kHalf = kBlock * 256;        // bytes of 128 rows of K, V or Q
-constexpr int kStage = 2 * kHalf;          // K and V of a tile
-constexpr int kWideSmem = 1024 + 2 * kStage + 2 * kHalf;
-constexpr int kColO = 256;                 // S_a 0, S_b 128, O_a 256, O_b 384
+constexpr int kTile = Wide::TK;            // keys of a tile
+constexpr int kBlock = 128;                // rows of a block
+constexpr int kHalf = kTile * 256;         // bytes of a tile's K or V
+constexpr int kStage = 2 * kHalf, kWideStages = 4;
+constexpr int kQBytes = kBlock * 256;      // of a block
+constexpr int kWideSmem = 1024 + kWideStages * kStage + 2 * kQBytes;
+constexpr int kColO = 256;                 // S_a 0 (and 64), S_b 128 (and 192), O_a 256, O_b 384
 
 __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lbo, uint32_t sbo) {  // 128-byte swizzle
   return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 | (uint64_t)((sbo >> 4) & 0x3FFF) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// kind::f16, fp32 accumulate, bf16 operands, M 128, N 128
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24);
-constexpr uint32_t kIdescV = kIdesc | (1u << 16);  // B with its N dimension major
+// kind::f16, fp32 accumulate, bf16 operands, M 128; N 64 (keys), and N 128 (values) with B's N dimension major
+constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 17) | (8u << 24);
+constexpr uint32_t kIdescV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (16u << 17) | (8u << 24);
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int accumulate) {
   asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
@@ -67,6 +71,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// True in one lane of a full warp, the same one each time. (Under `lane == 0` a product took 84 to 144 cycles to
+// issue: the compiler does not know that its operands are one thread's.)
+__device__ __forceinline__ bool elected() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(yes));
+  return yes != 0;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -92,6 +103,13 @@ __device__ __forceinline__ void tmem_put(uint32_t at, const uint32_t *x) {
 __device__ __forceinline__ void tmem_get_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// the smaller of two, a NaN if one is
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float z;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+
 // byte of (row, 16-byte chunk of its 16) in 128 rows as the TMA lays them
 __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
   return (row >> 3) * 2048 + (chunk >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
@@ -103,8 +121,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   grid_dependents_launch();
   constexpr int kWarps = kWideThreads / 32;
   extern __shared__ uint8_t smem[];
-  __shared__ __align__(8) uint64_t s_full[2], s_free[2];  // stages
-  __shared__ __align__(8) uint64_t s_q[2], s_s[2], s_p[2], s_o[2];  // blocks: Q written, S there, P written, last P V done
+  __shared__ __align__(8) uint64_t s_full[kWideStages], s_free[kWideStages];  // stages
+  __shared__ __align__(8) uint64_t s_q[2], s_s[2][2], s_p[2][2], s_o[2][2];  // blocks: Q written; by buffer S there, P written, P V done
   __shared__ __align__(8) uint64_t s_done;                // every product issued has finished
   __shared__ int s_dead, s_scan[kWarps], s_first_b, s_first_base;
   __shared__ uint32_t s_tmem;
@@ -115,17 +133,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = kv.batch;
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
-  uint8_t *qs = ring + 2 * kStage;  // Q of block a, of block b
+  uint8_t *qs = ring + kWideStages * kStage;  // Q of block a, of block b
   if (tid == 0) {
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < kWideStages; ++k) {
       bar_init(smem_at(&s_full[k]), 1);
-      bar_init(smem_at(&s_free[k]), 1);
-      bar_init(smem_at(&s_q[k]), 4);
-      bar_init(smem_at(&s_s[k]), 1);
-      bar_init(smem_at(&s_p[k]), 4);
-      bar_init(smem_at(&s_o[k]), 1);
+      bar_init(smem_at(&s_free[k]), 2);
     }
-    bar_init(smem_at(&s_done), 1);
+    for (int k = 0; k < 2; ++k) {
+      bar_init(smem_at(&s_q[k]), 4);
+      bar_init(smem_at(&s_s[k][0]), 1);
+      bar_init(smem_at(&s_s[k][1]), 1);
+      bar_init(smem_at(&s_p[k][0]), 4);
+      bar_init(smem_at(&s_p[k][1]), 4);
+      bar_init(smem_at(&s_o[k][0]), 1);
+      bar_init(smem_at(&s_o[k][1]), 1);
+    }
+    bar_init(smem_at(&s_done), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_dead = s_odd = 0;
     s_first_b = s_first_base = 0;
@@ -207,7 +230,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     dead = __any_sync(0xffffffffu, !landed || *(volatile int *)&s_dead != 0);
     if (dead) s_dead = 1;
   };
-  uint32_t tile0 = 0;  // tiles of the CTA's earlier pieces: tile x of the launch goes to stage x % 2
+  uint32_t tile0 = 0;  // tiles of the CTA's earlier pieces: tile x of the launch goes to stage x % kWideStages
   auto two_blocks = [&] { return P.G * at.s.n - p.rb * Wide::RB > kBlock; };
 
   if (warp >= kSoft) {
@@ -223,7 +246,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       int wbase = max(p.kt0 * Wide::TK, p.lo) >> bs_shift;
       int cur = load_id(wbase + lane), nxt = load_id(wbase + 32 + lane);
       for (int kt = p.kt0; kt < p.kt1; ++kt, ++tile0) {
-        const uint32_t st = tile0 & 1u;
+        const uint32_t st = tile0 % kWideStages;
         const int tok = kt * Wide::TK + box_row, first = max(kt * Wide::TK, p.lo) >> bs_shift;
         while (first >= wbase + 32) {  // uniform
           wbase += 32;
@@ -236,7 +259,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int id = src < 32 ? id0 : id1;
         const bool bad = want && (id < 0 || id >= kv.num_blocks), go = want && !bad;
         if (bad) record(a.status, SV_ERR_BAD_BLOCK_ID);
-        if (tile0 >= 2) wait(s_free[st], (tile0 / 2 - 1) & 1u);
+        if (tile0 >= kWideStages) wait(s_free[st], (tile0 / kWideStages - 1) & 1u);
         if (dead) break;  // nothing more is issued
         const uint32_t bar = smem_at(&s_full[st]);
         const int boxes = __popc(__ballot_sync(0xffffffffu, go));
@@ -250,64 +273,59 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       if (dead) break;
     }
-    } else if (warp == kSoft + 1) {
-    // ================= issuer =================
-    uint32_t cq[2] = {0, 0}, cp[2] = {0, 0};  // phases of s_q and s_p so far
-    auto issue_s = [&](int blk, uint32_t x) {
-      if (lane == 0) {
-        const uint32_t k = smem_at(ring) + (x & 1u) * kStage, q = smem_at(qs) + blk * kHalf;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 32;
-          mma_ss(tmem + blk * 128, operand(q + off, 16, 2048), operand(k + off, 16, 2048), kIdesc, kk > 0);
-        }
-        commit(smem_at(&s_s[blk]));
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int blk, uint32_t x) {
-      if (lane == 0) {
-        const uint32_t v = smem_at(ring) + (x & 1u) * kStage + kHalf;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + kColO + blk * 128, tmem + blk * 128 + kk * 8, operand(v + kk * 4096, 1024, 2048), kIdescV, 1);
-      }
-      __syncwarp();
-    };
-    auto commit_to = [&](uint64_t &bar) {
-      if (lane == 0) commit(smem_at(&bar));
-      __syncwarp();
-    };
+    } else if (warp <= kSoft + 2) {
+    // ================= issuers =================
+    const int blk = warp - kSoft - 1;
+    const uint32_t at_s = tmem + blk * 128, at_o = tmem + kColO + blk * 128, at_q = smem_at(qs) + blk * kQBytes;
+    uint32_t cq = 0, cs = 0, cp = 0;  // pieces, scores and weights of the block so far
     while (!dead && next_piece<Wide>(P, at, p)) {
-      const int n = p.kt1 - p.kt0, blocks = two_blocks() ? 2 : 1;
-      wait(s_full[tile0 & 1u], (tile0 / 2) & 1u);
-      for (int blk = 0; blk < blocks && !dead; ++blk) {
-        wait(s_q[blk], cq[blk]++ & 1u);
-        if (dead) break;
-        fence_after();
-        issue_s(blk, tile0);
+      const int n = p.kt1 - p.kt0;
+      if (blk == 1 && !two_blocks()) {  // no rows: the stages are the other block's
+        for (int t = 0; t < n && !dead; ++t) {
+          const uint32_t x = tile0 + t;
+          wait(s_full[x % kWideStages], (x / kWideStages) & 1u);
+          if (!dead && lane == 0) bar_arrive(smem_at(&s_free[x % kWideStages]));
+        }
+        tile0 += n;
+        continue;
       }
-      for (int t = 0; t < n && !dead; ++t) {
+      wait(s_q[blk], cq++ & 1u);
+      for (int t = -1; t < n && !dead; ++t) {
         const uint32_t x = tile0 + t;
-        for (int blk = 0; blk < blocks && !dead; ++blk) {
-          wait(s_p[blk], cp[blk]++ & 1u);
+        if (t + 1 < n) {
+          wait(s_full[(x + 1) % kWideStages], ((x + 1) / kWideStages) & 1u);
           if (dead) break;
           fence_after();
-          issue_pv(blk, x);
-          if (blk == blocks - 1) commit_to(s_free[x & 1u]);
-          if (t + 1 < n) {
-            if (blk == 0) wait(s_full[(x + 1) & 1u], ((x + 1) / 2) & 1u);
-            if (dead) break;
-            issue_s(blk, x + 1);
-          } else {
-            commit_to(s_o[blk]);
+          const uint32_t buf = cs++ & 1u, k = smem_at(ring) + (x + 1) % kWideStages * kStage;
+          if (elected()) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 32;
+              mma_ss(at_s + buf * 64, operand(at_q + off, 16, 2048), operand(k + off, 16, 2048), kIdescS, kk > 0);
+            }
+            commit(smem_at(&s_s[blk][buf]));
           }
+          __syncwarp();
         }
+        if (t < 0) continue;
+        const uint32_t buf = cp & 1u, v = smem_at(ring) + x % kWideStages * kStage + kHalf;
+        wait(s_p[blk][buf], (cp++ >> 1) & 1u);
+        if (dead) break;
+        fence_after();
+        if (elected()) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ts(at_o, at_s + buf * 64 + kk * 8, operand(v + kk * 4096, 1024, 2048), kIdescV, 1);
+          commit(smem_at(&s_o[blk][buf]));
+          commit(smem_at(&s_free[x % kWideStages]));
+        }
+        __syncwarp();
       }
       tile0 += n;
     }
     // every product issued finishes before tensor memory is released
-    commit_to(s_done);
+    if (elected()) commit(smem_at(&s_done));
+    __syncwarp();
     if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_at(&s_done), 0, kDrainBudgetNs))) dead = true;
     }
   } else {
@@ -315,7 +333,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     // ================= softmax: one row per thread =================
     const int blk = warp >> 2, row = (warp & 3) * 32 + lane, rl = blk * kBlock + row;  // row of the block, of the unit
     const uint32_t lane_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = lane_at + blk * 128, to = lane_at + kColO + blk * 128;
+    const uint32_t to = lane_at + kColO + blk * 128;
     const float sl2 = a.scale_log2, cap = P.s.cap, cap_in = P.cap_in;
     const bool biased = P.s.slopes != nullptr;
     const bool bounded = cap > 0.f && cap <= kBoundedCap && !biased;
@@ -326,7 +344,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       else asm volatile("bar.sync 2, 128;" ::: "memory");
     };
     bool first_piece = true;
-    uint32_t cs = 0, co = 0;  // phases of s_s and s_o so far
+    uint32_t cs = 0;  // tiles of the block so far: S in buffer cs & 1, the same buffer's s_o when its P V is done
     auto zero_o = [&] {
       uint32_t z[32];
 #pragma unroll
@@ -341,7 +359,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const uint4 *src = reinterpret_cast<const uint4 *>(
           reinterpret_cast<const __nv_bfloat16 *>(a.q) +
           (live ? ((size_t)(pl.s.row0 + i) * a.num_q_heads + pc.kvh * P.G + (r - i * P.G)) * 128 : 0));
-      uint8_t *dst = qs + blk * kHalf;
+      uint8_t *dst = qs + blk * kQBytes;
 #pragma unroll
       for (int c = 0; c < 16; ++c)
         *reinterpret_cast<uint4 *>(dst + chunk_at(row, c)) = live ? src[c] : make_uint4(0, 0, 0, 0);
@@ -393,19 +411,24 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       zero_o();
       fence_before();
       float m = bounded ? 0.f : kNone, l = 0.f;
-      for (int t = 0; t < n_tiles; ++t) {
-        const int key0 = (pc.kt0 + t) * Wide::TK, base = key0 - c;
-        const uint32_t x = tile0 + t;
-        wait(s_s[blk], cs++ & 1u);
+      for (int t = 0; t < n_tiles; ++t, ++cs) {
+        const int key0 = (pc.kt0 + t) * kTile, base = key0 - c;
+        const uint32_t x = tile0 + t, ts = lane_at + blk * 128 + (cs & 1u) * 64;
+        wait(s_s[blk][cs & 1u], (cs >> 1) & 1u);
         fence_after();
-        const bool edge = key0 + Wide::TK > min(c, ke) || key0 < all_see;  // the same for the whole CTA
-        uint8_t *vs = ring + (x & 1u) * kStage + kHalf;
+        // O may be touched once P V of the tile before is done (a barrier a buffer: its phase before that ended two tiles ago)
+        auto o_free = [&] {
+          if (t > 0) wait(s_o[blk][(cs - 1) & 1u], ((cs - 1) >> 1) & 1u);
+          fence_after();
+        };
+        const bool edge = key0 + kTile > min(c, ke) || key0 < all_see;  // the same for the whole CTA
+        uint8_t *vs = ring + x % kWideStages * kStage + kHalf;
         bool odd = false;
         if (edge) {
           // Values that no weight of zero may meet: slots past the end or before the first visible key hold
           // anything and become zeros; infinities and NaN among the others are looked for.
-          wait(s_full[x & 1u], (x / 2) & 1u);  // (landed: this makes the copies visible here)
-          for (int y = tid; y < kBlock * 16; y += two ? 256 : 128) {
+          wait(s_full[x % kWideStages], (x / kWideStages) & 1u);  // (landed: this makes the copies visible here)
+          for (int y = tid; y < kTile * 16; y += two ? 256 : 128) {
             const int key = y >> 4;
             uint4 *w = reinterpret_cast<uint4 *>(vs + chunk_at(key, y & 15));
             if (key0 + key >= ke || key0 + key < pc.lo) *w = make_uint4(0, 0, 0, 0);
@@ -417,28 +440,37 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           odd = *(volatile int *)&s_odd != 0;
         }
         if (warp_live || odd) {
-          uint32_t w[128];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_get(ts + k * 32, w + k * 32);
+          uint32_t w[kTile];
+          tmem_get(ts, w);
+          tmem_get(ts + 32, w + 32);
           tmem_get_wait();
           // ---- scores ----
           if (cap == 0.f) {
 #pragma unroll
-            for (int k = 0; k < 128; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * sl2);
-          } else {
+            for (int k = 0; k < kTile; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * sl2);
+          } else if (!edge) {
 #pragma unroll
-            for (int k = 0; k < 128; ++k)
+            for (int k = 0; k < kTile; k += 2) {  // 2^60 and more: tanh is 1, and the product stays finite
+              const float e0 = 1.f + ex2(min_nan(__uint_as_float(w[k]) * cap_in, 60.f));
+              const float e1 = 1.f + ex2(min_nan(__uint_as_float(w[k + 1]) * cap_in, 60.f));
+              const float both = -2.f * cap * rcp(e0 * e1);
+              w[k] = __float_as_uint(both * e1);
+              w[k + 1] = __float_as_uint(both * e0);
+            }
+          } else {  // a key that the row does not see may be a NaN: each by itself
+#pragma unroll
+            for (int k = 0; k < kTile; ++k)
               w[k] = __float_as_uint(-2.f * cap * rcp(1.f + ex2(__uint_as_float(w[k]) * cap_in)));
           }
           if (biased) {
             if (!edge) {
               const float f0 = (float)base;
 #pragma unroll
-              for (int k = 0; k < 128; ++k)
+              for (int k = 0; k < kTile; ++k)
                 w[k] = __float_as_uint(fmaf(slope, f0 + (float)k, __uint_as_float(w[k])));
             } else {
 #pragma unroll
-              for (int k = 0; k < 128; ++k) {
+              for (int k = 0; k < kTile; ++k) {
                 const int j = base + k;
                 const float place = (float)(j >= 0 && j < s.n ? s_place[j] : j);
                 w[k] = __float_as_uint(fmaf(slope, place, __uint_as_float(w[k])));
@@ -447,7 +479,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           if (edge) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // the row's view of 32 keys as bits
+            for (int q = 0; q < kTile / 32; ++q) {  // the row's view of 32 keys as bits
               const int b0 = base + 32 * q, first = reach + 1 - b0;
               const uint32_t old = b0 >= 0 ? 0u : b0 <= -32 ? ~0u : (1u << -b0) - 1u;
               const uint32_t near = first <= 0 ? ~0u : first >= 32 ? 0u : ~0u << first;
@@ -462,15 +494,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (!bounded) {
             float mx = kNone;
 #pragma unroll
-            for (int k = 0; k < 128; ++k) mx = fmaxf(mx, __uint_as_float(w[k]));
+            for (int k = 0; k < kTile; ++k) mx = fmaxf(mx, __uint_as_float(w[k]));
             const bool move = mx > m + kMoveAt<false>;
             if (__any_sync(0xffffffffu, move)) {
               const float f = move ? ex2(m - mx) : 1.f;
               if (move) m = mx;
               l *= f;
               uint32_t o[32];
+              o_free();
 #pragma unroll 1
-              for (int k = 0; k < 4; ++k) {  // S(t) is there, so P V(t - 1) is done
+              for (int k = 0; k < 4; ++k) {
                 tmem_get(to + k * 32, o);
                 tmem_get_wait();
 #pragma unroll
@@ -483,7 +516,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           // ---- P ----
           float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int k = 0; k < 128; ++k) {
+          for (int k = 0; k < kTile; ++k) {
             const float e = ex2(__uint_as_float(w[k]) - m);
             part[k & 3] += e;
             w[k] = __float_as_uint(e);
@@ -491,16 +524,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           l += (part[0] + part[1]) + (part[2] + part[3]);
           if (odd) {
             // infinities and NaN, for the rows that see their keys; then out of the tile
-            float weight[128];
+            float weight[kTile];
+            o_free();
 #pragma unroll
-            for (int k = 0; k < 128; ++k) weight[k] = __uint_as_float(w[k]);
+            for (int k = 0; k < kTile; ++k) weight[k] = __uint_as_float(w[k]);
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
               uint32_t o[32];
               tmem_get(to + k * 32, o);
               tmem_get_wait();
 #pragma unroll 1
-              for (int key = 0; key < kBlock; ++key) {
+              for (int key = 0; key < kTile; ++key) {
                 const float e = *(volatile float *)&weight[key];
                 if (!(e > 0.f)) continue;
 #pragma unroll
@@ -520,14 +554,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             tmem_put_wait();
           }
 #pragma unroll
-          for (int k = 0; k < 64; ++k) w[k] = pack2<false>(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+          for (int k = 0; k < kTile / 2; ++k) w[k] = pack2<false>(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
           tmem_put(ts, w);
-          tmem_put(ts + 32, w + 32);
           tmem_put_wait();
         }
         if (odd) {
           of_piece(two);  // every row has taken its share
-          for (int y = tid; y < kBlock * 16; y += two ? 256 : 128) {
+          for (int y = tid; y < kTile * 16; y += two ? 256 : 128) {
             uint32_t *w = reinterpret_cast<uint32_t *>(vs + chunk_at(y >> 4, y & 15));
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
@@ -542,13 +575,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(smem_at(&s_p[blk]));
+        if (lane == 0) bar_arrive(smem_at(&s_p[blk][cs & 1u]));  // (a warp may be a tile ahead of its block's slowest)
       }
       tile0 += n_tiles;
       // the piece's last S is done with Q: the next piece's rows take its place
       if (has && (blk == 0 || two_blocks())) load_q(at, p);
       // ---- the piece's rows ----
-      wait(s_o[blk], co++ & 1u);
+      wait(s_o[blk][(cs - 1) & 1u], ((cs - 1) >> 1) & 1u);
       fence_after();
       if (warp_live) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -589,8 +622,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   fence_after();
   // after a wait that gave up: the copies in flight land before the CTA's shared memory is released
   if (s_dead && warp == kSoft)
-    for (uint32_t x = tile0 > 2 ? tile0 - 2 : 0; x < tile0; ++x)
-      mbar_wait_bounded(smem_at(&s_full[x & 1u]), (x / 2) & 1u, kDrainBudgetNs);
+    for (uint32_t x = tile0 > kWideStages ? tile0 - kWideStages : 0; x < tile0; ++x)
+      mbar_wait_bounded(smem_at(&s_full[x % kWideStages]), (x / kWideStages) & 1u, kDrainBudgetNs);
   if (warp == kSoft + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
