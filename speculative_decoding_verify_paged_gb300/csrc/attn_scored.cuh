@@ -1029,7 +1029,9 @@ cudaError_t run(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream
   return launch_combine<C>(p, l, st);
 }
 
-constexpr int kWideRows = 96;  // units of more query rows go to attn_scored_wide.cu, where it takes them
+// Units of more query rows go to attn_scored_wide.cu, where it takes them: 32 x 72 rows a KV head over 2K to 4K
+// tokens 168 us here, 132 there; 64 rows 113 here, 132 there (a block of 128 rows costs the same).
+constexpr int kWideRows = 64;
 bool wide_fits(const ScoredArgs &sa);
 cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);
 

@@ -24,6 +24,10 @@
 // (128 keys a tile with one S buffer a block waited a third of its time for the next scores: 278 us on
 // 16 trees of 61 rows over 8192 tokens.) Two scores share a reciprocal: 1/a = b / (ab), 1/b = a / (ab).
 //
+// A unit of 128 rows or fewer is one block: a and b hold the same rows, take a tile each in turn, and merge
+// their rows at the end. The values of both lie in the same lanes of tensor memory, so a row's two warps
+// exchange m and l alone and write half of its values each.
+//
 // Edge tiles (new rows, the window's start, the end) see keys as bits of a row. Values past the end of
 // the sequence are set to zero in the stage; infinities and NaN of keys that some row does not see are
 // taken out of it too, and added to the rows that see them by hand.
@@ -109,12 +113,22 @@ __device__ __forceinline__ float min_nan(float x, float y) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
   return z;
 }
+// cap (tanh(x / cap') - 1) = -2 cap / (1 + 2^(x in)) of two scores with one reciprocal: 1/a = b / (ab), 1/b = a / (ab).
+// Past 2^60 tanh is 1 in fp32, and the product stays finite. A NaN in one is a NaN in both.
+// (The kernels of attn_scored.cuh gain nothing by it: other instructions bound them.)
+__device__ __forceinline__ void cap_two(float &x, float &y, float in, float cap) {
+  const float a = 1.f + ex2(min_nan(x * in, 60.f)), b = 1.f + ex2(min_nan(y * in, 60.f));
+  const float both = -2.f * cap * rcp(a * b);
+  x = both * b;
+  y = both * a;
+}
 
 // byte of (row, 16-byte chunk of its 16) in 128 rows as the TMA lays them
 __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
   return (row >> 3) * 2048 + (chunk >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
+template <bool ONE>
 __global__ void __launch_bounds__(kWideThreads, 1)
     attn_scored_wide_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params P) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
@@ -126,7 +140,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __shared__ __align__(8) uint64_t s_done;                // every product issued has finished
   __shared__ int s_dead, s_scan[kWarps], s_first_b, s_first_base;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_place[64], s_top[kSoft], s_odd;
+  __shared__ int s_place[64], s_top[kSoft], s_odd[2];
+  __shared__ float2 s_ml[2][kBlock];  // the blocks' m and l of one row, to be merged
 
   const AttnArgs &a = P.s.a;
   const KV &kv = a.kv;
@@ -150,7 +165,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     bar_init(smem_at(&s_done), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    s_dead = s_odd = 0;
+    s_dead = s_odd[0] = s_odd[1] = 0;
     s_first_b = s_first_base = 0;
   }
   if (warp == kSoft + 1) {
@@ -231,7 +246,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     if (dead) s_dead = 1;
   };
   uint32_t tile0 = 0;  // tiles of the CTA's earlier pieces: tile x of the launch goes to stage x % kWideStages
-  auto two_blocks = [&] { return P.G * at.s.n - p.rb * Wide::RB > kBlock; };
+  auto two_blocks = [&] { return !ONE && P.G * at.s.n - p.rb * Wide::RB > kBlock; };
+  auto active = [&](int blk) { return blk == 0 || (ONE ? p.kt1 - p.kt0 > 1 : two_blocks()); };  // has a part in the piece
 
   if (warp >= kSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -278,48 +294,64 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int blk = warp - kSoft - 1;
     const uint32_t at_s = tmem + blk * 128, at_o = tmem + kColO + blk * 128, at_q = smem_at(qs) + blk * kQBytes;
     uint32_t cq = 0, cs = 0, cp = 0;  // pieces, scores and weights of the block so far
+    auto issue_s = [&](uint32_t x) {
+      fence_after();
+      const uint32_t buf = cs++ & 1u, k = smem_at(ring) + x % kWideStages * kStage;
+      if (elected()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 32;
+          mma_ss(at_s + buf * 64, operand(at_q + off, 16, 2048), operand(k + off, 16, 2048), kIdescS, kk > 0);
+        }
+        commit(smem_at(&s_s[blk][buf]));
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](uint32_t x) {  // when P is there
+      const uint32_t buf = cp & 1u, v = smem_at(ring) + x % kWideStages * kStage + kHalf;
+      wait(s_p[blk][buf], (cp++ >> 1) & 1u);
+      if (dead) return;
+      fence_after();
+      if (elected()) {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts(at_o, at_s + buf * 64 + kk * 8, operand(v + kk * 4096, 1024, 2048), kIdescV, 1);
+        commit(smem_at(&s_o[blk][buf]));
+        commit(smem_at(&s_free[x % kWideStages]));
+      }
+      __syncwarp();
+    };
+    auto landed = [&](uint32_t x) { wait(s_full[x % kWideStages], (x / kWideStages) & 1u); };
     while (!dead && next_piece<Wide>(P, at, p)) {
       const int n = p.kt1 - p.kt0;
-      if (blk == 1 && !two_blocks()) {  // no rows: the stages are the other block's
-        for (int t = 0; t < n && !dead; ++t) {
-          const uint32_t x = tile0 + t;
-          wait(s_full[x % kWideStages], (x / kWideStages) & 1u);
-          if (!dead && lane == 0) bar_arrive(smem_at(&s_free[x % kWideStages]));
-        }
-        tile0 += n;
-        continue;
-      }
-      wait(s_q[blk], cq++ & 1u);
-      for (int t = -1; t < n && !dead; ++t) {
-        const uint32_t x = tile0 + t;
-        if (t + 1 < n) {
-          wait(s_full[(x + 1) % kWideStages], ((x + 1) / kWideStages) & 1u);
-          if (dead) break;
-          fence_after();
-          const uint32_t buf = cs++ & 1u, k = smem_at(ring) + (x + 1) % kWideStages * kStage;
-          if (elected()) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 32;
-              mma_ss(at_s + buf * 64, operand(at_q + off, 16, 2048), operand(k + off, 16, 2048), kIdescS, kk > 0);
-            }
-            commit(smem_at(&s_s[blk][buf]));
+      auto pass = [&](int t) {  // the other block's tile
+        landed(tile0 + t);
+        if (!dead && lane == 0) bar_arrive(smem_at(&s_free[(tile0 + t) % kWideStages]));
+      };
+      const bool work = active(blk);
+      if (work) wait(s_q[blk], cq++ & 1u);
+      if constexpr (ONE) {  // each sees every tile land, in turn
+        if (blk == 1) pass(0);
+        for (int t = blk - 2; t < n && !dead; t += 2) {
+          if (t >= 0 && t + 1 < n) pass(t + 1);
+          if (t + 2 < n) {
+            landed(tile0 + t + 2);
+            if (dead) break;
+            issue_s(tile0 + t + 2);
           }
-          __syncwarp();
+          if (t >= 0) issue_pv(tile0 + t);
         }
-        if (t < 0) continue;
-        const uint32_t buf = cp & 1u, v = smem_at(ring) + x % kWideStages * kStage + kHalf;
-        wait(s_p[blk][buf], (cp++ >> 1) & 1u);
-        if (dead) break;
-        fence_after();
-        if (elected()) {
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ts(at_o, at_s + buf * 64 + kk * 8, operand(v + kk * 4096, 1024, 2048), kIdescV, 1);
-          commit(smem_at(&s_o[blk][buf]));
-          commit(smem_at(&s_free[x % kWideStages]));
+      } else if (work) {
+        for (int t = -1; t < n && !dead; ++t) {
+          if (t + 1 < n) {
+            landed(tile0 + t + 1);
+            if (dead) break;
+            issue_s(tile0 + t + 1);
+          }
+          if (t >= 0) issue_pv(tile0 + t);
         }
-        __syncwarp();
+      } else {
+        for (int t = 0; t < n && !dead; ++t) pass(t);
       }
       tile0 += n;
     }
@@ -331,7 +363,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ================= softmax: one row per thread =================
-    const int blk = warp >> 2, row = (warp & 3) * 32 + lane, rl = blk * kBlock + row;  // row of the block, of the unit
+    const int blk = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the block
     const uint32_t lane_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t to = lane_at + kColO + blk * 128;
     const float sl2 = a.scale_log2, cap = P.s.cap, cap_in = P.cap_in;
@@ -339,9 +371,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const bool bounded = cap > 0.f && cap <= kBoundedCap && !biased;
     const int window = P.s.window;
     auto together = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };  // both blocks
-    auto of_piece = [&](bool two) {                                           // the blocks that have rows
+    auto of_tile = [&](bool two) {                                            // the threads at a tile
       if (two) asm volatile("bar.sync 2, 256;" ::: "memory");
-      else asm volatile("bar.sync 2, 128;" ::: "memory");
+      else if (!ONE || blk == 0) asm volatile("bar.sync 2, 128;" ::: "memory");
+      else asm volatile("bar.sync 3, 128;" ::: "memory");
     };
     bool first_piece = true;
     uint32_t cs = 0;  // tiles of the block so far: S in buffer cs & 1, the same buffer's s_o when its P V is done
@@ -354,7 +387,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       tmem_put_wait();
     };
     auto load_q = [&](const Place &pl, const Piece &pc) {  // this row of a piece's Q into shared memory
-      const int r = pc.rb * Wide::RB + rl, i = r / P.G;
+      const int r = pc.rb * Wide::RB + (ONE ? 0 : blk * kBlock) + row, i = r / P.G;
       const bool live = r < P.G * pl.s.n;
       const uint4 *src = reinterpret_cast<const uint4 *>(
           reinterpret_cast<const __nv_bfloat16 *>(a.q) +
@@ -368,13 +401,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (lane == 0) bar_arrive(smem_at(&s_q[blk]));
     };
     bool has = next_piece<Wide>(P, at, p);
-    if (has && (blk == 0 || two_blocks())) load_q(at, p);
+    if (has && active(blk)) load_q(at, p);
     while (has) {
       const Seq s = at.s;
       const Piece pc = p;
-      const bool two = two_blocks(), active = blk == 0 || two;  // the block has rows
+      const bool two = two_blocks(), mine = ONE || blk == 0 || two;  // a and b have rows; this block has
       has = next_piece<Wide>(P, at, p);                          // at and p: the next piece from here on
-      const int c = s.c, ke = pc.ke, r = pc.rb * Wide::RB + rl, n_tiles = pc.kt1 - pc.kt0;
+      const int c = s.c, ke = pc.ke, rl = (ONE ? 0 : blk * kBlock) + row, r = pc.rb * Wide::RB + rl;
+      const int n_tiles = pc.kt1 - pc.kt0, t0 = ONE ? blk : 0, tx = ONE ? tid & 127 : tid;
       const bool live = r < P.G * s.n;
       const int i = live ? r / P.G : 0, head = pc.kvh * P.G + (live ? r - i * P.G : 0);
       // ---- this row: position, new keys that it sees, reach (the last place out of its window) ----
@@ -401,24 +435,24 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
       for (int w = 1; w < kSoft; ++w) row_top = max(row_top, s_top[w]);
       const int all_see = window > 0 ? row_top - window + 1 : 0;  // keys from here to c are visible to every row
-      if (!active) {
+      if (!mine) {
         tile0 += n_tiles;
         first_piece = false;
-        if (has && two_blocks()) load_q(at, p);
+        if (has && active(blk)) load_q(at, p);
         continue;
       }
       const bool warp_live = __any_sync(0xffffffffu, live);
       zero_o();
       fence_before();
       float m = bounded ? 0.f : kNone, l = 0.f;
-      for (int t = 0; t < n_tiles; ++t, ++cs) {
+      for (int t = t0; t < n_tiles; t += ONE ? 2 : 1, ++cs) {
         const int key0 = (pc.kt0 + t) * kTile, base = key0 - c;
         const uint32_t x = tile0 + t, ts = lane_at + blk * 128 + (cs & 1u) * 64;
         wait(s_s[blk][cs & 1u], (cs >> 1) & 1u);
         fence_after();
         // O may be touched once P V of the tile before is done (a barrier a buffer: its phase before that ended two tiles ago)
         auto o_free = [&] {
-          if (t > 0) wait(s_o[blk][(cs - 1) & 1u], ((cs - 1) >> 1) & 1u);
+          if (t > t0) wait(s_o[blk][(cs - 1) & 1u], ((cs - 1) >> 1) & 1u);
           fence_after();
         };
         const bool edge = key0 + kTile > min(c, ke) || key0 < all_see;  // the same for the whole CTA
@@ -428,16 +462,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           // Values that no weight of zero may meet: slots past the end or before the first visible key hold
           // anything and become zeros; infinities and NaN among the others are looked for.
           wait(s_full[x % kWideStages], (x / kWideStages) & 1u);  // (landed: this makes the copies visible here)
-          for (int y = tid; y < kTile * 16; y += two ? 256 : 128) {
+          for (int y = tx; y < kTile * 16; y += two ? 256 : 128) {
             const int key = y >> 4;
             uint4 *w = reinterpret_cast<uint4 *>(vs + chunk_at(key, y & 15));
             if (key0 + key >= ke || key0 + key < pc.lo) *w = make_uint4(0, 0, 0, 0);
             else odd |= nonfinite2(w->x) | nonfinite2(w->y) | nonfinite2(w->z) | nonfinite2(w->w);
           }
-          if (odd) s_odd = 1;
+          int *flag = &s_odd[ONE ? blk : 0];
+          if (odd) *flag = 1;
           fence_async();
-          of_piece(two);
-          odd = *(volatile int *)&s_odd != 0;
+          of_tile(two);
+          odd = *(volatile int *)flag != 0;
         }
         if (warp_live || odd) {
           uint32_t w[kTile];
@@ -450,12 +485,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             for (int k = 0; k < kTile; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * sl2);
           } else if (!edge) {
 #pragma unroll
-            for (int k = 0; k < kTile; k += 2) {  // 2^60 and more: tanh is 1, and the product stays finite
-              const float e0 = 1.f + ex2(min_nan(__uint_as_float(w[k]) * cap_in, 60.f));
-              const float e1 = 1.f + ex2(min_nan(__uint_as_float(w[k + 1]) * cap_in, 60.f));
-              const float both = -2.f * cap * rcp(e0 * e1);
-              w[k] = __float_as_uint(both * e1);
-              w[k + 1] = __float_as_uint(both * e0);
+            for (int k = 0; k < kTile; k += 2) {
+              float x = __uint_as_float(w[k]), y = __uint_as_float(w[k + 1]);
+              cap_two(x, y, cap_in, cap);
+              w[k] = __float_as_uint(x);
+              w[k + 1] = __float_as_uint(y);
             }
           } else {  // a key that the row does not see may be a NaN: each by itself
 #pragma unroll
@@ -559,8 +593,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           tmem_put_wait();
         }
         if (odd) {
-          of_piece(two);  // every row has taken its share
-          for (int y = tid; y < kTile * 16; y += two ? 256 : 128) {
+          of_tile(two);  // every row has taken its share
+          for (int y = tx; y < kTile * 16; y += two ? 256 : 128) {
             uint32_t *w = reinterpret_cast<uint32_t *>(vs + chunk_at(y >> 4, y & 15));
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
@@ -569,9 +603,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
           fence_async();
-          of_piece(two);
-          if (tid == 0) s_odd = 0;
-          of_piece(two);
+          of_tile(two);
+          if (tx == 0) s_odd[ONE ? blk : 0] = 0;
+          of_tile(two);
         }
         fence_before();
         __syncwarp();
@@ -579,20 +613,29 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       tile0 += n_tiles;
       // the piece's last S is done with Q: the next piece's rows take its place
-      if (has && (blk == 0 || two_blocks())) load_q(at, p);
+      if (has && active(blk)) load_q(at, p);
       // ---- the piece's rows ----
-      wait(s_o[blk][(cs - 1) & 1u], ((cs - 1) >> 1) & 1u);
+      if (!ONE || t0 < n_tiles) wait(s_o[blk][(cs - 1) & 1u], ((cs - 1) >> 1) & 1u);
       fence_after();
+      float f_own = 1.f, f_other = 0.f;  // one block of rows: both warps of a row merge, each 64 of its values
+      if constexpr (ONE) {
+        s_ml[blk][row] = make_float2(m, l);
+        fence_before();
+        together();
+        const float2 other = s_ml[blk ^ 1][row];
+        const float top = fmaxf(m, other.x);
+        f_own = ex2(m - top);
+        f_other = ex2(other.x - top);
+        l = l * f_own + other.y * f_other;
+        m = top;
+        fence_after();
+      }
       if (warp_live) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t slot = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * P.rows_cap + rl;
-        if (live && !pc.whole) P.part_lse[slot] = l == 0.f ? -INFINITY : m + log2f(l);
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[32];
-          tmem_get(to + k * 32, o);
-          tmem_get_wait();
-          if (!live) continue;
+        if (live && !pc.whole && (!ONE || blk == 0)) P.part_lse[slot] = l == 0.f ? -INFINITY : m + log2f(l);
+        auto write = [&](int k, const uint32_t (&o)[32], float f) {  // values 32 k and on, times f
+          if (!live) return;
           if (pc.whole) {
             uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
                                                    ((size_t)(s.row0 + i) * a.num_q_heads + head) * 128 + k * 32);
@@ -601,16 +644,32 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               uint32_t q[4];
 #pragma unroll
               for (int z = 0; z < 4; ++z)
-                q[z] = pack2<false>(__uint_as_float(o[8 * y + 2 * z]) * inv, __uint_as_float(o[8 * y + 2 * z + 1]) * inv);
+                q[z] = pack2<false>(__uint_as_float(o[8 * y + 2 * z]) * f, __uint_as_float(o[8 * y + 2 * z + 1]) * f);
               dst[y] = make_uint4(q[0], q[1], q[2], q[3]);
             }
           } else {
             float4 *dst = reinterpret_cast<float4 *>(P.part_o + slot * 128 + k * 32);
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-              dst[y] = make_float4(__uint_as_float(o[4 * y]) * inv, __uint_as_float(o[4 * y + 1]) * inv,
-                                   __uint_as_float(o[4 * y + 2]) * inv, __uint_as_float(o[4 * y + 3]) * inv);
+              dst[y] = make_float4(__uint_as_float(o[4 * y]) * f, __uint_as_float(o[4 * y + 1]) * f,
+                                   __uint_as_float(o[4 * y + 2]) * f, __uint_as_float(o[4 * y + 3]) * f);
           }
+        };
+#pragma unroll 1
+        for (int k = ONE ? 2 * blk : 0, end = ONE ? k + 2 : 4; k < end; ++k) {
+          uint32_t o[32];
+          tmem_get(to + k * 32, o);
+          if constexpr (ONE) {
+            uint32_t u[32];
+            tmem_get(lane_at + kColO + (blk ^ 1) * 128 + k * 32, u);
+            tmem_get_wait();
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              o[y] = __float_as_uint(__uint_as_float(o[y]) * f_own + __uint_as_float(u[y]) * f_other);
+          } else {
+            tmem_get_wait();
+          }
+          write(k, o, inv);
         }
       }
       first_piece = false;
@@ -627,6 +686,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp == kSoft + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
+template <bool ONE>
+cudaError_t launch_wide(const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, cudaStream_t st) {
+  auto kernel = attn_scored_wide_kernel<ONE>;
+  static const bool split_fits = [&] {  // the kernel was compiled for the registers that its split shares out
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == kWideRegs;
+  }();
+  if (!split_fits) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
+  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(p.ctas), dim3(kWideThreads), (size_t)kWideSmem, st, mk, mv, p);
+}
+
 }  // namespace
 
 bool wide_fits(const ScoredArgs &sa) {
@@ -640,16 +711,11 @@ cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaS
   Params p;
   const Layout l = plan<Wide>(sa, workspace, bytes, &p);
   if (!go) return cudaSuccess;
-  static const bool split_fits = [] {  // the kernel was compiled for the registers that its split shares out
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, attn_scored_wide_kernel) == cudaSuccess && fa.numRegs == kWideRegs;
-  }();
-  if (!split_fits) return cudaErrorInvalidConfiguration;
   CUtensorMap mk, mv;
   if (!make_map<Wide>(&mk, kv.k_pool, kv, p.box) || !make_map<Wide>(&mv, kv.v_pool, kv, p.box)) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attn_scored_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_scored_wide_kernel, dim3(p.ctas), dim3(kWideThreads), (size_t)kWideSmem, st, mk, mv, p);
+  // One block of rows for all: 32 x 25 rows a head group of 4 over 2K to 4K tokens 170 -> 131 us with both blocks at work
+  const bool one = sa.a.num_q_heads / kv.num_kv_heads * sa.a.max_q <= kBlock;
+  const cudaError_t e = one ? launch_wide<true>(mk, mv, p, st) : launch_wide<false>(mk, mv, p, st);
   if (e != cudaSuccess) return e;
   return launch_combine<Wide>(p, l, st);
 }
