@@ -7,13 +7,20 @@
 // visible: t < c, or the new row t - c is (j <= i, or bit j of the row's tree mask); and
 // p_i - p_t < window. A key that a row does not see never enters its sums, whatever it holds.
 //
-// A CTA owns (key split, KV head, sequence) and all G n_b query rows of the KV head, 16 at a time;
-// keys go through shared memory as fp32, 32 at a time, in 16-byte reads; a warp keeps four rows' running
-// maximum and sum and their accumulators, a lane per key for the scores (four rows' products on
-// each 16-byte read of its key) and a lane per column for the weighted sum (four keys' weights a read).
-// Bound: latency for the short splits it is cut into (four CTAs an SM), the products for wide units.
+// A CTA owns (key split, KV head, sequence) and all G n_b query rows of the KV head, up to 32 at a time;
+// keys go through shared memory as fp32, 32 at a time: K of the next tile loads under the softmax and the
+// weighted sum, V under the scores (16-byte copies that no thread waits for; narrow caches are widened on
+// the way, and loaded in turn). A lane keeps a key for the scores and a column for the weighted sum.
+// Layouts, by the query rows a KV head can have:
+//  * more than 16: a warp keeps 8 rows (a 16-byte read of a key or a value meets 8 rows);
+//  * 5 to 16: a warp keeps 4;
+//  * 4 and fewer: the four warps share the rows: each takes a quarter of the head's values in the scores
+//    (summed through shared memory) and of the columns in the weighted sum. The softmax is computed four times.
+// Bound: shared-memory reads (one to four rows' products each) and, for short splits, latency.
 // Splits that the window leaves no key in write an empty partial (log-sum-exp -inf). A visible
 // NaN makes its row's sum and log-sum-exp NaN, and the merge of the splits carries it on.
+#include <type_traits>
+
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -24,7 +31,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kKeys = 32;         // keys per shared-memory tile
-constexpr int kRowsPerPass = 16;  // query rows per pass (4 per warp)
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -36,6 +42,17 @@ __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+// 16 bytes into shared memory, zeros if !there: nobody waits until copies_landed
+__device__ __forceinline__ void copy16(float *dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LATER /* groups that may still be on their way */>
+__device__ __forceinline__ void copies_landed() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
 }
 // 16 bytes of a row as fp32 into shared memory
 __device__ __forceinline__ void widen16(float *dst, uint4 w, float, const float *) {
@@ -59,16 +76,20 @@ __device__ __forceinline__ void widen16(float *dst, uint4 w, float scale, const 
   }
 }
 
-template <typename T, typename KT /* pool element */, int NK /* head_dim / 32 */>
+template <typename T, typename KT /* pool element */, int NK /* head_dim / 32 */, int RW /* rows a warp keeps */,
+          bool SHARED /* the warps share RW rows */>
 __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs sa) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
-  constexpr int D = NK * 32;
+  constexpr int D = NK * 32, kWarps = kThreads / 32;
   constexpr int kVec = 16 / sizeof(KT), kChunks = D / kVec;  // values in 16 bytes of a pool row; reads of a row
-  __shared__ __align__(16) float q_s[kRowsPerPass][D];
+  constexpr int kRows = SHARED ? RW : RW * kWarps;           // of a pass
+  constexpr int kCols = SHARED ? (NK + kWarps - 1) / kWarps : NK;  // columns a lane keeps
+  __shared__ __align__(16) float q_s[kRows][D];
   __shared__ __align__(16) float k_s[kKeys][D + 4];
   __shared__ __align__(16) float v_s[kKeys][D];
-  __shared__ __align__(16) float p_s[kRowsPerPass][kKeys];
+  __shared__ __align__(16) float p_s[RW * kWarps][kKeys];
+  __shared__ float part_s[SHARED ? kWarps : 1][RW][kKeys];  // a quarter's part of the scores
   __shared__ int s_bad;
 
   const AttnArgs &a = sa.a;
@@ -92,14 +113,42 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
   const int kb = max(split * a.chunk, first / kKeys * kKeys), ke = min(L, (split + 1) * a.chunk);
   const int G = a.num_q_heads / kv.num_kv_heads;
   const int R = G * n;
+  const int bs_shift = __ffs(kv.block_size) - 1;
   const T *qp = reinterpret_cast<const T *>(a.q);
   const KT *kp = reinterpret_cast<const KT *>(kv.k_pool);
   const KT *vp = reinterpret_cast<const KT *>(kv.v_pool);
   if (tid == 0) s_bad = 0;
 
-  for (int rg = 0; rg < R; rg += kRowsPerPass) {
+  // a lane's key of the tile at kt: its block id, or -1 (past the split; a bad id)
+  auto block_of = [&](int kt) {
+    const int t = kt + lane;
+    if (t >= ke) return -1;
+    const int id = kv.block_table[(size_t)b * kv.max_blocks + (t >> bs_shift)];
+    if (id >= 0 && id < kv.num_blocks) return id;
+    s_bad = 1;
+    return -1;
+  };
+  // the tile at kt of a pool into shared memory; all lanes take part
+  auto fetch = [&](float *dst, int pitch, const KT *pool, float scale, int kt, int ids) {
+    for (int x = tid; x < kKeys * kChunks; x += kThreads) {  // kKeys * kChunks is a multiple of 32
+      const int j = x / kChunks, d = x % kChunks * kVec, t = kt + j;
+      const int id = __shfl_sync(0xffffffffu, ids, j);
+      const size_t off = (((size_t)max(id, 0) * kv.num_kv_heads + kvh) * kv.block_size + (t & (kv.block_size - 1))) * D + d;
+      if constexpr (sizeof(KT) == 4) {
+        copy16(dst + j * pitch + d, pool + off, id >= 0);
+      } else {
+        const uint4 w = id >= 0 ? *reinterpret_cast<const uint4 *>(pool + off) : make_uint4(0, 0, 0, 0);
+        widen16(dst + j * pitch + d, w, scale, (const KT *)nullptr);
+      }
+    }
+    copies_end();
+  };
+
+  for (int rg = 0; rg < R; rg += kRows) {
     __syncthreads();
-    for (int x = tid; x < kRowsPerPass * D; x += kThreads) {
+    int ids = kb < ke ? block_of(kb) : -1;
+    if (kb < ke) fetch(&k_s[0][0], D + 4, kp, kv.k_scale, kb, ids);
+    for (int x = tid; x < kRows * D; x += kThreads) {
       const int rr = x / D, d = x % D, r = rg + rr;
       float val = 0.f;
       if (r < R) {
@@ -108,130 +157,145 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
       }
       q_s[rr][d] = val;
     }
-    float m[4], l[4], acc[4][NK], slope[4];
-    unsigned hide[4];  // keys of the tile that a row does not see
-    int pos[4];
+    const int rw = SHARED ? 0 : warp * RW;  // the warp's first row of the pass
+    float m[RW], l[RW], acc[RW][kCols], slope[RW];
+    unsigned hide[RW];  // keys of the tile that a row does not see
+    int pos[RW];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < RW; ++w) {
       m[w] = -INFINITY;
       l[w] = 0.f;
 #pragma unroll
-      for (int k = 0; k < NK; ++k) acc[w][k] = 0.f;
-      const int r = rg + warp * 4 + w, i = r < R ? r / G : 0, g = r < R ? r % G : 0;
+      for (int k = 0; k < kCols; ++k) acc[w][k] = 0.f;
+      const int r = rg + rw + w, i = r < R ? r / G : 0, g = r < R ? r % G : 0;
       pos[w] = n > 0 && sa.positions != nullptr ? sa.positions[row0 + i] : c + i;
       if (n > 0 && pos[w] < c && lane == 0) record(a.status, SV_ERR_BAD_LENGTH);
       slope[w] = sa.slopes != nullptr ? sa.slopes[kvh * G + g] * kLog2e : 0.f;
     }
     for (int kt = kb; kt < ke; kt += kKeys) {
-      __syncthreads();
-#pragma unroll 4
-      for (int x = tid; x < kKeys * kChunks; x += kThreads) {
-        const int j = x / kChunks, d = x % kChunks * kVec, t = kt + j;
-        uint4 kk = make_uint4(0, 0, 0, 0), vv = kk;
-        if (t < ke) {
-          const int blk = kv.block_table[(size_t)b * kv.max_blocks + t / kv.block_size];
-          if (blk >= 0 && blk < kv.num_blocks) {
-            const size_t off = (((size_t)blk * kv.num_kv_heads + kvh) * kv.block_size + t % kv.block_size) * D + d;
-            kk = *reinterpret_cast<const uint4 *>(kp + off);
-            vv = *reinterpret_cast<const uint4 *>(vp + off);
-          } else {
-            s_bad = 1;
-          }
-        }
-        widen16(&k_s[j][d], kk, kv.k_scale, (const KT *)nullptr);
-        widen16(&v_s[j][d], vv, kv.v_scale, (const KT *)nullptr);
-      }
-      __syncthreads();
+      copies_landed<0>();
+      __syncthreads();  // K is there, and the last tile's V is done with
+      fetch(&v_s[0][0], D, vp, kv.v_scale, kt, ids);
+      if (kt + kKeys < ke) ids = block_of(kt + kKeys);
+      const bool mine = rg + rw < R;  // some of the warp's rows exist
       const int t = kt + lane, j = t - c;
       int pt = t;
       if (j >= 0 && j < n && sa.positions != nullptr) pt = sa.positions[row0 + j];
-      if (rg + warp * 4 >= R) continue;  // none of this warp's rows
-      float dot[4] = {0.f, 0.f, 0.f, 0.f};
+      float dot[RW];
+#pragma unroll
+      for (int w = 0; w < RW; ++w) dot[w] = 0.f;
+      if (mine) {
+        constexpr int kSpan = SHARED ? D / kWarps : D;
+        const int d0 = SHARED ? warp * kSpan : 0;
 #pragma unroll 8
-      for (int d = 0; d < D; d += 4) {
-        const float4 kk = *reinterpret_cast<const float4 *>(&k_s[lane][d]);
+        for (int d = 0; d < kSpan; d += 4) {
+          const float4 kk = *reinterpret_cast<const float4 *>(&k_s[lane][d0 + d]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float4 qq = *reinterpret_cast<const float4 *>(&q_s[warp * 4 + w][d]);
-          dot[w] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, dot[w]))));
+          for (int w = 0; w < RW; ++w) {
+            const float4 qq = *reinterpret_cast<const float4 *>(&q_s[rw + w][d0 + d]);
+            dot[w] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, dot[w]))));
+          }
         }
       }
-      unsigned any = 0u;  // keys that some row of the warp sees
+      if constexpr (SHARED)
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int r = rg + warp * 4 + w, i = r < R ? r / G : 0;
-        bool vis = r < R && t < ke && (sa.window <= 0 || pos[w] - pt < sa.window);
-        if (vis && j >= 0)
-          vis = a.mask_kind == SV_MASK_CAUSAL ? j <= i : (j < 64 && ((a.tree_mask[row0 + i] >> j) & 1ull));
-        float s = -INFINITY;
-        if (vis) {
-          s = dot[w] * a.scale_log2;
-          if (sa.cap > 0.f) s = sa.cap * tanhf(s / sa.cap);  // both in units of log2
-          s -= slope[w] * (float)(pos[w] - pt);
-        }
-        const unsigned seen = __ballot_sync(0xffffffffu, vis);
-        float p = 0.f;
-        if (seen != 0u) {
-          const float mn = fmaxf(m[w], warp_max(s)), ref = mn == -INFINITY ? 0.f : mn;
-          p = vis ? exp2f(s - ref) : 0.f;
-          const float alpha = exp2f(m[w] - ref);
-          l[w] = l[w] * alpha + warp_sum(p);
+        for (int w = 0; w < RW; ++w) part_s[warp][w][lane] = dot[w];
+      __syncthreads();  // every warp is done with K
+      if (kt + kKeys < ke) fetch(&k_s[0][0], D + 4, kp, kv.k_scale, kt + kKeys, ids);
+      else copies_end();
+      unsigned any = 0u, hidden = 0u;  // keys that some row of the warp sees, that some row does not
+      if (mine) {
+        if constexpr (SHARED)
 #pragma unroll
-          for (int k = 0; k < NK; ++k) acc[w][k] *= alpha;
-          m[w] = mn;
+          for (int w = 0; w < RW; ++w)
+            dot[w] = (part_s[0][w][lane] + part_s[1][w][lane]) + (part_s[2][w][lane] + part_s[3][w][lane]);
+#pragma unroll
+        for (int w = 0; w < RW; ++w) {
+          const int r = rg + rw + w, i = r < R ? r / G : 0;
+          bool vis = r < R && t < ke && (sa.window <= 0 || pos[w] - pt < sa.window);
+          if (vis && j >= 0)
+            vis = a.mask_kind == SV_MASK_CAUSAL ? j <= i : (j < 64 && ((a.tree_mask[row0 + i] >> j) & 1ull));
+          float s = -INFINITY;
+          if (vis) {
+            s = dot[w] * a.scale_log2;
+            if (sa.cap > 0.f) s = sa.cap * tanhf(s / sa.cap);  // both in units of log2
+            s -= slope[w] * (float)(pos[w] - pt);
+          }
+          const unsigned seen = __ballot_sync(0xffffffffu, vis);
+          float p = 0.f;
+          if (seen != 0u) {
+            const float mn = fmaxf(m[w], warp_max(s)), ref = mn == -INFINITY ? 0.f : mn;
+            p = vis ? exp2f(s - ref) : 0.f;
+            const float alpha = exp2f(m[w] - ref);
+            l[w] = l[w] * alpha + warp_sum(p);
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) acc[w][k] *= alpha;
+            m[w] = mn;
+          }
+          p_s[warp * RW + w][lane] = p;
+          any |= seen;
+          hide[w] = r < R ? ~seen : 0u;
+          hidden |= hide[w];
         }
-        p_s[warp * 4 + w][lane] = p;
-        any |= seen;
-        hide[w] = r < R ? ~seen : 0u;
       }
-      __syncwarp();
+      copies_landed<1>();
+      __syncthreads();  // V is there
+      if (!mine) continue;
       // a row takes nothing of a key that it does not see, whatever the key's values are
       bool odd = false;
-      if ((any & hide[0]) | (any & hide[1]) | (any & hide[2]) | (any & hide[3]))
+      if (any & hidden)
         for (int d = 0; d < D; d += 4) {
           const float4 v = *reinterpret_cast<const float4 *>(&v_s[lane][d]);
           odd |= !(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) < INFINITY);
         }
       odd = __any_sync(0xffffffffu, odd && ((any >> lane) & 1u));
-      for (int x = 0; x < kKeys; x += 4) {
-        if (((any >> x) & 15u) == 0u) continue;
-        float4 pw[4];
+      auto column = [&](int k) { return lane + 32 * (SHARED ? warp + kWarps * k : k); };
+      auto add = [&](int x, auto checked) {  // four keys
+        float4 pw[RW];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) pw[w] = *reinterpret_cast<const float4 *>(&p_s[warp * 4 + w][x]);
+        for (int w = 0; w < RW; ++w) pw[w] = *reinterpret_cast<const float4 *>(&p_s[warp * RW + w][x]);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          if (!((any >> (x + y)) & 1u)) continue;
+          if (decltype(checked)::value && !((any >> (x + y)) & 1u)) continue;
 #pragma unroll
-          for (int k = 0; k < NK; ++k) {
-            const float v = v_s[x + y][lane + 32 * k];
+          for (int k = 0; k < kCols; ++k) {
+            if (SHARED && column(k) >= D) continue;
+            const float v = v_s[x + y][column(k)];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < RW; ++w) {
               const float pj = y == 0 ? pw[w].x : y == 1 ? pw[w].y : y == 2 ? pw[w].z : pw[w].w;
-              if (!odd || !((hide[w] >> (x + y)) & 1u)) acc[w][k] = fmaf(pj, v, acc[w][k]);
+              if (!decltype(checked)::value || !odd || !((hide[w] >> (x + y)) & 1u)) acc[w][k] = fmaf(pj, v, acc[w][k]);
             }
           }
         }
+      };
+      if (any == 0xffffffffu && hidden == 0u) {
+#pragma unroll 2
+        for (int x = 0; x < kKeys; x += 4) add(x, std::false_type{});
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < kKeys; x += 4)
+          if (((any >> x) & 15u) != 0u) add(x, std::true_type{});
       }
-      __syncwarp();
     }
+    copies_landed<0>();
     // write this pass's rows
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int r = rg + warp * 4 + w;
+    for (int w = 0; w < RW; ++w) {
+      const int r = rg + rw + w;
       if (r >= R) continue;
       const int i = r / G, g = r % G, h = kvh * G + g;
       const size_t qrow = (size_t)(row0 + i) * a.num_q_heads + h;
       const float inv = l[w] == 0.f ? 0.f : 1.f / l[w];  // a row that sees no key gets zeros
-      if (nsplit == 1) {
-        T *op = reinterpret_cast<T *>(a.out);
+      const size_t prow = (size_t)split * a.total_q * a.num_q_heads + qrow;
 #pragma unroll
-        for (int k = 0; k < NK; ++k) op[qrow * D + lane + 32 * k] = from_f32<T>(acc[w][k] * inv);
-      } else {
-        const size_t prow = (size_t)split * a.total_q * a.num_q_heads + qrow;
-#pragma unroll
-        for (int k = 0; k < NK; ++k) a.ws_o[prow * D + lane + 32 * k] = acc[w][k] * inv;
-        if (lane == 0) a.ws_lse[prow] = l[w] == 0.f ? -INFINITY : m[w] + log2f(l[w]);
+      for (int k = 0; k < kCols; ++k) {
+        const int d = lane + 32 * (SHARED ? warp + kWarps * k : k);
+        if (SHARED && d >= D) continue;
+        if (nsplit == 1) reinterpret_cast<T *>(a.out)[qrow * D + d] = from_f32<T>(acc[w][k] * inv);
+        else a.ws_o[prow * D + d] = acc[w][k] * inv;
       }
+      if (nsplit > 1 && lane == 0 && (!SHARED || warp == 0)) a.ws_lse[prow] = l[w] == 0.f ? -INFINITY : m[w] + log2f(l[w]);
     }
   }
   __syncthreads();
@@ -281,19 +345,26 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_combine(ScoredArgs 
     if (k * 32 < D) op[idx * D + lane + 32 * k] = from_f32<T>(den == 0.f ? 0.f : num[k] / den);
 }
 
-template <typename T, typename KT>
-cudaError_t launch_t(const ScoredArgs &sa, cudaStream_t st) {
+template <typename T, typename KT, int NK>
+cudaError_t launch_n(const ScoredArgs &sa, cudaStream_t st) {
   const dim3 grid(sa.a.max_splits, sa.a.kv.num_kv_heads, sa.a.kv.batch);
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kThreads), 0, st, sa); };
+  const long long rows = (long long)(sa.a.num_q_heads / sa.a.kv.num_kv_heads) * sa.a.max_q;
+  if (rows <= 4) return go(attn_scored_simt_kernel<T, KT, NK, 4, true>);
+  if (rows <= 16 || sizeof(KT) < 4) return go(attn_scored_simt_kernel<T, KT, NK, 4, false>);
+  return go(attn_scored_simt_kernel<T, KT, NK, 8, false>);
+}
+template <typename T, typename KT>
+cudaError_t launch_t(const ScoredArgs &sa, cudaStream_t st) {
   switch (sa.a.kv.head_dim / 32) {
-    case 1: return go(attn_scored_simt_kernel<T, KT, 1>);
-    case 2: return go(attn_scored_simt_kernel<T, KT, 2>);
-    case 3: return go(attn_scored_simt_kernel<T, KT, 3>);
-    case 4: return go(attn_scored_simt_kernel<T, KT, 4>);
-    case 5: return go(attn_scored_simt_kernel<T, KT, 5>);
-    case 6: return go(attn_scored_simt_kernel<T, KT, 6>);
-    case 7: return go(attn_scored_simt_kernel<T, KT, 7>);
-    default: return go(attn_scored_simt_kernel<T, KT, 8>);
+    case 1: return launch_n<T, KT, 1>(sa, st);
+    case 2: return launch_n<T, KT, 2>(sa, st);
+    case 3: return launch_n<T, KT, 3>(sa, st);
+    case 4: return launch_n<T, KT, 4>(sa, st);
+    case 5: return launch_n<T, KT, 5>(sa, st);
+    case 6: return launch_n<T, KT, 6>(sa, st);
+    case 7: return launch_n<T, KT, 7>(sa, st);
+    default: return launch_n<T, KT, 8>(sa, st);
   }
 }
 
