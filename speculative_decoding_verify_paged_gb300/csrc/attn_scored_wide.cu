@@ -52,9 +52,13 @@ static_assert(8 * kSoftRegs + 4 * kOtherRegs == 12 * kWideRegs, "a split above t
 constexpr int kTile = Wide::TK;            // keys of a tile
 constexpr int kBlock = 128;                // rows of a block
 constexpr int kHalf = kTile * 256;         // bytes of a tile's K or V
-constexpr int kStage = 2 * kHalf, kWideStages = 4;
+constexpr int kStage = 2 * kHalf;
 constexpr int kQBytes = kBlock * 256;      // of a block
-constexpr int kWideSmem = 1024 + kWideStages * kStage + 2 * kQBytes;
+// One block of rows: its Q once, and two stages more (the blocks hold two tiles each)
+template <bool ONE>
+constexpr int kStages = ONE ? 6 : 4;
+template <bool ONE>
+constexpr int kWideSmem = 1024 + kStages<ONE> * kStage + (ONE ? 1 : 2) * kQBytes;
 constexpr int kColO = 256;                 // S_a 0 (and 64), S_b 128 (and 192), O_a 256, O_b 384
 
 __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lbo, uint32_t sbo) {  // 128-byte swizzle
@@ -133,29 +137,30 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     attn_scored_wide_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params P) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
-  constexpr int kWarps = kWideThreads / 32;
+  constexpr int kWarps = kWideThreads / 32, kWideStages = kStages<ONE>;
   extern __shared__ uint8_t smem[];
   __shared__ __align__(8) uint64_t s_full[kWideStages], s_free[kWideStages];  // stages
   __shared__ __align__(8) uint64_t s_q[2], s_s[2][2], s_p[2][2], s_o[2][2];  // blocks: Q written; by buffer S there, P written, P V done
+  __shared__ __align__(8) uint64_t s_seen;                // one block of rows: the second issuer is past a piece without work
   __shared__ __align__(8) uint64_t s_done;                // every product issued has finished
   __shared__ int s_dead, s_scan[kWarps], s_first_b, s_first_base;
   __shared__ uint32_t s_tmem;
   __shared__ int s_place[64], s_top[kSoft], s_odd[2];
-  __shared__ float2 s_ml[2][kBlock];  // the blocks' m and l of one row, to be merged
+  __shared__ float2 s_ml[ONE ? kBlock : 1];  // a block's m and l, on their way to the other
 
   const AttnArgs &a = P.s.a;
   const KV &kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = kv.batch;
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
-  uint8_t *qs = ring + kWideStages * kStage;  // Q of block a, of block b
+  uint8_t *qs = ring + kWideStages * kStage;  // Q of block a, of block b (one block of rows: of both)
   if (tid == 0) {
     for (int k = 0; k < kWideStages; ++k) {
       bar_init(smem_at(&s_full[k]), 1);
       bar_init(smem_at(&s_free[k]), 2);
     }
     for (int k = 0; k < 2; ++k) {
-      bar_init(smem_at(&s_q[k]), 4);
+      bar_init(smem_at(&s_q[k]), ONE ? 8 : 4);
       bar_init(smem_at(&s_s[k][0]), 1);
       bar_init(smem_at(&s_s[k][1]), 1);
       bar_init(smem_at(&s_p[k][0]), 4);
@@ -163,6 +168,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       bar_init(smem_at(&s_o[k][0]), 1);
       bar_init(smem_at(&s_o[k][1]), 1);
     }
+    bar_init(smem_at(&s_seen), 1);
     bar_init(smem_at(&s_done), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_dead = s_odd[0] = s_odd[1] = 0;
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     } else if (warp <= kSoft + 2) {
     // ================= issuers =================
     const int blk = warp - kSoft - 1;
-    const uint32_t at_s = tmem + blk * 128, at_o = tmem + kColO + blk * 128, at_q = smem_at(qs) + blk * kQBytes;
+    const uint32_t at_s = tmem + blk * 128, at_o = tmem + kColO + blk * 128, at_q = smem_at(qs) + (ONE ? 0 : blk * kQBytes);
     uint32_t cq = 0, cs = 0, cp = 0;  // pieces, scores and weights of the block so far
     auto issue_s = [&](uint32_t x) {
       fence_after();
@@ -329,8 +335,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (!dead && lane == 0) bar_arrive(smem_at(&s_free[(tile0 + t) % kWideStages]));
       };
       const bool work = active(blk);
-      if (work) wait(s_q[blk], cq++ & 1u);
+      if (ONE || work) wait(s_q[ONE ? 0 : blk], cq++ & 1u);
       if constexpr (ONE) {  // each sees every tile land, in turn
+        if (!work && !dead && lane == 0) bar_arrive(smem_at(&s_seen));
         if (blk == 1) pass(0);
         for (int t = blk - 2; t < n && !dead; t += 2) {
           if (t >= 0 && t + 1 < n) pass(t + 1);
@@ -386,22 +393,32 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       for (int k = 0; k < 4; ++k) tmem_put(to + k * 32, z);
       tmem_put_wait();
     };
-    auto load_q = [&](const Place &pl, const Piece &pc) {  // this row of a piece's Q into shared memory
+    // A piece's Q into shared memory: this row, or half of it where both blocks have it
+    constexpr int kParts = ONE ? 8 : 16;
+    uint4 part[kParts];
+    auto get_q = [&](const Place &pl, const Piece &pc) {
       const int r = pc.rb * Wide::RB + (ONE ? 0 : blk * kBlock) + row, i = r / P.G;
       const bool live = r < P.G * pl.s.n;
       const uint4 *src = reinterpret_cast<const uint4 *>(
           reinterpret_cast<const __nv_bfloat16 *>(a.q) +
           (live ? ((size_t)(pl.s.row0 + i) * a.num_q_heads + pc.kvh * P.G + (r - i * P.G)) * 128 : 0));
-      uint8_t *dst = qs + blk * kQBytes;
 #pragma unroll
-      for (int c = 0; c < 16; ++c)
-        *reinterpret_cast<uint4 *>(dst + chunk_at(row, c)) = live ? src[c] : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < kParts; ++c) part[c] = live ? src[(ONE ? 8 * blk : 0) + c] : make_uint4(0, 0, 0, 0);
+    };
+    auto put_q = [&] {
+      uint8_t *dst = qs + (ONE ? 0 : blk * kQBytes);
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) *reinterpret_cast<uint4 *>(dst + chunk_at(row, (ONE ? 8 * blk : 0) + c)) = part[c];
       fence_async();
       __syncwarp();
-      if (lane == 0) bar_arrive(smem_at(&s_q[blk]));
+      if (lane == 0) bar_arrive(smem_at(&s_q[ONE ? 0 : blk]));
     };
+    uint32_t without = 0;  // pieces in which this block had no part
     bool has = next_piece<Wide>(P, at, p);
-    if (has && active(blk)) load_q(at, p);
+    if (has && (ONE || active(blk))) {
+      get_q(at, p);
+      put_q();
+    }
     while (has) {
       const Seq s = at.s;
       const Piece pc = p;
@@ -438,7 +455,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (!mine) {
         tile0 += n_tiles;
         first_piece = false;
-        if (has && active(blk)) load_q(at, p);
+        if (has && active(blk)) {
+          get_q(at, p);
+          put_q();
+        }
         continue;
       }
       const bool warp_live = __any_sync(0xffffffffu, live);
@@ -613,16 +633,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       tile0 += n_tiles;
       // the piece's last S is done with Q: the next piece's rows take its place
-      if (has && active(blk)) load_q(at, p);
+      if (has && (ONE || active(blk))) {
+        get_q(at, p);
+        if (!ONE) put_q();
+      }
       // ---- the piece's rows ----
       if (!ONE || t0 < n_tiles) wait(s_o[blk][(cs - 1) & 1u], ((cs - 1) >> 1) & 1u);
+      else wait(s_seen, without++ & 1u);  // (Q's barrier runs one piece ahead of its issuers at most)
       fence_after();
       float f_own = 1.f, f_other = 0.f;  // one block of rows: both warps of a row merge, each 64 of its values
       if constexpr (ONE) {
-        s_ml[blk][row] = make_float2(m, l);
+        float2 other;
+        if (blk == 1) s_ml[row] = make_float2(m, l);
         fence_before();
         together();
-        const float2 other = s_ml[blk ^ 1][row];
+        if (has) put_q();  // both blocks are done with Q
+        if (blk == 0) {
+          other = s_ml[row];
+          s_ml[row] = make_float2(m, l);
+        }
+        together();
+        if (blk == 1) other = s_ml[row];
         const float top = fmaxf(m, other.x);
         f_own = ex2(m - top);
         f_other = ex2(other.x - top);
@@ -694,8 +725,8 @@ cudaError_t launch_wide(const CUtensorMap &mk, const CUtensorMap &mv, const Para
     return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == kWideRegs;
   }();
   if (!split_fits) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
-  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(p.ctas), dim3(kWideThreads), (size_t)kWideSmem, st, mk, mv, p);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem<ONE>);
+  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(p.ctas), dim3(kWideThreads), (size_t)kWideSmem<ONE>, st, mk, mv, p);
 }
 
 }  // namespace
