@@ -7,8 +7,8 @@
 // over the pairs i < rot / 2 of y: (y_i, y_{i + rot/2}), or (y_2i, y_2i+1) when interleaved. All
 // of it in fp32 and one rounding at the end, to the output's type (for an E4M3 pool straight from
 // fp32 to the code nearest to y / scale: rounding to bf16 on the way would round twice). The
-// angle is the exact product of the position and the fp32 frequency up to one rounding in fp64,
-// reduced to a fraction of a turn there: in fp32 the angle of position 10^5 would be off by 4e-3.
+// angle is the product of the position and the fp32 frequency as a 64-bit fraction of a turn, rounded
+// once to fp32 (see turn): a product in fp32 would be off by 4e-3 at position 10^5.
 //
 // A lane holds 8 consecutive values of a head, a group of pow2ceil(D / 8) lanes a head, a warp
 // 32 / group heads at a time (an iteration). A warp's item is a chunk of one row's iterations, queries,
@@ -22,7 +22,12 @@
 // Bound: memory, every value read once and written once; next to it the issue of instructions (some
 // 80 an iteration of 512 bytes), which is why the head size is a template parameter where it is 64,
 // 128 or 256 and nothing but shuffles, products and conversions is left in the loop. Long
-// batches take whole rows as items; short ones are cut until every resident warp has a chunk.
+// batches take whole rows as items; short ones are cut, evenly, until every resident warp has a chunk.
+// Short calls are latency: a launch, then the chain of reads that finds a row's place.
+//
+// bf16, 32 + 8 heads of 128 values: 16384 rows 60.1 us (5.6 TB/s of rows), 4 rows 3.5 us; 640 rows of 64 + 8
+// heads 6.2 us. With the append: 256 x 64 rows 76.8 us (5.2 TB/s), 32 x 6 rows 6.2 us, 1.5K rows into an E4M3
+// pool 15.1 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -126,7 +131,9 @@ __device__ __forceinline__ int owner_of(const int32_t *cu, int n, int row) {
 }
 
 constexpr int kThreads = 128;
-constexpr int kCtasPerSm = 5;
+// Warps in residence against loads in flight (16384 rows; 256 x 64 appended): 5 CTAs an SM with 5 iterations ahead
+// 69 and 86 us, 6 with 4 63 and 78, 7 with 4 60 and 77, 7 with 3 65 and 83, 8 with 4 (spilling) 61 and 82.
+constexpr int kCtasPerSm = 7;
 
 // The pair's other values x' of a lane's 8.
 template <typename T> __device__ __forceinline__ void from_lane(const Vec8<T> &x, int lane, float (&p)[8]);
@@ -152,7 +159,7 @@ enum Pairs { kShuffle, kInLane, kExchange };  // where a value's pair is
 template <typename T, bool APPEND, int PAIRS, int DIM>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const HeadArgs a, int chunks, int per_chunk,
                                                                          long long items) {
-  constexpr int kAhead = sizeof(T) == 2 ? 5 : 3;  // iterations whose loads are in flight together
+  constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;  // iterations whose loads are in flight together
   constexpr int kEsz = sizeof(T);
   __shared__ float2 s_turn[kThreads / 32][128];
   __shared__ float s_swap[PAIRS == kExchange ? kThreads / 32 : 1][32 * 8];
@@ -350,8 +357,8 @@ cudaError_t launch_rows(const HeadArgs &a, int total_q, cudaStream_t st) {
   const int all = ceil_div(a.hq, hpw) + nk * (APPEND ? 2 : 1);
   // as many iterations an item as give every resident warp one, whole rows at most
   const long long warps = (long long)num_sms() * kCtasPerSm * (kThreads / 32);
-  const int per_chunk = (int)std::min<long long>(all, ((long long)all * total_q + warps - 1) / warps);
-  const int chunks = ceil_div(all, per_chunk);
+  const int most = (int)std::min<long long>(all, ((long long)all * total_q + warps - 1) / warps);
+  const int chunks = ceil_div(all, most), per_chunk = ceil_div(all, chunks);
   const long long items = (long long)total_q * chunks;
   const unsigned ctas = (unsigned)((items + kThreads / 32 - 1) / (kThreads / 32));
   auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(ctas), dim3(kThreads), 0, st, a, chunks, per_chunk, items); };
