@@ -147,6 +147,8 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// a factor that has overflowed (tiny caps) as the largest finite one: zero times it stays zero
+__host__ __device__ __forceinline__ float finite(float x) { return fminf(fmaxf(x, -3.4e38f), 3.4e38f); }
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
     float *merge = reinterpret_cast<float *>(ring + C::kRing);  // [consumer][8][kPad]
     auto together = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kC) : "memory"); };
     const float sl2 = F8 ? a.scale_log2 * kv.k_scale : a.scale_log2;
-    const float cap = P.s.cap, cap_in = F8 ? P.cap_in * kv.k_scale : P.cap_in;
+    const float cap = P.s.cap, cap_in = F8 ? finite(P.cap_in * kv.k_scale) : P.cap_in;
     const bool fast_cap = cap <= kFastCap * 1.4426950408889634f;
     const int window = P.s.window;
     const bool biased = P.s.slopes != nullptr;
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             for (int y = 0; y < kE; ++y) sv[y] = -2.f * cap * rcp(1.f + ex2(sv[y] * cap_in));
           } else {
 #pragma unroll
-            for (int y = 0; y < kE; ++y) sv[y] = cap * tanhf(sv[y] * sl2 / cap) - cap;
+            for (int y = 0; y < kE; ++y) sv[y] = cap * tanhf(sv[y] * sl2 / cap);
           }
           const bool edge = key0 + 16 * M > min(c, ke) || key0 < all_see;  // warp-uniform: some row may not see some key
           if (biased && !edge) {
@@ -990,7 +992,7 @@ Layout plan(const ScoredArgs &sa, void *workspace, size_t *bytes, Params *p) {
   p->G = sa.a.num_q_heads / kv.num_kv_heads;
   const Layout l = layout_of<C>(kv, p->G, sa.a.max_q, sa.a.max_seq_len);
   *bytes = l.bytes;
-  p->cap_in = sa.cap > 0.f ? sa.a.scale_log2 * 2.f * 1.4426950408889634f / sa.cap : 0.f;
+  p->cap_in = sa.cap > 0.f ? finite(sa.a.scale_log2 * 2.f * 1.4426950408889634f / sa.cap) : 0.f;
   p->ctas = l.ctas;
   p->alpha = kAlpha;
   p->rows_cap = l.rows_cap;

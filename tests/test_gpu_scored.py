@@ -119,6 +119,10 @@ SMALL = {
     "e4m3-wide": (24, [170, 0], [40, 64], 8, 2, 128, 16, "e4m3"),
     "f32-d128": (25, [400, 3], [6, 4], 8, 2, 128, 32, "f32"),
     "f32-d32": (26, [100, 3], [1, 4], 2, 1, 32, 4, "f32"),
+    "f32-few-rows": (41, [200, 33, 0], [2, 1, 2], 4, 2, 160, 16, "f32"),
+    "f32-d256-many-rows": (42, [150, 70], [9, 20], 8, 2, 256, 32, "f32"),
+    "e4m3-d96-few-rows": (43, [100, 31], [1, 1], 4, 2, 96, 16, "e4m3"),
+    "bf16-d160": (44, [100, 31], [9, 3], 8, 2, 160, 16, "bf16"),
 }
 
 
@@ -181,6 +185,43 @@ def test_large_scores():
     run(case, ScoreMod(slopes=-0.01 * slopes(8)), q_scale=1.0)  # a bias that grows with distance
 
 
+@pytest.mark.parametrize("dt,d,hq", [("bf16", 128, 8), ("bf16", 128, 64), ("bf16", 128, 128), ("e4m3", 128, 8), ("f32", 64, 8)])
+@pytest.mark.parametrize("cap", [1e-38, 1e-3, 250.0, 1e5])
+def test_caps_of_any_size(dt, d, hq, cap):
+    """Caps so small that a score is all or nothing, and so large that they change nothing (there the scores
+    keep their precision); queries of zeros score zero under any."""
+    case = W.custom(45, batch=2, ctx_lens=[200, 33], n_q=[4, 2], num_q_heads=hq, num_kv_heads=2, head_dim=d, block_size=16, vocab=16, dtype=dt,
+                    use_bank=False)
+    if cap >= 1.0:
+        run(case, ScoreMod(softcap=cap))
+    run(case, ScoreMod(softcap=cap), q_scale=0.0)
+
+
+WIDE = {
+    # name: (seed, ctx, n_q): eight query heads on two KV heads of 128 values
+    "one-block-many": (46, [(37 * i) % 250 for i in range(40)], [17 + i % 16 for i in range(40)]),
+    "one-block-long": (47, [9000, 2500, 70], [30, 20, 32]),
+    "two-blocks-many": (48, [(37 * i) % 250 for i in range(40)], [1 + (7 * i) % 64 for i in range(40)]),
+    "two-blocks-long": (49, [9000, 2500, 70], [64, 50, 33]),
+}
+
+
+@pytest.mark.parametrize("name", list(WIDE))
+def test_wide_units(name):
+    """Units of more than 64 rows: many short sequences (several a CTA, some of a single tile of keys) and long
+    ones (tiles over many CTAs); the same bits every time."""
+    seed, ctx, nq = WIDE[name]
+    case = W.custom(seed, batch=len(ctx), ctx_lens=ctx, n_q=nq, num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=16, vocab=16, use_bank=False)
+    run(case, ScoreMod(window=150))
+    kv, d, buf = run(case, ScoreMod(softcap=20.0, slopes=slopes(8)))
+    first = buf.attn_out.clone()
+    for _ in range(20):
+        buf.attn_out.zero_()
+        S.attention(kv, d, buf, max_seq_len(case.state, case.step))
+        torch.cuda.synchronize()
+        assert status_of(buf) == 0 and torch.equal(buf.attn_out, first)
+
+
 def test_long_context_and_loose_bound():
     case = W.custom(34, batch=3, ctx_lens=[9000, 10, 2500], n_q=[6, 6, 1], num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=16, vocab=16)
     run(case, ScoreMod(softcap=10.0, slopes=slopes(8)))
@@ -188,7 +229,7 @@ def test_long_context_and_loose_bound():
     run(case, ScoreMod(softcap=10.0, window=64))
 
 
-@pytest.mark.parametrize("dt,d,hq", [("bf16", 128, 8), ("bf16", 96, 8), ("f32", 64, 8), ("bf16", 128, 48), ("bf16", 64, 32), ("bf16", 256, 8)])
+@pytest.mark.parametrize("dt,d,hq", [("bf16", 128, 8), ("bf16", 96, 8), ("f32", 64, 8), ("f32", 160, 2), ("bf16", 128, 32), ("bf16", 128, 48), ("bf16", 64, 32), ("bf16", 256, 8)])
 def test_nonfinite_where_nothing_is_seen(dt, d, hq):
     """NaN and infinities in slots past the end of a sequence, before its window, and in draft rows
     that a row does not see: the rows that do not see them are as if they were not there."""
@@ -299,10 +340,11 @@ def test_repeatable_on_two_streams_and_in_graphs():
     assert torch.equal(outs[0], first) and torch.equal(outs[1], first)
 
 
-def test_wait_that_runs_out_then_recovers():
+@pytest.mark.parametrize("n", [6, 20, 40])  # rows of a warp-matrix unit, of a wide one, of two blocks
+def test_wait_that_runs_out_then_recovers(n):
     """The failure-path hook: nothing is issued, every wait runs out, the call records SV_ERR_TIMEOUT and
     the next one on the stream is right."""
-    case = W.custom(51, batch=4, ctx_lens=[700, 65, 1, 300], n_q=[6, 6, 6, 6], num_q_heads=32, num_kv_heads=8, head_dim=128, block_size=16, vocab=16,
+    case = W.custom(51, batch=4, ctx_lens=[700, 65, 1, 300], n_q=[n, n, n, n], num_q_heads=32, num_kv_heads=8, head_dim=128, block_size=16, vocab=16,
                     use_bank=False)
     mod = ScoreMod(softcap=20.0)
     kv, d, buf = run(case, mod)
@@ -311,7 +353,7 @@ def test_wait_that_runs_out_then_recovers():
     L.set_stall_for_test("attention")
     try:
         t0 = time.perf_counter()
-        S.attention(kv, d, buf, 706)
+        S.attention(kv, d, buf, 700 + n)
         torch.cuda.synchronize()
         assert time.perf_counter() - t0 < 1.0
     finally:
@@ -319,7 +361,7 @@ def test_wait_that_runs_out_then_recovers():
         L.set_wait_budget_us(L.DEFAULT_WAIT_BUDGET_US)
     assert status_of(buf) == L.SV_ERR_TIMEOUT
     buf.status.zero_()
-    S.attention(kv, d, buf, 706)
+    S.attention(kv, d, buf, 700 + n)
     torch.cuda.synchronize()
     assert status_of(buf) == 0 and torch.equal(buf.attn_out, first)
 
