@@ -591,7 +591,7 @@ sv_status sv_adaptive_k_current(const void *state, int32_t *k);
  *   SV_OPT_WAIT_BUDGET_US (value in microseconds, 1000 .. 2000000; default
  *     500000): how long a pipeline wait (a consumer waiting for the data its
  *     producer brings, a producer waiting for a free stage) of the tcgen05
- *     attention kernels, of the warp-matrix kernels of sv_spec_verify_attn_scored
+ *     attention kernels, of the tensor-core kernels of sv_spec_verify_attn_scored
  *     and of the sampler's statistics kernel may take before
  *     the kernel gives up, records SV_ERR_TIMEOUT in the status word and ends.
  *     A kernel that gives up still waits for the copies and matrix operations

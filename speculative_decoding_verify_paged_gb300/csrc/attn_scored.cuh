@@ -8,11 +8,16 @@
 // tanh(y) = 1 - 2 / (1 + 2^(2 y log2 e)): two special-function instructions; its absolute error,
 // about 2^-22, times the cap is what reaches a score (caps above kFastCap take tanhf).
 //
-// Bound: memory. A verify step's unit (one KV head of one sequence) has G n_b query rows, 1 to some
-// 40: at 4 flops per row and value of K and V that is far below the card's ratio of flops to bytes,
-// so the kernel is built to keep loads in flight; the matrix instructions of a warp, without tensor
-// memory and its hand-offs, leave time to spare at these row counts. (128 query rows and more per
-// unit are bound by the products.)
+// Bound: memory up to some 16 query rows a unit (one KV head of one sequence: G n_b rows), where 70 us for
+// 32 sequences of 2K to 4K tokens are 83% of the measured copy rate; the warps' matrix instructions beyond
+// (16 x 8 x 16 in 8 cycles of a quarter SM: with 24 rows a warp 1540 of the 1800 cycles that two warps'
+// steps take). Units of more than kWideRows rows go to attn_scored_wide.cu, whose blocks of 128 rows cost too
+// much for fewer (40 rows: 94 us here, 105 there; in sequences of 600 tokens 97 and 148).
+//
+// Times (us, 8 KV heads of 128 values; share of the copy rate): 32 sequences of 2K to 4K tokens in bf16 with 4,
+// 16, 32, 48, 64 rows a KV head 70 (83%), 74, 93 (67%), 97 (62%), 112 (51%); 32 x 6 rows over 0.5K to 4K tokens,
+// capped, 61 (71%); four sequences of 32K tokens in E4M3 57 (69%); 128 sequences in a window of 1024, biased, 95
+// (42%: 4 short units a CTA, each 7000 cycles of setting up and merging).
 //
 // Work: as many CTAs as fit the GPU stay for the whole launch. The key tiles of all units laid end
 // to end (each unit preceded by `alpha` positions, what starting and finishing one costs) are cut
@@ -35,11 +40,14 @@
 // Query rows sit on the n dimension, so that 24 rows (4 heads x 6) cost 24 and not 32. At the end
 // of a piece the WK key groups' (m, l, O) are merged through shared memory, 8 rows of each warp at a time.
 //
-// What decides the speed is the number of warps: a warp's 16 keys are a chain of products, special
-// functions and products again, some 1000 cycles of latency for 300 instructions. Few rows a warp (and
-// K and V read from shared memory once per row group) leave registers for 16 to 18 of them on an SM.
+// A warp's step is a chain of products, special functions and products again, so it is made large (16 or 32
+// keys for up to 24 rows) and two CTAs of four consumers share an SM: their registers go by role (kConsumerRegs).
+// (16 to 18 warps of 8 rows each, which read K and V from shared memory once a row group: 32 x 6 rows 62 us, but
+// wide units 154 against 96. No split of registers, three consumers: 70.) Steps at the edges (new rows, the
+// window's start) see keys as bits of a row and are kept out of the way of the others.
 //
-// A cap's constant term is dropped like the bias's: -2 cap / (1 + 2^(2 y log2 e)) is what is left.
+// A cap's constant term is dropped like the bias's: -2 cap / (1 + 2^(2 y log2 e)) is what is left (the tanhf form
+// keeps it: next to a large cap the rest would lose its last bits).
 // E4M3 codes become fp16 operands in registers (exactly). ldmatrix moves pairs of codes; which
 // dimension lands at which place of the operand differs from the bf16 form, and Q's registers and O's
 // columns follow it.
@@ -389,55 +397,55 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   if (warp >= C::kConsumers) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     if (warp == C::kConsumers) {
-    // ================= producer =================
-    // Lane 2 j (2 j + 1) takes the keys' (values') box of rows j box ... of a tile. Block ids come from a
-    // 64-block window of the block table, two entries per lane, loaded one window before they are used.
-    const int box = P.box, box_row = (lane >> 1) * box;
-    if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);  // failure-path test: a wait that nothing ends
-    while (next_piece<C>(P, at, p)) {
-      const int32_t *bt = kv.block_table + (size_t)at.b * kv.max_blocks;
-      const int last = (p.ke - 1) >> bs_shift;
-      auto load_id = [&](int blk) { return blk <= last ? bt[blk] : -1; };
-      int wbase = max(p.kt0 * TK, p.lo) >> bs_shift;
-      int cur = load_id(wbase + lane), nxt = load_id(wbase + 32 + lane);
-      {  // the piece's query rows on their way to L2
-        const int R = min(RB, P.G * at.s.n - p.rb * RB);
-        for (int x = lane; x < R * (D / 64); x += 32) {
-          const int r = p.rb * RB + x / (D / 64), i = r / P.G, head = p.kvh * P.G + r - i * P.G;
-          const char *q = reinterpret_cast<const char *>(a.q) + (((size_t)(at.s.row0 + i) * a.num_q_heads + head) * D + x % (D / 64) * 64) * 2;
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+      // ================= producer =================
+      // Lane 2 j (2 j + 1) takes the keys' (values') box of rows j box ... of a tile. Block ids come from a
+      // 64-block window of the block table, two entries per lane, loaded one window before they are used.
+      const int box = P.box, box_row = (lane >> 1) * box;
+      if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);  // failure-path test: a wait that nothing ends
+      while (next_piece<C>(P, at, p)) {
+        const int32_t *bt = kv.block_table + (size_t)at.b * kv.max_blocks;
+        const int last = (p.ke - 1) >> bs_shift;
+        auto load_id = [&](int blk) { return blk <= last ? bt[blk] : -1; };
+        int wbase = max(p.kt0 * TK, p.lo) >> bs_shift;
+        int cur = load_id(wbase + lane), nxt = load_id(wbase + 32 + lane);
+        {  // the piece's query rows on their way to L2
+          const int R = min(RB, P.G * at.s.n - p.rb * RB);
+          for (int x = lane; x < R * (D / 64); x += 32) {
+            const int r = p.rb * RB + x / (D / 64), i = r / P.G, head = p.kvh * P.G + r - i * P.G;
+            const char *q = reinterpret_cast<const char *>(a.q) + (((size_t)(at.s.row0 + i) * a.num_q_heads + head) * D + x % (D / 64) * 64) * 2;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+          }
         }
+        for (int kt = p.kt0; kt < p.kt1; ++kt, ++tile0) {
+          const uint32_t st = tile0 % ST;
+          const int tok = kt * TK + box_row, first = max(kt * TK, p.lo) >> bs_shift;
+          while (first >= wbase + 32) {  // uniform
+            wbase += 32;
+            cur = nxt;
+            nxt = load_id(wbase + 32 + lane);
+          }
+          // boxes without a key that some row may see are not read
+          const bool want = box_row < TK && tok < p.ke && tok + box > p.lo;
+          const int src = want ? (tok >> bs_shift) - wbase : 0;
+          const int id0 = __shfl_sync(0xffffffffu, cur, src & 31), id1 = __shfl_sync(0xffffffffu, nxt, src & 31);
+          const int id = src < 32 ? id0 : id1;
+          const bool bad = want && (id < 0 || id >= kv.num_blocks), go = want && !bad;
+          if (bad) record(a.status, SV_ERR_BAD_BLOCK_ID);
+          if (tile0 >= ST) wait(s_free[st], (tile0 / ST - 1) & 1u);
+          if (dead) break;  // nothing more is issued
+          const uint32_t bar = smem_at(&s_full[st]);
+          const int boxes = __popc(__ballot_sync(0xffffffffu, go));
+          if (lane == 0) bar_expect(bar, boxes * box * C::ROWB);
+          __syncwarp();
+          if (go) {
+            const int y = ((id * kv.num_kv_heads + p.kvh) << bs_shift) + (tok & (kv.block_size - 1));
+            load_box<C::ROWB>(ring_at + st * C::kStageBytes + (lane & 1) * TK * C::ROWB + box_row * C::ROWB,
+                              (lane & 1) ? &map_v : &map_k, y, bar);
+          }
+          __syncwarp();
+        }
+        if (dead) break;
       }
-      for (int kt = p.kt0; kt < p.kt1; ++kt, ++tile0) {
-        const uint32_t st = tile0 % ST;
-        const int tok = kt * TK + box_row, first = max(kt * TK, p.lo) >> bs_shift;
-        while (first >= wbase + 32) {  // uniform
-          wbase += 32;
-          cur = nxt;
-          nxt = load_id(wbase + 32 + lane);
-        }
-        // boxes without a key that some row may see are not read
-        const bool want = box_row < TK && tok < p.ke && tok + box > p.lo;
-        const int src = want ? (tok >> bs_shift) - wbase : 0;
-        const int id0 = __shfl_sync(0xffffffffu, cur, src & 31), id1 = __shfl_sync(0xffffffffu, nxt, src & 31);
-        const int id = src < 32 ? id0 : id1;
-        const bool bad = want && (id < 0 || id >= kv.num_blocks), go = want && !bad;
-        if (bad) record(a.status, SV_ERR_BAD_BLOCK_ID);
-        if (tile0 >= ST) wait(s_free[st], (tile0 / ST - 1) & 1u);
-        if (dead) break;  // nothing more is issued
-        const uint32_t bar = smem_at(&s_full[st]);
-        const int boxes = __popc(__ballot_sync(0xffffffffu, go));
-        if (lane == 0) bar_expect(bar, boxes * box * C::ROWB);
-        __syncwarp();
-        if (go) {
-          const int y = ((id * kv.num_kv_heads + p.kvh) << bs_shift) + (tok & (kv.block_size - 1));
-          load_box<C::ROWB>(ring_at + st * C::kStageBytes + (lane & 1) * TK * C::ROWB + box_row * C::ROWB,
-                            (lane & 1) ? &map_v : &map_k, y, bar);
-        }
-        __syncwarp();
-      }
-      if (dead) break;
-    }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
@@ -1031,8 +1039,8 @@ cudaError_t run(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream
   return launch_combine<C>(p, l, st);
 }
 
-// Units of more query rows go to attn_scored_wide.cu, where it takes them: 32 x 72 rows a KV head over 2K to 4K
-// tokens 168 us here, 132 there; 64 rows 113 here, 132 there (a block of 128 rows costs the same).
+// Units of more query rows go to attn_scored_wide.cu, where it takes them: 32 sequences of 2K to 4K tokens with 72 rows a
+// KV head 168 us here, 116 there; with 64 rows 112 and 105, but short sequences cost more there (its pieces start slowly).
 constexpr int kWideRows = 64;
 bool wide_fits(const ScoredArgs &sa);
 cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);

@@ -3,16 +3,23 @@
 // heads of 128 values. The mathematics, the work order, the partials and their merge are those of
 // attn_scored.cuh.
 //
-// Bound: the special functions and the products. 256 query rows a unit are 256 flops per byte of K and
-// V, past what memory limits; a capped score costs two 2^x and a reciprocal (2048 cycles of an SM per
-// 128 x 128 scores) next to 1024 cycles of tensor core for the two products.
+// Bound: the special functions and what surrounds them. 256 query rows a unit are 256 flops per byte of K
+// and V, past what memory limits. Of 64 keys for 256 rows the two products take an estimated 1000 cycles of an SM
+// (Q is read from shared memory again for each tile), the softmax 1300 with a cap (two 2^x and a quarter of a
+// reciprocal a score) and 500 without. Measured is 3000 and 2800 a tile: a warp's read, cap, maximum, weights
+// and write are a chain, and two warps a scheduler hide only part of it.
+//
+// Times (us, bf16, 8 KV heads of 128 values; in brackets the warp-matrix kernels of attn_scored.cuh):
+//   16 trees of 61 rows x 4 heads over 8192 tokens, capped 206 [455], 650 TFLOP/s;
+//   32 sequences over 2K to 4K tokens: 256 rows a KV head 192 capped, 164 without [407 capped],
+//   128 rows 126, 117 [270], 100 rows 116 [271], 72 rows 116 [168].
 //
 // A unit is one KV head of one sequence and up to 256 query rows, as two blocks of 128, one row per
 // tensor-memory lane, so that K and V are read once for all of them. One CTA an SM, eleven warps:
 //  * softmax a and b, four warps each: a thread keeps one row. It reads its 64 scores from tensor memory,
 //    caps, biases and masks them, moves its running maximum if they pass it by far (then rescales its
 //    row of O), and writes P = 2^(s - m) as bf16 over the scores;
-//  * the producer: K and V tiles of 64 keys (2 x 16 KB) by TMA into four stages;
+//  * the producer: K and V tiles of 64 keys (2 x 16 KB) by TMA into the stages;
 //  * two issuers, a block each (one lane): S = Q K^T (M 128, N 64, both operands in shared memory) into one
 //    of the block's two S buffers, then O += P V (P in tensor memory, V with its dimensions major):
 //      S(t + 1), P V(t), S(t + 2), P V(t + 1), ...
@@ -21,12 +28,14 @@
 // Tensor memory: S_a, S_b (two buffers of 64 columns each, P over them), O_a, O_b (128 each): all 512 columns.
 // Before a piece its rows zero O, so every P V accumulates.
 //
-// (128 keys a tile with one S buffer a block waited a third of its time for the next scores: 278 us on
-// 16 trees of 61 rows over 8192 tokens.) Two scores share a reciprocal: 1/a = b / (ab), 1/b = a / (ab).
+// (128 keys a tile with one S buffer a block waited a third of its time for the next scores, one issuer for
+// both blocks made each wait for the other: the trees took 278 and 274 us, against 247 with these in place of
+// them.) Where a cap bounds the scores, 32 of them become weights while the other 32 are read, with no maximum.
 //
 // A unit of 128 rows or fewer is one block: a and b hold the same rows, take a tile each in turn, and merge
 // their rows at the end. The values of both lie in the same lanes of tensor memory, so a row's two warps
-// exchange m and l alone and write half of its values each.
+// exchange m and l alone and write half of its values each. (100 rows, with b idle: 170 us; both at work with
+// four stages 130, with Q once and six 116.) Launches whose units may be larger leave b idle in smaller ones.
 //
 // Edge tiles (new rows, the window's start, the end) see keys as bits of a row. Values past the end of
 // the sequence are set to zero in the stage; infinities and NaN of keys that some row does not see are
@@ -117,14 +126,19 @@ __device__ __forceinline__ float min_nan(float x, float y) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
   return z;
 }
-// cap (tanh(x / cap') - 1) = -2 cap / (1 + 2^(x in)) of two scores with one reciprocal: 1/a = b / (ab), 1/b = a / (ab).
-// Past 2^60 tanh is 1 in fp32, and the product stays finite. A NaN in one is a NaN in both.
-// (The kernels of attn_scored.cuh gain nothing by it: other instructions bound them.)
-__device__ __forceinline__ void cap_two(float &x, float &y, float in, float cap) {
-  const float a = 1.f + ex2(min_nan(x * in, 60.f)), b = 1.f + ex2(min_nan(y * in, 60.f));
-  const float both = -2.f * cap * rcp(a * b);
-  x = both * b;
-  y = both * a;
+// cap (tanh(x / cap') - 1) = -2 cap / (1 + 2^(x in)) of four scores with one reciprocal: 1/a = bcd / (abcd) and so
+// on. Past 2^30 tanh is 1 in fp32, and the product stays finite. A NaN in one is a NaN in all.
+// (16 trees of 61 rows over 8192 tokens: a reciprocal each 278 us, for two 218, for four 206. The kernels of
+// attn_scored.cuh gain nothing by it: other instructions bound them.)
+__device__ __forceinline__ void cap_four(float (&x)[4], float in, float cap) {
+  float e[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) e[y] = 1.f + ex2(min_nan(x[y] * in, 30.f));
+  const float ab = e[0] * e[1], cd = e[2] * e[3], all = -2.f * cap * rcp(ab * cd), of_ab = all * cd, of_cd = all * ab;
+  x[0] = of_ab * e[1];
+  x[1] = of_ab * e[0];
+  x[2] = of_cd * e[3];
+  x[3] = of_cd * e[2];
 }
 
 // byte of (row, 16-byte chunk of its 16) in 128 rows as the TMA lays them
@@ -258,114 +272,115 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp >= kSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSoft) {
-    // ================= producer =================
-    const int bs_shift = __ffs(kv.block_size) - 1, box = P.box, box_row = (lane >> 1) * box;
-    if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);  // failure-path test: a wait that nothing ends
-    while (next_piece<Wide>(P, at, p)) {
-      const int32_t *bt = kv.block_table + (size_t)at.b * kv.max_blocks;
-      const int last = (p.ke - 1) >> bs_shift;
-      auto load_id = [&](int blk) { return blk <= last ? bt[blk] : -1; };
-      int wbase = max(p.kt0 * Wide::TK, p.lo) >> bs_shift;
-      int cur = load_id(wbase + lane), nxt = load_id(wbase + 32 + lane);
-      for (int kt = p.kt0; kt < p.kt1; ++kt, ++tile0) {
-        const uint32_t st = tile0 % kWideStages;
-        const int tok = kt * Wide::TK + box_row, first = max(kt * Wide::TK, p.lo) >> bs_shift;
-        while (first >= wbase + 32) {  // uniform
-          wbase += 32;
-          cur = nxt;
-          nxt = load_id(wbase + 32 + lane);
+      // ================= producer =================
+      const int bs_shift = __ffs(kv.block_size) - 1, box = P.box, box_row = (lane >> 1) * box;
+      if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);  // failure-path test: a wait that nothing ends
+      while (next_piece<Wide>(P, at, p)) {
+        const int32_t *bt = kv.block_table + (size_t)at.b * kv.max_blocks;
+        const int last = (p.ke - 1) >> bs_shift;
+        auto load_id = [&](int blk) { return blk <= last ? bt[blk] : -1; };
+        int wbase = max(p.kt0 * Wide::TK, p.lo) >> bs_shift;
+        int cur = load_id(wbase + lane), nxt = load_id(wbase + 32 + lane);
+        for (int kt = p.kt0; kt < p.kt1; ++kt, ++tile0) {
+          const uint32_t st = tile0 % kWideStages;
+          const int tok = kt * Wide::TK + box_row, first = max(kt * Wide::TK, p.lo) >> bs_shift;
+          while (first >= wbase + 32) {  // uniform
+            wbase += 32;
+            cur = nxt;
+            nxt = load_id(wbase + 32 + lane);
+          }
+          const bool want = box_row < Wide::TK && tok < p.ke && tok + box > p.lo;
+          const int src = want ? (tok >> bs_shift) - wbase : 0;
+          const int id0 = __shfl_sync(0xffffffffu, cur, src & 31), id1 = __shfl_sync(0xffffffffu, nxt, src & 31);
+          const int id = src < 32 ? id0 : id1;
+          const bool bad = want && (id < 0 || id >= kv.num_blocks), go = want && !bad;
+          if (bad) record(a.status, SV_ERR_BAD_BLOCK_ID);
+          if (tile0 >= kWideStages) wait(s_free[st], (tile0 / kWideStages - 1) & 1u);
+          if (dead) break;  // nothing more is issued
+          const uint32_t bar = smem_at(&s_full[st]);
+          const int boxes = __popc(__ballot_sync(0xffffffffu, go));
+          if (lane == 0) bar_expect(bar, boxes * box * Wide::ROWB);
+          __syncwarp();
+          if (go) {
+            const int y = ((id * kv.num_kv_heads + p.kvh) << bs_shift) + (tok & (kv.block_size - 1));
+            load_box<Wide::ROWB>(smem_at(ring) + st * kStage + (lane & 1) * kHalf + box_row * Wide::ROWB,
+                                 (lane & 1) ? &map_v : &map_k, y, bar);
+          }
+          __syncwarp();
         }
-        const bool want = box_row < Wide::TK && tok < p.ke && tok + box > p.lo;
-        const int src = want ? (tok >> bs_shift) - wbase : 0;
-        const int id0 = __shfl_sync(0xffffffffu, cur, src & 31), id1 = __shfl_sync(0xffffffffu, nxt, src & 31);
-        const int id = src < 32 ? id0 : id1;
-        const bool bad = want && (id < 0 || id >= kv.num_blocks), go = want && !bad;
-        if (bad) record(a.status, SV_ERR_BAD_BLOCK_ID);
-        if (tile0 >= kWideStages) wait(s_free[st], (tile0 / kWideStages - 1) & 1u);
-        if (dead) break;  // nothing more is issued
-        const uint32_t bar = smem_at(&s_full[st]);
-        const int boxes = __popc(__ballot_sync(0xffffffffu, go));
-        if (lane == 0) bar_expect(bar, boxes * box * Wide::ROWB);
-        __syncwarp();
-        if (go) {
-          const int y = ((id * kv.num_kv_heads + p.kvh) << bs_shift) + (tok & (kv.block_size - 1));
-          load_box<Wide::ROWB>(smem_at(ring) + st * kStage + (lane & 1) * kHalf + box_row * Wide::ROWB, (lane & 1) ? &map_v : &map_k, y, bar);
-        }
-        __syncwarp();
+        if (dead) break;
       }
-      if (dead) break;
-    }
     } else if (warp <= kSoft + 2) {
-    // ================= issuers =================
-    const int blk = warp - kSoft - 1;
-    const uint32_t at_s = tmem + blk * 128, at_o = tmem + kColO + blk * 128, at_q = smem_at(qs) + (ONE ? 0 : blk * kQBytes);
-    uint32_t cq = 0, cs = 0, cp = 0;  // pieces, scores and weights of the block so far
-    auto issue_s = [&](uint32_t x) {
-      fence_after();
-      const uint32_t buf = cs++ & 1u, k = smem_at(ring) + x % kWideStages * kStage;
-      if (elected()) {
+      // ================= issuers =================
+      const int blk = warp - kSoft - 1;
+      const uint32_t at_s = tmem + blk * 128, at_o = tmem + kColO + blk * 128, at_q = smem_at(qs) + (ONE ? 0 : blk * kQBytes);
+      uint32_t cq = 0, cs = 0, cp = 0;  // pieces, scores and weights of the block so far
+      auto issue_s = [&](uint32_t x) {
+        fence_after();
+        const uint32_t buf = cs++ & 1u, k = smem_at(ring) + x % kWideStages * kStage;
+        if (elected()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 32;
-          mma_ss(at_s + buf * 64, operand(at_q + off, 16, 2048), operand(k + off, 16, 2048), kIdescS, kk > 0);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 32;
+            mma_ss(at_s + buf * 64, operand(at_q + off, 16, 2048), operand(k + off, 16, 2048), kIdescS, kk > 0);
+          }
+          commit(smem_at(&s_s[blk][buf]));
         }
-        commit(smem_at(&s_s[blk][buf]));
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](uint32_t x) {  // when P is there
-      const uint32_t buf = cp & 1u, v = smem_at(ring) + x % kWideStages * kStage + kHalf;
-      wait(s_p[blk][buf], (cp++ >> 1) & 1u);
-      if (dead) return;
-      fence_after();
-      if (elected()) {
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_ts(at_o, at_s + buf * 64 + kk * 8, operand(v + kk * 4096, 1024, 2048), kIdescV, 1);
-        commit(smem_at(&s_o[blk][buf]));
-        commit(smem_at(&s_free[x % kWideStages]));
-      }
-      __syncwarp();
-    };
-    auto landed = [&](uint32_t x) { wait(s_full[x % kWideStages], (x / kWideStages) & 1u); };
-    while (!dead && next_piece<Wide>(P, at, p)) {
-      const int n = p.kt1 - p.kt0;
-      auto pass = [&](int t) {  // the other block's tile
-        landed(tile0 + t);
-        if (!dead && lane == 0) bar_arrive(smem_at(&s_free[(tile0 + t) % kWideStages]));
+        __syncwarp();
       };
-      const bool work = active(blk);
-      if (ONE || work) wait(s_q[ONE ? 0 : blk], cq++ & 1u);
-      if constexpr (ONE) {  // each sees every tile land, in turn
-        if (!work && !dead && lane == 0) bar_arrive(smem_at(&s_seen));
-        if (blk == 1) pass(0);
-        for (int t = blk - 2; t < n && !dead; t += 2) {
-          if (t >= 0 && t + 1 < n) pass(t + 1);
-          if (t + 2 < n) {
-            landed(tile0 + t + 2);
-            if (dead) break;
-            issue_s(tile0 + t + 2);
-          }
-          if (t >= 0) issue_pv(tile0 + t);
+      auto issue_pv = [&](uint32_t x) {  // when P is there
+        const uint32_t buf = cp & 1u, v = smem_at(ring) + x % kWideStages * kStage + kHalf;
+        wait(s_p[blk][buf], (cp++ >> 1) & 1u);
+        if (dead) return;
+        fence_after();
+        if (elected()) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ts(at_o, at_s + buf * 64 + kk * 8, operand(v + kk * 4096, 1024, 2048), kIdescV, 1);
+          commit(smem_at(&s_o[blk][buf]));
+          commit(smem_at(&s_free[x % kWideStages]));
         }
-      } else if (work) {
-        for (int t = -1; t < n && !dead; ++t) {
-          if (t + 1 < n) {
-            landed(tile0 + t + 1);
-            if (dead) break;
-            issue_s(tile0 + t + 1);
+        __syncwarp();
+      };
+      auto landed = [&](uint32_t x) { wait(s_full[x % kWideStages], (x / kWideStages) & 1u); };
+      while (!dead && next_piece<Wide>(P, at, p)) {
+        const int n = p.kt1 - p.kt0;
+        auto pass = [&](int t) {  // the other block's tile
+          landed(tile0 + t);
+          if (!dead && lane == 0) bar_arrive(smem_at(&s_free[(tile0 + t) % kWideStages]));
+        };
+        const bool work = active(blk);
+        if (ONE || work) wait(s_q[ONE ? 0 : blk], cq++ & 1u);
+        if constexpr (ONE) {  // each sees every tile land, in turn
+          if (!work && !dead && lane == 0) bar_arrive(smem_at(&s_seen));
+          if (blk == 1) pass(0);
+          for (int t = blk - 2; t < n && !dead; t += 2) {
+            if (t >= 0 && t + 1 < n) pass(t + 1);
+            if (t + 2 < n) {
+              landed(tile0 + t + 2);
+              if (dead) break;
+              issue_s(tile0 + t + 2);
+            }
+            if (t >= 0) issue_pv(tile0 + t);
           }
-          if (t >= 0) issue_pv(tile0 + t);
+        } else if (work) {
+          for (int t = -1; t < n && !dead; ++t) {
+            if (t + 1 < n) {
+              landed(tile0 + t + 1);
+              if (dead) break;
+              issue_s(tile0 + t + 1);
+            }
+            if (t >= 0) issue_pv(tile0 + t);
+          }
+        } else {
+          for (int t = 0; t < n && !dead; ++t) pass(t);
         }
-      } else {
-        for (int t = 0; t < n && !dead; ++t) pass(t);
+        tile0 += n;
       }
-      tile0 += n;
-    }
-    // every product issued finishes before tensor memory is released
-    if (elected()) commit(smem_at(&s_done));
-    __syncwarp();
-    if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_at(&s_done), 0, kDrainBudgetNs))) dead = true;
+      // every product issued finishes before tensor memory is released
+      if (elected()) commit(smem_at(&s_done));
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_at(&s_done), 0, kDrainBudgetNs))) dead = true;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -376,6 +391,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const float sl2 = a.scale_log2, cap = P.s.cap, cap_in = P.cap_in;
     const bool biased = P.s.slopes != nullptr;
     const bool bounded = cap > 0.f && cap <= kBoundedCap && !biased;
+    const bool plain = cap == 0.f && !biased && sl2 >= 0.f;
     const int window = P.s.window;
     auto together = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };  // both blocks
     auto of_tile = [&](bool two) {                                            // the threads at a tile
@@ -475,6 +491,24 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (t > t0) wait(s_o[blk][(cs - 1) & 1u], ((cs - 1) >> 1) & 1u);
           fence_after();
         };
+        auto raise = [&](float mx) {  // the running maximum, if this one passes it by far
+          const bool move = mx > m + kMoveAt<false>;
+          if (!__any_sync(0xffffffffu, move)) return;
+          const float f = move ? ex2(m - mx) : 1.f;
+          if (move) m = mx;
+          l *= f;
+          uint32_t o[32];
+          o_free();
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            tmem_get(to + k * 32, o);
+            tmem_get_wait();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+            tmem_put(to + k * 32, o);
+          }
+          tmem_put_wait();
+        };
         const bool edge = key0 + kTile > min(c, ke) || key0 < all_see;  // the same for the whole CTA
         uint8_t *vs = ring + x % kWideStages * kStage + kHalf;
         bool odd = false;
@@ -497,118 +531,144 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (warp_live || odd) {
           uint32_t w[kTile];
           tmem_get(ts, w);
-          tmem_get(ts + 32, w + 32);
-          tmem_get_wait();
-          // ---- scores ----
-          if (cap == 0.f) {
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          if (bounded && !edge) {
+            // no maximum, no bias, every key is seen: 32 keys' weights while the other 32 scores are on their way
+            tmem_get_wait();
+            tmem_get(ts + 32, w + 32);
 #pragma unroll
-            for (int k = 0; k < kTile; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * sl2);
-          } else if (!edge) {
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1) tmem_get_wait();
 #pragma unroll
-            for (int k = 0; k < kTile; k += 2) {
-              float x = __uint_as_float(w[k]), y = __uint_as_float(w[k + 1]);
-              cap_two(x, y, cap_in, cap);
-              w[k] = __float_as_uint(x);
-              w[k + 1] = __float_as_uint(y);
-            }
-          } else {  // a key that the row does not see may be a NaN: each by itself
+              for (int k = 32 * h; k < 32 * h + 32; k += 4) {
+                float x[4];
 #pragma unroll
-            for (int k = 0; k < kTile; ++k)
-              w[k] = __float_as_uint(-2.f * cap * rcp(1.f + ex2(__uint_as_float(w[k]) * cap_in)));
-          }
-          if (biased) {
-            if (!edge) {
-              const float f0 = (float)base;
+                for (int y = 0; y < 4; ++y) x[y] = __uint_as_float(w[k + y]);
+                cap_four(x, cap_in, cap);
 #pragma unroll
-              for (int k = 0; k < kTile; ++k)
-                w[k] = __float_as_uint(fmaf(slope, f0 + (float)k, __uint_as_float(w[k])));
-            } else {
-#pragma unroll
-              for (int k = 0; k < kTile; ++k) {
-                const int j = base + k;
-                const float place = (float)(j >= 0 && j < s.n ? s_place[j] : j);
-                w[k] = __float_as_uint(fmaf(slope, place, __uint_as_float(w[k])));
+                for (int y = 0; y < 4; ++y) {
+                  x[y] = ex2(x[y]);
+                  part[y] += x[y];
+                }
+                w[k / 2] = pack2<false>(x[0], x[1]);
+                w[k / 2 + 1] = pack2<false>(x[2], x[3]);
               }
             }
-          }
-          if (edge) {
-#pragma unroll
-            for (int q = 0; q < kTile / 32; ++q) {  // the row's view of 32 keys as bits
-              const int b0 = base + 32 * q, first = reach + 1 - b0;
-              const uint32_t old = b0 >= 0 ? 0u : b0 <= -32 ? ~0u : (1u << -b0) - 1u;
-              const uint32_t near = first <= 0 ? ~0u : first >= 32 ? 0u : ~0u << first;
-              const uint32_t fresh = b0 >= 0 ? (b0 < 64 ? (uint32_t)(mask >> b0) : 0u) : (b0 > -32 ? (uint32_t)mask << -b0 : 0u);
-              const uint32_t seen = (old & near) | fresh;
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((seen >> k) & 1u)) w[q * 32 + k] = 0xff800000u;  // -inf
-            }
-          }
-          // ---- the running maximum ----
-          if (!bounded) {
+            l += (part[0] + part[1]) + (part[2] + part[3]);
+          } else if (plain && !edge) {  // scores as they are, times a factor that keeps their order
+            tmem_get(ts + 32, w + 32);
+            tmem_get_wait();
             float mx = kNone;
 #pragma unroll
             for (int k = 0; k < kTile; ++k) mx = fmaxf(mx, __uint_as_float(w[k]));
-            const bool move = mx > m + kMoveAt<false>;
-            if (__any_sync(0xffffffffu, move)) {
-              const float f = move ? ex2(m - mx) : 1.f;
-              if (move) m = mx;
-              l *= f;
-              uint32_t o[32];
+            raise(mx * sl2);
+#pragma unroll
+            for (int k = 0; k < kTile; k += 2) {
+              const float x = ex2(fmaf(__uint_as_float(w[k]), sl2, -m)), y = ex2(fmaf(__uint_as_float(w[k + 1]), sl2, -m));
+              part[k & 2] += x;
+              part[(k & 2) + 1] += y;
+              w[k / 2] = pack2<false>(x, y);
+            }
+            l += (part[0] + part[1]) + (part[2] + part[3]);
+          } else {
+            tmem_get(ts + 32, w + 32);
+            tmem_get_wait();
+            // ---- scores ----
+            if (cap == 0.f) {
+#pragma unroll
+              for (int k = 0; k < kTile; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * sl2);
+            } else if (!edge) {
+#pragma unroll
+              for (int k = 0; k < kTile; k += 4) {
+                float x[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) x[y] = __uint_as_float(w[k + y]);
+                cap_four(x, cap_in, cap);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) w[k + y] = __float_as_uint(x[y]);
+              }
+            } else {  // a key that the row does not see may be a NaN: each by itself
+#pragma unroll
+              for (int k = 0; k < kTile; ++k)
+                w[k] = __float_as_uint(-2.f * cap * rcp(1.f + ex2(__uint_as_float(w[k]) * cap_in)));
+            }
+            if (biased) {
+              if (!edge) {
+                const float f0 = (float)base;
+#pragma unroll
+                for (int k = 0; k < kTile; ++k)
+                  w[k] = __float_as_uint(fmaf(slope, f0 + (float)k, __uint_as_float(w[k])));
+              } else {
+#pragma unroll
+                for (int k = 0; k < kTile; ++k) {
+                  const int j = base + k;
+                  const float place = (float)(j >= 0 && j < s.n ? s_place[j] : j);
+                  w[k] = __float_as_uint(fmaf(slope, place, __uint_as_float(w[k])));
+                }
+              }
+            }
+            if (edge) {
+#pragma unroll
+              for (int q = 0; q < kTile / 32; ++q) {  // the row's view of 32 keys as bits
+                const int b0 = base + 32 * q, first = reach + 1 - b0;
+                const uint32_t old = b0 >= 0 ? 0u : b0 <= -32 ? ~0u : (1u << -b0) - 1u;
+                const uint32_t near = first <= 0 ? ~0u : first >= 32 ? 0u : ~0u << first;
+                const uint32_t fresh = b0 >= 0 ? (b0 < 64 ? (uint32_t)(mask >> b0) : 0u) : (b0 > -32 ? (uint32_t)mask << -b0 : 0u);
+                const uint32_t seen = (old & near) | fresh;
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!((seen >> k) & 1u)) w[q * 32 + k] = 0xff800000u;  // -inf
+              }
+            }
+            // ---- the running maximum ----
+            if (!bounded) {
+              float mx = kNone;
+#pragma unroll
+              for (int k = 0; k < kTile; ++k) mx = fmaxf(mx, __uint_as_float(w[k]));
+              raise(mx);
+            }
+            // ---- P ----
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) {
+              const float e = ex2(__uint_as_float(w[k]) - m);
+              part[k & 3] += e;
+              w[k] = __float_as_uint(e);
+            }
+            l += (part[0] + part[1]) + (part[2] + part[3]);
+            if (odd) {
+              // infinities and NaN, for the rows that see their keys; then out of the tile
+              float weight[kTile];
               o_free();
+#pragma unroll
+              for (int k = 0; k < kTile; ++k) weight[k] = __uint_as_float(w[k]);
 #pragma unroll 1
               for (int k = 0; k < 4; ++k) {
+                uint32_t o[32];
                 tmem_get(to + k * 32, o);
                 tmem_get_wait();
+#pragma unroll 1
+                for (int key = 0; key < kTile; ++key) {
+                  const float e = *(volatile float *)&weight[key];
+                  if (!(e > 0.f)) continue;
 #pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                  for (int y = 0; y < 4; ++y) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(vs + chunk_at(key, k * 4 + y));
+                    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) {
+                      const uint32_t v = (word[z >> 1] >> (16 * (z & 1))) & 0xffffu;
+                      if ((v & 0x7f80u) == 0x7f80u)
+                        o[y * 8 + z] = __float_as_uint(__uint_as_float(o[y * 8 + z]) + e * __uint_as_float(v << 16));
+                    }
+                  }
+                }
                 tmem_put(to + k * 32, o);
               }
               tmem_put_wait();
             }
+#pragma unroll
+            for (int k = 0; k < kTile / 2; ++k) w[k] = pack2<false>(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
           }
-          // ---- P ----
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < kTile; ++k) {
-            const float e = ex2(__uint_as_float(w[k]) - m);
-            part[k & 3] += e;
-            w[k] = __float_as_uint(e);
-          }
-          l += (part[0] + part[1]) + (part[2] + part[3]);
-          if (odd) {
-            // infinities and NaN, for the rows that see their keys; then out of the tile
-            float weight[kTile];
-            o_free();
-#pragma unroll
-            for (int k = 0; k < kTile; ++k) weight[k] = __uint_as_float(w[k]);
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              uint32_t o[32];
-              tmem_get(to + k * 32, o);
-              tmem_get_wait();
-#pragma unroll 1
-              for (int key = 0; key < kTile; ++key) {
-                const float e = *(volatile float *)&weight[key];
-                if (!(e > 0.f)) continue;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const uint4 u = *reinterpret_cast<const uint4 *>(vs + chunk_at(key, k * 4 + y));
-                  const uint32_t word[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                  for (int z = 0; z < 8; ++z) {
-                    const uint32_t v = (word[z >> 1] >> (16 * (z & 1))) & 0xffffu;
-                    if ((v & 0x7f80u) == 0x7f80u)
-                      o[y * 8 + z] = __float_as_uint(__uint_as_float(o[y * 8 + z]) + e * __uint_as_float(v << 16));
-                  }
-                }
-              }
-              tmem_put(to + k * 32, o);
-            }
-            tmem_put_wait();
-          }
-#pragma unroll
-          for (int k = 0; k < kTile / 2; ++k) w[k] = pack2<false>(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
           tmem_put(ts, w);
           tmem_put_wait();
         }
