@@ -884,7 +884,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 }
 
 // Merges the partials of every unit that two or more CTAs shared: o = sum_p 2^lse_p o_p / sum_p 2^lse_p,
-// in the order of the CTAs. A thread takes 8 values of a row, four pieces' loads in flight.
+// in the order of the CTAs. A thread takes 8 values of a row, the loads of four pieces in flight, or of eight
+// where a unit has 8 rows at most: those may be cut into many (one sequence of 32K tokens 41 -> 36 us), while
+// wider ones mostly have two or three (32 x 6 rows 61 -> 63 us with eight).
 template <class C>
 __global__ void __launch_bounds__(512) attn_scored_combine(const Params P) {
   grid_dependents_launch();
@@ -901,7 +903,7 @@ __global__ void __launch_bounds__(512) attn_scored_combine(const Params P) {
   if (c0 == c1) return;  // one CTA held the whole unit and wrote its rows
   // the unit is CTA c0's first piece only if its range starts within the unit's lead-in
   const int slot0 = range_start(c0, W, P.ctas) >= T0 - P.alpha ? 0 : 1;
-  constexpr int kPc = 4;
+  constexpr int kPc = C::RB <= 8 ? 8 : 4;
   const int rows = min(C::RB, P.G * s.n - rb * C::RB);
   for (int x = threadIdx.x; x < rows * (D / 8); x += blockDim.x) {
     const int rl = x / (D / 8), d8 = (x % (D / 8)) * 8;
@@ -914,7 +916,7 @@ __global__ void __launch_bounds__(512) attn_scored_combine(const Params P) {
 #pragma unroll
       for (int k = 0; k < kPc; ++k) {
         // a CTA whose range is empty (more CTAs than positions) holds nothing
-        const bool in = cb + k <= c1 && range_start(cb + k, W, P.ctas) < range_start(cb + k + 1, W, P.ctas);
+        const bool in = cb + k <= c1 && (W >= P.ctas || range_start(cb + k, W, P.ctas) < range_start(cb + k + 1, W, P.ctas));
         const int cc = in ? cb + k : c0;
         const size_t at = ((size_t)cc * 2 + (cc == c0 ? slot0 : 0)) * P.rows_cap + rl;
         lse[k] = in ? __ldcg(P.part_lse + at) : -INFINITY;
