@@ -16,11 +16,18 @@
 //  * 5 to 16: a warp keeps 4;
 //  * 4 and fewer: the four warps share the rows: each takes a quarter of the head's values in the scores
 //    (summed through shared memory) and of the columns in the weighted sum. The softmax is computed four times.
-// Bound: shared-memory reads (one to four rows' products each) and, for short splits, latency.
+// Up to eight splits of a sequence are one thread-block cluster, whose CTAs merge their rows through shared
+// memory; more leave partials in the workspace for a second kernel.
+//
+// Bound: shared-memory reads (8 + 4 wavefronts to 32 FMAs of a warp in the scores), and latency for short
+// splits. fp32, us: 4 sequences of 37 to 200 tokens, 5 rows, two heads of 64 values 12; 8 sequences of 1K to 2K
+// tokens, eight heads of 128 values: 4, 16 and 64 rows a KV head 45, 65, 275 (without asynchronous copies, four
+// rows a warp throughout: 91, 105, 357).
 // Splits that the window leaves no key in write an empty partial (log-sum-exp -inf). A visible
 // NaN makes its row's sum and log-sum-exp NaN, and the merge of the splits carries it on.
 #include <type_traits>
 
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -28,6 +35,8 @@
 
 namespace sv {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kThreads = 128;
 constexpr int kKeys = 32;         // keys per shared-memory tile
@@ -54,10 +63,7 @@ template <int LATER /* groups that may still be on their way */>
 __device__ __forceinline__ void copies_landed() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
 }
-// 16 bytes of a row as fp32 into shared memory
-__device__ __forceinline__ void widen16(float *dst, uint4 w, float, const float *) {
-  *reinterpret_cast<uint4 *>(dst) = w;
-}
+// 16 bytes of a narrow row as fp32 into shared memory
 __device__ __forceinline__ void widen16(float *dst, uint4 w, float, const __nv_bfloat16 *) {
   reinterpret_cast<float4 *>(dst)[0] = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                                                    __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
@@ -89,6 +95,7 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
   __shared__ __align__(16) float k_s[kKeys][D + 4];
   __shared__ __align__(16) float v_s[kKeys][D];
   __shared__ __align__(16) float p_s[RW * kWarps][kKeys];
+  __shared__ float lse_s[kRows];
   __shared__ float part_s[SHARED ? kWarps : 1][RW][kKeys];  // a quarter's part of the scores
   __shared__ int s_bad;
 
@@ -107,7 +114,8 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
   }
   const int L = (int)L64;
   const int nsplit = (L + a.chunk - 1) / a.chunk;
-  if (split >= nsplit) return;
+  const bool merge_here = sa.cluster && nsplit > 1;  // the same for the whole cluster
+  if (split >= nsplit && !merge_here) return;
   // no row is before position c, so no row sees a key before c - window + 1
   const int first = sa.window > 0 ? max(0, c - sa.window + 1) : 0;
   const int kb = max(split * a.chunk, first / kKeys * kKeys), ke = min(L, (split + 1) * a.chunk);
@@ -279,6 +287,9 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
       }
     }
     copies_landed<0>();
+    float(*o_s)[D] = v_s;  // this split's rows, when every warp is done with the values
+    static_assert(kRows <= kKeys, "the rows take the values' place");
+    if (merge_here) __syncthreads();
     // write this pass's rows
 #pragma unroll
     for (int w = 0; w < RW; ++w) {
@@ -287,15 +298,38 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
       const int i = r / G, g = r % G, h = kvh * G + g;
       const size_t qrow = (size_t)(row0 + i) * a.num_q_heads + h;
       const float inv = l[w] == 0.f ? 0.f : 1.f / l[w];  // a row that sees no key gets zeros
+      const float lse = l[w] == 0.f ? -INFINITY : m[w] + log2f(l[w]);
       const size_t prow = (size_t)split * a.total_q * a.num_q_heads + qrow;
 #pragma unroll
       for (int k = 0; k < kCols; ++k) {
         const int d = lane + 32 * (SHARED ? warp + kWarps * k : k);
         if (SHARED && d >= D) continue;
         if (nsplit == 1) reinterpret_cast<T *>(a.out)[qrow * D + d] = from_f32<T>(acc[w][k] * inv);
+        else if (merge_here) o_s[rw + w][d] = acc[w][k] * inv;
         else a.ws_o[prow * D + d] = acc[w][k] * inv;
       }
-      if (nsplit > 1 && lane == 0 && (!SHARED || warp == 0)) a.ws_lse[prow] = l[w] == 0.f ? -INFINITY : m[w] + log2f(l[w]);
+      if (nsplit > 1 && lane == 0 && (!SHARED || warp == 0)) *(merge_here ? &lse_s[rw + w] : &a.ws_lse[prow]) = lse;
+    }
+    if (merge_here) {  // a row to a warp of the cluster, from every CTA's shared memory
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      for (int x = split * kWarps + warp; x < min(kRows, R - rg); x += gridDim.x * kWarps) {
+        const float lse = lane < nsplit ? *cluster.map_shared_rank(&lse_s[x], lane) : -INFINITY;
+        const float M = warp_max(lse), wt = exp2f(lse - (M == -INFINITY ? 0.f : M)), den = warp_sum(wt);
+        float num[NK];
+#pragma unroll
+        for (int k = 0; k < NK; ++k) num[k] = 0.f;
+        for (int y = 0; y < nsplit; ++y) {
+          const float *o = cluster.map_shared_rank(&o_s[x][0], y), wy = __shfl_sync(0xffffffffu, wt, y);
+#pragma unroll
+          for (int k = 0; k < NK; ++k) num[k] = fmaf(wy, o[lane + 32 * k], num[k]);
+        }
+        const int r = rg + x, i = r / G, h = kvh * G + r % G;
+        T *op = reinterpret_cast<T *>(a.out) + ((size_t)(row0 + i) * a.num_q_heads + h) * D + lane;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) op[32 * k] = from_f32<T>(den == 0.f ? 0.f : num[k] / den);
+      }
+      cluster.sync();  // the others' rows have been read
     }
   }
   __syncthreads();
@@ -348,7 +382,21 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_combine(ScoredArgs 
 template <typename T, typename KT, int NK>
 cudaError_t launch_n(const ScoredArgs &sa, cudaStream_t st) {
   const dim3 grid(sa.a.max_splits, sa.a.kv.num_kv_heads, sa.a.kv.batch);
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kThreads), 0, st, sa); };
+  auto go = [&](auto kernel) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)sa.a.max_splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = sa.cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, sa);
+  };
   const long long rows = (long long)(sa.a.num_q_heads / sa.a.kv.num_kv_heads) * sa.a.max_q;
   if (rows <= 4) return go(attn_scored_simt_kernel<T, KT, NK, 4, true>);
   if (rows <= 16 || sizeof(KT) < 4) return go(attn_scored_simt_kernel<T, KT, NK, 4, false>);
@@ -374,7 +422,7 @@ cudaError_t launch_attn_scored_simt(const ScoredArgs &sa, int dtype, cudaStream_
   cudaError_t e;
   if (dtype == SV_DTYPE_E4M3) e = launch_t<__nv_bfloat16, uint8_t>(sa, st);  // bf16 queries and outputs
   else e = dtype == SV_DTYPE_BF16 ? launch_t<__nv_bfloat16, __nv_bfloat16>(sa, st) : launch_t<float, float>(sa, st);
-  if (e != cudaSuccess || sa.a.max_splits <= 1) return e;
+  if (e != cudaSuccess || sa.a.max_splits <= 1 || sa.cluster) return e;
   const dim3 grid((unsigned)ceil_div(sa.a.max_q * sa.a.num_q_heads, kThreads / 32), (unsigned)sa.a.kv.batch);
   return dtype == SV_DTYPE_F32 ? launch_pdl(attn_scored_simt_combine<float>, grid, dim3(kThreads), 0, st, sa)
                                : launch_pdl(attn_scored_simt_combine<__nv_bfloat16>, grid, dim3(kThreads), 0, st, sa);

@@ -56,6 +56,7 @@ namespace {
 constexpr int kMaxQ = 64;
 constexpr int kGranule = 64;
 constexpr int kScoredGranule = 32;  // one tile of the CUDA-core kernel: short caches are all latency
+constexpr int kScoredCluster = 8;   // its splits that fit a portable cluster
 constexpr float kLog2e = 1.4426950408889634f;
 int g_attn_path = SV_ATTN_AUTO;
 unsigned long long g_wait_ns = kDefaultWaitNs;  // budget of the kernels' pipeline waits
@@ -97,12 +98,20 @@ bool keys_usable(const sv_paged_kv *kv, int32_t num_q_heads, int32_t max_q, int3
 }
 
 // Split-KV partials of the kernels that take one CTA per key split.
-size_t split_workspace(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q, int32_t max_seq_len,
-                       int granule = kGranule) {
-  const SplitPlan p = plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, granule);
+size_t split_workspace(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q, const SplitPlan &p) {
   if (p.max_splits <= 1) return 0;
   const size_t rows = (size_t)p.max_splits * total_q * num_q_heads;
   return rows * (size_t)kv->head_dim * sizeof(float) + rows * sizeof(float) + 256;
+}
+size_t split_workspace(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q, int32_t max_seq_len) {
+  return split_workspace(kv, num_q_heads, total_q, plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kGranule));
+}
+
+// Splits of sv_spec_verify_attn_scored's CUDA-core kernel. Up to kScoredCluster of them merge without a second
+// kernel (4 sequences of up to 205 tokens 14.4 -> 12.3 us); cutting twice as many to that number instead, of two
+// tiles each, gains nothing (16.4 us both ways for up to 485 tokens).
+SplitPlan scored_splits(const sv_paged_kv *kv, int32_t max_seq_len) {
+  return plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kScoredGranule);
 }
 
 // Checks a head transform and puts it into the kernels' arguments.
@@ -357,7 +366,10 @@ size_t sv_spec_verify_attn_scored_workspace_bytes(const sv_paged_kv *kv, int32_t
   sa.a.num_q_heads = num_q_heads;
   sa.a.max_q = max_q_per_seq;
   sa.a.max_seq_len = max_seq_len;
-  if (!attn_scored_mma_fits(sa)) return split_workspace(kv, num_q_heads, total_q, max_seq_len, kScoredGranule);
+  if (!attn_scored_mma_fits(sa)) {
+    const SplitPlan p = scored_splits(kv, max_seq_len);
+    return p.max_splits <= kScoredCluster ? 0 : split_workspace(kv, num_q_heads, total_q, p);
+  }
   size_t need = 0;
   launch_attn_scored_mma(sa, nullptr, &need, nullptr, false);
   return need;
@@ -383,7 +395,7 @@ sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void 
       sv_spec_verify_attn_scored_workspace_bytes(kv, num_q_heads, total_q, max_q_per_seq, max_seq_len);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || ((uintptr_t)workspace & 255u) != 0))
     return SV_ERR_WORKSPACE;
-  const SplitPlan p = plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kScoredGranule);
+  const SplitPlan p = scored_splits(kv, max_seq_len);
   const size_t rows = (size_t)p.max_splits * total_q * num_q_heads;
   ScoredArgs sa;
   AttnArgs &a = sa.a;
@@ -392,8 +404,10 @@ sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void 
   a.out = out;
   a.cu_q = cu_q;
   a.tree_mask = tree_mask;
-  a.ws_o = p.max_splits > 1 ? (float *)workspace : nullptr;
-  a.ws_lse = p.max_splits > 1 ? (float *)workspace + rows * (size_t)kv->head_dim : nullptr;
+  sa.cluster = p.max_splits > 1 && p.max_splits <= kScoredCluster;
+  const bool parts = p.max_splits > 1 && !sa.cluster;
+  a.ws_o = parts ? (float *)workspace : nullptr;
+  a.ws_lse = parts ? (float *)workspace + rows * (size_t)kv->head_dim : nullptr;
   a.status = status_dev;
   a.num_q_heads = num_q_heads;
   a.total_q = total_q;

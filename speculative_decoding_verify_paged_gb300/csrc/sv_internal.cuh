@@ -174,6 +174,7 @@ struct AttnArgs {
 struct ScoredArgs {
   AttnArgs a;
   float cap;                 // softcap * log2(e); 0: none
+  bool cluster;              // CUDA cores: the splits of a sequence are a cluster and merge there
   int window;                // keys at a distance >= window are not visible; 0: no limit
   const float *slopes;       // [num_q_heads] or null
   const int32_t *positions;  // [total_q] or null: c_b + i
