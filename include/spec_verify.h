@@ -345,7 +345,9 @@ typedef struct sv_score_mod {
  *              contents need no initialisation. Calls that may overlap on the
  *              GPU need workspaces of their own
  * The other arguments, types, sizes and errors are those of
- * sv_spec_verify_attn. SV_OPT_ATTN_PATH has no say here.
+ * sv_spec_verify_attn; max_seq_len above 2^30 and more than 65535 sequences
+ * are SV_ERR_UNSUPPORTED.
+ * SV_OPT_ATTN_PATH has no say here.
  */
 size_t sv_spec_verify_attn_scored_workspace_bytes(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q,
                                                   int32_t max_q_per_seq, int32_t max_seq_len);
@@ -603,9 +605,8 @@ sv_status sv_adaptive_k_current(const void *state, int32_t *k);
  *     fail, hence the 1 ms floor.
  *   SV_OPT_STALL_FOR_TEST (SV_STALL_NONE, the default; SV_STALL_ATTENTION;
  *     SV_STALL_SAMPLER): for tests of the failure path only. The producer warp
- *     of the tensor-core attention kernel (every warp of
- *     sv_spec_verify_attn_scored's), or of the sampler's statistics
- *     kernel, first waits on a barrier that nothing ever completes, as a
+ *     of the tensor-core attention kernels (sv_spec_verify_attn_scored's
+ *     too), or of the sampler's statistics kernel, first waits on a barrier that nothing ever completes, as a
  *     producer whose data never arrives would; that wait runs out after the
  *     wait budget, the producer issues nothing, and every pipeline wait of its
  *     consumers runs out in turn. The call then records SV_ERR_TIMEOUT and its

@@ -56,6 +56,7 @@ namespace {
 constexpr int kMaxQ = 64;
 constexpr int kGranule = 64;
 constexpr int kScoredGranule = 32;  // one tile of the CUDA-core kernel: short caches are all latency
+constexpr int kScoredTokens = 1 << 30;  // places relative to a sequence's length stay within 31 bits
 constexpr int kScoredCluster = 8;   // its splits that fit a portable cluster
 constexpr float kLog2e = 1.4426950408889634f;
 int g_attn_path = SV_ATTN_AUTO;
@@ -358,7 +359,7 @@ sv_status sv_kv_append_rope(const sv_paged_kv *kv, const sv_head_transform *tran
 size_t sv_spec_verify_attn_scored_workspace_bytes(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q,
                                                   int32_t max_q_per_seq, int32_t max_seq_len) {
   if (kv == nullptr || num_q_heads <= 0 || kv->num_kv_heads <= 0 || num_q_heads % kv->num_kv_heads != 0 ||
-      total_q < 0 || max_q_per_seq < 1 || max_q_per_seq > kMaxQ || max_seq_len <= 0)
+      total_q < 0 || max_q_per_seq < 1 || max_q_per_seq > kMaxQ || max_seq_len <= 0 || max_seq_len > kScoredTokens)
     return 0;
   ScoredArgs sa;
   std::memset(&sa, 0, sizeof sa);
@@ -390,7 +391,7 @@ sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void 
     return SV_ERR_INVALID_ARG;
   if (kv->batch == 0 || total_q == 0) return SV_OK;
   if (q == nullptr || out == nullptr || cu_q == nullptr || !aligned16(q) || !aligned16(out)) return SV_ERR_INVALID_ARG;
-  if (kv->head_dim % 32 != 0 || kv->batch > 65535) return SV_ERR_UNSUPPORTED;
+  if (kv->head_dim % 32 != 0 || kv->batch > 65535 || max_seq_len > kScoredTokens) return SV_ERR_UNSUPPORTED;
   size_t need =
       sv_spec_verify_attn_scored_workspace_bytes(kv, num_q_heads, total_q, max_q_per_seq, max_seq_len);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || ((uintptr_t)workspace & 255u) != 0))

@@ -92,24 +92,26 @@ float real(PyObject *o) {
   return (float)x;
 }
 
-struct Held {  // an attribute, released at the end of the call
-  PyObject *o;
-  Held(PyObject *from, PyObject *name) : o(PyObject_GetAttr(from, name)) {
-    if (o == nullptr) throw TypeError("");
+struct Held {  // attributes, released at the end of the call
+  PyObject *o[24];
+  int n = 0;
+  PyObject *get(PyObject *from, PyObject *name) {
+    PyObject *x = PyObject_GetAttr(from, name);
+    if (x == nullptr) throw TypeError("");
+    return o[n++] = x;
   }
-  ~Held() { Py_DECREF(o); }
+  ~Held() {
+    while (n > 0) Py_DECREF(o[--n]);
+  }
 };
 
 PyObject *s_names[16];
 enum { kK, kV, kTable, kLens, kFree, kTop, kRef, kKScale, kVScale, kFreq, kQW, kKW, kEps, kOffset, kInter, kNames };
 
-// A PagedKV; its tensors are alive as long as the object.
-sv_paged_kv cache_of(PyObject *kv) {
+// A PagedKV, with its tensors held.
+sv_paged_kv cache_of(PyObject *kv, Held &held) {
   sv_paged_kv p = {};
-  auto field = [&](int name) -> const at::Tensor * {
-    Held h(kv, s_names[name]);
-    return tensor(h.o);
-  };
+  auto field = [&](int name) { return tensor(held.get(kv, s_names[name])); };
   const at::Tensor *k = field(kK), *v = field(kV), *table = field(kTable), *lens = field(kLens);
   if (k == nullptr || v == nullptr || table == nullptr || lens == nullptr || k->dim() != 4 || table->dim() != 2)
     value_error("a cache has pools [blocks, heads, block_size, head_dim], a block table and lengths");
@@ -128,27 +130,26 @@ sv_paged_kv cache_of(PyObject *kv) {
   p.free_top = values<int32_t>(field(kTop), at::kInt, 1, "free_top");
   p.ref_count = values<int32_t>(field(kRef), at::kInt, p.num_blocks, "ref_count");
   p.dtype = k->scalar_type() == at::kByte ? SV_DTYPE_E4M3 : row_type(*k);
-  Held ks(kv, s_names[kKScale]), vs(kv, s_names[kVScale]);
-  p.k_scale = real(ks.o);
-  p.v_scale = real(vs.o);
+  p.k_scale = real(held.get(kv, s_names[kKScale]));
+  p.v_scale = real(held.get(kv, s_names[kVScale]));
   return p;
 }
 
-// A HeadTransform for rows like `rows`.
-sv_head_transform transform_of(PyObject *t, const at::Tensor &rows) {
+// A HeadTransform for rows like `rows`, with its tensors held.
+sv_head_transform transform_of(PyObject *t, const at::Tensor &rows, Held &held) {
   sv_head_transform p = {};
-  Held freq(t, s_names[kFreq]), qw(t, s_names[kQW]), kw(t, s_names[kKW]), eps(t, s_names[kEps]), off(t, s_names[kOffset]),
-      inter(t, s_names[kInter]);
-  if (const at::Tensor *f = tensor(freq.o)) {
+  auto field = [&](int name) { return held.get(t, s_names[name]); };
+  if (const at::Tensor *f = tensor(field(kFreq))) {
     if (f->scalar_type() != at::kFloat) throw TypeError("inv_freq is float32");
     p.rotary_dim = narrow(2 * f->numel());
     p.inv_freq = p.rotary_dim > 0 ? static_cast<const float *>(contiguous(f)) : nullptr;
   }
-  p.q_weight = values<void>(tensor(qw.o), rows.scalar_type(), rows.size(2), "a norm weight");
-  p.k_weight = values<void>(tensor(kw.o), rows.scalar_type(), rows.size(2), "a norm weight");
-  p.eps = real(eps.o);
-  p.weight_offset = real(off.o);
-  p.interleaved = PyObject_IsTrue(inter.o);
+  p.q_weight = values<void>(tensor(field(kQW)), rows.scalar_type(), rows.size(2), "a norm weight");
+  p.k_weight = values<void>(tensor(field(kKW)), rows.scalar_type(), rows.size(2), "a norm weight");
+  p.eps = real(field(kEps));
+  p.weight_offset = real(field(kOffset));
+  p.interleaved = PyObject_IsTrue(field(kInter));
+  if (p.interleaved < 0) throw TypeError("");
   return p;
 }
 
@@ -193,7 +194,8 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
       if (k->size(0) != some->size(0) || k->size(2) != some->size(2) || k->scalar_type() != some->scalar_type())
         value_error("q and k have the same rows, head_dim and type");
     }
-    const sv_head_transform t = transform_of(a[0], *some);
+    Held held;
+    const sv_head_transform t = transform_of(a[0], *some, held);
     const int rows = narrow(some->size(0));
     return g_heads(&t, rq.at, rq.stride, rqo.at, rqo.stride, hq, rk.at, rk.stride, rko.at, rko.stride, hkv,
                    narrow(some->size(2)), row_type(*some), rows, values<int32_t>(tensor(a[3]), at::kInt, rows, "positions"),
@@ -204,7 +206,8 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (kv, transform, new_k, new_v, cu_q, status, q, q_out, positions, stream)
 PyObject *kv_append_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return answer(n, 10, [&] {
-    const sv_paged_kv kv = cache_of(a[0]);
+    Held held;
+    const sv_paged_kv kv = cache_of(a[0], held);
     const at::Tensor &k = needed(a[2], "new_k");
     const Rows rk = rows_of(k, nullptr), rv = rows_of(needed(a[3], "new_v"), &k);
     const int want = kv.dtype == SV_DTYPE_F32 ? SV_DTYPE_F32 : SV_DTYPE_BF16;
@@ -220,7 +223,7 @@ PyObject *kv_append_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
       rqo = rows_of(needed(a[7], "q_out"), q);
       hq = narrow(q->size(1));
     }
-    const sv_head_transform t = transform_of(a[1], k);
+    const sv_head_transform t = transform_of(a[1], k, held);
     return g_append(&kv, &t, rk.at, rk.stride, rv.at, rv.stride, rq.at, rq.stride, rqo.at, rqo.stride, hq,
                     values<int32_t>(tensor(a[4]), at::kInt, (int64_t)kv.batch + 1, "cu_q"), rows,
                     values<int32_t>(tensor(a[8]), at::kInt, rows, "positions"),
@@ -232,7 +235,8 @@ PyObject *kv_append_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // stream); without a workspace one is taken here, from the current stream's allocator
 PyObject *spec_verify_attn_scored(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return answer(n, 16, [&] {
-    const sv_paged_kv kv = cache_of(a[0]);
+    Held held;
+    const sv_paged_kv kv = cache_of(a[0], held);
     const at::Tensor &q = needed(a[1], "q"), &out = needed(a[2], "out");
     const int want = kv.dtype == SV_DTYPE_F32 ? SV_DTYPE_F32 : SV_DTYPE_BF16;
     if (q.dim() != 3 || row_type(q) != want || q.size(2) != kv.head_dim || out.sizes() != q.sizes() ||

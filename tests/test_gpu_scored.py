@@ -109,6 +109,7 @@ SMALL = {
     "bf16-d256": (16, [290, 31], [2, 4], 8, 2, 256, 32, "bf16"),
     "bf16-d96": (17, [130, 31], [2, 4], 6, 2, 96, 8, "bf16"),
     "bf16-wide": (18, [200, 90], [64, 33], 8, 1, 128, 64, "bf16"),
+    "bf16-wide-bs256": (50, [700, 255], [40, 64], 8, 2, 128, 256, "bf16"),
     "bf16-one-block": (29, [300, 129], [26, 25], 8, 2, 128, 16, "bf16"),
     "bf16-two-blocks-ragged": (30, [1000, 5, 127, 128], [33, 64, 1, 40], 16, 4, 128, 32, "bf16"),
     "bf16-d256-wide": (19, [150], [30], 8, 1, 256, 16, "bf16"),

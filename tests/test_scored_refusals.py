@@ -78,6 +78,8 @@ def test_attention(lib):
                 dict(mask=1), dict(q=None), dict(q=264), dict(cu=None)):
         assert attend(lib, cache(), mod(), **bad) == INVALID, bad
     assert attend(lib, cache(head_dim=40), mod()) == UNSUPPORTED
+    assert attend(lib, cache(), mod(), max_len=(1 << 30) + 1) == UNSUPPORTED
+    assert attend(lib, cache(batch=65536), mod()) == UNSUPPORTED
 
 
 def test_workspace(lib):
@@ -87,5 +89,5 @@ def test_workspace(lib):
     assert attend(lib, kv, L.sv_score_mod(), rows=8, max_len=10000) == WORKSPACE
     assert attend(lib, kv, L.sv_score_mod(), rows=8, max_len=10000, ws=256, wb=need - 1) == WORKSPACE
     assert attend(lib, kv, L.sv_score_mod(), rows=8, max_len=10000, ws=264, wb=need) == WORKSPACE
-    for bad in ((3, 8, 4, 64), (4, -1, 4, 64), (4, 8, 0, 64), (4, 8, 65, 64), (4, 8, 4, 0)):
+    for bad in ((3, 8, 4, 64), (4, -1, 4, 64), (4, 8, 0, 64), (4, 8, 65, 64), (4, 8, 4, 0), (4, 8, 4, (1 << 30) + 1)):
         assert lib.sv_spec_verify_attn_scored_workspace_bytes(ctypes.byref(kv), *bad) == 0
