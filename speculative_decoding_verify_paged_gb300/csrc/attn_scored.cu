@@ -33,11 +33,11 @@ bool attn_scored_mma_fits(const ScoredArgs &sa) {
   const KV &kv = sa.a.kv;
   if (kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return false;
   if (kv.block_size < 8 || (long long)kv.num_blocks * kv.num_kv_heads * kv.block_size >= (1LL << 31)) return false;
-  // positions of the work order (at most two tiles and a few lead-in positions more per unit of 64
-  // rows) and the combine's grid stay in range
+  // positions of the work order (at most two tiles and a few lead-in positions more per unit of 64 rows) stay
+  // in range
   const long long rows = (long long)(sa.a.num_q_heads / kv.num_kv_heads) * sa.a.max_q;
   const long long units = (long long)kv.batch * kv.num_kv_heads * ((rows + 63) / 64);
-  return units * (sa.a.max_seq_len / 64 + 8) < (1LL << 30) && kv.num_kv_heads * ((rows + 63) / 64) <= 65535;
+  return units * (sa.a.max_seq_len / 64 + 8) < (1LL << 30);
 }
 
 cudaError_t launch_attn_scored_mma(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {

@@ -83,7 +83,7 @@ struct Params {
   ScoredArgs s;
   float cap_in;  // what a product is multiplied with to give 2 y log2(e)
   int G;         // query heads per KV head
-  int ctas, alpha, rows_cap, rb_max;
+  int ctas, alpha, rows_cap;
   int box;       // rows of a TMA box: min(block_size, TK)
   float *part_o;    // [ctas][2][rows_cap][D]
   float *part_lse;  // [ctas][2][rows_cap], log2
@@ -884,28 +884,56 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 }
 
 // Merges the partials of every unit that two or more CTAs shared: o = sum_p 2^lse_p o_p / sum_p 2^lse_p,
-// in the order of the CTAs. A thread takes 8 values of a row, the loads of four pieces in flight, or of eight
-// where a unit has 8 rows at most: those may be cut into many (one sequence of 32K tokens 41 -> 36 us), while
-// wider ones mostly have two or three (32 x 6 rows 61 -> 63 us with eight).
-template <class C>
-__global__ void __launch_bounds__(512) attn_scored_combine(const Params P) {
+// in the order of the CTAs. A thread takes 8 values of a row, the loads of four pieces in flight, or of eight where
+// a unit has 8 rows at most: those may be cut into many (one sequence of 32K tokens 41 -> 36 us), while wider
+// ones mostly have two or three (32 x 6 rows 61 -> 63 us with eight).
+// CTA (x, y) has kMergeThreads items of unit x, or (BORDERS) of the unit on the border between the ranges of CTAs x
+// and x + 1, if that is its first. Launches with more units than CTAs go by borders, most units being whole
+// (128 x 5 rows over 600 tokens 95.4 -> 93.8 us); for the others finding a border's unit costs more (32 x 6 rows
+// 60.9 -> 62.7).
+constexpr int kMergeThreads = 256;
+template <class C, bool BORDERS>
+__global__ void __launch_bounds__(kMergeThreads) attn_scored_combine(const Params P) {
   grid_dependents_launch();
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   constexpr int D = C::D;
   const AttnArgs &a = P.s.a;
-  const int b = blockIdx.x, kvh = blockIdx.y / P.rb_max, rb = blockIdx.y % P.rb_max;
-  const int W = P.prefix[a.kv.batch], base = P.prefix[b];
+  const int B = a.kv.batch, W = P.prefix[B];
+  int b, of_seq = 0, border = 0;  // the unit's sequence, and its place in it or the border
+  if (BORDERS) {
+    if (W <= 0) return;
+    border = range_start(blockIdx.x + 1, W, P.ctas);
+    if (border >= W) return;
+    const int lane = threadIdx.x & 31;
+    b = 0;  // the last sequence that begins there or before
+    for (int len = B; len > 1;) {
+      const int step = (len + 31) >> 5;
+      const bool below = lane * step < len && P.prefix[b + lane * step] <= border;
+      const int k = max(0, __popc(__ballot_sync(0xffffffffu, below)) - 1);
+      b += k * step;
+      len = min(step, len - k * step);
+    }
+  } else {
+    b = blockIdx.x % B;
+    of_seq = blockIdx.x / B;
+  }
   bool bad;
+  const int base = P.prefix[b];
   const Seq s = load_seq(P, b, C::TK, C::RB, &bad);
-  if (s.tiles <= 0 || rb >= s.rbs) return;
-  const int T0 = base + (kvh * s.rbs + rb) * (s.tiles + P.alpha) + P.alpha, T1 = T0 + s.tiles;
+  if (s.tiles <= 0) return;
+  const int U = s.tiles + P.alpha, unit = BORDERS ? (border - base) / U : of_seq;
+  if (!BORDERS && unit >= a.kv.num_kv_heads * s.rbs) return;
+  const int kvh = unit / s.rbs, rb = unit - kvh * s.rbs;
+  const int T0 = base + unit * U + P.alpha, T1 = T0 + s.tiles;
   const int c0 = range_owner(T0, W, P.ctas), c1 = range_owner(T1 - 1, W, P.ctas);
-  if (c0 == c1) return;  // one CTA held the whole unit and wrote its rows
+  // one CTA held the whole unit and wrote its rows, or another border of it comes first
+  if (c0 == c1 || (BORDERS && c0 != (int)blockIdx.x)) return;
   // the unit is CTA c0's first piece only if its range starts within the unit's lead-in
   const int slot0 = range_start(c0, W, P.ctas) >= T0 - P.alpha ? 0 : 1;
   constexpr int kPc = C::RB <= 8 ? 8 : 4;
   const int rows = min(C::RB, P.G * s.n - rb * C::RB);
-  for (int x = threadIdx.x; x < rows * (D / 8); x += blockDim.x) {
+  const int x = blockIdx.y * kMergeThreads + threadIdx.x;
+  if (x < rows * (D / 8)) {
     const int rl = x / (D / 8), d8 = (x % (D / 8)) * 8;
     float M = -INFINITY, den = 0.f, acc[8];
 #pragma unroll
@@ -952,15 +980,17 @@ __global__ void __launch_bounds__(512) attn_scored_combine(const Params P) {
 }
 
 struct Layout {
-  int ctas, rows_cap, rb_max;
+  int ctas, rows_cap;
+  long long units;  // if every sequence has max_q rows
   size_t lse_offset, prefix_offset, bytes;
 };
 
 template <class C>
 Layout layout_of(const KV &kv, int G, int max_q, int max_seq_len) {
   Layout l;
-  l.rb_max = (G * max_q + C::RB - 1) / C::RB;
-  const long long tiles = (long long)kv.batch * kv.num_kv_heads * l.rb_max * ((max_seq_len + C::TK - 1) / C::TK);
+  const int blocks = (G * max_q + C::RB - 1) / C::RB;
+  l.units = (long long)kv.batch * kv.num_kv_heads * blocks;
+  const long long tiles = l.units * ((max_seq_len + C::TK - 1) / C::TK);
   l.ctas = (int)std::max(1LL, std::min<long long>((long long)C::kCtasPerSm * num_sms(), tiles));
   l.rows_cap = std::min(C::RB, G * max_q);
   const size_t slots = (size_t)l.ctas * 2 * l.rows_cap;
@@ -1006,7 +1036,6 @@ Layout plan(const ScoredArgs &sa, void *workspace, size_t *bytes, Params *p) {
   p->ctas = l.ctas;
   p->alpha = kAlpha;
   p->rows_cap = l.rows_cap;
-  p->rb_max = l.rb_max;
   p->box = std::min(kv.block_size, C::TK);
   p->part_o = reinterpret_cast<float *>(workspace);
   p->part_lse = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + l.lse_offset);
@@ -1015,9 +1044,10 @@ Layout plan(const ScoredArgs &sa, void *workspace, size_t *bytes, Params *p) {
 }
 
 template <class C> cudaError_t launch_combine(const Params &p, const Layout &l, cudaStream_t st) {
-  const KV &kv = p.s.a.kv;
-  const int items = std::min(512, (l.rows_cap * (C::D / 8) + 31) / 32 * 32);  // threads: one item each, if they fit
-  return launch_pdl(attn_scored_combine<C>, dim3(kv.batch, kv.num_kv_heads * p.rb_max), dim3(items), 0, st, p);
+  if (l.ctas <= 1) return cudaSuccess;  // no borders
+  const unsigned y = (l.rows_cap * (C::D / 8) + kMergeThreads - 1) / kMergeThreads;
+  if (l.units > l.ctas) return launch_pdl(attn_scored_combine<C, true>, dim3(l.ctas - 1, y), dim3(kMergeThreads), 0, st, p);
+  return launch_pdl(attn_scored_combine<C, false>, dim3((unsigned)l.units, y), dim3(kMergeThreads), 0, st, p);
 }
 
 // Launches (`go`) or sizes one instance.
