@@ -37,7 +37,7 @@ bool attn_scored_mma_fits(const ScoredArgs &sa) {
   // in range
   const long long rows = (long long)(sa.a.num_q_heads / kv.num_kv_heads) * sa.a.max_q;
   const long long units = (long long)kv.batch * kv.num_kv_heads * ((rows + 63) / 64);
-  return units * (sa.a.max_seq_len / 64 + 8) < (1LL << 30);
+  return units * (sa.a.max_seq_len / 64 + 16) < (1LL << 30);
 }
 
 cudaError_t launch_attn_scored_mma(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {

@@ -98,6 +98,9 @@ struct Cfg {
   static constexpr int kConsumers = 4, kThreads = 256, kCtasPerSm = 2;
   static_assert(WK * WR == kConsumers, "a consumer on each quarter of the SM");
   static constexpr int ROWB = D * (F8 ? 1 : 2);  // bytes of a key's row
+  // Positions of a unit's lead-in. 24 rows a warp: 5 against 4 90 and 94 us (128 units a window), 60.4 and 61.6 (32 x 6
+  // rows), 7 gains nothing more; fewer rows: one token of 32 sequences 69.4 and 68.5 us.
+  static constexpr int kAlpha = NT >= 3 ? 5 : 4;
   static constexpr int TK = 8192 / ROWB;         // keys of a tile: 16 KB of K and V
   // a step: M x 16 keys; two where registers allow, so that a chain of products hides another
   static constexpr int M = TK >= 32 && D_ * NT_ <= (WR_ == 4 ? 384 : 256) && (WK_ < 4 || TK >= 64) ? 2 : 1;
@@ -1000,8 +1003,6 @@ Layout layout_of(const KV &kv, int G, int max_q, int max_seq_len) {
   return l;
 }
 
-constexpr int kAlpha = 4;  // positions of a unit's lead-in
-
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1034,7 +1035,7 @@ Layout plan(const ScoredArgs &sa, void *workspace, size_t *bytes, Params *p) {
   *bytes = l.bytes;
   p->cap_in = sa.cap > 0.f ? finite(sa.a.scale_log2 * 2.f * 1.4426950408889634f / sa.cap) : 0.f;
   p->ctas = l.ctas;
-  p->alpha = kAlpha;
+  p->alpha = C::kAlpha;
   p->rows_cap = l.rows_cap;
   p->box = std::min(kv.block_size, C::TK);
   p->part_o = reinterpret_cast<float *>(workspace);

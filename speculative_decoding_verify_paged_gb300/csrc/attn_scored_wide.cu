@@ -52,6 +52,8 @@ namespace {
 
 struct Wide {  // what the work order and the merge need
   static constexpr int D = 128, TK = 64, RB = 256, ROWB = 256, kCtasPerSm = 1;
+  // (72, 128 and 256 rows a KV head over 2K to 4K tokens: 4 111, 123 and 186 us, 13 106, 115 and 177, 26 111, 118, 188)
+  static constexpr int kAlpha = 12;
 };
 constexpr int kSoft = 8;                   // softmax warps
 constexpr int kWideThreads = (kSoft + 4) * 32;  // the last warp does nothing: register shares go by four warps
