@@ -12,12 +12,12 @@
 // 32 sequences of 2K to 4K tokens are 83% of the measured copy rate; the warps' matrix instructions beyond
 // (16 x 8 x 16 in 8 cycles of a quarter SM: with 24 rows a warp 1540 of the 1800 cycles that two warps'
 // steps take). Units of more than kWideRows rows go to attn_scored_wide.cu, whose blocks of 128 rows cost too
-// much for fewer (40 rows: 94 us here, 105 there; in sequences of 600 tokens 97 and 148).
+// much for fewer (40 rows: 93 us here, 97 there; in sequences of 600 tokens 94 and 121).
 //
 // Times (us, 8 KV heads of 128 values; share of the copy rate): 32 sequences of 2K to 4K tokens in bf16 with 4,
-// 16, 32, 48, 64 rows a KV head 70 (83%), 74, 93 (67%), 97 (62%), 112 (51%); 32 x 6 rows over 0.5K to 4K tokens,
-// capped, 61 (71%); four sequences of 32K tokens in E4M3 57 (69%); 128 sequences in a window of 1024, biased, 95
-// (42%: 4 short units a CTA, each 7000 cycles of setting up and merging).
+// 16, 32 and 48 rows a KV head 69 (85%), 75, 94 (66%), 96 (63%); 32 x 6 rows over 0.5K to 4K tokens, capped, 60.5
+// (72%); four sequences of 32K tokens in E4M3 53 (73%); 128 sequences in a window of 1024, biased, 90 (45%: 4
+// short units a CTA, each 7000 cycles of setting up and merging).
 //
 // Work: as many CTAs as fit the GPU stay for the whole launch. The key tiles of all units laid end
 // to end (each unit preceded by `alpha` positions, what starting and finishing one costs) are cut
@@ -1072,9 +1072,9 @@ cudaError_t run(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream
   return launch_combine<C>(p, l, st);
 }
 
-// Units of more query rows go to attn_scored_wide.cu, where it takes them: 32 sequences of 2K to 4K tokens with 72 rows a
-// KV head 168 us here, 116 there; with 64 rows 112 and 105, but short sequences cost more there (its pieces start slowly).
-constexpr int kWideRows = 64;
+// Units of more query rows go to attn_scored_wide.cu, where it takes them: with 64 rows a KV head 32 sequences of 2K to
+// 4K tokens take 106 us here and 97 there, 64 of 200 to 300 tokens 64 and 50; with 48 rows 96 and 100.
+constexpr int kWideRows = 48;
 bool wide_fits(const ScoredArgs &sa);
 cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);
 
@@ -1096,13 +1096,13 @@ cudaError_t pick(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStrea
     if (rows <= 24) return on(Cfg<D, 3, 1, 4, F8>());
     if (rows <= 32) return on(Cfg<D, 2, 2, 2, F8>());
     if (rows <= 48) return on(Cfg<D, 3, 2, 2, F8>());
-    if (rows <= 64) return on(Cfg<D, 2, 4, 1, F8>());
-    if (!wide_fits(sa)) return on(Cfg<D, 3, 4, 1, F8>());
+    auto here = [&] { return rows <= 64 ? on(Cfg<D, 2, 4, 1, F8>()) : on(Cfg<D, 3, 4, 1, F8>()); };
+    if (!wide_fits(sa)) return here();
     // a cap past the two-instruction tanh stays here; the workspace suits both
     size_t most = 0;
     run_wide(sa, nullptr, &most, st, false);
     if (go && sa.cap <= kFastCap * 1.4426950408889634f) return run_wide(sa, workspace, bytes, st, go);
-    const cudaError_t e = on(Cfg<D, 3, 4, 1, F8>());
+    const cudaError_t e = here();
     *bytes = std::max(*bytes, most);
     return e;
   } else {

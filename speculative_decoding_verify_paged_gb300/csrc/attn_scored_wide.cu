@@ -10,9 +10,9 @@
 // and write are a chain, and two warps a scheduler hide only part of it.
 //
 // Times (us, bf16, 8 KV heads of 128 values; in brackets the warp-matrix kernels of attn_scored.cuh):
-//   16 trees of 61 rows x 4 heads over 8192 tokens, capped 206 [455], 650 TFLOP/s;
-//   32 sequences over 2K to 4K tokens: 256 rows a KV head 192 capped, 164 without [407 capped],
-//   128 rows 126, 117 [270], 100 rows 116 [271], 72 rows 116 [168].
+//   16 trees of 61 rows x 4 heads over 8192 tokens, capped 194 [455], 690 TFLOP/s;
+//   32 sequences over 2K to 4K tokens: 256 rows a KV head 177 capped, 147 without [407 capped],
+//   128 rows 116, 108 [270], 100 rows 107 [271], 72 rows 106 [168], 64 rows 97 [106].
 //
 // A unit is one KV head of one sequence and up to 256 query rows, as two blocks of 128, one row per
 // tensor-memory lane, so that K and V are read once for all of them. One CTA an SM, eleven warps:
@@ -35,7 +35,8 @@
 // A unit of 128 rows or fewer is one block: a and b hold the same rows, take a tile each in turn, and merge
 // their rows at the end. The values of both lie in the same lanes of tensor memory, so a row's two warps
 // exchange m and l alone and write half of its values each. (100 rows, with b idle: 170 us; both at work with
-// four stages 130, with Q once and six 116.) Launches whose units may be larger leave b idle in smaller ones.
+// four stages 130, with Q once and six 116; 107 with pieces cut by what starting one costs.) Launches whose
+// units may be larger leave b idle in smaller ones.
 //
 // Edge tiles (new rows, the window's start, the end) see keys as bits of a row. Values past the end of
 // the sequence are set to zero in the stage; infinities and NaN of keys that some row does not see are
