@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const H
     }
   };
   const int kind0 = i0 < nq ? 0 : i0 < nq + nk ? 1 : 2;
-  load(kind0 == 0 ? in_q : kind0 == 1 ? in_k : in_v, kind0 == 0 ? a.hq : a.hkv, i0, min(i1, kind0 == 0 ? nq : kind0 == 1 ? nq + nk : all), kind0 == 0 ? 0 : kind0 == 1 ? nq : nq + nk);
+  load(kind0 == 0 ? in_q : kind0 == 1 ? in_k : in_v, kind0 == 0 ? a.hq : a.hkv, i0,
+       min(i1, kind0 == 0 ? nq : kind0 == 1 ? nq + nk : all), kind0 == 0 ? 0 : kind0 == 1 ? nq : nq + nk);
   int b = 0, i = 0, n = 1, c = 0;
   if (APPEND) {
     b = owner_of(a.cu_q, a.kv.batch, row);
@@ -290,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const H
       }
     }
     for (int it = lo; it < end; it += kAhead) {
-      if (it > i0) load(kind == 0 ? in_q : kind == 1 ? in_k : in_v, count, it, end, first);  // the item's first loads are on their way since its start
+      // (the item's first loads are on their way since its start)
+      if (it > i0) load(kind == 0 ? in_q : kind == 1 ? in_k : in_v, count, it, end, first);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         if (it + u >= end) break;  // uniform
