@@ -120,7 +120,11 @@ __device__ __forceinline__ void tmem_put(uint32_t at, const uint32_t *x) {
       SV_I8(x, 0), SV_I8(x, 8), SV_I8(x, 16), SV_I8(x, 24)
       : "memory");
 }
-__device__ __forceinline__ void tmem_get_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// What this thread has asked for has arrived; x passes through, so that nothing is made of it before
+#define SV_P8(x, o) "+r"(x[o]), "+r"(x[o + 1]), "+r"(x[o + 2]), "+r"(x[o + 3]), "+r"(x[o + 4]), "+r"(x[o + 5]), "+r"(x[o + 6]), "+r"(x[o + 7])
+__device__ __forceinline__ void tmem_landed(uint32_t *x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SV_P8(x, 0), SV_P8(x, 8), SV_P8(x, 16), SV_P8(x, 24)::"memory");
+}
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // the smaller of two, a NaN if one is
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             tmem_get(to + k * 32, o);
-            tmem_get_wait();
+            tmem_landed(o);
 #pragma unroll
             for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
             tmem_put(to + k * 32, o);
@@ -537,11 +541,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           float part[4] = {0.f, 0.f, 0.f, 0.f};
           if (bounded && !edge) {
             // no maximum, no bias, every key is seen: 32 keys' weights while the other 32 scores are on their way
-            tmem_get_wait();
+            tmem_landed(w);
             tmem_get(ts + 32, w + 32);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (h == 1) tmem_get_wait();
+              if (h == 1) tmem_landed(w + 32);
 #pragma unroll
               for (int k = 32 * h; k < 32 * h + 32; k += 4) {
                 float x[4];
@@ -560,7 +564,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             l += (part[0] + part[1]) + (part[2] + part[3]);
           } else if (plain && !edge) {  // scores as they are, times a factor that keeps their order
             tmem_get(ts + 32, w + 32);
-            tmem_get_wait();
+            tmem_landed(w);
+            tmem_landed(w + 32);
             float mx = kNone;
 #pragma unroll
             for (int k = 0; k < kTile; ++k) mx = fmaxf(mx, __uint_as_float(w[k]));
@@ -575,7 +580,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             l += (part[0] + part[1]) + (part[2] + part[3]);
           } else {
             tmem_get(ts + 32, w + 32);
-            tmem_get_wait();
+            tmem_landed(w);
+            tmem_landed(w + 32);
             // ---- scores ----
             if (cap == 0.f) {
 #pragma unroll
@@ -648,7 +654,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               for (int k = 0; k < 4; ++k) {
                 uint32_t o[32];
                 tmem_get(to + k * 32, o);
-                tmem_get_wait();
+                tmem_landed(o);
 #pragma unroll 1
                 for (int key = 0; key < kTile; ++key) {
                   const float e = *(volatile float *)&weight[key];
@@ -756,12 +762,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if constexpr (ONE) {
             uint32_t u[32];
             tmem_get(lane_at + kColO + (blk ^ 1) * 128 + k * 32, u);
-            tmem_get_wait();
+            tmem_landed(o);
+            tmem_landed(u);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
               o[y] = __float_as_uint(__uint_as_float(o[y]) * f_own + __uint_as_float(u[y]) * f_other);
           } else {
-            tmem_get_wait();
+            tmem_landed(o);
           }
           write(k, o, inv);
         }

@@ -310,16 +310,17 @@ def test_no_sequences_rows_or_context():
     assert torch.equal(out[:3], buf.attn_out[:3])
 
 
-def test_repeatable_on_two_streams_and_in_graphs():
+@pytest.mark.parametrize("nq", [[6, 1, 4, 2], [32, 1, 20, 2], [64, 3, 40, 1]])
+def test_repeatable_on_two_streams_and_in_graphs(nq):
     """The same call twice, two at once on their own streams, and captured: the same bits."""
-    case = W.custom(39, batch=4, ctx_lens=[900, 40, 2000, 3], n_q=[6, 1, 4, 2], num_q_heads=32, num_kv_heads=8, head_dim=128, block_size=16, vocab=16,
+    case = W.custom(39, batch=4, ctx_lens=[900, 40, 2000, 3], n_q=nq, num_q_heads=32, num_kv_heads=8, head_dim=128, block_size=16, vocab=16,
                     use_bank=False)
     mod = ScoreMod(softcap=20.0, slopes=slopes(32))
     kv, d, buf = run(case, mod)
     first = buf.attn_out.clone()
     outs = [torch.empty_like(first) for _ in range(3)]
     streams = [torch.cuda.Stream() for _ in range(2)]
-    call = lambda o, st: L.spec_verify_attn_scored(kv, d.q, o, d.cu_q, max_q=6, max_seq_len=2004, scale=d.scale, mod=mod, stream=st)  # noqa: E731
+    call = lambda o, st: L.spec_verify_attn_scored(kv, d.q, o, d.cu_q, max_q=nq[0], max_seq_len=2000 + nq[2], scale=d.scale, mod=mod, stream=st)  # noqa: E731
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())
     for _ in range(5):
