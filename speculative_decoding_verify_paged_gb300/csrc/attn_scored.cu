@@ -28,16 +28,15 @@ cudaError_t pick(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStrea
 }
 
 // bf16 and E4M3 caches with heads of 64, 128 or 256 values in blocks of 8 tokens and more
-// (attn_scored.cuh); a TMA row coordinate is a 32-bit number.
-bool attn_scored_mma_fits(const ScoredArgs &sa) {
+// (attn_scored.cuh); a TMA row coordinate is a 32-bit number, and so are a unit's rows.
+size_t attn_scored_mma_workspace(const ScoredArgs &sa) {
   const KV &kv = sa.a.kv;
-  if (kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return false;
-  if (kv.block_size < 8 || (long long)kv.num_blocks * kv.num_kv_heads * kv.block_size >= (1LL << 31)) return false;
-  // positions of the work order (at most two tiles and a few lead-in positions more per unit of 64 rows) stay
-  // in range
-  const long long rows = (long long)(sa.a.num_q_heads / kv.num_kv_heads) * sa.a.max_q;
-  const long long units = (long long)kv.batch * kv.num_kv_heads * ((rows + 63) / 64);
-  return units * (sa.a.max_seq_len / 64 + 16) < (1LL << 30);
+  if (kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return 0;
+  if (kv.block_size < 8 || (long long)kv.num_blocks * kv.num_kv_heads * kv.block_size >= (1LL << 31)) return 0;
+  if ((long long)(sa.a.num_q_heads / kv.num_kv_heads) * sa.a.max_q >= (1LL << 30)) return 0;
+  size_t bytes = 0;
+  launch_attn_scored_mma(sa, nullptr, &bytes, nullptr, false);
+  return bytes;
 }
 
 cudaError_t launch_attn_scored_mma(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {

@@ -985,7 +985,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_scored_combine(const Param
 struct Layout {
   int ctas, rows_cap;
   long long units;  // if every sequence has max_q rows
-  size_t lse_offset, prefix_offset, bytes;
+  size_t lse_offset, prefix_offset, bytes;  // bytes 0: the work order does not fit its 32-bit positions
 };
 
 template <class C>
@@ -993,13 +993,17 @@ Layout layout_of(const KV &kv, int G, int max_q, int max_seq_len) {
   Layout l;
   const int blocks = (G * max_q + C::RB - 1) / C::RB;
   l.units = (long long)kv.batch * kv.num_kv_heads * blocks;
-  const long long tiles = l.units * ((max_seq_len + C::TK - 1) / C::TK);
+  const int unit_tiles = (max_seq_len + C::TK - 1) / C::TK;
+  const long long tiles = l.units * unit_tiles;
   l.ctas = (int)std::max(1LL, std::min<long long>((long long)C::kCtasPerSm * num_sms(), tiles));
   l.rows_cap = std::min(C::RB, G * max_q);
   const size_t slots = (size_t)l.ctas * 2 * l.rows_cap;
   l.lse_offset = slots * C::D * sizeof(float);
   l.prefix_offset = (l.lse_offset + slots * sizeof(float) + 255) / 256 * 256;
-  l.bytes = l.prefix_offset + ((size_t)kv.batch + 1) * sizeof(int);
+  // A unit has at most unit_tiles + kAlpha positions, with this instance's own tile and block of rows; positions,
+  // their sums over the batch and the prefix are 32-bit.
+  const bool fits = l.units <= INT_MAX / (unit_tiles + C::kAlpha);
+  l.bytes = fits ? l.prefix_offset + ((size_t)kv.batch + 1) * sizeof(int) : 0;
   return l;
 }
 
@@ -1025,7 +1029,7 @@ template <class C> bool make_map(CUtensorMap *map, void *pool, const KV &kv, int
             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A call's parameters and the size of its workspace.
+// A call's parameters and the size of its workspace (0: not a call for this instance).
 template <class C>
 Layout plan(const ScoredArgs &sa, void *workspace, size_t *bytes, Params *p) {
   const KV &kv = sa.a.kv;
@@ -1057,7 +1061,7 @@ cudaError_t run(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream
   const KV &kv = sa.a.kv;
   Params p;
   const Layout l = plan<C>(sa, workspace, bytes, &p);
-  if (!go) return cudaSuccess;
+  if (!go || *bytes == 0) return cudaSuccess;
   static const bool split_fits = [] {  // the kernel was compiled for the registers that its split shares out
     cudaFuncAttributes fa;
     return cudaFuncGetAttributes(&fa, attn_scored_kernel<C>) == cudaSuccess && fa.numRegs == kLaunchRegs;
@@ -1098,12 +1102,12 @@ cudaError_t pick(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStrea
     if (rows <= 48) return on(Cfg<D, 3, 2, 2, F8>());
     auto here = [&] { return rows <= 64 ? on(Cfg<D, 2, 4, 1, F8>()) : on(Cfg<D, 3, 4, 1, F8>()); };
     if (!wide_fits(sa)) return here();
-    // a cap past the two-instruction tanh stays here; the workspace suits both
+    // a cap past the two-instruction tanh stays here; the workspace suits both, and so do the positions
     size_t most = 0;
     run_wide(sa, nullptr, &most, st, false);
     if (go && sa.cap <= kFastCap * 1.4426950408889634f) return run_wide(sa, workspace, bytes, st, go);
     const cudaError_t e = here();
-    *bytes = std::max(*bytes, most);
+    *bytes = *bytes == 0 || most == 0 ? 0 : std::max(*bytes, most);
     return e;
   } else {
     if (rows <= 16) return on(Cfg<D, 1, 2, 2, F8>());

@@ -811,7 +811,7 @@ cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaS
   const KV &kv = sa.a.kv;
   Params p;
   const Layout l = plan<Wide>(sa, workspace, bytes, &p);
-  if (!go) return cudaSuccess;
+  if (!go || *bytes == 0) return cudaSuccess;
   CUtensorMap mk, mv;
   if (!make_map<Wide>(&mk, kv.k_pool, kv, p.box) || !make_map<Wide>(&mv, kv.v_pool, kv, p.box)) return cudaErrorInvalidValue;
   // One block of rows for all: 32 x 25 rows a head group of 4 over 2K to 4K tokens 170 -> 131 us with both blocks at work

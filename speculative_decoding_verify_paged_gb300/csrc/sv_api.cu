@@ -367,13 +367,10 @@ size_t sv_spec_verify_attn_scored_workspace_bytes(const sv_paged_kv *kv, int32_t
   sa.a.num_q_heads = num_q_heads;
   sa.a.max_q = max_q_per_seq;
   sa.a.max_seq_len = max_seq_len;
-  if (!attn_scored_mma_fits(sa)) {
-    const SplitPlan p = scored_splits(kv, max_seq_len);
-    return p.max_splits <= kScoredCluster ? 0 : split_workspace(kv, num_q_heads, total_q, p);
-  }
-  size_t need = 0;
-  launch_attn_scored_mma(sa, nullptr, &need, nullptr, false);
-  return need;
+  const size_t need = attn_scored_mma_workspace(sa);
+  if (need > 0) return need;
+  const SplitPlan p = scored_splits(kv, max_seq_len);
+  return p.max_splits <= kScoredCluster ? 0 : split_workspace(kv, num_q_heads, total_q, p);
 }
 
 sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void *out, const int32_t *cu_q,
@@ -425,7 +422,7 @@ sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void 
   sa.slopes = mod->slopes;
   sa.positions = positions;
   cudaStream_t st = (cudaStream_t)stream;
-  if (attn_scored_mma_fits(sa)) return cuda_status(launch_attn_scored_mma(sa, workspace, &need, st, true));
+  if (attn_scored_mma_workspace(sa) > 0) return cuda_status(launch_attn_scored_mma(sa, workspace, &need, st, true));
   return cuda_status(launch_attn_scored_simt(sa, kv->dtype, st));
 }
 

@@ -218,9 +218,9 @@ int kv_max_seq_bits();   // batch limit of fork and release
 // Head rows: the append's second half after launch_kv_alloc (append), or into q_out and k_out.
 cudaError_t launch_head_rows(const HeadArgs &a, int dtype, int total_q, bool append, cudaStream_t st);
 cudaError_t launch_attn_scored_simt(const ScoredArgs &sa, int dtype, cudaStream_t st);
-// The warp-matrix kernels (attn_scored.cuh): whether they take a call; its workspace into *bytes and, with
-// `go`, the launches (workspace: that many bytes, 256-aligned).
-bool attn_scored_mma_fits(const ScoredArgs &sa);
+// The tensor-core kernels (attn_scored.cuh, attn_scored_wide.cu): the workspace of a call, 0 for one that they do not
+// take; that into *bytes and, with `go`, the launches (workspace: that many bytes, 256-aligned).
+size_t attn_scored_mma_workspace(const ScoredArgs &sa);
 cudaError_t launch_attn_scored_mma(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);
 cudaError_t launch_attn_simt(const AttnArgs &a, int dtype, cudaStream_t st);
 cudaError_t launch_attn_combine(const AttnArgs &a, int dtype, cudaStream_t st);
