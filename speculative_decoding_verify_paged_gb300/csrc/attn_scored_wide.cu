@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __shared__ __align__(8) uint64_t s_done;                // every product issued has finished
   __shared__ int s_dead, s_scan[kWarps], s_first_b, s_first_base;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_place[64], s_top[kSoft], s_odd[2];
+  __shared__ int s_place[64], s_top[kSoft];
   __shared__ float2 s_ml[ONE ? kBlock : 1];  // a block's m and l, on their way to the other
 
   const AttnArgs &a = P.s.a;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     bar_init(smem_at(&s_seen), 1);
     bar_init(smem_at(&s_done), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    s_dead = s_odd[0] = s_odd[1] = 0;
+    s_dead = 0;
     s_first_b = s_first_base = 0;
   }
   if (warp == kSoft + 1) {
@@ -406,6 +406,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       else if (!ONE || blk == 0) asm volatile("bar.sync 2, 128;" ::: "memory");
       else asm volatile("bar.sync 3, 128;" ::: "memory");
     };
+    // ... and whether any of them has one. (The barrier itself carries the vote: a flag in shared memory could be set for the
+    // next tile by a warp that is ahead before a slow one has read it, and the barriers would no longer pair up.)
+    auto any_of_tile = [&](bool two, bool one) {
+      uint32_t any;
+      auto vote = [&](auto id, auto threads) {
+        asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                     : "=r"(any)
+                     : "r"((uint32_t)one), "n"(decltype(id)::value), "n"(decltype(threads)::value)
+                     : "memory");
+      };
+      using std::integral_constant;
+      if (two) vote(integral_constant<int, 2>(), integral_constant<int, 256>());
+      else if (!ONE || blk == 0) vote(integral_constant<int, 2>(), integral_constant<int, 128>());
+      else vote(integral_constant<int, 3>(), integral_constant<int, 128>());
+      return any != 0u;
+    };
     bool first_piece = true;
     uint32_t cs = 0;  // tiles of the block so far: S in buffer cs & 1, the same buffer's s_o when its P V is done
     auto zero_o = [&] {
@@ -529,11 +545,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (key0 + key >= ke || key0 + key < pc.lo) *w = make_uint4(0, 0, 0, 0);
             else odd |= nonfinite2(w->x) | nonfinite2(w->y) | nonfinite2(w->z) | nonfinite2(w->w);
           }
-          int *flag = &s_odd[ONE ? blk : 0];
-          if (odd) *flag = 1;
           fence_async();
-          of_tile(two);
-          odd = *(volatile int *)flag != 0;
+          odd = any_of_tile(two, odd);
         }
         if (warp_live || odd) {
           uint32_t w[kTile];
@@ -692,8 +705,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
           fence_async();
-          of_tile(two);
-          if (tx == 0) s_odd[ONE ? blk : 0] = 0;
           of_tile(two);
         }
         fence_before();

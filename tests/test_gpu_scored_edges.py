@@ -1,0 +1,63 @@
+"""Scored attention where rows see different keys: infinities and NaN next to finite values, tile after tile.
+
+A row that does not see such a key has the bits that it has with a finite value in the key's place: weights of unseen
+keys are zero either way. Nothing here is compared within a tolerance unless a test says so."""
+import numpy as np
+import pytest
+import torch
+
+from speculative_decoding_verify_paged_gb300 import ScoreMod
+from speculative_decoding_verify_paged_gb300 import step as S
+from speculative_decoding_verify_paged_gb300 import workloads as W
+
+import test_gpu_scored as T
+from _helpers import max_seq_len, status_of
+
+pytestmark = pytest.mark.gpu
+
+
+def make(seed, ctx, nq, hq, hkv, d, dt, mod, **kw):
+    case = W.custom(seed, batch=len(ctx), ctx_lens=ctx, n_q=nq, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=16, vocab=16, dtype=dt,
+                    use_bank=False)
+    kv, step, buf = T.run(case, mod, **kw)
+    return kv, step, buf, max_seq_len(case.state, case.step)
+
+
+def put(kv, b, t, value, pool="v_pool"):
+    """The value (an E4M3 pool: the code) in every head's first place of key t of sequence b, and in one more."""
+    rows = getattr(kv, pool)[int(kv.block_table[b, t // 16]), :, t % 16]
+    rows[:, 0] = value
+    rows[:, rows.shape[1] // 2 + 1] = value
+
+
+def again(kv, step, buf, msl):
+    buf.attn_out.zero_()
+    S.attention(kv, step, buf, msl)
+    torch.cuda.synchronize()
+    assert status_of(buf) == 0
+    return buf.attn_out.clone()
+
+
+@pytest.mark.parametrize("n", [16, 32, 40, 64])  # 64 and 128 rows a unit: one block; 160 and 256: two
+def test_nonfinite_values_in_some_of_many_edge_tiles(n):
+    """Wide units whose tiles are all at an edge (a window as long as the draft), some with an infinity or NaN and some
+    without, in many short sequences: rows that do not see them keep their bits, over and over."""
+    window, count = 64, 24
+    ctx = [130 + 7 * i for i in range(count)]
+    kv, step, buf, msl = make(60, ctx, [n] * count, 8, 2, 128, "bf16", ScoreMod(softcap=20.0, window=window))
+    clean = buf.attn_out.clone()
+    hit = np.zeros(len(clean), bool)
+    for b, c in enumerate(ctx):
+        if b % 3 != 2:  # the window's first key: row 0 alone sees it
+            put(kv, b, c - window + 1, float("inf"))
+            hit[b * n] = True
+        if b % 3 != 1:  # the last new row: itself alone
+            put(kv, b, c + n - 1, float("nan"))
+            hit[b * n + n - 1] = True
+    first = None
+    for _ in range(30):
+        out = again(kv, step, buf, msl)
+        assert torch.equal(out[~hit], clean[~hit])
+        assert not torch.isfinite(out[hit].float()).all(-1).any()
+        assert first is None or torch.equal(first.view(torch.int16), out.view(torch.int16))
+        first = out
