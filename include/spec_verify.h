@@ -124,8 +124,10 @@ typedef enum sv_mask_kind { SV_MASK_CAUSAL = 0, SV_MASK_TREE = 1 } sv_mask_kind;
  * scale per pool): the new rows given to sv_kv_append and the queries and
  * outputs of sv_spec_verify_attn are bf16. Append stores each new element x as
  * the E4M3 code nearest to x / scale (fp32 division; ties to the even
- * mantissa; saturating at +-448), so it never writes the NaN codes 0x7F and
- * 0xFF; a pool must not hold them. Attention reads code * scale: the CUDA-core
+ * mantissa; saturating at +-448); a NaN becomes the NaN code 0x7F, and nothing
+ * else the codes 0x7F and 0xFF. sv_spec_verify_attn wants a pool without them;
+ * in sv_spec_verify_attn_scored one is a NaN to the rows that see its key and
+ * nothing to the others. Attention reads code * scale: the CUDA-core
  * kernel in fp32; the tcgen05 kernel (head_dim 128) widens the codes to fp16
  * exactly, rounds the queries and the softmax weights to fp16 and applies the
  * scales to the scores and the outputs in fp32, so a query element beyond the

@@ -768,6 +768,37 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           };
           if (!odd) pv(std::false_type());
           else pv(std::true_type());
+          if (F8 && odd) {
+            // the NaN codes set to zero above, for the rows that see their keys: O's values 2 g and 2 g + 1 of 16
+            const uint8_t *vs = ring + st * C::kStageBytes + (TK + (step % S) * 16 * M) * C::ROWB;
+#pragma unroll 1
+            for (int key = 0; key < 16 * M; ++key) {
+              const int place = key0 + key - c;
+              const uint8_t *row = vs + (key >> 3) * 8 * C::ROWB + (key & 7) * kRow;
+              bool sees[NT][2];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int rl = (wr * NT + nt) * 8 + 2 * t + e;
+                  sees[nt][e] = place < 0 ? place > s_reach[rl] : place < 64 && ((s_mask[rl] >> place) & 1ull) != 0;
+                }
+#pragma unroll
+              for (int mt = 0; mt < KT; ++mt) {
+                const int chunk = CH >= 8 ? (mt >> 3) * 64 + ((mt & 7) ^ (key & 7)) : mt ^ ((key >> 1) & 3);
+                const uint32_t two = *reinterpret_cast<const uint16_t *>(row + chunk * 16 + 2 * g);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  if (((two >> (8 * y)) & 0x7fu) != 0x7fu) continue;
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                      if (sees[nt][e]) o[mt][nt][2 * y + e] = __uint_as_float(0x7fffffffu);  // NaN
+                }
+              }
+            }
+          }
           if (!F8 && odd) {
             // the values set to zero above, for the rows that see their keys
             const uint8_t *vs = ring + st * C::kStageBytes + (TK + (step % S) * 16 * M) * C::ROWB;

@@ -61,3 +61,24 @@ def test_nonfinite_values_in_some_of_many_edge_tiles(n):
         assert not torch.isfinite(out[hit].float()).all(-1).any()
         assert first is None or torch.equal(first.view(torch.int16), out.view(torch.int16))
         first = out
+
+
+@pytest.mark.parametrize("dt,d,hq", [("e4m3", 64, 8), ("e4m3", 64, 64), ("e4m3", 128, 8), ("e4m3", 128, 24), ("e4m3", 128, 64), ("e4m3", 256, 8),
+                                     ("e4m3", 256, 32), ("e4m3", 96, 8), ("bf16", 64, 8), ("bf16", 128, 8), ("bf16", 128, 48), ("bf16", 256, 8),
+                                     ("bf16", 96, 8), ("f32", 64, 8)])
+def test_a_seen_nan_reaches_its_rows_and_no_others(dt, d, hq):
+    """A NaN among the values of a draft row and of the window's first key: it stands in the same places of the rows that
+    see the key, and nowhere else."""
+    window = 50
+    masks = torch.tensor([1, 3, 5, 9, 17, 1, 3, 5, 9, 17, 33], dtype=torch.int64, device="cuda")
+    kv, step, buf, msl = make(61, [200, 37], [5, 6], hq, 2, d, dt, ScoreMod(softcap=20.0, window=window), tree_mask=masks)
+    want = buf.attn_out.clone()
+    nan = 0x7F if dt == "e4m3" else float("nan")
+    minus = 0xFF if dt == "e4m3" else float("nan")
+    for b, t, row, code in ((0, 200 + 4, 4, nan), (0, 200 - window + 1, 0, minus), (1, 37 + 2, 7, minus)):
+        put(kv, b, t, code)
+        want[row, :, 0] = want[row, :, d // 2 + 1] = float("nan")
+    out = again(kv, step, buf, msl)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    keep = ~torch.isnan(want)
+    assert torch.equal(out[keep], want[keep])
