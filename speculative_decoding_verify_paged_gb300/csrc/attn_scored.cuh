@@ -231,18 +231,15 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
   asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(y) : "r"(w));
   return y;
 }
-__device__ __forceinline__ uint32_t without_nan(uint32_t x) {  // an fp16 pair, NaN halves set to zero
-  if ((x & 0x7c00u) == 0x7c00u) x &= 0xffff0000u;
-  if ((x & 0x7c000000u) == 0x7c000000u) x &= 0xffffu;
-  return x;
+// The bytes of a word that are E4M3 NaN codes, the halves that are bf16 infinities or NaN, as masks
+__device__ __forceinline__ uint32_t nan_codes(uint32_t x) {
+  const uint32_t top = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return (top << 1) - (top >> 7);
 }
-
-__device__ __forceinline__ bool nan_code4(uint32_t x) {  // four E4M3 codes
-  return (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
+__device__ __forceinline__ uint32_t nonfinite(uint32_t x) {
+  return ((x & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
 }
-__device__ __forceinline__ bool nonfinite2(uint32_t x) {  // a bf16 pair
-  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
-}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // A CTA's position in the work order: the sequence that holds it and where that one's positions begin.
 struct Place {
@@ -300,6 +297,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   __shared__ float s_slope[RB];
   __shared__ int s_place[64];  // position of a new row minus c
   __shared__ float s_m[WK][RB], s_l[WK][RB];
+  __shared__ int s_patch;  // E4M3: a key of the piece's edge steps has a NaN code among its values
   __shared__ int s_scan[kWarps], s_first_b, s_first_base, s_top[kWarps];
 
   const AttnArgs &a = P.s.a;
@@ -507,6 +505,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       for (int x = tid; x < s.n; x += kC) s_place[x] = P.s.positions != nullptr ? P.s.positions[s.row0 + x] - c : x;
       top = __reduce_max_sync(0xffffffffu, top);
       if (lane == 0) s_top[warp] = top;
+      if (F8 && tid == 0) s_patch = 0;
 
       // ---- Q into registers ----
       uint32_t q[NT][KT][2];
@@ -671,14 +670,33 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               }
             // Do the step's values hold what must not meet a weight of zero? (E4M3: NaN codes of unused slots.)
             constexpr int kChunks = 16 * M * C::ROWB / 16;
-            const uint8_t *vs = ring + st * C::kStageBytes + (TK + (step % S) * 16 * M) * C::ROWB;
+            uint8_t *vs = ring + st * C::kStageBytes + (TK + (step % S) * 16 * M) * C::ROWB;
 #pragma unroll 4
             for (int y = lane; y < kChunks; y += 32) {
               const uint4 w = *reinterpret_cast<const uint4 *>(vs + y * 16);
-              odd |= F8 ? nan_code4(w.x) | nan_code4(w.y) | nan_code4(w.z) | nan_code4(w.w)
-                        : nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w);
+              odd |= (F8 ? nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w)
+                         : nonfinite(w.x) | nonfinite(w.y) | nonfinite(w.z) | nonfinite(w.w)) != 0u;
             }
             odd = __any_sync(0xffffffffu, odd);
+            if constexpr (F8) {  // NaN codes become zeros in the stage; the rows that see a key get them at the piece's end
+              if (odd) {
+#pragma unroll 1
+                for (int y = lane; y < kChunks * 4; y += 32) {
+                  uint32_t *w = reinterpret_cast<uint32_t *>(vs) + y;
+                  const uint32_t out = nan_codes(*w);
+                  if (out == 0u) continue;
+                  *w &= ~out;
+                  const int key = key0 + (C::ROWB >= 128 ? y / (2 * C::ROWB) * 8 + y / 32 % 8 : y / 16);
+                  if (key >= lo && key < ke) s_patch = 1;
+                }
+                fence_async();  // before the next copies into the stage
+              }
+              if (odd || WR > 1) {  // (another row group may have been here since the first values were read)
+                __syncwarp();
+#pragma unroll
+                for (int y = 0; y < PV - 1; ++y) ldm4t(vf[y], v_at(y));
+              }
+            }
           }
           // ---- the running maximum ----
           if (!bounded) {
@@ -755,50 +773,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                 for (int h = 0; h < 2; ++h) {
                   // a word: two dimensions of one key below, of the next key above; pairs of keys are wanted
                   const uint32_t w0 = __byte_perm(w[2 * h], 0u, 0x3120), w1 = __byte_perm(w[2 * h + 1], 0u, 0x3120);
-                  uint32_t e[4] = {widen(w0), widen(w0 >> 16), widen(w1), widen(w1 >> 16)};
-                  if (kCheck) {  // slots that no row sees may hold anything
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) e[y] = without_nan(e[y]);
-                  }
+                  const uint32_t e[4] = {widen(w0), widen(w0 >> 16), widen(w1), widen(w1 >> 16)};
 #pragma unroll
                   for (int nt = 0; nt < NT; ++nt) mma<true>(o[mt * 2 + h][nt], e, pb[u][nt][0], pb[u][nt][1]);
                 }
               }
             }
           };
-          if (!odd) pv(std::false_type());
+          if (F8 || !odd) pv(std::false_type());
           else pv(std::true_type());
-          if (F8 && odd) {
-            // the NaN codes set to zero above, for the rows that see their keys: O's values 2 g and 2 g + 1 of 16
-            const uint8_t *vs = ring + st * C::kStageBytes + (TK + (step % S) * 16 * M) * C::ROWB;
-#pragma unroll 1
-            for (int key = 0; key < 16 * M; ++key) {
-              const int place = key0 + key - c;
-              const uint8_t *row = vs + (key >> 3) * 8 * C::ROWB + (key & 7) * kRow;
-              bool sees[NT][2];
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int rl = (wr * NT + nt) * 8 + 2 * t + e;
-                  sees[nt][e] = place < 0 ? place > s_reach[rl] : place < 64 && ((s_mask[rl] >> place) & 1ull) != 0;
-                }
-#pragma unroll
-              for (int mt = 0; mt < KT; ++mt) {
-                const int chunk = CH >= 8 ? (mt >> 3) * 64 + ((mt & 7) ^ (key & 7)) : mt ^ ((key >> 1) & 3);
-                const uint32_t two = *reinterpret_cast<const uint16_t *>(row + chunk * 16 + 2 * g);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  if (((two >> (8 * y)) & 0x7fu) != 0x7fu) continue;
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                      if (sees[nt][e]) o[mt][nt][2 * y + e] = __uint_as_float(0x7fffffffu);  // NaN
-                }
-              }
-            }
-          }
           if (!F8 && odd) {
             // the values set to zero above, for the rows that see their keys
             const uint8_t *vs = ring + st * C::kStageBytes + (TK + (step % S) * 16 * M) * C::ROWB;
@@ -851,6 +834,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           }
         }
       const size_t slot = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * P.rows_cap;
+      bool patch = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -866,6 +850,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           }
           together();
           if (nt == 0 && d0 == 0) {  // every group's weight in a row, over the rows' total
+            patch = F8 && s_patch != 0;
             for (int rl = tid; rl < rows; rl += kC) {
               float mx = s_m[0][rl], tot = 0.f;
 #pragma unroll
@@ -906,6 +891,35 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           }
           together();
         }
+      if (patch) {
+        // The NaN codes that edge steps took out, for the rows that see their keys: looked for in the pool again and put over what
+        // has been written. (This hardly ever runs. In the steps' loop, as for bf16, it made four sequences of 32K
+        // tokens take 60 us, without it 54, here 53; bf16 in this form 32 x 6 rows 61.7 us, 40 rows in short sequences
+        // 97, in the loop 60.4 and 92.)
+#pragma unroll 1
+        for (int x = tid; x < rows * D; x += kC) {
+          const int rl = x / D, d = x % D;
+          bool hit = false;
+#pragma unroll 1
+          for (int key = max(p.kt0 * TK, lo); key < ke && !hit; ++key) {
+            const int key0 = key & ~(16 * M - 1), place = key - c;
+            if (!(key0 + 16 * M > min(c, ke) || key0 < all_see)) continue;  // not an edge step
+            if (!(place < 0 ? place > s_reach[rl] : (s_mask[rl] >> place) & 1ull)) continue;
+            const int id = kv.block_table[(size_t)at.b * kv.max_blocks + (key >> bs_shift)];
+            if (id < 0 || id >= kv.num_blocks) continue;
+            const size_t row = ((size_t)id * kv.num_kv_heads + kvh) * kv.block_size + (key & (kv.block_size - 1));
+            hit = (static_cast<const uint8_t *>(kv.v_pool)[row * D + d] & 0x7f) == 0x7f;
+          }
+          if (!hit) continue;
+          if (p.whole) {
+            const int i = s_row[rl], head = kvh * P.G + (rb * RB + rl) - i * P.G;
+            reinterpret_cast<uint16_t *>(a.out)[((size_t)(s.row0 + i) * a.num_q_heads + head) * D + d] = 0x7fff;
+          } else {
+            P.part_o[(slot + rl) * D + d] = __uint_as_float(0x7fffffffu);
+          }
+        }
+        together();
+      }
       first_piece = false;
     }
   }

@@ -101,7 +101,6 @@ __device__ __forceinline__ bool elected() {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 #define SV_O8(x, o) "=r"(x[o]), "=r"(x[o + 1]), "=r"(x[o + 2]), "=r"(x[o + 3]), "=r"(x[o + 4]), "=r"(x[o + 5]), "=r"(x[o + 6]), "=r"(x[o + 7])
 #define SV_I8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
@@ -543,7 +542,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int key = y >> 4;
             uint4 *w = reinterpret_cast<uint4 *>(vs + chunk_at(key, y & 15));
             if (key0 + key >= ke || key0 + key < pc.lo) *w = make_uint4(0, 0, 0, 0);
-            else odd |= nonfinite2(w->x) | nonfinite2(w->y) | nonfinite2(w->z) | nonfinite2(w->w);
+            else odd |= (nonfinite(w->x) | nonfinite(w->y) | nonfinite(w->z) | nonfinite(w->w)) != 0u;
           }
           fence_async();
           odd = any_of_tile(two, odd);
