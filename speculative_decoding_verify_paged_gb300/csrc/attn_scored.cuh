@@ -780,38 +780,37 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               }
             }
           };
-          if (F8 || !odd) pv(std::false_type());
-          else pv(std::true_type());
-          if (!F8 && odd) {
-            // the values set to zero above, for the rows that see their keys
+          if (F8 || !odd) {
+            pv(std::false_type());
+          } else {
+            pv(std::true_type());
+            // The infinities and NaN set to zero above, for the rows that see their keys, whatever the weight: a weight that
+            // is zero in fp32 is not zero.
             const uint8_t *vs = ring + st * C::kStageBytes + (TK + (step % S) * 16 * M) * C::ROWB;
 #pragma unroll 1
             for (int key = 0; key < 16 * M; ++key) {
-              const int h = key >> 3;
+              const int place = key0 + key - c;
+              bool sees[NT][2];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float e0 = sc[0][nt][0], e1 = sc[0][nt][1];
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int y = 1; y < 2 * M; ++y)
-                  if (h == y) {
-                    e0 = sc[y >> 1][nt][2 * (y & 1)];
-                    e1 = sc[y >> 1][nt][2 * (y & 1) + 1];
-                  }
-                const float p0 = __shfl_sync(0xffffffffu, e0, (key & 7) * 4 + t);
-                const float p1 = __shfl_sync(0xffffffffu, e1, (key & 7) * 4 + t);
+                for (int e = 0; e < 2; ++e) {
+                  const int rl = (wr * NT + nt) * 8 + 2 * t + e;
+                  sees[nt][e] = place < 0 ? place > s_reach[rl] : place < 64 && ((s_mask[rl] >> place) & 1ull) != 0;
+                }
 #pragma unroll
-                for (int mt = 0; mt < KT; ++mt)
+              for (int mt = 0; mt < KT; ++mt)
 #pragma unroll
-                  for (int y = 0; y < 2; ++y) {
-                    const uint32_t w =
-                        *reinterpret_cast<const uint16_t *>(vs + h * 8 * C::ROWB + (key & 7) * 128 + (mt >> 2) * 1024 +
-                                                            ((((mt & 3) * 2 + y) ^ (key & 7)) << 4) + g * 2);
-                    if ((w & 0x7f80u) != 0x7f80u) continue;
-                    const float v = __uint_as_float(w << 16);
-                    if (p0 > 0.f) o[mt][nt][2 * y] += p0 * v;
-                    if (p1 > 0.f) o[mt][nt][2 * y + 1] += p1 * v;
-                  }
-              }
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t w = *reinterpret_cast<const uint16_t *>(vs + (key >> 3) * 8 * C::ROWB + (key & 7) * 128 + (mt >> 2) * 1024 +
+                                                                         ((((mt & 3) * 2 + y) ^ (key & 7)) << 4) + g * 2);
+                  if ((w & 0x7f80u) != 0x7f80u) continue;
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                      if (sees[nt][e]) o[mt][nt][2 * y + e] += __uint_as_float(w << 16);
+                }
             }
           }
         }

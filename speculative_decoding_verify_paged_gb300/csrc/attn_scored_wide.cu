@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             tmem_get(ts + 32, w + 32);
             tmem_landed(w);
             tmem_landed(w + 32);
+            uint32_t seen[kTile / 32];  // at an edge: the row's view of the tile's keys as bits
             // ---- scores ----
             if (cap == 0.f) {
 #pragma unroll
@@ -630,15 +631,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
             if (edge) {
 #pragma unroll
-              for (int q = 0; q < kTile / 32; ++q) {  // the row's view of 32 keys as bits
+              for (int q = 0; q < kTile / 32; ++q) {
                 const int b0 = base + 32 * q, first = reach + 1 - b0;
                 const uint32_t old = b0 >= 0 ? 0u : b0 <= -32 ? ~0u : (1u << -b0) - 1u;
                 const uint32_t near = first <= 0 ? ~0u : first >= 32 ? 0u : ~0u << first;
                 const uint32_t fresh = b0 >= 0 ? (b0 < 64 ? (uint32_t)(mask >> b0) : 0u) : (b0 > -32 ? (uint32_t)mask << -b0 : 0u);
-                const uint32_t seen = (old & near) | fresh;
+                seen[q] = (old & near) | fresh;
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                  if (!((seen >> k) & 1u)) w[q * 32 + k] = 0xff800000u;  // -inf
+                  if (!((seen[q] >> k) & 1u)) w[q * 32 + k] = 0xff800000u;  // -inf
               }
             }
             // ---- the running maximum ----
@@ -657,11 +658,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
             l += (part[0] + part[1]) + (part[2] + part[3]);
             if (odd) {
-              // infinities and NaN, for the rows that see their keys; then out of the tile
-              float weight[kTile];
+              // infinities and NaN, for the rows that see their keys, whatever the weight (one that is zero in fp32 is not
+              // zero); then out of the tile
               o_free();
-#pragma unroll
-              for (int k = 0; k < kTile; ++k) weight[k] = __uint_as_float(w[k]);
 #pragma unroll 1
               for (int k = 0; k < 4; ++k) {
                 uint32_t o[32];
@@ -669,8 +668,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 tmem_landed(o);
 #pragma unroll 1
                 for (int key = 0; key < kTile; ++key) {
-                  const float e = *(volatile float *)&weight[key];
-                  if (!(e > 0.f)) continue;
+                  if (!(((key < 32 ? seen[0] : seen[1]) >> (key & 31)) & 1u)) continue;
 #pragma unroll
                   for (int y = 0; y < 4; ++y) {
                     const uint4 u = *reinterpret_cast<const uint4 *>(vs + chunk_at(key, k * 4 + y));
@@ -678,8 +676,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                     for (int z = 0; z < 8; ++z) {
                       const uint32_t v = (word[z >> 1] >> (16 * (z & 1))) & 0xffffu;
-                      if ((v & 0x7f80u) == 0x7f80u)
-                        o[y * 8 + z] = __float_as_uint(__uint_as_float(o[y * 8 + z]) + e * __uint_as_float(v << 16));
+                      if ((v & 0x7f80u) == 0x7f80u) o[y * 8 + z] = __float_as_uint(__uint_as_float(o[y * 8 + z]) + __uint_as_float(v << 16));
                     }
                   }
                 }

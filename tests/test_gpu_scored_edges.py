@@ -82,3 +82,18 @@ def test_a_seen_nan_reaches_its_rows_and_no_others(dt, d, hq):
     assert torch.equal(torch.isnan(out), torch.isnan(want))
     keep = ~torch.isnan(want)
     assert torch.equal(out[keep], want[keep])
+
+
+@pytest.mark.parametrize("dt,d,hq", [("bf16", 64, 8), ("bf16", 128, 8), ("bf16", 128, 32), ("bf16", 128, 48), ("bf16", 256, 8), ("bf16", 96, 8),
+                                     ("e4m3", 128, 8), ("e4m3", 256, 8), ("f32", 64, 8)])
+def test_a_seen_nonfinite_value_counts_whatever_its_weight(dt, d, hq):
+    """A bias so steep that all weights but the nearest key's are zero in fp32: an infinity (E4M3: a NaN) among the
+    values of a key that is further back still reaches the rows that see it."""
+    kv, step, buf, msl = make(62, [200, 37], [5, 6], hq, 2, d, dt, ScoreMod(slopes=torch.full((hq,), 1000.0, device="cuda")))
+    clean = buf.attn_out.clone()
+    put(kv, 0, 202, 0x7F if dt == "e4m3" else float("inf"))  # the third of the new keys: rows 2 to 4 see it
+    out = again(kv, step, buf, msl)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[2:5, :, 0] = hit[2:5, :, d // 2 + 1] = True
+    assert not torch.isfinite(out[hit].float()).any()
+    assert torch.equal(out[~hit], clean[~hit])
