@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <limits>
 
 #include "sv_internal.cuh"
 
@@ -417,7 +418,7 @@ sv_status sv_spec_verify_attn_scored(const sv_paged_kv *kv, const void *q, void 
   a.scale_log2 = scale * kLog2e;
   a.wait_ns = g_wait_ns;
   a.stall = g_stall;
-  sa.cap = mod->softcap * kLog2e;
+  sa.cap = std::min(mod->softcap * kLog2e, std::numeric_limits<float>::max());  // (one that large changes no score)
   sa.window = mod->window;
   sa.slopes = mod->slopes;
   sa.positions = positions;

@@ -97,3 +97,10 @@ def test_a_seen_nonfinite_value_counts_whatever_its_weight(dt, d, hq):
     hit[2:5, :, 0] = hit[2:5, :, d // 2 + 1] = True
     assert not torch.isfinite(out[hit].float()).any()
     assert torch.equal(out[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("dt,d,hq", [("bf16", 128, 8), ("bf16", 128, 64), ("bf16", 96, 8), ("e4m3", 128, 8), ("f32", 64, 8)])
+@pytest.mark.parametrize("cap", [2.5e38, 3.4028234e38])
+def test_the_largest_caps_change_nothing(dt, d, hq, cap):
+    """Caps whose product with log2(e) is past fp32's range."""
+    make(63, [200, 33], [4, 2], hq, 2, d, dt, ScoreMod(softcap=cap))
