@@ -305,8 +305,13 @@ sv_status sv_qk_norm_rope(const sv_head_transform *transform, const void *q, int
  *   new_k, new_v, q, q_out  rows as in sv_qk_norm_rope, of kv->dtype (bf16 for an
  *              E4M3 pool); new_k and new_v with kv->num_kv_heads heads
  *   positions  int32 [total_q], or NULL: c_b + i for row i of sequence b (chains)
- * Rows past cu_q[batch] and every row of a call that fails are not written, in
- * the cache or in q_out.
+ * Rows past cu_q[batch] are not written, in the cache or in q_out, nor is any
+ * row of a call that finds an error in the status word or fails by one of
+ * sv_kv_append's all-or-nothing errors. A bad id that the table itself holds, for
+ * the partly filled block of a sequence, is one of those with ref_count; without,
+ * SV_ERR_BAD_BLOCK_ID is recorded when a row comes to it: the blocks have been
+ * taken by then, no row is written through that id, and how much of the call's
+ * other rows is written is open. Committed rows stay as they are.
  */
 sv_status sv_kv_append_rope(const sv_paged_kv *kv, const sv_head_transform *transform, const void *new_k,
                             int64_t k_row_stride, const void *new_v, int64_t v_row_stride, const void *q,
