@@ -2,9 +2,11 @@
 // warp-level matrix instructions; instantiated per head size in attn_scored_d*.cu.
 //
 // The mathematics (base-2 exponents; p_t the position of key t, c the committed tokens):
-//   s_t = cap tanh(scale <q, k_t> / cap) + slope (p_t - c),   o = sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m)
-// with everything in units of log2. The distance bias -slope (p_i - p_t) differs from the term above
-// by a constant of the row, which the softmax cancels: a key's term is the same for all rows of a head.
+//   s_t = cap tanh(scale <q, k_t> / cap) + slope (p_t - p_0),   o = sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m)
+// with everything in units of log2 and p_0 the position of the sequence's first row. The distance bias
+// -slope (p_i - p_t) differs from the term above by a constant of the row, which the softmax cancels: a key's
+// term is the same for all rows of a head. (Counted from c instead, rows whose positions lie far past c would
+// have terms so large that fp32 has no bits left for the scores.)
 // tanh(y) = 1 - 2 / (1 + 2^(2 y log2 e)): two special-function instructions; its absolute error,
 // about 2^-22, times the cap is what reaches a score (caps above kFastCap take tanhf).
 //
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   __shared__ uint64_t s_mask[RB];         // new keys that a row sees
   __shared__ int s_reach[RB], s_row[RB];  // last place out of the window, and row of the sequence (-1: padding)
   __shared__ float s_slope[RB];
-  __shared__ int s_place[64];  // position of a new row minus c
+  __shared__ int s_place[64];  // position of a new row minus the first one's
   __shared__ float s_m[WK][RB], s_l[WK][RB];
   __shared__ int s_patch;  // E4M3: a key of the piece's edge steps has a NaN code among its values
   __shared__ int s_scan[kWarps], s_first_b, s_first_base, s_top[kWarps];
@@ -502,7 +504,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
         s_slope[x] = biased ? P.s.slopes[head] * 1.4426950408889634f : 0.f;
         top = max(top, live ? pos : c);
       }
-      for (int x = tid; x < s.n; x += kC) s_place[x] = P.s.positions != nullptr ? P.s.positions[s.row0 + x] - c : x;
+      const int origin = P.s.positions != nullptr ? P.s.positions[s.row0] : c;  // the bias counts from here
+      for (int x = tid; x < s.n; x += kC) s_place[x] = P.s.positions != nullptr ? P.s.positions[s.row0 + x] - origin : x;
       top = __reduce_max_sync(0xffffffffu, top);
       if (lane == 0) s_top[warp] = top;
       if (F8 && tid == 0) s_patch = 0;
@@ -625,7 +628,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               const float2 sl = *reinterpret_cast<const float2 *>(&s_slope[(wr * NT + nt) * 8 + 2 * t]);
 #pragma unroll
               for (int u = 0; u < M; ++u) {
-                const float d0 = (float)(key0 + 16 * u + g - c), d1 = d0 + 8.f;
+                const float d0 = (float)(key0 + 16 * u + g - origin), d1 = (float)(key0 + 16 * u + g + 8 - origin);
                 sc[u][nt][0] = fmaf(sl.x, d0, sc[u][nt][0]);
                 sc[u][nt][1] = fmaf(sl.y, d0, sc[u][nt][1]);
                 sc[u][nt][2] = fmaf(sl.x, d1, sc[u][nt][2]);
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 #pragma unroll
               for (int h = 0; h < 2 * M; ++h) {
                 const int j = base + g + 8 * h;
-                const float place = (float)(j >= 0 && j < s.n ? s_place[j] : j);
+                const float place = (float)(j >= 0 && j < s.n ? s_place[j] : c + j - origin);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

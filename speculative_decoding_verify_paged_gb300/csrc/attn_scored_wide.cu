@@ -482,7 +482,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
       }
       together();  // both blocks are done with the previous piece's places
-      if (tid < s.n) s_place[tid] = P.s.positions != nullptr ? P.s.positions[s.row0 + tid] - c : tid;
+      const int origin = P.s.positions != nullptr ? P.s.positions[s.row0] : c;  // the bias counts from here
+      if (tid < s.n) s_place[tid] = P.s.positions != nullptr ? P.s.positions[s.row0 + tid] - origin : tid;
       const int warp_top = __reduce_max_sync(0xffffffffu, live ? where : c);
       if (lane == 0) s_top[warp] = warp_top;
       together();
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
             if (biased) {
               if (!edge) {
-                const float f0 = (float)base;
+                const float f0 = (float)(key0 - origin);
 #pragma unroll
                 for (int k = 0; k < kTile; ++k)
                   w[k] = __float_as_uint(fmaf(slope, f0 + (float)k, __uint_as_float(w[k])));
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kTile; ++k) {
                   const int j = base + k;
-                  const float place = (float)(j >= 0 && j < s.n ? s_place[j] : j);
+                  const float place = (float)(j >= 0 && j < s.n ? s_place[j] : c + j - origin);
                   w[k] = __float_as_uint(fmaf(slope, place, __uint_as_float(w[k])));
                 }
               }

@@ -104,3 +104,14 @@ def test_a_seen_nonfinite_value_counts_whatever_its_weight(dt, d, hq):
 def test_the_largest_caps_change_nothing(dt, d, hq, cap):
     """Caps whose product with log2(e) is past fp32's range."""
     make(63, [200, 33], [4, 2], hq, 2, d, dt, ScoreMod(softcap=cap))
+
+
+@pytest.mark.parametrize("dt,d,hq,n", [("bf16", 128, 8, 6), ("bf16", 128, 32, 6), ("bf16", 128, 8, 40), ("bf16", 64, 8, 6), ("e4m3", 128, 8, 6),
+                                       ("e4m3", 256, 8, 6), ("f32", 64, 8, 6)])
+@pytest.mark.parametrize("far", [1000, 1000000, 2000000000])
+def test_a_bias_between_positions_far_past_the_cache(dt, d, hq, n, far):
+    """Rows whose positions begin far past the committed keys: the bias goes by the distance between them, however
+    large the positions are (the usual tolerance of these caches)."""
+    ctx = [200, 37]
+    pos = np.concatenate([c + far + np.arange(n) // 2 for c in ctx])
+    make(64, ctx, [n, n], hq, 2, d, dt, ScoreMod(slopes=T.slopes(hq)), positions=torch.from_numpy(pos.astype(np.int32)).cuda())
