@@ -9,6 +9,7 @@ an error.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 from dataclasses import dataclass
@@ -302,9 +303,14 @@ _calls = None
 
 
 def _bound():
-    """The extension module with the library's entry points."""
+    """The extension module with the library's entry points, built first if it is absent or fits another torch."""
     global _calls
     lib = load()
+    from . import build as _build
+    with _lock:
+        if not _build.calls_fit():
+            _build.build_calls()
+            importlib.invalidate_caches()
     from . import _calls as module
     at = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
           for n in ("sv_qk_norm_rope", "sv_kv_append_rope", "sv_spec_verify_attn_scored",

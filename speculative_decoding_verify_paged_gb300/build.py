@@ -4,7 +4,7 @@ Each translation unit under csrc/ (CUDA .cu, host-only .cpp) compiles in its
 own nvcc process, in parallel; the objects link into one shared library with the CUDA runtime
 linked statically. csrc/torch_calls.cpp becomes the extension module _calls (g++,
 against the installed torch's headers). Rebuilds only when a source or header is
-newer than the built files.
+newer than the built files, one of them is missing, or another torch is installed.
 """
 from __future__ import annotations
 
@@ -23,6 +23,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 CALLS = os.path.join(PKG, "_calls.so")
+CALLS_FOR = os.path.join(BUILD, "calls_for")  # what _calls.so was built against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I" + INCLUDE, "-I" + CSRC]
@@ -43,14 +44,28 @@ def _deps():
     return _sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
+def _torch_here() -> str:
+    """The torch and the interpreter that _calls.so has to fit."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def calls_fit() -> bool:
+    """Whether _calls.so is there and was built against the torch that is installed."""
+    if not os.path.exists(CALLS) or not os.path.exists(CALLS_FOR):
+        return False
+    with open(CALLS_FOR) as f:
+        return f.read() == _torch_here()
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    if not os.path.exists(LIB) or not calls_fit():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def _build_calls() -> None:
+def build_calls() -> None:
     """The extension module _calls, against the torch that is installed."""
     import sysconfig
 
@@ -59,6 +74,7 @@ def _build_calls() -> None:
     gxx = os.environ.get("CXX") or shutil.which("g++")
     if not gxx:
         raise RuntimeError("g++ not found: the Python bindings cannot be built")
+    os.makedirs(BUILD, exist_ok=True)
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = [gxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I" + INCLUDE,
@@ -68,6 +84,8 @@ def _build_calls() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(CALLS_SRC)}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
+    with open(CALLS_FOR, "w") as f:
+        f.write(_torch_here())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -88,7 +106,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     srcs = _sources()
     with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        calls = ex.submit(_build_calls)
+        calls = ex.submit(build_calls)
         objs = list(ex.map(compile_one, srcs))
         calls.result()
     tmp = LIB + f".tmp{os.getpid()}"
