@@ -200,8 +200,10 @@ def run_step(kv: L.PagedKV, d: DeviceStep, buf: StepBuffers, max_seq_len: int, s
 
 
 def launches_per_step(d: DeviceStep, max_seq_len: int, kv: L.PagedKV) -> int:
-    """Kernels the library launches for one run_step (append 2, attention 1 or
-    2, sampler 2: statistics and decisions, rollback 1 or 2)."""
+    """Kernels the library launches for one run_step (append 2, and 1 for the private copies where a
+    transforming append may share blocks; attention 1 or 2, sampler 2: statistics and decisions, rollback
+    1 or 2)."""
     ws = attn_workspace_bytes(kv, d, max_seq_len)
-    n = 2 + (2 if ws > 0 else 1) + 2 + (2 if d.mask_kind == L.SV_MASK_TREE else 1)
+    n = 2 + (d.transform is not None and kv.ref_count is not None)
+    n += (2 if ws > 0 else 1) + 2 + (2 if d.mask_kind == L.SV_MASK_TREE else 1)
     return n
