@@ -50,3 +50,69 @@ def test_a_bad_id_of_a_partly_filled_block(batch, which, shared):
             assert ((y == x) | (y == z)).all()
         block = int(case.state.block_table[which, 0])  # what the bad id stands in for: untouched
         assert torch.equal(held[0][block], before[0][block]) and torch.equal(held[1][block], before[1][block])
+
+
+def nearest_code(y):
+    """The E4M3 code nearest to each y (ties to the even mantissa, saturating), and how far y is from the border to the
+    code on its other side, from the format: sign, exponent with bias 7, three mantissa bits, 448 the largest."""
+    c = np.arange(0x7F)
+    size = np.where(c < 8, c * 2.0 ** -9, (1 + c % 8 / 8) * 2.0 ** (c // 8 - 7.0))
+    a = np.minimum(np.abs(y), size[-1])
+    hi = np.searchsorted(size, a).clip(1, len(c) - 1)
+    lo = hi - 1
+    middle = (size[lo] + size[hi]) / 2
+    code = np.where((a > middle) | ((a == middle) & (hi % 2 == 0)), hi, lo)
+    other = np.minimum(np.abs(a - middle), np.where(code == hi, np.where(hi + 1 < len(c), (size[hi] + size[np.minimum(hi + 1, len(c) - 1)]) / 2 - a, np.inf),
+                                                    np.where(lo > 0, a - (size[np.maximum(lo - 1, 0)] + size[lo]) / 2, np.inf)))
+    return np.where(np.signbit(y), code | 0x80, code), other
+
+
+def test_keys_are_the_nearest_codes():
+    """Normalised and rotated keys in an E4M3 pool: the code nearest to the 64-bit y / scale wherever y is further from
+    a border between two codes than the fp32 arithmetic is off (2^-20 of the pair's size, as for the rows). Many of the values
+    would get another code if they went through bf16."""
+    for d, rot, kw in ((128, 128, {}), (64, 32, {"interleaved": True, "offset": 1.0}), (128, 64, {"norm": False})):
+        n, hkv = 64, 4
+        case = W.custom(72, batch=1, ctx_lens=[7], n_q=[n], num_q_heads=hkv, num_kv_heads=hkv, head_dim=d, block_size=16, vocab=16, dtype="e4m3",
+                        use_bank=False)
+        kv, step, buf = upload(case)
+        _, k, v, t, _ = T.make(n, hkv, hkv, d, torch.bfloat16, rot, **kw)
+        L.kv_append_rope(kv, t, k, v, step.cu_q, buf.status)
+        torch.cuda.synchronize()
+        assert status_of(buf) == 0
+        at = torch.arange(7, 7 + n, device="cuda")
+        got = kv.k_pool[kv.block_table[0][at // 16].long(), :, at % 16].cpu().numpy()
+        y, size = T.want_of(k, t.k_weight, np.arange(7, 7 + n), t)
+        want, room = nearest_code(y / kv.k_scale)
+        clear = room > 2.0 ** -20 * size / kv.k_scale
+        if t.k_weight is None:  # values that are neither normalised nor rotated are exact, ties (one in 32 of them) among them
+            clear[:, :, rot:] = True
+        assert clear.mean() > 0.99
+        # signs of zeros are the arithmetic's own
+        same = (got == want) | (((got | want) & 0x7F) == 0)
+        assert same[clear].all()
+        through_bf16, _ = nearest_code(torch.from_numpy(y).to(torch.bfloat16).double().numpy() / kv.k_scale)
+        assert (through_bf16 != want)[clear].sum() > 100
+
+
+def test_codes_of_nonfinite_values():
+    """A NaN is stored as the code 0x7F, an infinity as the largest finite value, by both appends alike."""
+    case = W.custom(73, batch=1, ctx_lens=[3], n_q=[4], num_q_heads=2, num_kv_heads=2, head_dim=64, block_size=16, vocab=16, dtype="e4m3", use_bank=False)
+    x = torch.randn(4, 2, 64, device="cuda").to(torch.bfloat16)
+    x[0, :, 3], x[1, :, 4] = float("nan"), -float("nan")
+    x[2, :, 5], x[3, :, 6] = float("inf"), -float("inf")
+    x.view(torch.int16)[0, 0, 9] = -1  # a NaN with every bit set
+    for rope in (False, True):
+        kv, d, buf = upload(case)
+        if rope:
+            L.kv_append_rope(kv, L.HeadTransform(), x, x, d.cu_q, buf.status)
+        else:
+            L.kv_append(kv, x, x, d.cu_q, buf.status)
+        torch.cuda.synchronize()
+        assert status_of(buf) == 0
+        at = torch.arange(3, 7, device="cuda")
+        for pool in (kv.k_pool, kv.v_pool):
+            got = pool[kv.block_table[0][at // 16].long(), :, at % 16]
+            assert (got[0, :, 3] == 0x7F).all() and (got[1, :, 4] == 0x7F).all() and got[0, 0, 9] == 0x7F
+            assert (got[2, :, 5] == 0x7E).all() and (got[3, :, 6] == 0xFE).all()
+            assert ((got & 0x7F) == 0x7F).sum() == 5
