@@ -111,6 +111,7 @@ __device__ __forceinline__ float2 turn(int position, float freq) {
                                    : s > 0 ? (hi << (64 - s)) | (lo >> s) : (s > -64 ? lo << -s : 0ull);
   if (bits >> 31) per = 0ull - per;
   const unsigned long long f = (unsigned long long)(long long)position * per;
+  if (e == 255) return make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));  // no angle: NaN
   float sn, cs;
   sincospif((float)(int)(f >> 32) * 4.656612873077393e-10f /* 2^-31 */, &sn, &cs);
   return make_float2(cs, sn);

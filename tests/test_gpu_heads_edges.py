@@ -116,3 +116,18 @@ def test_codes_of_nonfinite_values():
             assert (got[0, :, 3] == 0x7F).all() and (got[1, :, 4] == 0x7F).all() and got[0, 0, 9] == 0x7F
             assert (got[2, :, 5] == 0x7E).all() and (got[3, :, 6] == 0xFE).all()
             assert ((got & 0x7F) == 0x7F).sum() == 5
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,rot,kw", [(128, 128, {}), (64, 64, {"interleaved": True}), (40, 24, {})])
+def test_a_frequency_that_is_no_number(d, rot, kw, dtype):
+    """The angle of an infinite or NaN frequency is a NaN, in its pair of every head and nowhere else."""
+    q, k, _, t, pos = T.make(5, 4, 2, d, dtype, rot, **kw)
+    qo, ko, q1, k1 = (torch.empty(x.shape, dtype=dtype, device="cuda") for x in (q, k, q, k))
+    L.qk_norm_rope(t, q, k, pos, qo, ko)
+    t.inv_freq[1], t.inv_freq[3], t.inv_freq[4] = float("nan"), float("inf"), -float("inf")
+    L.qk_norm_rope(t, q, k, pos, q1, k1)
+    bad = [x for i in (1, 3, 4) for x in ((2 * i, 2 * i + 1) if kw.get("interleaved") else (i, i + rot // 2))]
+    good = [x for x in range(d) if x not in bad]
+    for x, y in ((qo, q1), (ko, k1)):
+        assert torch.isnan(y[:, :, bad]).all() and torch.equal(y[:, :, good], x[:, :, good])
