@@ -12,8 +12,8 @@
 // weighted sum, V under the scores (16-byte copies that no thread waits for; narrow caches are widened on
 // the way, and loaded in turn). A lane keeps a key for the scores and a column for the weighted sum.
 // Layouts, by the query rows a KV head can have:
-//  * more than 16: a warp keeps 8 rows (a 16-byte read of a key or a value meets 8 rows);
-//  * 5 to 16: a warp keeps 4;
+//  * more than 16, fp32 caches: a warp keeps 8 rows (a 16-byte read of a key or a value meets 8 rows);
+//  * 5 and more: a warp keeps 4;
 //  * 4 and fewer: the four warps share the rows: each takes a quarter of the head's values in the scores
 //    (summed through shared memory) and of the columns in the weighted sum. The softmax is computed four times.
 // Up to eight splits of a sequence are one thread-block cluster, whose CTAs merge their rows through shared
@@ -194,15 +194,24 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
       for (int w = 0; w < RW; ++w) dot[w] = 0.f;
       if (mine) {
         constexpr int kSpan = SHARED ? D / kWarps : D;
+        constexpr int kSum = kSpan % 32 == 0 ? 32 : kSpan;  // values of a partial sum: a sum in sums of 32 rounds less
         const int d0 = SHARED ? warp * kSpan : 0;
-#pragma unroll 8
-        for (int d = 0; d < kSpan; d += 4) {
-          const float4 kk = *reinterpret_cast<const float4 *>(&k_s[lane][d0 + d]);
+#pragma unroll 1
+        for (int d1 = d0; d1 < d0 + kSpan; d1 += kSum) {
+          float sum[RW];
 #pragma unroll
-          for (int w = 0; w < RW; ++w) {
-            const float4 qq = *reinterpret_cast<const float4 *>(&q_s[rw + w][d0 + d]);
-            dot[w] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, dot[w]))));
+          for (int w = 0; w < RW; ++w) sum[w] = 0.f;
+#pragma unroll
+          for (int d = 0; d < kSum; d += 4) {
+            const float4 kk = *reinterpret_cast<const float4 *>(&k_s[lane][d1 + d]);
+#pragma unroll
+            for (int w = 0; w < RW; ++w) {
+              const float4 qq = *reinterpret_cast<const float4 *>(&q_s[rw + w][d1 + d]);
+              sum[w] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, sum[w]))));
+            }
           }
+#pragma unroll
+          for (int w = 0; w < RW; ++w) dot[w] += sum[w];
         }
       }
       if constexpr (SHARED)
@@ -399,8 +408,9 @@ cudaError_t launch_n(const ScoredArgs &sa, cudaStream_t st) {
   };
   const long long rows = (long long)(sa.a.num_q_heads / sa.a.kv.num_kv_heads) * sa.a.max_q;
   if (rows <= 4) return go(attn_scored_simt_kernel<T, KT, NK, 4, true>);
-  if (rows <= 16 || sizeof(KT) < 4) return go(attn_scored_simt_kernel<T, KT, NK, 4, false>);
-  return go(attn_scored_simt_kernel<T, KT, NK, 8, false>);
+  if constexpr (sizeof(KT) == 4)
+    if (rows > 16) return go(attn_scored_simt_kernel<T, KT, NK, 8, false>);
+  return go(attn_scored_simt_kernel<T, KT, NK, 4, false>);
 }
 template <typename T, typename KT>
 cudaError_t launch_t(const ScoredArgs &sa, cudaStream_t st) {

@@ -115,3 +115,22 @@ def test_a_bias_between_positions_far_past_the_cache(dt, d, hq, n, far):
     ctx = [200, 37]
     pos = np.concatenate([c + far + np.arange(n) // 2 for c in ctx])
     make(64, ctx, [n, n], hq, 2, d, dt, ScoreMod(slopes=T.slopes(hq)), positions=torch.from_numpy(pos.astype(np.int32)).cuda())
+
+
+@pytest.mark.parametrize("hq,n", [(2, 1), (8, 1), (8, 3)])  # the CUDA-core kernels' three layouts of rows
+def test_small_products_next_to_large_ones(hq, n):
+    """fp32 caches: a score is a sum of sums of 32 products, so products that are each less than half a step of the whole
+    are not lost one by one. Key 0 has 224 products of 2^-5 next to one of 2^20 (a step there is 2^-3), the others none:
+    their scores differ by 7 scale. What is left is the rounding of the scores themselves, in base 2 of 378000, to half of 2^-5:
+    two of them move a weight p by 2 * 2^-6 ln 2 p (1 - p) <= 0.0055."""
+    kv, step, buf, msl = make(67, [1], [n], hq, 1, 256, "f32", ScoreMod())
+    blk, scale = int(kv.block_table[0, 0]), 0.25
+    kv.k_pool.zero_(), kv.v_pool.zero_(), step.q.fill_(1.0)
+    kv.k_pool[blk, 0, :1 + n, 0] = 2.0 ** 20
+    kv.k_pool[blk, 0, 0, 32:] = 2.0 ** -5
+    kv.v_pool[blk, 0, 0] = 1.0
+    step.scale = scale
+    out = T.f64(again(kv, step, buf, msl))
+    e = np.exp(7 * scale)
+    for i in range(n):
+        assert np.all(np.abs(out[i] - e / (e + i + 1)) <= 0.0055)
