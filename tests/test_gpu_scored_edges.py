@@ -2,6 +2,10 @@
 
 A row that does not see such a key has the bits that it has with a finite value in the key's place: weights of unseen
 keys are zero either way. Nothing here is compared within a tolerance unless a test says so."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -115,6 +119,54 @@ def test_a_bias_between_positions_far_past_the_cache(dt, d, hq, n, far):
     ctx = [200, 37]
     pos = np.concatenate([c + far + np.arange(n) // 2 for c in ctx])
     make(64, ctx, [n, n], hq, 2, d, dt, ScoreMod(slopes=T.slopes(hq)), positions=torch.from_numpy(pos.astype(np.int32)).cuda())
+
+
+@pytest.mark.parametrize("dt,d,n", [("bf16", 128, 2), ("e4m3", 64, 1), ("bf16", 128, 17), ("f32", 32, 1)])
+def test_more_sequences_than_threads(dt, d, n):
+    """Batches past the 256 and 384 sequences that a CTA's threads take at once."""
+    count = 900
+    ctx = [(13 * b) % 50 for b in range(count)]
+    nq = [1 + b % n for b in range(count)]
+    make(65, ctx, nq, 4, 1, d, dt, ScoreMod(softcap=20.0, window=33))
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+from speculative_decoding_verify_paged_gb300 import HeadTransform, ScoreMod, _lib as L, step as S, workloads as W
+case = W.custom(66, batch=2, ctx_lens=[40, 90], n_q=[{n}, {n}], num_q_heads=8, num_kv_heads=2, head_dim={d}, block_size=16, vocab=16, dtype={dt!r}, use_bank=False)
+kv, d = S.device_kv(case.state, "cuda"), S.DeviceStep.from_host(case.step, "cuda")
+inv = torch.full(({d} // 2,), 0.1, device="cuda")
+d.transform, d.mod = HeadTransform(inv_freq=inv), ScoreMod(softcap=20.0, window=30)
+buf = S.StepBuffers.make(kv, d, 90 + {n})
+table, free, top = kv.block_table.clone(), kv.free_list.clone(), kv.free_top.clone()
+buf.attn_out.zero_()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    S.append(kv, d, buf)
+    S.attention(kv, d, buf, 90 + {n})
+g.replay()
+torch.cuda.synchronize()
+assert int(buf.status.item()) == 0
+first = buf.attn_out.clone()
+kv.block_table.copy_(table), kv.free_list.copy_(free), kv.free_top.copy_(top)
+S.append(kv, d, buf)
+S.attention(kv, d, buf, 90 + {n})
+torch.cuda.synchronize()
+assert int(buf.status.item()) == 0 and torch.equal(first, buf.attn_out) and bool((first != 0).any())
+"""
+
+
+@pytest.mark.parametrize("dt,d,n", [("bf16", 128, 3), ("bf16", 128, 40), ("e4m3", 64, 3), ("f32", 64, 3)])
+def test_the_first_call_of_a_process_may_be_captured(dt, d, n):
+    """Nothing has run yet when the transforming append and the attention are captured; the graph gives the bits of the
+    calls."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL_IN_A_CAPTURE.format(root=os.path.dirname(here), tests=here, dt=dt, d=d, n=n)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("hq,n", [(2, 1), (8, 1), (8, 3)])  # the CUDA-core kernels' three layouts of rows
