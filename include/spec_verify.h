@@ -256,8 +256,8 @@ sv_status sv_spec_verify_attn_no_alloc(const sv_paged_kv *kv, const void *q, voi
  *   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
  * over the pairs i < rotary_dim / 2 of the head's first rotary_dim values:
  * (y_i, y_{i + rotary_dim/2}), or (y_2i, y_{2i+1}) when interleaved is 1. The
- * arithmetic is fp32, the angle fp64 up to its reduction to a fraction of a
- * turn, and the result is rounded once, to the output's type.
+ * arithmetic is fp32, the angle a fraction of a turn in 64 bits up to its one
+ * rounding to fp32, and the result is rounded once, to the output's type.
  *   inv_freq       float [rotary_dim / 2], device; NULL with rotary_dim 0 (no
  *                  rotation). rotary_dim is even, at most head_dim
  *   q_weight, k_weight  [head_dim] of the rows' type, device, 16-byte aligned;
@@ -341,9 +341,17 @@ typedef struct sv_score_mod {
  *   cap(scale * <q, k_t>) - slopes[h] * (p_i - p_t).
  * Committed keys are at p_t = t, new row j at p_j = positions[cu_q[b] + j], or
  * c_b + j with positions NULL. A key is visible if sv_spec_verify_attn's mask
- * shows it and its distance is below the window. Softmax and accumulation are
- * fp32; a row that sees no key gets zeros; what a key that no row sees holds
- * (NaN and infinities too) does not reach the output.
+ * shows it and its distance is below the window. A row that sees no key gets
+ * zeros; what a key holds (NaN and infinities too) reaches the rows that see it
+ * and no others.
+ * Scores, softmax statistics and sums are fp32, and the output is rounded once.
+ * Fewer bits are in two places of the tensor-core kernels (bf16 and E4M3 pools,
+ * head_dim 64, 128 or 256, blocks of 8 tokens and more): the weights that V is
+ * multiplied with are rounded to bf16 (off by 2^-8 of themselves at most; over an
+ * E4M3 pool to fp16, 2^-11), and over an E4M3 pool so are the queries, to fp16:
+ * 2^-11, elements below 2^-14 by up to 2^-25, and one beyond 65504 records
+ * SV_ERR_NONFINITE. The CUDA-core kernels (the other sizes, and fp32) round
+ * neither. A capped score is off by at most 2^-19 of the cap.
  *   positions  int32 [total_q] or NULL; each at least c_b, the first position
  *              after the committed keys (a smaller one sets SV_ERR_BAD_LENGTH
  *              and leaves that sequence's rows undefined)

@@ -10,15 +10,24 @@
 // tanh(y) = 1 - 2 / (1 + 2^(2 y log2 e)): two special-function instructions; its absolute error,
 // about 2^-22, times the cap is what reaches a score (caps above kFastCap take tanhf).
 //
+// Fewer bits than fp32, and why: the weights are rounded to the type of V's operand, bf16 (off by 2^-8 of themselves at
+// most) or, over E4M3 pools, fp16 (2^-11), since a matrix instruction takes operands of one type; the sum of the weights
+// is of the unrounded ones. Over E4M3 pools the queries are fp16 for the same reason (2^-11; what lies below 2^-14
+// is off by up to 2^-25, beyond 65504 the call records SV_ERR_NONFINITE). The cap's 2^x and reciprocal are the
+// approximate ones: 2^-19 of the cap at most, far below what the rounded weights leave. Against 64 bits a bf16 row is off by
+// 0.0023 of its size, where one rounding of the output alone leaves 0.0017.
+//
 // Bound: memory up to some 16 query rows a unit (one KV head of one sequence: G n_b rows), where 70 us for
-// 32 sequences of 2K to 4K tokens are 83% of the measured copy rate; the warps' matrix instructions beyond
-// (16 x 8 x 16 in 8 cycles of a quarter SM: with 24 rows a warp 1540 of the 1800 cycles that two warps'
-// steps take). Units of more than kWideRows rows go to attn_scored_wide.cu, whose blocks of 128 rows cost too
-// much for fewer (40 rows: 93 us here, 97 there; in sequences of 600 tokens 94 and 121).
+// 32 sequences of 2K to 4K tokens are 83% of the measured copy rate; beyond, the chain of a warp's step, ldmatrix ->
+// products -> scores -> movmatrix -> products, of which the two warps of a scheduler hide only a part: with 24 rows a warp a step of
+// 16 keys is 48 products of 16 x 8 x 16 at 8 cycles of a quarter SM, and two warps' 768 cycles of products
+// stand in the 1800 that their steps take (43%). Units of more than kWideRows rows go to
+// attn_scored_wide.cu, whose blocks of 128 rows cost too much for fewer (40 rows: 93 us here, 97 there; in
+// sequences of 600 tokens 94 and 121).
 //
 // Times (us, 8 KV heads of 128 values; share of the copy rate): 32 sequences of 2K to 4K tokens in bf16 with 4,
 // 16, 32 and 48 rows a KV head 69 (85%), 75, 94 (66%), 96 (63%); 32 x 6 rows over 0.5K to 4K tokens, capped, 60.5
-// (72%); four sequences of 32K tokens in E4M3 53 (73%); 128 sequences in a window of 1024, biased, 90 (45%: 4
+// (72%); four sequences of 32K tokens in E4M3 53 (74%); 128 sequences in a window of 1024, biased, 88 (46%: 4
 // short units a CTA, each 7000 cycles of setting up and merging).
 //
 // Work: as many CTAs as fit the GPU stay for the whole launch. The key tiles of all units laid end
@@ -42,8 +51,8 @@
 // Query rows sit on the n dimension, so that 24 rows (4 heads x 6) cost 24 and not 32. At the end
 // of a piece the WK key groups' (m, l, O) are merged through shared memory, 8 rows of each warp at a time.
 //
-// A warp's step is a chain of products, special functions and products again, so it is made large (16 or 32
-// keys for up to 24 rows) and two CTAs of four consumers share an SM: their registers go by role (kConsumerRegs).
+// A warp's step is a chain of products, special functions and products again, so it is made large (32 keys where
+// registers allow, Cfg::M, else 16) and two CTAs of four consumers share an SM: their registers go by role (kConsumerRegs).
 // (16 to 18 warps of 8 rows each, which read K and V from shared memory once a row group: 32 x 6 rows 62 us, but
 // wide units 154 against 96. No split of registers, three consumers: 70.) Steps at the edges (new rows, the
 // window's start) see keys as bits of a row and are kept out of the way of the others.

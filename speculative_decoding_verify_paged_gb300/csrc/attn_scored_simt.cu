@@ -21,7 +21,7 @@
 //
 // Bound: shared-memory reads (8 + 4 wavefronts to 32 FMAs of a warp in the scores), and latency for short
 // splits. fp32, us: 4 sequences of 37 to 200 tokens, 5 rows, two heads of 64 values 12; 8 sequences of 1K to 2K
-// tokens, eight heads of 128 values: 4, 16 and 64 rows a KV head 45, 65, 275 (without asynchronous copies, four
+// tokens, eight heads of 128 values: 4, 16 and 64 rows a KV head 45, 63, 260 (without asynchronous copies, four
 // rows a warp throughout: 91, 105, 357).
 // Splits that the window leaves no key in write an empty partial (log-sum-exp -inf). A visible
 // NaN makes its row's sum and log-sum-exp NaN, and the merge of the splits carries it on.

@@ -10,7 +10,7 @@
 // and write are a chain, and two warps a scheduler hide only part of it.
 //
 // Times (us, bf16, 8 KV heads of 128 values; in brackets the warp-matrix kernels of attn_scored.cuh):
-//   16 trees of 61 rows x 4 heads over 8192 tokens, capped 194 [455], 690 TFLOP/s;
+//   16 trees of 61 rows x 4 heads over 8192 tokens, capped 192 [455], 690 TFLOP/s;
 //   32 sequences over 2K to 4K tokens: 256 rows a KV head 177 capped, 147 without [407 capped],
 //   128 rows 116, 108 [270], 100 rows 107 [271], 72 rows 106 [168], 64 rows 97 [106].
 //
@@ -41,6 +41,9 @@
 // Edge tiles (new rows, the window's start, the end) see keys as bits of a row. Values past the end of
 // the sequence are set to zero in the stage; infinities and NaN of keys that some row does not see are
 // taken out of it too, and added to the rows that see them by hand.
+//
+// Weights are bf16 for the product with V (2^-8 of themselves at most), and the cap's reciprocals and 2^x the approximate
+// ones (2^-19 of the cap), as in attn_scored.cuh.
 //
 // All waits are bounded, as in attn_scored.cuh.
 #include <algorithm>

@@ -100,7 +100,9 @@ __device__ __forceinline__ uint2 quantize8(const float (&x)[8], float scale, flo
 
 // cos and sin of position * freq. A turn is 2^64: freq = M 2^E turns by M 2^E / (2 pi) per position, the
 // product of M with the first 64 bits of 2^66 / (2 pi), shifted; times the position it wraps exactly.
-// Off by under |position freq| 2^-64 turns; the upper 32 bits, rounded to fp32, go to sincospif.
+// The cut digits of 1 / (2 pi) leave a position's turn off by |freq| / 4 units of 2^-64 and the shift by one more, so
+// the whole by |position| (1 + |freq| / 4) 2^-64 turns (2^-33 at position 2^31); its upper 32 bits, which leave out 2^-32 of a
+// turn, are rounded to fp32 and go to sincospif.
 __device__ __forceinline__ float2 turn(int position, float freq) {
   const uint32_t bits = __float_as_uint(freq);
   const int e = (bits >> 23) & 255;
