@@ -914,7 +914,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
 #pragma unroll 1
           for (int key = max(p.kt0 * TK, lo); key < ke && !hit; ++key) {
             const int key0 = key & ~(16 * M - 1), place = key - c;
-            if (!(key0 + 16 * M > min(c, ke) || key0 < all_see)) continue;  // not an edge step
+            if (!(key0 + 16 * M > min(c, ke) || key0 < all_see)) {  // on to the next edge step
+              key = (min(c, ke) & ~(16 * M - 1)) - 1;
+              continue;
+            }
             if (!(place < 0 ? place > s_reach[rl] : (s_mask[rl] >> place) & 1ull)) continue;
             const int id = kv.block_table[(size_t)at.b * kv.max_blocks + (key >> bs_shift)];
             if (id < 0 || id >= kv.num_blocks) continue;

@@ -186,3 +186,18 @@ def test_small_products_next_to_large_ones(hq, n):
     e = np.exp(7 * scale)
     for i in range(n):
         assert np.all(np.abs(out[i] - e / (e + i + 1)) <= 0.0055)
+
+
+@pytest.mark.parametrize("dt,d,hq", [("e4m3", 128, 8), ("e4m3", 64, 48), ("bf16", 128, 8), ("bf16", 128, 64), ("f32", 64, 8)])
+def test_nan_among_committed_and_new_keys_of_long_sequences(dt, d, hq):
+    """A NaN in the middle of the committed keys reaches every row, one in a new key the rows from it on; over many splits."""
+    n = 5
+    kv, step, buf, msl = make(68, [9000, 40], [n, n], hq, 2, d, dt, ScoreMod(softcap=20.0))
+    want = buf.attn_out.clone()
+    nan = 0x7F if dt == "e4m3" else float("nan")
+    for t, first in ((9002, 2), (4321, 0)):
+        put(kv, 0, t, nan)
+        want[first:n, :, 0] = want[first:n, :, d // 2 + 1] = float("nan")
+        out = again(kv, step, buf, msl)
+        assert torch.equal(torch.isnan(out), torch.isnan(want))
+        assert torch.equal(out[~torch.isnan(want)], want[~torch.isnan(want)])
