@@ -109,6 +109,12 @@ struct Cfg {
   static constexpr int kConsumers = 4, kThreads = 256, kCtasPerSm = 2;
   static_assert(WK * WR == kConsumers, "a consumer on each quarter of the SM");
   static constexpr int ROWB = D * (F8 ? 1 : 2);  // bytes of a key's row
+  // Infinities and NaN that an edge step takes out of its values come back to the rows that see their keys at the
+  // end of the piece, from the pool, else in the step. One way or the other hardly ever runs; what it does to the loop's
+  // code is what differs (us, 32 sequences of 0.5K to 4K tokens): heads of 64, one and six tokens 35.1 and 37.8 here, 41.9
+  // and 40.5 in the step; heads of 128 60.7 and 59.5, 40 rows in short sequences 97 and 92; E4M3, four
+  // sequences of 32K tokens 53 and 60.
+  static constexpr bool kLate = F8 || D == 64;
   // Positions of a unit's lead-in. 24 rows a warp: 5 against 4 90 and 94 us (128 units a window), 60.4 and 61.6 (32 x 6
   // rows), 7 gains nothing more; fewer rows: one token of 32 sequences 69.4 and 68.5 us.
   static constexpr int kAlpha = NT >= 3 ? 5 : 4;
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
   __shared__ float s_slope[RB];
   __shared__ int s_place[64];  // position of a new row minus the first one's
   __shared__ float s_m[WK][RB], s_l[WK][RB];
-  __shared__ int s_patch;  // E4M3: a key of the piece's edge steps has a NaN code among its values
+  __shared__ int s_patch;  // a key of the piece's edge steps has an infinity or NaN among its values (kLate)
   __shared__ int s_scan[kWarps], s_first_b, s_first_base, s_top[kWarps];
 
   const AttnArgs &a = P.s.a;
@@ -517,7 +523,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
       for (int x = tid; x < s.n; x += kC) s_place[x] = P.s.positions != nullptr ? P.s.positions[s.row0 + x] - origin : x;
       top = __reduce_max_sync(0xffffffffu, top);
       if (lane == 0) s_top[warp] = top;
-      if (F8 && tid == 0) s_patch = 0;
+      if (C::kLate && tid == 0) s_patch = 0;
 
       // ---- Q into registers ----
       uint32_t q[NT][KT][2];
@@ -690,20 +696,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                          : nonfinite(w.x) | nonfinite(w.y) | nonfinite(w.z) | nonfinite(w.w)) != 0u;
             }
             odd = __any_sync(0xffffffffu, odd);
-            if constexpr (F8) {  // NaN codes become zeros in the stage; the rows that see a key get them at the piece's end
+            if constexpr (C::kLate) {  // the rows that see a key get them at the piece's end
               if (odd) {
 #pragma unroll 1
                 for (int y = lane; y < kChunks * 4; y += 32) {
                   uint32_t *w = reinterpret_cast<uint32_t *>(vs) + y;
-                  const uint32_t out = nan_codes(*w);
+                  const uint32_t out = F8 ? nan_codes(*w) : nonfinite(*w);
                   if (out == 0u) continue;
-                  *w &= ~out;
+                  if (F8) *w &= ~out;  // (one product for all steps)
                   const int key = key0 + (C::ROWB >= 128 ? y / (2 * C::ROWB) * 8 + y / 32 % 8 : y / 16);
                   if (key >= lo && key < ke) s_patch = 1;
                 }
-                fence_async();  // before the next copies into the stage
+                if (F8) fence_async();  // before the next copies into the stage
               }
-              if (odd || WR > 1) {  // (another row group may have been here since the first values were read)
+              if (F8 && (odd || WR > 1)) {  // (another row group may have been here since the first values were read)
                 __syncwarp();
 #pragma unroll
                 for (int y = 0; y < PV - 1; ++y) ldm4t(vf[y], v_at(y));
@@ -794,6 +800,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           };
           if (F8 || !odd) {
             pv(std::false_type());
+          } else if (C::kLate) {
+            pv(std::true_type());
           } else {
             pv(std::true_type());
             // The infinities and NaN set to zero above, for the rows that see their keys, whatever the weight: a weight that
@@ -861,7 +869,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           }
           together();
           if (nt == 0 && d0 == 0) {  // every group's weight in a row, over the rows' total
-            patch = F8 && s_patch != 0;
+            patch = C::kLate && s_patch != 0;
             for (int rl = tid; rl < rows; rl += kC) {
               float mx = s_m[0][rl], tot = 0.f;
 #pragma unroll
@@ -903,16 +911,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
           together();
         }
       if (patch) {
-        // The NaN codes that edge steps took out, for the rows that see their keys: looked for in the pool again and put over what
-        // has been written. (This hardly ever runs. In the steps' loop, as for bf16, it made four sequences of 32K
-        // tokens take 60 us, without it 54, here 53; bf16 in this form 32 x 6 rows 61.7 us, 40 rows in short sequences
-        // 97, in the loop 60.4 and 92.)
+        // The infinities and NaN that edge steps took out, for the rows that see their keys, whatever the weight: looked for in
+        // the pool again and added to what has been written.
 #pragma unroll 1
         for (int x = tid; x < rows * D; x += kC) {
           const int rl = x / D, d = x % D;
-          bool hit = false;
+          float add = 0.f;
 #pragma unroll 1
-          for (int key = max(p.kt0 * TK, lo); key < ke && !hit; ++key) {
+          for (int key = max(p.kt0 * TK, lo); key < ke; ++key) {
             const int key0 = key & ~(16 * M - 1), place = key - c;
             if (!(key0 + 16 * M > min(c, ke) || key0 < all_see)) {  // on to the next edge step
               key = (min(c, ke) & ~(16 * M - 1)) - 1;
@@ -921,15 +927,17 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
             if (!(place < 0 ? place > s_reach[rl] : (s_mask[rl] >> place) & 1ull)) continue;
             const int id = kv.block_table[(size_t)at.b * kv.max_blocks + (key >> bs_shift)];
             if (id < 0 || id >= kv.num_blocks) continue;
-            const size_t row = ((size_t)id * kv.num_kv_heads + kvh) * kv.block_size + (key & (kv.block_size - 1));
-            hit = (static_cast<const uint8_t *>(kv.v_pool)[row * D + d] & 0x7f) == 0x7f;
+            const size_t from = (((size_t)id * kv.num_kv_heads + kvh) * kv.block_size + (key & (kv.block_size - 1))) * D + d;
+            const uint32_t w = F8 ? static_cast<const uint8_t *>(kv.v_pool)[from] : static_cast<const uint16_t *>(kv.v_pool)[from];
+            if ((F8 ? nan_codes(w) : nonfinite(w)) != 0u) add += __uint_as_float(F8 ? 0x7fffffffu : w << 16);
           }
-          if (!hit) continue;
+          if (add == 0.f) continue;
           if (p.whole) {
             const int i = s_row[rl], head = kvh * P.G + (rb * RB + rl) - i * P.G;
-            reinterpret_cast<uint16_t *>(a.out)[((size_t)(s.row0 + i) * a.num_q_heads + head) * D + d] = 0x7fff;
+            __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(a.out) + ((size_t)(s.row0 + i) * a.num_q_heads + head) * D + d;
+            *dst = __float2bfloat16_rn(__bfloat162float(*dst) + add);
           } else {
-            P.part_o[(slot + rl) * D + d] = __uint_as_float(0x7fffffffu);
+            P.part_o[(slot + rl) * D + d] += add;
           }
         }
         together();
