@@ -4,6 +4,7 @@
 // are handed over by address (bind), so this module links to nothing of it.
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <stdexcept>
@@ -168,8 +169,8 @@ template <typename F> PyObject *answer(Py_ssize_t n, Py_ssize_t want, F call) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, e.what());
   } catch (const std::invalid_argument &e) {
     PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const std::exception &e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own, as torch raises them (out of memory among them)
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -11,6 +11,7 @@ import pytest
 import torch
 
 from speculative_decoding_verify_paged_gb300 import ScoreMod
+from speculative_decoding_verify_paged_gb300 import _lib as L
 from speculative_decoding_verify_paged_gb300 import step as S
 from speculative_decoding_verify_paged_gb300 import workloads as W
 
@@ -201,3 +202,25 @@ def test_nan_among_committed_and_new_keys_of_long_sequences(dt, d, hq):
         out = again(kv, step, buf, msl)
         assert torch.equal(torch.isnan(out), torch.isnan(want))
         assert torch.equal(out[~torch.isnan(want)], want[~torch.isnan(want)])
+
+
+def test_no_memory_for_the_workspace():
+    """The workspace that a call takes for itself fails as any tensor does, and the call is none the worse for it."""
+    kv, step, buf, _ = make(69, [300], [40], 8, 2, 128, "bf16", ScoreMod())
+    clean = buf.attn_out.clone()
+    out = torch.zeros_like(clean)
+    call = lambda: L.spec_verify_attn_scored(kv, step.q, out, step.cu_q, max_q=40, max_seq_len=1 << 20, scale=step.scale, mod=ScoreMod(), status=buf.status)  # noqa: E731
+    need = L.spec_verify_attn_scored_workspace_bytes(kv, 8, 40, 40, 1 << 20)
+    assert need > 20 << 20  # not from the allocator's small blocks
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(1e-6)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            call()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert not out.any()
+    call()
+    torch.cuda.synchronize()
+    assert status_of(buf) == 0 and torch.isfinite(out.float()).all() and out.any()
