@@ -15,8 +15,10 @@
  *
  * For models with head norms and rotary positions sv_kv_append_rope takes the
  * place of sv_kv_append (sv_qk_norm_rope does the same to rows outside the
- * cache), and for models with capped scores, a distance bias or a sliding
- * window sv_spec_verify_attn_scored that of sv_spec_verify_attn.
+ * cache; the _axes forms of both take positions with several axes), and for
+ * models with capped scores, a distance bias or a sliding window
+ * sv_spec_verify_attn_scored that of sv_spec_verify_attn. sv_kv_gather reads
+ * rows back out of the cache.
  *
  * Between steps, on the host, sv_adaptive_k_update turns the accept counts
  * into each sequence's draft length for the next step. sv_kv_fork lets new
@@ -85,8 +87,9 @@ typedef enum sv_status {
 } sv_status;
 
 /* SV_DTYPE_E4M3 (8-bit floating point: sign, 4 exponent bits with bias 7, 3
- * mantissa bits, no infinity, largest finite 448) is a KV-pool type only. */
-typedef enum sv_dtype { SV_DTYPE_BF16 = 0, SV_DTYPE_F32 = 1, SV_DTYPE_E4M3 = 2 } sv_dtype;
+ * mantissa bits, no infinity, largest finite 448) and SV_DTYPE_E2M1 (4-bit codes
+ * with a scale for each 16 of them, see sv_paged_kv) are KV-pool types only. */
+typedef enum sv_dtype { SV_DTYPE_BF16 = 0, SV_DTYPE_F32 = 1, SV_DTYPE_E4M3 = 2, SV_DTYPE_E2M1 = 3 } sv_dtype;
 
 typedef enum sv_mask_kind { SV_MASK_CAUSAL = 0, SV_MASK_TREE = 1 } sv_mask_kind;
 
@@ -113,10 +116,14 @@ typedef enum sv_mask_kind { SV_MASK_CAUSAL = 0, SV_MASK_TREE = 1 } sv_mask_kind;
  *                    below keep it so.
  *   k_scale, v_scale dequantisation scales of an SV_DTYPE_E4M3 pool (the value
  *                    of a stored code is its E4M3 value times the scale);
- *                    finite and > 0; ignored for the other types.
+ *                    finite and > 0; and of an SV_DTYPE_E2M1 pool (times its
+ *                    block scale too), in [2^-64, 2^64]; ignored for the
+ *                    other types.
+ *   k_block_scales, v_block_scales  of an SV_DTYPE_E2M1 pool, else not read:
+ *                    uint8 [num_blocks, num_kv_heads, block_size, head_dim / 16],
+ *                    16-byte aligned: E4M3 codes, one for 16 values of a row
  * block_size: a power of two in [1, 256]; head_dim: a multiple of 8 in
- * [8, 256] (of 16 for E4M3); dtype: SV_DTYPE_BF16, SV_DTYPE_F32 or
- * SV_DTYPE_E4M3.
+ * [8, 256] (of 16 for E4M3, of 32 for E2M1); dtype: an sv_dtype.
  *
  * fp8 pools (SV_DTYPE_E4M3; the pages mention KV-cache quantisation without a
  * format, "LLM serving: speculative decoding and PagedAttention memory
@@ -132,6 +139,20 @@ typedef enum sv_mask_kind { SV_MASK_CAUSAL = 0, SV_MASK_TREE = 1 } sv_mask_kind;
  * exactly, rounds the queries and the softmax weights to fp16 and applies the
  * scales to the scores and the outputs in fp32, so a query element beyond the
  * fp16 range (|q| > 65504) records SV_ERR_NONFINITE there.
+ *
+ * 4-bit pools (SV_DTYPE_E2M1): k_pool and v_pool hold [num_blocks, num_kv_heads,
+ * block_size, head_dim / 2] bytes, two codes each, the value of the even index
+ * in the lower four bits. A code is a sign, two exponent bits and one of the
+ * mantissa: 0, 0.5, 1, 1.5, 2, 3, 4 or 6. A value of the cache is code * s *
+ * scale, with s the E4M3 number in the block scales that stands for the 16
+ * values of its row from a multiple of 16 on: 4.5 bits a value. New rows,
+ * queries and outputs are bf16. The appends store, in fp32 with each operation
+ * rounded to nearest,
+ *   s    = the E4M3 number nearest to max |x| * (1 / (6 * scale)) over the 16 values,
+ *   code = the E2M1 number nearest to x * (1 / (s * scale)), zero where s is zero,
+ * ties to the even mantissa, saturating (at 448 and 6; an infinity too). A NaN
+ * makes the scale of its 16 values the NaN code 0x7F, and nothing else does;
+ * attention and sv_kv_gather read 16 NaN there.
  */
 typedef struct sv_paged_kv {
   void *k_pool;
@@ -150,6 +171,8 @@ typedef struct sv_paged_kv {
   int32_t *ref_count;
   float k_scale;
   float v_scale;
+  void *k_block_scales;
+  void *v_block_scales;
 } sv_paged_kv;
 
 /*
@@ -170,7 +193,8 @@ typedef struct sv_paged_kv {
  * So of w writers into a block held by r, the first min(w, r - 1) copy and a
  * last writer that holds the only remaining reference writes in place. New
  * blocks get count 1.
- *   new_k, new_v  [total_q, num_kv_heads, head_dim] of kv->dtype (bf16 for an E4M3 pool)
+ *   new_k, new_v  [total_q, num_kv_heads, head_dim] of kv->dtype (bf16 for an E4M3 or
+ *                 E2M1 pool)
  *   cu_q          int32 [batch + 1], cu_q[0] = 0, cu_q[batch] = total_q
  *   status_dev    int32 [1], required
  * All or nothing: if the blocks would not fit the block table
@@ -212,6 +236,8 @@ size_t sv_spec_verify_attn_workspace_bytes(const sv_paged_kv *kv, int32_t num_q_
  *   status_dev  int32 [1] or NULL
  * Block ids outside [0, num_blocks) set SV_ERR_BAD_BLOCK_ID; the rows of that
  * sequence are then undefined, no out-of-bounds memory is touched.
+ * Over an SV_DTYPE_E2M1 pool this is sv_spec_verify_attn_scored with nothing
+ * modified, with that call's workspace, limits and precision.
  */
 sv_status sv_spec_verify_attn(const sv_paged_kv *kv, const void *q, void *out, const int32_t *cu_q,
                               int32_t num_q_heads, int32_t total_q, int32_t max_q_per_seq,
@@ -299,11 +325,11 @@ sv_status sv_qk_norm_rope(const sv_head_transform *transform, const void *q, int
  *
  * Block allocation, copy-on-write, order, errors and the status word are those
  * of sv_kv_append. The stored key is the transformed one, rounded once to the
- * pool's type (for SV_DTYPE_E4M3 from fp32: nearest code to y / k_scale);
- * values are stored as sv_kv_append stores them. With num_q_heads > 0 the
+ * pool's type (for SV_DTYPE_E4M3 from fp32: nearest code to y / k_scale; for
+ * SV_DTYPE_E2M1 from fp32 too); values are stored as sv_kv_append stores them. With num_q_heads > 0 the
  * transformed queries go to q_out in the same pass.
  *   new_k, new_v, q, q_out  rows as in sv_qk_norm_rope, of kv->dtype (bf16 for an
- *              E4M3 pool); new_k and new_v with kv->num_kv_heads heads
+ *              E4M3 or E2M1 pool); new_k and new_v with kv->num_kv_heads heads
  *   positions  int32 [total_q], or NULL: c_b + i for row i of sequence b (chains)
  * Rows past cu_q[batch] are not written, in the cache or in q_out, nor is any
  * row of a call that finds an error in the status word or fails by one of
@@ -318,6 +344,57 @@ sv_status sv_kv_append_rope(const sv_paged_kv *kv, const sv_head_transform *tran
                             int64_t q_row_stride, void *q_out, int64_t q_out_row_stride, int32_t num_q_heads,
                             const int32_t *cu_q, int32_t total_q, const int32_t *positions, int32_t *status_dev,
                             void *stream);
+
+/*
+ * Positions with several axes (time, height and width of an image's or a
+ * video's tokens): pair i of a head turns by the position on axis[i].
+ *   num_axes  1 .. SV_MAX_AXES
+ *   axis      host values, below num_axes, for i < rotary_dim / 2
+ * sv_qk_norm_rope_axes and sv_kv_append_rope_axes are the calls above with
+ *   positions  int32 [num_axes, total_q], a row of positions for each axis; in
+ *              the append NULL still means c_b + i, on every axis
+ * (SV_ERR_INVALID_ARG: axes NULL, num_axes or an axis out of range). With one
+ * axis, or the same positions on all, they do what those do, bit for bit.
+ */
+#define SV_MAX_AXES 8
+typedef struct sv_rotary_axes {
+  int32_t num_axes;
+  uint8_t axis[128];
+} sv_rotary_axes;
+
+sv_status sv_qk_norm_rope_axes(const sv_head_transform *transform, const sv_rotary_axes *axes, const void *q,
+                               int64_t q_row_stride, void *q_out, int64_t q_out_row_stride, int32_t num_q_heads,
+                               const void *k, int64_t k_row_stride, void *k_out, int64_t k_out_row_stride,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t dtype, int32_t total_q,
+                               const int32_t *positions, void *stream);
+sv_status sv_kv_append_rope_axes(const sv_paged_kv *kv, const sv_head_transform *transform, const sv_rotary_axes *axes,
+                                 const void *new_k, int64_t k_row_stride, const void *new_v, int64_t v_row_stride,
+                                 const void *q, int64_t q_row_stride, void *q_out, int64_t q_out_row_stride,
+                                 int32_t num_q_heads, const int32_t *cu_q, int32_t total_q, const int32_t *positions,
+                                 int32_t *status_dev, void *stream);
+
+/*
+ * sv_kv_gather -- rows of the cache as dense rows (for a dense attention over
+ * what the cache holds, or another cache).
+ *
+ * Row cu_rows[b] + i of the outputs takes what sequence b holds at logical
+ * position first[b] + i, for every KV head: values of the pool's type, or the
+ * value of an E4M3 or E2M1 code times its scales, in fp32, rounded once to bf16
+ * (E2M1: (s * scale) is rounded to fp32 before it meets the code).
+ *   out_k, out_v  [total_rows, num_kv_heads, head_dim] of kv->dtype (bf16 for an E4M3
+ *                 or E2M1 pool), 16-byte aligned; either may be NULL (not wanted)
+ *   cu_rows       int32 [batch + 1], cu_rows[0] = 0; rows past cu_rows[batch] are not
+ *                 written
+ *   first         int32 [batch], or NULL: the committed lengths, after which the
+ *                 step's new rows stand
+ *   status_dev    int32 [1] or NULL. A sequence whose rows do not lie within its row
+ *                 of the block table records SV_ERR_BAD_LENGTH, a row whose block id
+ *                 is out of range SV_ERR_BAD_BLOCK_ID; those rows are not written.
+ *                 What the word holds before does not matter
+ * Positions past a sequence's rows read whatever the block holds.
+ */
+sv_status sv_kv_gather(const sv_paged_kv *kv, void *out_k, void *out_v, const int32_t *cu_rows, int32_t total_rows,
+                       const int32_t *first, int32_t *status_dev, void *stream);
 
 /*
  * How sv_spec_verify_attn_scored changes the scores.

@@ -24,15 +24,17 @@ SV_OK = 0
 SV_ERR_INVALID_ARG = 1
 SV_ERR_NONFINITE = 9
 SV_ERR_WORKSPACE = 10
-SV_DTYPE_BF16, SV_DTYPE_F32, SV_DTYPE_E4M3 = 0, 1, 2
+SV_DTYPE_BF16, SV_DTYPE_F32, SV_DTYPE_E4M3, SV_DTYPE_E2M1 = 0, 1, 2, 3
 SV_MASK_CAUSAL, SV_MASK_TREE = 0, 1
+SV_MAX_AXES = 8
 STATUS_NAMES = {
     0: "SV_OK", 1: "SV_ERR_INVALID_ARG", 2: "SV_ERR_UNSUPPORTED", 3: "SV_ERR_CUDA",
     4: "SV_ERR_OUT_OF_BLOCKS", 5: "SV_ERR_TIMEOUT", 6: "SV_ERR_BAD_BLOCK_ID", 7: "SV_ERR_BAD_LENGTH",
     8: "SV_ERR_BAD_TOKEN", 9: "SV_ERR_NONFINITE", 10: "SV_ERR_WORKSPACE",
 }
 
-EXPORTS = ("sv_kv_append", "sv_kv_append_rope", "sv_qk_norm_rope", "sv_spec_verify_attn_scored_workspace_bytes",
+EXPORTS = ("sv_kv_append", "sv_kv_append_rope", "sv_kv_append_rope_axes", "sv_kv_gather", "sv_qk_norm_rope", "sv_qk_norm_rope_axes",
+           "sv_spec_verify_attn_scored_workspace_bytes",
            "sv_spec_verify_attn_scored", "sv_spec_verify_attn_workspace_bytes", "sv_spec_verify_attn",
            "sv_spec_verify_attn_no_alloc", "sv_spec_rejection_sample_workspace_bytes", "sv_spec_rejection_sample",
            "sv_tree_greedy_accept", "sv_tree_rejection_sample", "sv_kv_rollback", "sv_kv_fork", "sv_kv_release", "sv_adaptive_k_state_bytes", "sv_adaptive_k_init",
@@ -65,6 +67,7 @@ class sv_paged_kv(ctypes.Structure):
         ("max_blocks_per_seq", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
         ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32), ("dtype", ctypes.c_int32),
         ("ref_count", ctypes.c_void_p), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+        ("k_block_scales", ctypes.c_void_p), ("v_block_scales", ctypes.c_void_p),
     ]
 
 
@@ -74,6 +77,10 @@ class sv_head_transform(ctypes.Structure):
         ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("rotary_dim", ctypes.c_int32),
         ("interleaved", ctypes.c_int32),
     ]
+
+
+class sv_rotary_axes(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 128)]
 
 
 class sv_score_mod(ctypes.Structure):
@@ -100,10 +107,14 @@ def load(path: Optional[str] = None, build_if_missing: bool = True) -> ctypes.CD
         P, I, F, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
         KVP = ctypes.POINTER(sv_paged_kv)
         HTP, SMP, I64 = ctypes.POINTER(sv_head_transform), ctypes.POINTER(sv_score_mod), ctypes.c_int64
+        AXP = ctypes.POINTER(sv_rotary_axes)
         sig = {
             "sv_kv_append": (I, [KVP, P, P, P, I, P, P]),
             "sv_kv_append_rope": (I, [KVP, HTP, P, I64, P, I64, P, I64, P, I64, I, P, I, P, P, P]),
             "sv_qk_norm_rope": (I, [HTP, P, I64, P, I64, I, P, I64, P, I64, I, I, I, I, P, P]),
+            "sv_kv_append_rope_axes": (I, [KVP, HTP, AXP, P, I64, P, I64, P, I64, P, I64, I, P, I, P, P, P]),
+            "sv_qk_norm_rope_axes": (I, [HTP, AXP, P, I64, P, I64, I, P, I64, P, I64, I, I, I, I, P, P]),
+            "sv_kv_gather": (I, [KVP, P, P, P, I, P, P, P]),
             "sv_spec_verify_attn_scored_workspace_bytes": (S, [KVP, I, I, I, I]),
             "sv_spec_verify_attn_scored": (I, [KVP, P, P, P, I, I, I, I, F, SMP, P, I, P, P, S, P, P]),
             "sv_spec_verify_attn_workspace_bytes": (S, [KVP, I, I, I, I]),
@@ -198,23 +209,38 @@ def _dtype_code(t: torch.Tensor) -> int:
 class PagedKV:
     """One layer's paged KV cache held in torch CUDA tensors (see sv_paged_kv)."""
 
-    k_pool: torch.Tensor  # [num_blocks, num_kv_heads, block_size, head_dim]
+    k_pool: torch.Tensor  # [num_blocks, num_kv_heads, block_size, head_dim]; E2M1: uint8, head_dim / 2 bytes
     v_pool: torch.Tensor
     block_table: torch.Tensor  # int32 [batch, max_blocks_per_seq]
     seq_lens: torch.Tensor  # int32 [batch]
     free_list: torch.Tensor  # int32 [num_blocks]
     free_top: torch.Tensor  # int32 [1]
     ref_count: Optional[torch.Tensor] = None  # int32 [num_blocks]: copy-on-write sharing when given
-    k_scale: float = 1.0  # E4M3 pools (uint8 codes): dequantisation scales
+    k_scale: float = 1.0  # E4M3 pools (uint8 codes) and E2M1 pools: dequantisation scales
     v_scale: float = 1.0
+    # With both the pools are E2M1: uint8 [num_blocks, num_kv_heads, block_size, head_dim / 16]
+    k_block_scales: Optional[torch.Tensor] = None
+    v_block_scales: Optional[torch.Tensor] = None
+
+    @property
+    def is_e2m1(self) -> bool:
+        return self.k_block_scales is not None
 
     def struct(self) -> sv_paged_kv:
         nb, hkv, bs, d = self.k_pool.shape
+        dtype = SV_DTYPE_E4M3 if self.k_pool.dtype == torch.uint8 else _dtype_code(self.k_pool)
+        if self.k_block_scales is not None or self.v_block_scales is not None:
+            dtype, d = SV_DTYPE_E2M1, 2 * d
+            for pool, scales in ((self.k_pool, self.k_block_scales), (self.v_pool, self.v_block_scales)):
+                if scales is None or pool.dtype != torch.uint8 or scales.dtype != torch.uint8 or d % 32 or \
+                        tuple(pool.shape) != (nb, hkv, bs, d // 2) or tuple(scales.shape) != (nb, hkv, bs, d // 16):
+                    raise ValueError("an E2M1 cache has uint8 pools [blocks, heads, block_size, head_dim / 2] and block scales "
+                                     "[blocks, heads, block_size, head_dim / 16] for both")
         return sv_paged_kv(
             _at(self.k_pool), _at(self.v_pool), _at(self.block_table), _at(self.seq_lens),
             _at(self.free_list), _at(self.free_top), nb, bs, self.block_table.shape[1], hkv, d,
-            self.seq_lens.shape[0], SV_DTYPE_E4M3 if self.k_pool.dtype == torch.uint8 else _dtype_code(self.k_pool),
-            _at(self.ref_count), self.k_scale, self.v_scale)
+            self.seq_lens.shape[0], dtype, _at(self.ref_count), self.k_scale, self.v_scale,
+            _at(self.k_block_scales), _at(self.v_block_scales))
 
     @property
     def batch(self) -> int:
@@ -223,6 +249,11 @@ class PagedKV:
 
 def kv_append(kv: PagedKV, new_k: torch.Tensor, new_v: torch.Tensor, cu_q: torch.Tensor,
               status: torch.Tensor, stream=None) -> None:
+    if kv.is_e2m1:
+        rc = (_calls or _bound()).kv_append(kv, new_k, new_v, cu_q, status, _stream_of(new_k, stream))
+        if rc:
+            raise SVError(rc, "sv_kv_append")
+        return
     s = kv.struct()
     _check(load().sv_kv_append(ctypes.byref(s), _ptr(new_k), _ptr(new_v), _ptr(cu_q), int(new_k.shape[0]),
                                _ptr(status), _stream(stream)), "sv_kv_append")
@@ -269,7 +300,9 @@ def spec_verify_attn_no_alloc(kv: PagedKV, q: torch.Tensor, out: torch.Tensor, c
 class HeadTransform:
     """What a layer does to its query and key heads before attention (see
     sv_head_transform): a norm per head (where a weight is given), then the
-    rotation of the first 2 * len(inv_freq) values by the row's position."""
+    rotation of the first 2 * len(inv_freq) values by the row's position. With `axes`
+    (rotary_axes makes them) positions are int32 [num_axes, n], and pair i turns by its
+    axis's."""
 
     inv_freq: Optional[torch.Tensor] = None  # float32 [rotary_dim / 2]; None: no rotation
     q_weight: Optional[torch.Tensor] = None  # [head_dim] of the rows' type; None: no norm
@@ -277,6 +310,23 @@ class HeadTransform:
     eps: float = 1e-6
     weight_offset: float = 0.0  # 1 for weights stored as w - 1
     interleaved: bool = False  # pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2)
+    axes: Optional[bytes] = None  # the axis of each pair; None: one axis
+
+
+def rotary_axes(sections, in_turn: bool = False) -> bytes:
+    """The axis of each rotated pair, for HeadTransform.axes, from the number of pairs that each axis
+    has: one axis's after the other's, or (in_turn) pair i to axis i mod n while that axis has not
+    had its share, and what is left over to the first."""
+    sections = [int(s) for s in sections]
+    if not sections or len(sections) > SV_MAX_AXES or min(sections) < 0:
+        raise ValueError(f"1 to {SV_MAX_AXES} sections of 0 and more pairs")
+    n = len(sections)
+    if not in_turn:
+        return bytes(a for a, s in enumerate(sections) for _ in range(s))
+    out = bytes(i % n if i < n * sections[i % n] else 0 for i in range(sum(sections)))
+    if any(out.count(a) != s for a, s in enumerate(sections)):
+        raise ValueError("dealt in turn, an axis would not get its share: the first has to be the largest")
+    return out
 
 
 @dataclass
@@ -313,8 +363,8 @@ def _bound():
             importlib.invalidate_caches()
     from . import _calls as module
     at = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
-          for n in ("sv_qk_norm_rope", "sv_kv_append_rope", "sv_spec_verify_attn_scored",
-                    "sv_spec_verify_attn_scored_workspace_bytes")]
+          for n in ("sv_qk_norm_rope_axes", "sv_kv_append_rope_axes", "sv_spec_verify_attn_scored",
+                    "sv_spec_verify_attn_scored_workspace_bytes", "sv_kv_append", "sv_kv_gather", "sv_qk_norm_rope", "sv_kv_append_rope")]
     module.bind(*at)
     _calls = module
     return module
@@ -337,7 +387,8 @@ def qk_norm_rope(transform: HeadTransform, q: Optional[torch.Tensor], k: Optiona
                  positions: Optional[torch.Tensor], q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor],
                  stream=None) -> None:
     """Head norms and rotation of query rows [n, heads, head_dim] and key rows (either may be
-    None) into q_out and k_out, which may be the inputs themselves. positions: int32 [n]."""
+    None) into q_out and k_out, which may be the inputs themselves. positions: int32 [n], or
+    [num_axes, n] with transform.axes."""
     some = q if q is not None else k
     if some is None:
         raise ValueError("no rows: q and k are both None")
@@ -350,11 +401,26 @@ def kv_append_rope(kv: PagedKV, transform: HeadTransform, new_k: torch.Tensor, n
                    status: torch.Tensor, *, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
                    positions: Optional[torch.Tensor] = None, stream=None) -> None:
     """kv_append with the keys normalised and rotated on the way into the cache; with q, the
-    queries too, into q_out (which may be q). positions: int32 [n], or None for chains."""
+    queries too, into q_out (which may be q). positions: int32 [n] ([num_axes, n] with
+    transform.axes), or None for chains."""
     rc = (_calls or _bound()).kv_append_rope(kv, transform, new_k, new_v, cu_q, status, q, q_out, positions,
                                              _stream_of(new_k, stream))
     if rc:
         raise SVError(rc, "sv_kv_append_rope")
+
+
+def kv_gather(kv: PagedKV, out_k: Optional[torch.Tensor], out_v: Optional[torch.Tensor], cu_rows: torch.Tensor,
+              status: Optional[torch.Tensor] = None, *, first: Optional[torch.Tensor] = None, stream=None) -> None:
+    """What the cache holds at positions first[b], first[b] + 1, ... of each sequence (int32 [batch];
+    None: from the committed length on, the step's new rows) into rows cu_rows[b] ..
+    cu_rows[b + 1] - 1 of out_k and out_v [n, num_kv_heads, head_dim] (either may be None): of the
+    pool's type, bf16 for E4M3 and E2M1 pools."""
+    some = out_k if out_k is not None else out_v
+    if some is None:
+        raise ValueError("no outputs: out_k and out_v are both None")
+    rc = (_calls or _bound()).kv_gather(kv, out_k, out_v, cu_rows, status, first, _stream_of(some, stream))
+    if rc:
+        raise SVError(rc, "sv_kv_gather")
 
 
 def spec_verify_attn_scored_workspace_bytes(kv: PagedKV, num_q_heads: int, total_q: int, max_q: int,

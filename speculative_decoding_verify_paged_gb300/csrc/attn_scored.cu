@@ -31,7 +31,7 @@ cudaError_t pick(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStrea
 // (attn_scored.cuh); a TMA row coordinate is a 32-bit number, and so are a unit's rows.
 size_t attn_scored_mma_workspace(const ScoredArgs &sa) {
   const KV &kv = sa.a.kv;
-  if (kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return 0;
+  if (kv.fp4 || kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return 0;
   if (kv.block_size < 8 || (long long)kv.num_blocks * kv.num_kv_heads * kv.block_size >= (1LL << 31)) return 0;
   if ((long long)(sa.a.num_q_heads / kv.num_kv_heads) * sa.a.max_q >= (1LL << 30)) return 0;
   size_t bytes = 0;

@@ -31,6 +31,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "e2m1.cuh"
 #include "sv_internal.cuh"
 
 namespace sv {
@@ -82,13 +83,31 @@ __device__ __forceinline__ void widen16(float *dst, uint4 w, float scale, const 
   }
 }
 
+struct Codes4 {};  // an E2M1 pool's element: half a byte
+// 32 E2M1 codes and their two block scales
+__device__ __forceinline__ void widen16(float *dst, uint4 w, float scale, uint32_t block_scales) {
+  const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float step = __fmul_rn(e4m3_value((block_scales >> (8 * (q >> 1))) & 255u), scale);
+    uint32_t p[4];
+    widen8(word[q], p[0], p[1], p[2], p[3]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 a = pair_of(p[2 * h]), b = pair_of(p[2 * h + 1]);
+      reinterpret_cast<float4 *>(dst)[2 * q + h] = make_float4(a.x * step, a.y * step, b.x * step, b.y * step);
+    }
+  }
+}
+
 template <typename T, typename KT /* pool element */, int NK /* head_dim / 32 */, int RW /* rows a warp keeps */,
           bool SHARED /* the warps share RW rows */>
 __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs sa) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
   constexpr int D = NK * 32, kWarps = kThreads / 32;
-  constexpr int kVec = 16 / sizeof(KT), kChunks = D / kVec;  // values in 16 bytes of a pool row; reads of a row
+  constexpr bool F4 = std::is_same<KT, Codes4>::value;
+  constexpr int kVec = F4 ? 32 : 16 / sizeof(KT), kChunks = D / kVec;  // values in 16 bytes of a pool row; reads of a row
   constexpr int kRows = SHARED ? RW : RW * kWarps;           // of a pass
   constexpr int kCols = SHARED ? (NK + kWarps - 1) / kWarps : NK;  // columns a lane keeps
   __shared__ __align__(16) float q_s[kRows][D];
@@ -137,12 +156,20 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
     return -1;
   };
   // the tile at kt of a pool into shared memory; all lanes take part
-  auto fetch = [&](float *dst, int pitch, const KT *pool, float scale, int kt, int ids) {
+  auto fetch = [&](float *dst, int pitch, const KT *pool, const uint8_t *block_scales, float scale, int kt, int ids) {
     for (int x = tid; x < kKeys * kChunks; x += kThreads) {  // kKeys * kChunks is a multiple of 32
       const int j = x / kChunks, d = x % kChunks * kVec, t = kt + j;
       const int id = __shfl_sync(0xffffffffu, ids, j);
       const size_t off = (((size_t)max(id, 0) * kv.num_kv_heads + kvh) * kv.block_size + (t & (kv.block_size - 1))) * D + d;
-      if constexpr (sizeof(KT) == 4) {
+      if constexpr (F4) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        uint32_t bs = 0u;
+        if (id >= 0) {
+          w = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(pool) + off / 2);
+          bs = *reinterpret_cast<const uint16_t *>(block_scales + off / 16);
+        }
+        widen16(dst + j * pitch + d, w, scale, bs);
+      } else if constexpr (sizeof(KT) == 4) {
         copy16(dst + j * pitch + d, pool + off, id >= 0);
       } else {
         const uint4 w = id >= 0 ? *reinterpret_cast<const uint4 *>(pool + off) : make_uint4(0, 0, 0, 0);
@@ -155,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
   for (int rg = 0; rg < R; rg += kRows) {
     __syncthreads();
     int ids = kb < ke ? block_of(kb) : -1;
-    if (kb < ke) fetch(&k_s[0][0], D + 4, kp, kv.k_scale, kb, ids);
+    if (kb < ke) fetch(&k_s[0][0], D + 4, kp, kv.k_bs, kv.k_scale, kb, ids);
     for (int x = tid; x < kRows * D; x += kThreads) {
       const int rr = x / D, d = x % D, r = rg + rr;
       float val = 0.f;
@@ -183,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
     for (int kt = kb; kt < ke; kt += kKeys) {
       copies_landed<0>();
       __syncthreads();  // K is there, and the last tile's V is done with
-      fetch(&v_s[0][0], D, vp, kv.v_scale, kt, ids);
+      fetch(&v_s[0][0], D, vp, kv.v_bs, kv.v_scale, kt, ids);
       if (kt + kKeys < ke) ids = block_of(kt + kKeys);
       const bool mine = rg + rw < R;  // some of the warp's rows exist
       const int t = kt + lane, j = t - c;
@@ -218,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) attn_scored_simt_kernel(ScoredArgs s
 #pragma unroll
         for (int w = 0; w < RW; ++w) part_s[warp][w][lane] = dot[w];
       __syncthreads();  // every warp is done with K
-      if (kt + kKeys < ke) fetch(&k_s[0][0], D + 4, kp, kv.k_scale, kt + kKeys, ids);
+      if (kt + kKeys < ke) fetch(&k_s[0][0], D + 4, kp, kv.k_bs, kv.k_scale, kt + kKeys, ids);
       else copies_end();
       unsigned any = 0u, hidden = 0u;  // keys that some row of the warp sees, that some row does not
       if (mine) {
@@ -430,7 +457,8 @@ cudaError_t launch_t(const ScoredArgs &sa, cudaStream_t st) {
 
 cudaError_t launch_attn_scored_simt(const ScoredArgs &sa, int dtype, cudaStream_t st) {
   cudaError_t e;
-  if (dtype == SV_DTYPE_E4M3) e = launch_t<__nv_bfloat16, uint8_t>(sa, st);  // bf16 queries and outputs
+  if (dtype == SV_DTYPE_E2M1) e = launch_t<__nv_bfloat16, Codes4>(sa, st);  // bf16 queries and outputs, as for E4M3
+  else if (dtype == SV_DTYPE_E4M3) e = launch_t<__nv_bfloat16, uint8_t>(sa, st);
   else e = dtype == SV_DTYPE_BF16 ? launch_t<__nv_bfloat16, __nv_bfloat16>(sa, st) : launch_t<float, float>(sa, st);
   if (e != cudaSuccess || sa.a.max_splits <= 1 || sa.cluster) return e;
   const dim3 grid((unsigned)ceil_div(sa.a.max_q * sa.a.num_q_heads, kThreads / 32), (unsigned)sa.a.kv.batch);

@@ -3,10 +3,11 @@
 //
 // For a head x of D values, its norm weight w (if given) and its row's position p:
 //   y_e = x_e * rsqrt(mean_e x_e^2 + eps) * (w_e + offset)              (y = x without a weight)
-//   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[i],
+//   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[i]  (p: on pair i's axis, if there are several),
 // over the pairs i < rot / 2 of y: (y_i, y_{i + rot/2}), or (y_2i, y_2i+1) when interleaved. All
 // of it in fp32 and one rounding at the end, to the output's type (for an E4M3 pool straight from
-// fp32 to the code nearest to y / scale: rounding to bf16 on the way would round twice). The
+// fp32 to the code nearest to y / scale: rounding to bf16 on the way would round twice; into an E2M1 pool as in
+// e2m1.cuh, two neighbouring lanes to a scale). The
 // angle is the product of the position and the fp32 frequency as a 64-bit fraction of a turn, rounded
 // once to fp32 (see turn): a product in fp32 would be off by 4e-3 at position 10^5.
 //
@@ -32,6 +33,7 @@
 
 #include <algorithm>
 
+#include "e2m1.cuh"
 #include "kv_rows.cuh"
 
 namespace sv {
@@ -119,20 +121,6 @@ __device__ __forceinline__ float2 turn(int position, float freq) {
   return make_float2(cs, sn);
 }
 
-// The last b < n with cu[b] <= row (0 if none), by the whole warp: 32 probes at a time.
-__device__ __forceinline__ int owner_of(const int32_t *cu, int n, int row) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, len = n;
-  while (len > 1) {
-    const int step = (len + 31) >> 5;
-    const bool below = lane * step < len && cu[lo + lane * step] <= row;
-    const int k = max(0, __popc(__ballot_sync(0xffffffffu, below)) - 1);
-    lo += k * step;
-    len = min(step, len - k * step);
-  }
-  return lo;
-}
-
 constexpr int kThreads = 128;
 // Warps in residence against loads in flight (16384 rows; 256 x 64 appended): 5 CTAs an SM with 5 iterations ahead
 // 69 and 86 us, 6 with 4 63 and 78, 7 with 4 60 and 77, 7 with 3 65 and 83, 8 with 4 (spilling) 61 and 82.
@@ -158,8 +146,8 @@ template <> __device__ __forceinline__ void from_lane(const Vec8<float> &x, int 
 enum Pairs { kShuffle, kInLane, kExchange };  // where a value's pair is
 
 // APPEND: keys and values go to the cache (kv, cu_q, status); else keys go to k_out. DIM: the head
-// size, or 0: any (with PAIRS == kExchange). A warp takes chunk x % chunks of row x / chunks.
-template <typename T, bool APPEND, int PAIRS, int DIM>
+// size, or 0: any (with PAIRS == kExchange). F4: an E2M1 pool. A warp takes chunk x % chunks of row x / chunks.
+template <typename T, bool APPEND, int PAIRS, int DIM, bool F4>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const HeadArgs a, int chunks, int per_chunk,
                                                                          long long items) {
   constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;  // iterations whose loads are in flight together
@@ -216,13 +204,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const H
     c = a.kv.seq_lens[b];
   }
   if (kind0 < 2 && half > 0) {
-    const int pos = a.positions != nullptr ? a.positions[row] : c + i;
-    for (int e = lane; e < half; e += 32) s_turn[warp][e] = turn(pos, a.inv_freq[e]);
+    if (a.axes > 1 && a.positions != nullptr) {
+      for (int e = lane; e < half; e += 32) s_turn[warp][e] = turn(a.positions[(size_t)a.axis[e] * a.rows + row], a.inv_freq[e]);
+    } else {
+      const int pos = a.positions != nullptr ? a.positions[row] : c + i;
+      for (int e = lane; e < half; e += 32) s_turn[warp][e] = turn(pos, a.inv_freq[e]);
+    }
     __syncwarp();
   }
   uint8_t *out[3] = {a.q_out + (size_t)row * a.q_out_stride + in_head * kEsz,
                      APPEND ? nullptr : a.k_out + (size_t)row * a.k_out_stride + in_head * kEsz, nullptr};
   size_t out_step[2] = {(size_t)step * kEsz, (size_t)step * kEsz};  // of an iteration: queries; keys and values
+  size_t scale_at = 0, scale_step = 0;                              // F4: of the lane's block scale
   if (APPEND) {
     grid_dependency_wait();
     grid_dependents_launch();
@@ -235,11 +228,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const H
       return;
     }
     const int eb = a.kv.elem_bytes;
-    const size_t off =
-        (((((size_t)blk * a.hkv + sub) << bsh) + (at & (a.kv.block_size - 1))) * dim + place * 8) * eb;
+    const size_t value = ((((size_t)blk * a.hkv + sub) << bsh) + (at & (a.kv.block_size - 1))) * dim + place * 8;
+    const size_t off = F4 ? value / 2 : value * eb;
     out[1] = reinterpret_cast<uint8_t *>(a.kv.k_pool) + off;
     out[2] = reinterpret_cast<uint8_t *>(a.kv.v_pool) + off;
-    out_step[1] = ((size_t)hpw * dim << bsh) * eb;
+    out_step[1] = F4 ? ((size_t)hpw * dim << bsh) / 2 : ((size_t)hpw * dim << bsh) * eb;
+    scale_at = value / 16;
+    scale_step = ((size_t)hpw * dim << bsh) / 16;
   }
 
   const int other = place < hl ? place + hl : place < 2 * hl ? place - hl : place;  // the pair's place (kShuffle)
@@ -301,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const H
         if (it + u >= end) break;  // uniform
         const int k = it + u - first;
         float y[8];
-        if (kind < 2 || a.kv.fp8) x[u].get(y);
+        if (kind < 2 || a.kv.fp8 || F4) x[u].get(y);
         if (kind < 2) {
           float r = 1.f;
           if (weight != nullptr) {
@@ -340,10 +335,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const H
             y[j] = r * (rotate ? fmaf(p[j], Bf[j], y[j] * A[j]) : y[j] * A[j]);
           }
         }
+        float top = 0.f;  // F4: the largest of the lane's and its neighbour's values
+        if (F4 && kind > 0) {
+          top = top_of(y);
+          top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        }
         if (!holds || k * hpw + sub >= count) continue;
         // the output, rounded once
         uint8_t *dst = out[kind] + (size_t)k * out_step[kind > 0];
-        if (APPEND && kind > 0 && a.kv.fp8) {
+        if (F4 && kind > 0) {
+          const uint32_t s = block_scale(top, kind == 2 ? a.v_inv : a.k_inv);
+          *reinterpret_cast<uint32_t *>(dst) = codes8(y, code_factor(s, kind == 2 ? a.kv.v_scale : a.kv.k_scale));
+          if ((place & 1) == 0) (kind == 2 ? a.kv.v_bs : a.kv.k_bs)[scale_at + (size_t)k * scale_step] = (uint8_t)s;
+        } else if (APPEND && kind > 0 && a.kv.fp8) {
           *reinterpret_cast<uint2 *>(dst) = quantize8(y, kind == 2 ? a.kv.v_scale : a.kv.k_scale, kind == 2 ? a.v_inv : a.k_inv);
         } else {
           if (kind < 2) x[u].set(y);  // values are copied as they are
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) head_rows_kernel(const H
   }
 }
 
-template <typename T, bool APPEND>
+template <typename T, bool APPEND, bool F4 = false>
 cudaError_t launch_rows(const HeadArgs &a, int total_q, cudaStream_t st) {
   int gl = 1;
   while (gl < a.head_dim / 8) gl *= 2;
@@ -370,13 +374,13 @@ cudaError_t launch_rows(const HeadArgs &a, int total_q, cudaStream_t st) {
   const int d = a.head_dim;
   if (d == 64 || d == 128 || d == 256) {
     if (!a.interleaved && a.rot % 16 == 0)
-      return d == 64 ? go(head_rows_kernel<T, APPEND, kShuffle, 64>) : d == 128 ? go(head_rows_kernel<T, APPEND, kShuffle, 128>)
-                                                                               : go(head_rows_kernel<T, APPEND, kShuffle, 256>);
+      return d == 64 ? go(head_rows_kernel<T, APPEND, kShuffle, 64, F4>) : d == 128 ? go(head_rows_kernel<T, APPEND, kShuffle, 128, F4>)
+                                                                                   : go(head_rows_kernel<T, APPEND, kShuffle, 256, F4>);
     if (a.interleaved && a.rot % 8 == 0)
-      return d == 64 ? go(head_rows_kernel<T, APPEND, kInLane, 64>) : d == 128 ? go(head_rows_kernel<T, APPEND, kInLane, 128>)
-                                                                              : go(head_rows_kernel<T, APPEND, kInLane, 256>);
+      return d == 64 ? go(head_rows_kernel<T, APPEND, kInLane, 64, F4>) : d == 128 ? go(head_rows_kernel<T, APPEND, kInLane, 128, F4>)
+                                                                                  : go(head_rows_kernel<T, APPEND, kInLane, 256, F4>);
   }
-  return go(head_rows_kernel<T, APPEND, kExchange, 0>);
+  return go(head_rows_kernel<T, APPEND, kExchange, 0, F4>);
 }
 
 // One CTA per sequence whose first new row lands in a private copy of a shared block.
@@ -388,16 +392,21 @@ __global__ void __launch_bounds__(256) kv_private_copy_kernel(KV kv, const int32
   if (cu_q[b + 1] - cu_q[b] < 1 || slot == 0) return;
   const int blk = kv.block_table[(size_t)b * kv.max_blocks + c / kv.block_size];
   if (blk < 0 || blk >= kv.num_blocks) return;  // the rows' kernel reports it
-  copy_shared_block(kv, blk, slot, kv.head_dim * kv.elem_bytes, status);
+  copy_shared_block(kv, blk, slot, kv.row_bytes, status);
 }
 
 }  // namespace
 
+cudaError_t launch_private_copies(const KV &kv, const int32_t *cu_q, int32_t *status, cudaStream_t st) {
+  return launch_pdl(kv_private_copy_kernel, dim3(kv.batch), dim3(256), 0, st, kv, cu_q, status);
+}
+
 cudaError_t launch_head_rows(const HeadArgs &a, int dtype, int total_q, bool append, cudaStream_t st) {
   if (append && a.kv.ref_count != nullptr) {
-    const cudaError_t e = launch_pdl(kv_private_copy_kernel, dim3(a.kv.batch), dim3(256), 0, st, a.kv, a.cu_q, a.status);
+    const cudaError_t e = launch_private_copies(a.kv, a.cu_q, a.status, st);
     if (e != cudaSuccess) return e;
   }
+  if (append && a.kv.fp4) return launch_rows<__nv_bfloat16, true, true>(a, total_q, st);
   if (dtype == SV_DTYPE_F32) return append ? launch_rows<float, true>(a, total_q, st) : launch_rows<float, false>(a, total_q, st);
   return append ? launch_rows<__nv_bfloat16, true>(a, total_q, st) : launch_rows<__nv_bfloat16, false>(a, total_q, st);
 }

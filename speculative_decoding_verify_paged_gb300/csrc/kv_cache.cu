@@ -345,7 +345,7 @@ __global__ void kv_tree_compact_kernel(KV kv, const int32_t *cu_q, const int32_t
     if (threadIdx.x == 0) record(status, SV_ERR_BAD_LENGTH);
     return;
   }
-  const int row_bytes = kv.head_dim * kv.elem_bytes;
+  const int row_bytes = kv.row_bytes;
   const int vec_per_row = row_bytes / 16;
   const int total = kv.num_kv_heads * vec_per_row;
   for (int j = 1; j <= a; ++j) {
@@ -366,6 +366,16 @@ __global__ void kv_tree_compact_kernel(KV kv, const int32_t *cu_q, const int32_t
         const uint4 vv = *reinterpret_cast<const uint4 *>((const uint8_t *)kv.v_pool + so);
         *reinterpret_cast<uint4 *>((uint8_t *)kv.k_pool + d_o) = kk;
         *reinterpret_cast<uint4 *>((uint8_t *)kv.v_pool + d_o) = vv;
+      }
+      if (kv.fp4) {  // the rows' block scales, an even number of bytes
+        const int words = kv.head_dim / 32;
+        for (int x = threadIdx.x; x < kv.num_kv_heads * words; x += blockDim.x) {
+          const int h = x / words, v = x % words;
+          const size_t so = ((((size_t)sblk * kv.num_kv_heads + h) * kv.block_size + ss) * words + v) * 2;
+          const size_t d_o = ((((size_t)dblk * kv.num_kv_heads + h) * kv.block_size + ds) * words + v) * 2;
+          *reinterpret_cast<uint16_t *>(kv.k_bs + d_o) = *reinterpret_cast<const uint16_t *>(kv.k_bs + so);
+          *reinterpret_cast<uint16_t *>(kv.v_bs + d_o) = *reinterpret_cast<const uint16_t *>(kv.v_bs + so);
+        }
       }
     }
     __syncthreads();  // the next copy may read this one's destination
@@ -684,6 +694,7 @@ cudaError_t launch_kv_append(const KV &kv, const void *new_k, const void *new_v,
                              int total_q, int32_t *status, cudaStream_t st) {
   cudaError_t e = launch_kv_alloc(kv, cu_q, status, st);
   if (e != cudaSuccess || total_q == 0) return e;
+  if (kv.fp4) return launch_kv_store_e2m1(kv, new_k, new_v, cu_q, total_q, status, st);
   return launch_pdl(kv_scatter_kernel, dim3((unsigned)total_q), dim3(kScatterThreads), 0, st, kv, (const uint8_t *)new_k,
                     (const uint8_t *)new_v, cu_q, status);
 }

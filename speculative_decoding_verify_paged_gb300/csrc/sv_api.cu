@@ -73,11 +73,20 @@ sv_status check_kv(const sv_paged_kv *kv, bool need_free) {
     return SV_ERR_INVALID_ARG;
   if (!pow2(kv->block_size) || kv->block_size > 256) return SV_ERR_INVALID_ARG;
   if (kv->head_dim < 8 || kv->head_dim > 256 || kv->head_dim % 8 != 0) return SV_ERR_INVALID_ARG;
-  if (kv->dtype != SV_DTYPE_BF16 && kv->dtype != SV_DTYPE_F32 && kv->dtype != SV_DTYPE_E4M3) return SV_ERR_INVALID_ARG;
+  if (kv->dtype != SV_DTYPE_BF16 && kv->dtype != SV_DTYPE_F32 && kv->dtype != SV_DTYPE_E4M3 && kv->dtype != SV_DTYPE_E2M1)
+    return SV_ERR_INVALID_ARG;
   if (kv->dtype == SV_DTYPE_E4M3 &&
       (kv->head_dim % 16 != 0 || !(kv->k_scale > 0.f) || !(kv->v_scale > 0.f) || kv->k_scale == INFINITY ||
        kv->v_scale == INFINITY))
     return SV_ERR_INVALID_ARG;
+  if (kv->dtype == SV_DTYPE_E2M1) {
+    // scales whose sixfold and whose products with block scales (2^-9 .. 448) have normal inverses
+    auto usable = [](float x) { return x >= 0x1p-64f && x <= 0x1p64f; };
+    if (kv->head_dim % 32 != 0 || !usable(kv->k_scale) || !usable(kv->v_scale)) return SV_ERR_INVALID_ARG;
+    if (kv->k_block_scales == nullptr || kv->v_block_scales == nullptr || !aligned16(kv->k_block_scales) ||
+        !aligned16(kv->v_block_scales))
+      return SV_ERR_INVALID_ARG;
+  }
   if (kv->batch > 0 && (kv->block_table == nullptr || kv->seq_lens == nullptr)) return SV_ERR_INVALID_ARG;
   if (kv->k_pool == nullptr || kv->v_pool == nullptr) return SV_ERR_INVALID_ARG;
   if (!aligned16(kv->k_pool) || !aligned16(kv->v_pool)) return SV_ERR_INVALID_ARG;
@@ -116,8 +125,8 @@ SplitPlan scored_splits(const sv_paged_kv *kv, int32_t max_seq_len) {
   return plan_splits(kv->batch, kv->num_kv_heads, max_seq_len, kScoredGranule);
 }
 
-// Checks a head transform and puts it into the kernels' arguments.
-sv_status head_args(HeadArgs *a, const sv_head_transform *t, int head_dim, int dtype) {
+// Checks a head transform and puts it into the kernels' arguments. axes: null for one.
+sv_status head_args(HeadArgs *a, const sv_head_transform *t, const sv_rotary_axes *axes, int head_dim, int dtype) {
   if (t == nullptr || head_dim < 8 || head_dim > 256 || head_dim % 8 != 0) return SV_ERR_INVALID_ARG;
   if (t->rotary_dim < 0 || t->rotary_dim > head_dim || t->rotary_dim % 2 != 0) return SV_ERR_INVALID_ARG;
   if (t->rotary_dim > 0 && t->inv_freq == nullptr) return SV_ERR_INVALID_ARG;
@@ -135,6 +144,15 @@ sv_status head_args(HeadArgs *a, const sv_head_transform *t, int head_dim, int d
   a->eps = t->eps;
   a->offset = t->weight_offset;
   a->inv_dim = 1.f / (float)head_dim;
+  a->axes = 1;
+  if (axes != nullptr) {
+    if (axes->num_axes < 1 || axes->num_axes > SV_MAX_AXES) return SV_ERR_INVALID_ARG;
+    a->axes = axes->num_axes;
+    for (int i = 0; i < t->rotary_dim / 2; ++i) {
+      if (axes->axis[i] >= axes->num_axes) return SV_ERR_INVALID_ARG;
+      a->axis[i] = axes->axis[i];
+    }
+  }
   return SV_OK;
 }
 
@@ -160,6 +178,7 @@ bool head_rows(P *at, long long *bytes, const void *p, int64_t stride, int heads
 // CUDA-core and mma.sync kernels, or the tcgen05 kernel's slots and tile prefix.
 size_t attn_workspace(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q, int32_t max_q,
                       int32_t max_seq_len) {
+  if (kv->dtype == SV_DTYPE_E2M1) return sv_spec_verify_attn_scored_workspace_bytes(kv, num_q_heads, total_q, max_q, max_seq_len);
   size_t need = split_workspace(kv, num_q_heads, total_q, max_seq_len);
   if (kv->batch > 0 && umma_usable(kv, num_q_heads, max_q, max_seq_len))
     need = std::max(need, attn_umma_workspace_bytes(make_kv(*kv), num_q_heads, max_q, max_seq_len));
@@ -198,7 +217,7 @@ const char *sv_status_string(int32_t status) {
   }
 }
 
-int32_t sv_version(void) { return 30200; }
+int32_t sv_version(void) { return 30300; }
 
 sv_status sv_set_option(int32_t option, int32_t value) {
   if (option == SV_OPT_ATTN_PATH && value >= SV_ATTN_AUTO && value <= SV_ATTN_KEYS_MAJOR) {
@@ -243,6 +262,11 @@ sv_status sv_spec_verify_attn(const sv_paged_kv *kv, const void *q, void *out, c
                               void *workspace, size_t workspace_bytes, int32_t *status_dev, void *stream) {
   sv_status s = check_kv(kv, false);
   if (s != SV_OK) return s;
+  if (kv->dtype == SV_DTYPE_E2M1) {
+    const sv_score_mod none = {};
+    return sv_spec_verify_attn_scored(kv, q, out, cu_q, num_q_heads, total_q, max_q_per_seq, max_seq_len, scale, &none, nullptr,
+                                      mask_kind, tree_mask, workspace, workspace_bytes, status_dev, stream);
+  }
   if (num_q_heads <= 0 || num_q_heads % kv->num_kv_heads != 0) return SV_ERR_INVALID_ARG;
   if (total_q < 0 || max_q_per_seq < 1 || max_q_per_seq > kMaxQ || max_seq_len < 1) return SV_ERR_INVALID_ARG;
   if (mask_kind != SV_MASK_CAUSAL && mask_kind != SV_MASK_TREE) return SV_ERR_INVALID_ARG;
@@ -302,14 +326,17 @@ sv_status sv_spec_verify_attn(const sv_paged_kv *kv, const void *q, void *out, c
   return cuda_status(launch_attn_combine(a, kv->dtype, st));
 }
 
-sv_status sv_qk_norm_rope(const sv_head_transform *transform, const void *q, int64_t q_row_stride, void *q_out,
-                          int64_t q_out_row_stride, int32_t num_q_heads, const void *k, int64_t k_row_stride,
-                          void *k_out, int64_t k_out_row_stride, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
-                          int32_t total_q, const int32_t *positions, void *stream) {
+}  // extern "C"
+
+namespace {
+sv_status norm_rope(const sv_head_transform *transform, const sv_rotary_axes *axes, const void *q, int64_t q_row_stride, void *q_out,
+                    int64_t q_out_row_stride, int32_t num_q_heads, const void *k, int64_t k_row_stride, void *k_out,
+                    int64_t k_out_row_stride, int32_t num_kv_heads, int32_t head_dim, int32_t dtype, int32_t total_q,
+                    const int32_t *positions, void *stream) {
   if (dtype != SV_DTYPE_BF16 && dtype != SV_DTYPE_F32) return SV_ERR_INVALID_ARG;
   if (num_q_heads < 0 || num_kv_heads < 0 || total_q < 0) return SV_ERR_INVALID_ARG;
   HeadArgs a;
-  const sv_status s = head_args(&a, transform, head_dim, dtype);
+  const sv_status s = head_args(&a, transform, axes, head_dim, dtype);
   if (s != SV_OK) return s;
   if (total_q == 0 || (num_q_heads == 0 && num_kv_heads == 0)) return SV_OK;
   if (transform->rotary_dim > 0 && positions == nullptr) return SV_ERR_INVALID_ARG;
@@ -321,21 +348,21 @@ sv_status sv_qk_norm_rope(const sv_head_transform *transform, const void *q, int
   a.hq = num_q_heads;
   a.hkv = num_kv_heads;
   a.positions = positions;
+  a.rows = total_q;
   return cuda_status(launch_head_rows(a, dtype, total_q, false, (cudaStream_t)stream));
 }
 
-sv_status sv_kv_append_rope(const sv_paged_kv *kv, const sv_head_transform *transform, const void *new_k,
-                            int64_t k_row_stride, const void *new_v, int64_t v_row_stride, const void *q,
-                            int64_t q_row_stride, void *q_out, int64_t q_out_row_stride, int32_t num_q_heads,
-                            const int32_t *cu_q, int32_t total_q, const int32_t *positions, int32_t *status_dev,
-                            void *stream) {
+sv_status append_rope(const sv_paged_kv *kv, const sv_head_transform *transform, const sv_rotary_axes *axes, const void *new_k,
+                      int64_t k_row_stride, const void *new_v, int64_t v_row_stride, const void *q, int64_t q_row_stride,
+                      void *q_out, int64_t q_out_row_stride, int32_t num_q_heads, const int32_t *cu_q, int32_t total_q,
+                      const int32_t *positions, int32_t *status_dev, void *stream) {
   sv_status s = check_kv(kv, true);
   if (s != SV_OK) return s;
   if (status_dev == nullptr || total_q < 0 || num_q_heads < 0 || (kv->batch > 0 && cu_q == nullptr))
     return SV_ERR_INVALID_ARG;
   const int dtype = kv->dtype == SV_DTYPE_F32 ? SV_DTYPE_F32 : SV_DTYPE_BF16;  // of the rows
   HeadArgs a;
-  s = head_args(&a, transform, kv->head_dim, dtype);
+  s = head_args(&a, transform, axes, kv->head_dim, dtype);
   if (s != SV_OK) return s;
   if (total_q > 0 && (!head_rows(&a.k, &a.k_stride, new_k, k_row_stride, kv->num_kv_heads, kv->head_dim, dtype) ||
                       !head_rows(&a.v, &a.v_stride, new_v, v_row_stride, kv->num_kv_heads, kv->head_dim, dtype) ||
@@ -347,14 +374,65 @@ sv_status sv_kv_append_rope(const sv_paged_kv *kv, const sv_head_transform *tran
   a.hq = num_q_heads;
   a.hkv = kv->num_kv_heads;
   a.positions = positions;
+  a.rows = total_q;
   a.kv = make_kv(*kv);
   a.cu_q = cu_q;
   a.status = status_dev;
-  a.k_inv = exact_inverse(kv->k_scale);
-  a.v_inv = exact_inverse(kv->v_scale);
+  a.k_inv = a.kv.fp4 ? 1.f / (6.f * kv->k_scale) : exact_inverse(kv->k_scale);
+  a.v_inv = a.kv.fp4 ? 1.f / (6.f * kv->v_scale) : exact_inverse(kv->v_scale);
   const cudaError_t e = launch_kv_alloc(a.kv, cu_q, status_dev, (cudaStream_t)stream);
   if (e != cudaSuccess || total_q == 0) return cuda_status(e);
   return cuda_status(launch_head_rows(a, dtype, total_q, true, (cudaStream_t)stream));
+}
+}  // namespace
+
+extern "C" {
+
+sv_status sv_qk_norm_rope(const sv_head_transform *transform, const void *q, int64_t q_row_stride, void *q_out,
+                          int64_t q_out_row_stride, int32_t num_q_heads, const void *k, int64_t k_row_stride,
+                          void *k_out, int64_t k_out_row_stride, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                          int32_t total_q, const int32_t *positions, void *stream) {
+  return norm_rope(transform, nullptr, q, q_row_stride, q_out, q_out_row_stride, num_q_heads, k, k_row_stride, k_out,
+                   k_out_row_stride, num_kv_heads, head_dim, dtype, total_q, positions, stream);
+}
+
+sv_status sv_qk_norm_rope_axes(const sv_head_transform *transform, const sv_rotary_axes *axes, const void *q,
+                               int64_t q_row_stride, void *q_out, int64_t q_out_row_stride, int32_t num_q_heads,
+                               const void *k, int64_t k_row_stride, void *k_out, int64_t k_out_row_stride,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t dtype, int32_t total_q,
+                               const int32_t *positions, void *stream) {
+  if (axes == nullptr) return SV_ERR_INVALID_ARG;
+  return norm_rope(transform, axes, q, q_row_stride, q_out, q_out_row_stride, num_q_heads, k, k_row_stride, k_out,
+                   k_out_row_stride, num_kv_heads, head_dim, dtype, total_q, positions, stream);
+}
+
+sv_status sv_kv_append_rope(const sv_paged_kv *kv, const sv_head_transform *transform, const void *new_k,
+                            int64_t k_row_stride, const void *new_v, int64_t v_row_stride, const void *q,
+                            int64_t q_row_stride, void *q_out, int64_t q_out_row_stride, int32_t num_q_heads,
+                            const int32_t *cu_q, int32_t total_q, const int32_t *positions, int32_t *status_dev,
+                            void *stream) {
+  return append_rope(kv, transform, nullptr, new_k, k_row_stride, new_v, v_row_stride, q, q_row_stride, q_out, q_out_row_stride,
+                     num_q_heads, cu_q, total_q, positions, status_dev, stream);
+}
+
+sv_status sv_kv_append_rope_axes(const sv_paged_kv *kv, const sv_head_transform *transform, const sv_rotary_axes *axes,
+                                 const void *new_k, int64_t k_row_stride, const void *new_v, int64_t v_row_stride,
+                                 const void *q, int64_t q_row_stride, void *q_out, int64_t q_out_row_stride,
+                                 int32_t num_q_heads, const int32_t *cu_q, int32_t total_q, const int32_t *positions,
+                                 int32_t *status_dev, void *stream) {
+  if (axes == nullptr) return SV_ERR_INVALID_ARG;
+  return append_rope(kv, transform, axes, new_k, k_row_stride, new_v, v_row_stride, q, q_row_stride, q_out, q_out_row_stride,
+                     num_q_heads, cu_q, total_q, positions, status_dev, stream);
+}
+
+sv_status sv_kv_gather(const sv_paged_kv *kv, void *out_k, void *out_v, const int32_t *cu_rows, int32_t total_rows,
+                       const int32_t *first, int32_t *status_dev, void *stream) {
+  const sv_status s = check_kv(kv, false);
+  if (s != SV_OK) return s;
+  if (total_rows < 0 || !aligned16(out_k) || !aligned16(out_v)) return SV_ERR_INVALID_ARG;
+  if (kv->batch == 0 || total_rows == 0) return SV_OK;
+  if (cu_rows == nullptr || (out_k == nullptr && out_v == nullptr)) return SV_ERR_INVALID_ARG;
+  return cuda_status(launch_kv_gather(make_kv(*kv), out_k, out_v, cu_rows, total_rows, first, status_dev, (cudaStream_t)stream));
 }
 
 size_t sv_spec_verify_attn_scored_workspace_bytes(const sv_paged_kv *kv, int32_t num_q_heads, int32_t total_q,

@@ -126,9 +126,12 @@ struct KV {
   int32_t *free_top;
   int32_t *ref_count;  // null: no sharing
   int num_blocks, block_size, max_blocks, num_kv_heads, head_dim, batch;
-  int elem_bytes;
+  int elem_bytes;          // of a pool's value (0: E2M1)
+  int row_bytes;           // of a head's row in a pool
   bool fp8;                // E4M3 pool: 1-byte codes, bf16 rows in and out
-  float k_scale, v_scale;  // E4M3 dequantisation scales
+  bool fp4;                // E2M1 pool: two codes a byte and block scales, bf16 rows in and out
+  float k_scale, v_scale;  // E4M3 and E2M1 dequantisation scales
+  uint8_t *k_bs, *v_bs;    // E2M1 block scales, head_dim / 16 a row (else null)
 };
 
 inline KV make_kv(const sv_paged_kv &p) {
@@ -146,10 +149,14 @@ inline KV make_kv(const sv_paged_kv &p) {
   k.num_kv_heads = p.num_kv_heads;
   k.head_dim = p.head_dim;
   k.batch = p.batch;
-  k.elem_bytes = p.dtype == SV_DTYPE_BF16 ? 2 : (p.dtype == SV_DTYPE_E4M3 ? 1 : 4);
+  k.elem_bytes = p.dtype == SV_DTYPE_BF16 ? 2 : p.dtype == SV_DTYPE_E4M3 ? 1 : p.dtype == SV_DTYPE_E2M1 ? 0 : 4;
   k.fp8 = p.dtype == SV_DTYPE_E4M3;
+  k.fp4 = p.dtype == SV_DTYPE_E2M1;
+  k.row_bytes = k.fp4 ? p.head_dim / 2 : p.head_dim * k.elem_bytes;
   k.k_scale = p.k_scale;
   k.v_scale = p.v_scale;
+  k.k_bs = k.fp4 ? (uint8_t *)p.k_block_scales : nullptr;  // (read for this type alone)
+  k.v_bs = k.fp4 ? (uint8_t *)p.v_block_scales : nullptr;
   return k;
 }
 
@@ -187,11 +194,13 @@ struct HeadArgs {
   long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
   const float *inv_freq;
   const uint8_t *q_weight, *k_weight;  // of the rows' type, or null: no norm
-  const int32_t *positions;            // [rows] or null (append only): c_b + i
+  const int32_t *positions;            // [axes][rows] or null (append only): c_b + i
+  int axes, rows;                      // of positions
+  uint8_t axis[128];                   // of each pair, with more than one axis
   int hq, hkv, head_dim, rot;
   bool interleaved;
   float eps, offset, inv_dim;
-  float k_inv, v_inv;  // 1 / scale of an E4M3 pool where that is exact, else 0
+  float k_inv, v_inv;  // 1 / scale of an E4M3 pool where that is exact, else 0; 1 / (6 scale) of an E2M1 pool
   KV kv;  // append only, with cu_q and status
   const int32_t *cu_q;
   int32_t *status;
@@ -217,6 +226,13 @@ int kv_cow_max_batch();  // batch limit of append and rollback with reference co
 int kv_max_seq_bits();   // batch limit of fork and release
 // Head rows: the append's second half after launch_kv_alloc (append), or into q_out and k_out.
 cudaError_t launch_head_rows(const HeadArgs &a, int dtype, int total_q, bool append, cudaStream_t st);
+// The append's second half for an E2M1 pool, rows stored as they are (kv_e2m1.cu).
+cudaError_t launch_kv_store_e2m1(const KV &kv, const void *new_k, const void *new_v, const int32_t *cu_q, int total_q,
+                                 int32_t *status, cudaStream_t st);
+cudaError_t launch_kv_gather(const KV &kv, void *out_k, void *out_v, const int32_t *cu_rows, int total_rows,
+                             const int32_t *first, int32_t *status, cudaStream_t st);
+// Private copies of shared blocks that an append has taken (the sequences' first new rows land in them).
+cudaError_t launch_private_copies(const KV &kv, const int32_t *cu_q, int32_t *status, cudaStream_t st);
 cudaError_t launch_attn_scored_simt(const ScoredArgs &sa, int dtype, cudaStream_t st);
 // The tensor-core kernels (attn_scored.cuh, attn_scored_wide.cu): the workspace of a call, 0 for one that they do not
 // take; that into *bytes and, with `go`, the launches (workspace: that many bytes, 256-aligned).

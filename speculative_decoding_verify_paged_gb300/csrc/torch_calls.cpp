@@ -7,6 +7,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <stdexcept>
 #include <string>
 
@@ -16,10 +17,18 @@ namespace {
 
 using QkNormRope = decltype(&sv_qk_norm_rope);
 using KvAppendRope = decltype(&sv_kv_append_rope);
+using QkNormRopeAxes = decltype(&sv_qk_norm_rope_axes);
+using KvAppendRopeAxes = decltype(&sv_kv_append_rope_axes);
+using KvAppend = decltype(&sv_kv_append);
+using KvGather = decltype(&sv_kv_gather);
 using AttnScored = decltype(&sv_spec_verify_attn_scored);
 using AttnScoredBytes = decltype(&sv_spec_verify_attn_scored_workspace_bytes);
 QkNormRope g_heads;
 KvAppendRope g_append;
+QkNormRopeAxes g_heads_axes;
+KvAppendRopeAxes g_append_axes;
+KvAppend g_store;
+KvGather g_gather;
 AttnScored g_attn;
 AttnScoredBytes g_attn_bytes;
 
@@ -106,8 +115,8 @@ struct Held {  // attributes, released at the end of the call
   }
 };
 
-PyObject *s_names[16];
-enum { kK, kV, kTable, kLens, kFree, kTop, kRef, kKScale, kVScale, kFreq, kQW, kKW, kEps, kOffset, kInter, kNames };
+PyObject *s_names[24];
+enum { kK, kV, kTable, kLens, kFree, kTop, kRef, kKScale, kVScale, kKBs, kVBs, kFreq, kQW, kKW, kEps, kOffset, kInter, kAxes, kNames };
 
 // A PagedKV, with its tensors held.
 sv_paged_kv cache_of(PyObject *kv, Held &held) {
@@ -133,6 +142,21 @@ sv_paged_kv cache_of(PyObject *kv, Held &held) {
   p.dtype = k->scalar_type() == at::kByte ? SV_DTYPE_E4M3 : row_type(*k);
   p.k_scale = real(held.get(kv, s_names[kKScale]));
   p.v_scale = real(held.get(kv, s_names[kVScale]));
+  const at::Tensor *kb = field(kKBs), *vb = field(kVBs);
+  if (kb != nullptr || vb != nullptr) {
+    if (kb == nullptr || vb == nullptr || p.dtype != SV_DTYPE_E4M3 /* uint8 */ || p.head_dim % 16 != 0)
+      value_error("an E2M1 cache has uint8 pools of head_dim / 2 bytes a row and block scales for both");
+    p.dtype = SV_DTYPE_E2M1;
+    p.head_dim = narrow(2LL * p.head_dim);
+    auto scales = [&](const at::Tensor &t) {
+      if (t.dim() != 4 || t.size(0) != p.num_blocks || t.size(1) != p.num_kv_heads || t.size(2) != p.block_size ||
+          t.size(3) != p.head_dim / 16 || t.scalar_type() != at::kByte)
+        value_error("block scales are uint8 [blocks, heads, block_size, head_dim / 16]");
+      return contiguous(&t);
+    };
+    p.k_block_scales = scales(*kb);
+    p.v_block_scales = scales(*vb);
+  }
   return p;
 }
 
@@ -152,6 +176,30 @@ sv_head_transform transform_of(PyObject *t, const at::Tensor &rows, Held &held) 
   p.interleaved = PyObject_IsTrue(field(kInter));
   if (p.interleaved < 0) throw TypeError("");
   return p;
+}
+
+// The axes of a HeadTransform (false: one axis), and the positions of `rows` rows that go with them.
+bool axes_of(PyObject *t, const sv_head_transform &p, const at::Tensor *positions, int rows, sv_rotary_axes *axes,
+             const int32_t **at, Held &held) {
+  PyObject *o = held.get(t, s_names[kAxes]);
+  if (o == Py_None) {
+    *at = values<int32_t>(positions, at::kInt, rows, "positions");
+    return false;
+  }
+  if (!PyBytes_Check(o)) throw TypeError("axes are bytes, one for each pair");
+  if (PyBytes_GET_SIZE(o) != p.rotary_dim / 2 || p.rotary_dim / 2 > (int)sizeof axes->axis)
+    value_error("axes hold one byte for each pair");
+  const uint8_t *b = reinterpret_cast<const uint8_t *>(PyBytes_AS_STRING(o));
+  int most = 0;
+  for (int i = 0; i < p.rotary_dim / 2; ++i) most = std::max<int>(most, axes->axis[i] = b[i]);
+  axes->num_axes = most + 1;
+  if (positions != nullptr) {
+    if (positions->dim() != 2 || positions->size(0) <= most || positions->size(1) != rows)
+      value_error("positions are int32 [axes, n]");
+    axes->num_axes = narrow(positions->size(0));
+    *at = values<int32_t>(positions, at::kInt, positions->numel(), "positions");
+  }
+  return true;
 }
 
 void *address(PyObject *stream) { return reinterpret_cast<void *>(static_cast<uintptr_t>(integer(stream))); }
@@ -198,9 +246,13 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Held held;
     const sv_head_transform t = transform_of(a[0], *some, held);
     const int rows = narrow(some->size(0));
+    sv_rotary_axes axes;
+    const int32_t *positions = nullptr;
+    if (axes_of(a[0], t, tensor(a[3]), rows, &axes, &positions, held))
+      return g_heads_axes(&t, &axes, rq.at, rq.stride, rqo.at, rqo.stride, hq, rk.at, rk.stride, rko.at, rko.stride, hkv,
+                          narrow(some->size(2)), row_type(*some), rows, positions, address(a[6]));
     return g_heads(&t, rq.at, rq.stride, rqo.at, rqo.stride, hq, rk.at, rk.stride, rko.at, rko.stride, hkv,
-                   narrow(some->size(2)), row_type(*some), rows, values<int32_t>(tensor(a[3]), at::kInt, rows, "positions"),
-                   address(a[6]));
+                   narrow(some->size(2)), row_type(*some), rows, positions, address(a[6]));
   });
 }
 
@@ -225,10 +277,51 @@ PyObject *kv_append_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
       hq = narrow(q->size(1));
     }
     const sv_head_transform t = transform_of(a[1], k, held);
-    return g_append(&kv, &t, rk.at, rk.stride, rv.at, rv.stride, rq.at, rq.stride, rqo.at, rqo.stride, hq,
-                    values<int32_t>(tensor(a[4]), at::kInt, (int64_t)kv.batch + 1, "cu_q"), rows,
-                    values<int32_t>(tensor(a[8]), at::kInt, rows, "positions"),
-                    values<int32_t>(tensor(a[5]), at::kInt, 1, "status"), address(a[9]));
+    const int32_t *cu = values<int32_t>(tensor(a[4]), at::kInt, (int64_t)kv.batch + 1, "cu_q");
+    int32_t *status = values<int32_t>(tensor(a[5]), at::kInt, 1, "status");
+    sv_rotary_axes axes;
+    const int32_t *positions = nullptr;
+    if (axes_of(a[1], t, tensor(a[8]), rows, &axes, &positions, held))
+      return g_append_axes(&kv, &t, &axes, rk.at, rk.stride, rv.at, rv.stride, rq.at, rq.stride, rqo.at, rqo.stride, hq, cu, rows,
+                           positions, status, address(a[9]));
+    return g_append(&kv, &t, rk.at, rk.stride, rv.at, rv.stride, rq.at, rq.stride, rqo.at, rqo.stride, hq, cu, rows, positions,
+                    status, address(a[9]));
+  });
+}
+
+// Dense rows of a cache, [n, num_kv_heads, head_dim] of its row type
+int dense_rows(const sv_paged_kv &kv, const at::Tensor &t) {
+  if (t.dim() != 3 || row_type(t) != (kv.dtype == SV_DTYPE_F32 ? SV_DTYPE_F32 : SV_DTYPE_BF16) || t.size(1) != kv.num_kv_heads ||
+      t.size(2) != kv.head_dim)
+    value_error("rows are [n, num_kv_heads, head_dim] of the cache's row type");
+  return narrow(t.size(0));
+}
+
+// (kv, new_k, new_v, cu_q, status, stream)
+PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return answer(n, 6, [&] {
+    Held held;
+    const sv_paged_kv kv = cache_of(a[0], held);
+    const at::Tensor &k = needed(a[1], "new_k"), &v = needed(a[2], "new_v");
+    const int rows = dense_rows(kv, k);
+    if (dense_rows(kv, v) != rows) value_error("new_k and new_v have the same rows");
+    return g_store(&kv, contiguous(&k), contiguous(&v), values<int32_t>(tensor(a[3]), at::kInt, (int64_t)kv.batch + 1, "cu_q"), rows,
+                   values<int32_t>(tensor(a[4]), at::kInt, 1, "status"), address(a[5]));
+  });
+}
+
+// (kv, out_k, out_v, cu_rows, status, first, stream)
+PyObject *kv_gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return answer(n, 7, [&] {
+    Held held;
+    const sv_paged_kv kv = cache_of(a[0], held);
+    const at::Tensor *k = tensor(a[1]), *v = tensor(a[2]);
+    if (k == nullptr && v == nullptr) value_error("no outputs: out_k and out_v are both None");
+    const int rows = dense_rows(kv, k != nullptr ? *k : *v);
+    if (v != nullptr && dense_rows(kv, *v) != rows) value_error("out_k and out_v have the same rows");
+    return g_gather(&kv, contiguous(k), contiguous(v), values<int32_t>(tensor(a[3]), at::kInt, (int64_t)kv.batch + 1, "cu_rows"), rows,
+                    values<int32_t>(tensor(a[5]), at::kInt, kv.batch, "first"), values<int32_t>(tensor(a[4]), at::kInt, 1, "status"),
+                    address(a[6]));
   });
 }
 
@@ -267,11 +360,15 @@ PyObject *spec_verify_attn_scored(PyObject *, PyObject *const *a, Py_ssize_t n) 
 
 // The library's entry points, by address.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return answer(n, 4, [&] {
-    g_heads = reinterpret_cast<QkNormRope>(address(a[0]));
-    g_append = reinterpret_cast<KvAppendRope>(address(a[1]));
+  return answer(n, 8, [&] {
+    g_heads_axes = reinterpret_cast<QkNormRopeAxes>(address(a[0]));
+    g_append_axes = reinterpret_cast<KvAppendRopeAxes>(address(a[1]));
     g_attn = reinterpret_cast<AttnScored>(address(a[2]));
     g_attn_bytes = reinterpret_cast<AttnScoredBytes>(address(a[3]));
+    g_store = reinterpret_cast<KvAppend>(address(a[4]));
+    g_gather = reinterpret_cast<KvGather>(address(a[5]));
+    g_heads = reinterpret_cast<QkNormRope>(address(a[6]));
+    g_append = reinterpret_cast<KvAppendRope>(address(a[7]));
     return 0;
   });
 }
@@ -280,6 +377,8 @@ PyMethodDef g_methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(bind), METH_FASTCALL, nullptr},
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(qk_norm_rope), METH_FASTCALL, nullptr},
     {"kv_append_rope", reinterpret_cast<PyCFunction>(kv_append_rope), METH_FASTCALL, nullptr},
+    {"kv_append", reinterpret_cast<PyCFunction>(kv_append), METH_FASTCALL, nullptr},
+    {"kv_gather", reinterpret_cast<PyCFunction>(kv_gather), METH_FASTCALL, nullptr},
     {"spec_verify_attn_scored", reinterpret_cast<PyCFunction>(spec_verify_attn_scored), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
@@ -288,7 +387,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods,
 
 extern "C" __attribute__((visibility("default"))) PyObject *PyInit__calls() {
   static const char *names[kNames] = {"k_pool",  "v_pool",  "block_table", "seq_lens", "free_list", "free_top",      "ref_count",  "k_scale",
-                                      "v_scale", "inv_freq", "q_weight",    "k_weight", "eps",       "weight_offset", "interleaved"};
+                                      "v_scale", "k_block_scales", "v_block_scales", "inv_freq", "q_weight", "k_weight", "eps",
+                                      "weight_offset", "interleaved", "axes"};
   for (int k = 0; k < kNames; ++k)
     if ((s_names[k] = PyUnicode_InternFromString(names[k])) == nullptr) return nullptr;
   return PyModule_Create(&g_module);

@@ -82,6 +82,7 @@ class DeviceStep:
     transform: Optional[L.HeadTransform] = None  # head norms and rotation of new_k and q
     mod: Optional[L.ScoreMod] = None  # modified attention scores
     positions: Optional[torch.Tensor] = None  # int32 [total_q] of the rows (trees); None: c_b + i
+    axis_positions: Optional[torch.Tensor] = None  # int32 [axes, total_q], for a transform with axes; None: c_b + i
 
     @property
     def batch(self) -> int:
@@ -152,8 +153,11 @@ def attn_workspace_bytes(kv, d: DeviceStep, max_seq_len: int) -> int:
 
 def append(kv, d: DeviceStep, buf: StepBuffers, stream=None):
     if d.transform is not None:
+        with_axes = d.transform.axes is not None
+        if with_axes and d.axis_positions is None and d.positions is not None:
+            raise ValueError("a transform with axes takes axis_positions [axes, total_q] where rows are not at c_b + i")
         L.kv_append_rope(kv, d.transform, d.new_k, d.new_v, d.cu_q, buf.status, q=d.q, q_out=buf.q_rot,
-                         positions=d.positions, stream=stream)
+                         positions=d.axis_positions if with_axes else d.positions, stream=stream)
         return
     L.kv_append(kv, d.new_k, d.new_v, d.cu_q, buf.status, stream=stream)
 
@@ -201,9 +205,9 @@ def run_step(kv: L.PagedKV, d: DeviceStep, buf: StepBuffers, max_seq_len: int, s
 
 def launches_per_step(d: DeviceStep, max_seq_len: int, kv: L.PagedKV) -> int:
     """Kernels the library launches for one run_step (append 2, and 1 for the private copies where a
-    transforming append may share blocks; attention 1 or 2, sampler 2: statistics and decisions, rollback
-    1 or 2)."""
+    transforming append, or one into an E2M1 pool, may share blocks; attention 1 or 2, sampler 2: statistics
+    and decisions, rollback 1 or 2)."""
     ws = attn_workspace_bytes(kv, d, max_seq_len)
-    n = 2 + (d.transform is not None and kv.ref_count is not None)
+    n = 2 + ((d.transform is not None or getattr(kv, "k_block_scales", None) is not None) and kv.ref_count is not None)
     n += (2 if ws > 0 else 1) + 2 + (2 if d.mask_kind == L.SV_MASK_TREE else 1)
     return n
