@@ -25,13 +25,15 @@ EncodeTiledFn tensor_map_encoder() {
 }
 template <int D, bool F8>
 cudaError_t pick(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);
+template <int D>
+cudaError_t pick4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);
 }
 
-// bf16 and E4M3 caches with heads of 64, 128 or 256 values in blocks of 8 tokens and more
-// (attn_scored.cuh); a TMA row coordinate is a 32-bit number, and so are a unit's rows.
+// bf16, E4M3 and E2M1 caches with heads of 64, 128 or 256 values in blocks of 8 tokens and more
+// (attn_scored.cuh, attn_e2m1.cuh); a TMA row coordinate is a 32-bit number, and so are a unit's rows.
 size_t attn_scored_mma_workspace(const ScoredArgs &sa) {
   const KV &kv = sa.a.kv;
-  if (kv.fp4 || kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return 0;
+  if (kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return 0;
   if (kv.block_size < 8 || (long long)kv.num_blocks * kv.num_kv_heads * kv.block_size >= (1LL << 31)) return 0;
   if ((long long)(sa.a.num_q_heads / kv.num_kv_heads) * sa.a.max_q >= (1LL << 30)) return 0;
   size_t bytes = 0;
@@ -41,6 +43,10 @@ size_t attn_scored_mma_workspace(const ScoredArgs &sa) {
 
 cudaError_t launch_attn_scored_mma(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {
   const bool f8 = sa.a.kv.fp8;
+  if (sa.a.kv.fp4)
+    return sa.a.kv.head_dim == 64    ? scored::pick4<64>(sa, workspace, bytes, st, go)
+           : sa.a.kv.head_dim == 128 ? scored::pick4<128>(sa, workspace, bytes, st, go)
+                                     : scored::pick4<256>(sa, workspace, bytes, st, go);
   switch (sa.a.kv.head_dim) {
     case 64: return f8 ? scored::pick<64, true>(sa, workspace, bytes, st, go) : scored::pick<64, false>(sa, workspace, bytes, st, go);
     case 128: return f8 ? scored::pick<128, true>(sa, workspace, bytes, st, go) : scored::pick<128, false>(sa, workspace, bytes, st, go);
