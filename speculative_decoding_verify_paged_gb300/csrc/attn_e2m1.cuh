@@ -8,7 +8,7 @@
 // bits stay, and what lies 2^-28 below that value is off by 2^-39 of it at most. No query is too large. Weights are rounded to fp16
 // (2^-11 of themselves, 2^-25 where that is more), their sum is of the unrounded ones.
 //
-// A CTA is four warps, and each works by itself until the end of a piece: it takes 16 of a tile's 64 keys, for all RB = 8
+// A CTA is four warps, and each works by itself until the end of a piece: it takes M x 16 of a tile's keys, for all RB = 8
 // NT rows of the unit, through a ring of stages of its own (16 keys' codes and scales: 18 D bytes), filled with 16-byte
 // asynchronous copies that run on into the CTA's next piece. Nothing waits for another warp, so no barrier can run out. In
 // a step
@@ -27,22 +27,28 @@
 namespace sv {
 namespace scored {
 
-template <int D_, int NT_, int CTAS_, int STAGES_>
+template <int D_, int NT_, int M_, int CTAS_, int STAGES_>
 struct Cfg4 {
   static constexpr int D = D_, NT = NT_, RB = NT_ * 8, kCtasPerSm = CTAS_, kStages = STAGES_;
-  static constexpr int kWarps = 4, kThreads = 128, TK = 64;
-  static constexpr int kAlpha = 4;                  // positions of a unit's lead-in
+  static constexpr int M = M_, kKeys = 16 * M;  // keys of a step
+  static constexpr int kWarps = 4, kThreads = 128, TK = kWarps * kKeys;
+  static constexpr int kAlpha = M == 1 ? 4 : 2;  // positions of a unit's lead-in
   static constexpr int KT = D / 16;
-  static constexpr int kCodes = 8 * D, kScales = D;  // bytes of 16 keys (or values): codes, block scales
+  static constexpr int kCodes = 8 * D * M, kScales = D * M;  // bytes of a step's keys (or values): codes, block scales
   static constexpr int kStage = 2 * (kCodes + kScales);
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kTiles = KT < 8 ? KT : 8;     // 16-value tiles of O that are merged at a time
   static constexpr int kPad = kTiles * 16 + 4;       // floats of a row in the merge buffer
-  static constexpr int kSmem = kRing + kWarps * 8 * kPad * 4;
+  static constexpr int kMerge = kWarps * 8 * kPad * 4;
+  static constexpr bool kQs = NT * KT > 16;  // Q in shared memory: registers are better spent on two chains of products
+  static constexpr int kSmem = kRing + kMerge + (kQs ? NT * KT * 256 : 0);
   static_assert(kCtasPerSm * (kSmem + 3072) <= 227 * 1024, "shared memory of an SM");
 };
 
 template <int LEFT> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+__device__ __forceinline__ void copy_all(uint32_t dst, const uint8_t *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // 16 bytes into shared memory, zeros from byte n on
 __device__ __forceinline__ void copy_some(uint32_t dst, const uint8_t *src, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -73,7 +79,7 @@ template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(const Params P) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
-  constexpr int D = C::D, NT = C::NT, TK = C::TK, RB = C::RB, KT = C::KT, ST = C::kStages;
+  constexpr int D = C::D, NT = C::NT, TK = C::TK, RB = C::RB, KT = C::KT, ST = C::kStages, M = C::M, kKeys = C::kKeys;
   constexpr int kThreads = C::kThreads, kWarps = C::kWarps;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t s_mask[RB];         // new keys that a row sees
@@ -81,7 +87,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
   __shared__ float s_slope[RB];
   __shared__ int s_place[64];  // position of a new row minus the first one's
   __shared__ float s_m[kWarps][RB], s_l[kWarps][RB];
-  __shared__ int s_patch;  // a key of the piece's edge steps has a NaN among its values
+  __shared__ float s_in[RB];  // what a row's products are multiplied with
+  __shared__ int s_patch;     // a key of the piece's edge steps has a NaN among its values
   __shared__ int s_scan[kWarps], s_first_b, s_first_base, s_top[kWarps];
 
   const AttnArgs &a = P.s.a;
@@ -155,56 +162,66 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
   // ---- the ring: this warp's stages, and its way ahead of what is being used ----
   const uint32_t ring = smem_at(smem) + warp * ST * C::kStage;
   const int bs = kv.block_size, bs_shift = __ffs(bs) - 1;
-  // What a lane copies of a stage: `kPer` times 16 bytes of the keys' codes and as many of the values', rows of 16 keys
-  // kPer x 32 chunks in all; then 16 bytes of scales. Key r of the step stands in row r; value row p holds key vkey(p),
-  // so that the four keys of one read (p = 4 j + t) are 2 t + (j & 1) + 8 (j >> 1), as a B operand has them.
-  constexpr int kChunks = D / 32, kPer = D / 64;  // 16-byte chunks of a row; of a stage to a lane
-  auto vkey = [](int p) { return 2 * (p & 3) + ((p >> 2) & 1) + 8 * (p >> 3); };
+  // What a lane copies of a stage: kPer times 16 bytes of the keys' codes and as many of the values'; then 16 bytes of scales.
+  // Key r of the step stands in row r; of each 16 value rows row p holds key vkey(p), so that the four keys of one read
+  // (p = 4 j + t) are 2 t + (j & 1) + 8 (j >> 1), as a B operand has them.
+  constexpr int kChunks = D / 32, kPer = M * D / 64;  // 16-byte chunks of a row; of a stage to a lane
+  auto vkey = [](int p) { return (p & 16) + 2 * (p & 3) + ((p >> 2) & 1) + 8 * ((p >> 3) & 1); };
   // (chunk c of row r stands in place c ^ these)
   auto k_turn = [](int r) { return D == 256 ? 4 * (r & 1) : 0; };
   auto v_turn = [](int p) { return D == 256 ? 2 * (p & 3) : D == 128 ? 2 * ((p >> 1) & 1) : 0; };
-  struct Tile {
-    int b, kvh, ke, lo, key0;  // key0: the first of this warp's keys
+  // where the warp's copies are: the piece that they belong to, its tiles left, and the next one's first key
+  int ahead_left = 0, ahead_key = 0, ahead_b = 0, ahead_kvh = 0, ahead_ke = 0, ahead_lo = 0, id = -1;
+  auto load_ids = [&] {  // lane 4 k + j: of the block with the j-th 8 of the next tile's keys; -1: none to be read
+    const int key = ahead_key + 8 * (lane & (2 * M - 1));
+    id = -1;
+    if (key < ahead_ke && key + 8 > ahead_lo) {
+      id = kv.block_table[(size_t)ahead_b * kv.max_blocks + (key >> bs_shift)];
+      if (id < 0 || id >= kv.num_blocks) {
+        record(a.status, SV_ERR_BAD_BLOCK_ID);
+        id = -1;
+      }
+    }
   };
-  auto ids_of = [&](const Tile &x, int &i0, int &i1) {  // of the blocks that hold the first and the last 8 keys; -2: not wanted
-    const int32_t *bt = kv.block_table + (size_t)x.b * kv.max_blocks;
-    i0 = x.key0 < x.ke && x.key0 + 8 > x.lo ? bt[x.key0 >> bs_shift] : -2;
-    i1 = x.key0 + 8 < x.ke && x.key0 + 16 > x.lo ? bt[(x.key0 + 8) >> bs_shift] : -2;
-  };
-  auto bring = [&](const Tile &x, int i0, int i1, uint32_t stage) {
-    const bool ok0 = i0 >= 0 && i0 < kv.num_blocks, ok1 = i1 >= 0 && i1 < kv.num_blocks;
-    if ((i0 != -2 && !ok0) || (i1 != -2 && !ok1)) record(a.status, SV_ERR_BAD_BLOCK_ID);
-    if (ok0 || ok1) {  // (a stage that no row needs is not read)
-      // rows of the pool where key0, and key0 + 8 less 8, stand
-      const size_t row0 = (((size_t)(ok0 ? i0 : 0) * kv.num_kv_heads + x.kvh) << bs_shift) + (x.key0 & (bs - 1));
-      const size_t row1 = (((size_t)(ok1 ? i1 : 0) * kv.num_kv_heads + x.kvh) << bs_shift) + ((x.key0 + 8) & (bs - 1)) - 8;
+  auto bring = [&](uint32_t stage) {
+    const int key0 = ahead_key, ke = ahead_ke, lo = ahead_lo;
+    auto row_of = [&](int i8) {  // the pool's row of the i8-th 8 keys, less their place in the step
+      const int x = __shfl_sync(0xffffffffu, id, i8);
+      return (((size_t)max(x, 0) * kv.num_kv_heads + ahead_kvh) << bs_shift) + ((key0 + 8 * i8) & (bs - 1)) - 8 * i8;
+    };
+    const bool all = __all_sync(0xffffffffu, id >= 0) && key0 >= lo && key0 + kKeys <= ke;  // every key is there
 #pragma unroll
-      for (int y = 0; y < kPer; ++y) {
-        const int q = lane + 32 * y, r = q / kChunks, c = q % kChunks, rv = vkey(r);
-        // rows and value rows from 8 on are the last 8 keys
-        const bool last = r >= 8, ok = last ? ok1 : ok0;
-        const size_t row = last ? row1 : row0;
-        const int kk = x.key0 + r, vk = x.key0 + rv;
-        copy_some(stage + r * (D / 2) + ((c ^ k_turn(r)) << 4), (const uint8_t *)kv.k_pool + (ok ? (row + r) * (D / 2) + c * 16 : 0),
-                  ok && kk < x.ke && kk >= x.lo ? 16 : 0);
-        copy_some(stage + C::kCodes + r * (D / 2) + ((c ^ v_turn(r)) << 4),
-                  (const uint8_t *)kv.v_pool + (ok ? (row + rv) * (D / 2) + c * 16 : 0), ok && vk < x.ke && vk >= x.lo ? 16 : 0);
+    for (int y = 0; y < kPer; ++y) {
+      const int q = lane + 32 * y, r = q / kChunks, c = q % kChunks, rv = vkey(r), i8 = r >> 3;
+      const size_t row = row_of(i8);
+      const uint32_t kd = stage + r * (D / 2) + ((c ^ k_turn(r)) << 4), vd = stage + C::kCodes + r * (D / 2) + ((c ^ v_turn(r)) << 4);
+      const uint8_t *ks = (const uint8_t *)kv.k_pool + (row + r) * (D / 2) + c * 16, *vs = (const uint8_t *)kv.v_pool + (row + rv) * (D / 2) + c * 16;
+      if (all) {
+        copy_all(kd, ks);
+        copy_all(vd, vs);
+      } else {
+        const bool there = __shfl_sync(0xffffffffu, id, i8) >= 0;
+        const int kk = key0 + r, vk = key0 + rv;
+        copy_some(kd, ks, there && kk < ke && kk >= lo ? 16 : 0);
+        copy_some(vd, vs, there && vk < ke && vk >= lo ? 16 : 0);
       }
-      const int l = lane & 15;
-      if (l < D / 16) {  // scales: lanes 0 .. 15 the keys', the others the values'
-        const int r = l * (256 / D);
-        const bool last = r >= 8, ok = last ? ok1 : ok0;
-        // those of keys past the end are zeros: what they scale is of no one
-        const int n = ok ? max(0, min(16, (x.ke - x.key0 - r) * (D / 16))) : 0;
-        copy_some(stage + 2 * C::kCodes + (lane >> 4) * C::kScales + l * 16,
-                  (lane < 16 ? kv.k_bs : kv.v_bs) + (ok ? ((last ? row1 : row0) + r) * (D / 16) : 0), n);
-      }
+    }
+#pragma unroll
+    for (int y = 0; y < (M * D / 16 + 15) / 16; ++y) {  // scales: lanes 0 .. 15 the keys', the others the values'
+      const int l = (lane & 15) + 16 * y, r = l * (256 / D), i8 = (r >> 3) & (2 * M - 1);
+      const size_t row = row_of(i8);
+      const bool there = __shfl_sync(0xffffffffu, id, i8) >= 0;
+      // those of keys past the end are zeros: what they scale is of no one
+      if (l < M * D / 16)
+        copy_some(stage + 2 * C::kCodes + (lane >> 4) * C::kScales + l * 16, (lane < 16 ? kv.k_bs : kv.v_bs) + (row + r) * (D / 16),
+                  all ? 16 : there ? max(0, min(16, (ke - key0 - r) * (D / 16))) : 0);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   // ---- constants of the launch ----
   float *merge = reinterpret_cast<float *>(smem + C::kRing);  // [warp][8][kPad]
+  const uint32_t q_at = smem_at(smem) + C::kRing + C::kMerge + lane * 8;  // Q's operands, [n tile][16 values][lane]
   const float cap = P.s.cap;
   const bool fast_cap = cap <= kFastCap * 1.4426950408889634f;
   const int window = P.s.window;
@@ -212,9 +229,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
   // what a product is multiplied with, less the row's own factor
   const float factor = (cap > 0.f && fast_cap ? P.cap_in : a.scale_log2) * kv.k_scale;
 
-  bool first_piece = true, primed = false;
-  int filled = 0, nid0 = -2, nid1 = -2;  // tiles on their way or there; the next one's blocks, if primed
-  uint32_t get = 0, put = 0;             // stages
+  bool first_piece = true;
+  int filled = 0;             // tiles on their way or there
+  uint32_t get = 0, put = 0;  // stages
   Piece pn = {};
   int bn = 0;
   Seq sn = {};
@@ -224,30 +241,41 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
     sn = at.s;
     return has;
   };
-  bool has = next();
+  bool has = next(), ahead_is_next = true;  // the copies have gone on (or go first) to the piece in pn
+  auto start_copies = [&] {
+    ahead_left = pn.kt1 - pn.kt0;
+    ahead_key = pn.kt0 * TK + warp * kKeys;
+    ahead_b = bn;
+    ahead_kvh = pn.kvh;
+    ahead_ke = pn.ke;
+    ahead_lo = pn.lo;
+    load_ids();
+  };
+  if (has) start_copies();
   while (has) {
     const Piece p = pn;
     const Seq s = sn;
     const int b = bn;
     has = next();
-    const int n_tiles = p.kt1 - p.kt0, n_next = has ? pn.kt1 - pn.kt0 : 0;
+    if (ahead_is_next && ahead_left == 0 && has) start_copies();  // the copies had come to the end of what was known
+    else ahead_is_next = false;
+    const int n_tiles = p.kt1 - p.kt0;
     const int c = s.c, ke = p.ke, lo = p.lo, kvh = p.kvh, rb = p.rb;
-    auto tile_of = [&](int x) {  // tile x from this piece's first on (the next one's after its last)
-      return x < n_tiles ? Tile{b, kvh, ke, lo, (p.kt0 + x) * TK + warp * 16}
-                         : Tile{bn, pn.kvh, pn.ke, pn.lo, (pn.kt0 + x - n_tiles) * TK + warp * 16};
-    };
-    auto top_up = [&](int now) {
-      while (filled < ST && now + filled < n_tiles + n_next) {
-        const Tile x = tile_of(now + filled);
-        if (!primed) ids_of(x, nid0, nid1);
-        bring(x, nid0, nid1, ring + put * C::kStage);
+    auto top_up = [&] {
+      while (filled < ST && ahead_left > 0) {
+        bring(ring + put * C::kStage);
         put = put + 1 == ST ? 0 : put + 1;
         ++filled;
-        primed = now + filled < n_tiles + n_next;
-        if (primed) ids_of(tile_of(now + filled), nid0, nid1);
+        ahead_key += TK;
+        if (--ahead_left > 0) {
+          load_ids();
+        } else if (!ahead_is_next && has) {
+          ahead_is_next = true;
+          start_copies();
+        }
       }
     };
-    top_up(0);
+    top_up();
     const int rows = min(RB, P.G * s.n - rb * RB);  // live rows of the block
 
     // ---- rows of the block and the new keys' places (every warp is done with the previous piece's) ----
@@ -280,11 +308,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
     if (lane == 0) s_top[warp] = top;
     if (tid == 0) s_patch = 0;
 
-    // ---- Q into registers: fp16, each row next to a power of two ----
-    uint32_t q[NT][KT][2];
-    float in[NT][2];  // what a score is multiplied with: of rows 2 t and 2 t + 1 of each n tile
+    // ---- Q: fp16, each row next to a power of two; its operands in registers, or in shared memory for all warps ----
+    uint32_t q[C::kQs ? 1 : NT][KT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      uint32_t(&w)[KT][2] = q[C::kQs ? 0 : nt];
+      if (C::kQs && nt % kWarps != warp) continue;
       const int rl = nt * 8 + g, r = rb * RB + rl, i = r / P.G;
       const bool live = rl < rows;
       const uint2 *src = reinterpret_cast<const uint2 *>(a.q) +
@@ -293,8 +322,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
 #pragma unroll
       for (int kk = 0; kk < KT; ++kk) {  // four values from a lane's run (256: two runs) of the head
         const uint2 x = live ? src[(D == 256 ? 32 * (kk >> 3) + 8 * t + (kk & 7) : KT * t + kk)] : make_uint2(0, 0);
-        q[nt][kk][0] = x.x;
-        q[nt][kk][1] = x.y;
+        w[kk][0] = x.x;
+        w[kk][1] = x.y;
         most = max(most, max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu), max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu)));
       }
       most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
@@ -305,9 +334,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
       for (int kk = 0; kk < KT; ++kk)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          q[nt][kk][h] = pack2<true>(__uint_as_float(q[nt][kk][h] << 16) * up, __uint_as_float(q[nt][kk][h] & 0xffff0000u) * up);
+          w[kk][h] = pack2<true>(__uint_as_float(w[kk][h] << 16) * up, __uint_as_float(w[kk][h] & 0xffff0000u) * up);
+      if (t == 0 && (C::kQs || warp == 0)) s_in[rl] = finite(factor * down);
+      if constexpr (C::kQs)
 #pragma unroll
-      for (int e2 = 0; e2 < 2; ++e2) in[nt][e2] = finite(factor * __shfl_sync(0xffffffffu, down, (2 * t + e2) * 4));
+        for (int kk = 0; kk < KT; ++kk)
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_at + (nt * KT + kk) * 256), "r"(w[kk][0]), "r"(w[kk][1]) : "memory");
     }
     __syncthreads();
     int row_top = s_top[0];
@@ -315,6 +347,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
     for (int w = 1; w < kWarps; ++w) row_top = max(row_top, s_top[w]);
     const int all_see = window > 0 ? row_top - window + 1 : 0;  // keys from here to c are visible to every row
 
+    float in[NT][2];  // of rows 2 t and 2 t + 1 of each n tile
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 x = *reinterpret_cast<const float2 *>(&s_in[nt * 8 + 2 * t]);
+      in[nt][0] = x.x;
+      in[nt][1] = x.y;
+    }
     float o[KT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -326,117 +365,131 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
 
     for (int tile = 0; tile < n_tiles; ++tile) {
       __syncwarp();  // every lane is done with the stage that is filled next
-      top_up(tile);
+      top_up();
       if (filled == ST) copies_wait<ST - 1>();
       else copies_wait<0>();
       __syncwarp();
-      const int key0 = (p.kt0 + tile) * TK + warp * 16;
+      const int key0 = (p.kt0 + tile) * TK + warp * kKeys;
       const uint32_t stage = ring + get * C::kStage;
       get = get + 1 == ST ? 0 : get + 1;
       --filled;
-      if (key0 >= ke || key0 + 16 <= lo) continue;  // warp-uniform: nothing to see here
+      if (key0 >= ke || key0 + kKeys <= lo) continue;  // warp-uniform: nothing to see here
       // ---- S^T = K Q^T ----
       constexpr int kWords = D / 32;  // a lane's words of a key's codes; of a value's half as many
-      uint32_t kw[2][kWords], ks[2][(kWords + 1) / 2];
+      constexpr int kVw = kWords / 2, kVs = D == 256 ? 2 : 1;
+      uint32_t kw[M][2][kWords], ks[M][2][(kWords + 1) / 2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = g + 8 * h;
-        const uint32_t row = stage + r * (D / 2), sc = stage + 2 * C::kCodes + r * (D / 16);
-        if constexpr (D == 64) {
-          read_words<8>(row + t * 8, kw[h]);
-          ks[h][0] = read_byte(sc + t);
-        } else if constexpr (D == 128) {
-          read_words<16>(row + t * 16, kw[h]);
-          ks[h][0] = read_half(sc + 2 * t);
-        } else {
-          read_words<16>(row + ((t ^ k_turn(r)) << 4), kw[h]);
-          read_words<16>(row + (((t + 4) ^ k_turn(r)) << 4), kw[h] + 4);
-          ks[h][0] = read_half(sc + 2 * t);
-          ks[h][1] = read_half(sc + 8 + 2 * t);
+      for (int u = 0; u < M; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * u + g + 8 * h;
+          const uint32_t row = stage + r * (D / 2), sc = stage + 2 * C::kCodes + r * (D / 16);
+          if constexpr (D == 64) {
+            read_words<8>(row + t * 8, kw[u][h]);
+            ks[u][h][0] = read_byte(sc + t);
+          } else if constexpr (D == 128) {
+            read_words<16>(row + t * 16, kw[u][h]);
+            ks[u][h][0] = read_half(sc + 2 * t);
+          } else {
+            read_words<16>(row + ((t ^ k_turn(r)) << 4), kw[u][h]);
+            read_words<16>(row + (((t + 4) ^ k_turn(r)) << 4), kw[u][h] + 4);
+            ks[u][h][0] = read_half(sc + 2 * t);
+            ks[u][h][1] = read_half(sc + 8 + 2 * t);
+          }
         }
-      }
-      // the values' words and scales: keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-      constexpr int kVw = kWords / 2;
-      uint32_t vw[4][kVw], vs[2][D == 256 ? 2 : 1];  // vs: two keys' scales, a byte each
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int pr = 4 * j + t;
-        const uint32_t row = stage + C::kCodes + pr * (D / 2);
-        if constexpr (D == 64) read_words<4>(row + g * 4, vw[j]);
-        else if constexpr (D == 128) read_words<8>(row + (((g >> 1) ^ v_turn(pr)) << 4) + (g & 1) * 8, vw[j]);
-        else read_words<16>(row + ((g ^ v_turn(pr)) << 4), vw[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t sc = stage + 2 * C::kCodes + C::kScales + (2 * t + 8 * j) * (D / 16);
-        if constexpr (D == 256) {
-          const uint32_t x = read_half(sc + 2 * g), y = read_half(sc + 16 + 2 * g);
-          vs[j][0] = __byte_perm(x, y, 0x3340);
-          vs[j][1] = __byte_perm(x, y, 0x3351);
-        } else {
-          const int gr = D == 64 ? g >> 1 : g;
-          vs[j][0] = read_byte(sc + gr) | read_byte(sc + D / 16 + gr) << 8;
-        }
-      }
-      float sc[NT][4];
+      float sc[M][NT][4];
       {
-        constexpr int kSplit = NT == 1 ? 2 : 1;  // chains of products
-        float part[kSplit][NT][4];
+        constexpr int kSplit = NT * M == 1 ? 2 : 1;  // chains of products
+        float part[kSplit][M][NT][4];
 #pragma unroll
-        for (int y = 0; y < kSplit; ++y)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) part[y][nt][0] = part[y][nt][1] = part[y][nt][2] = part[y][nt][3] = 0.f;
-        uint32_t scale[2];
+        for (int y = 0; y < kSplit * M * NT * 4; ++y) (&part[0][0][0][0])[y] = 0.f;
+        uint32_t scale[M][2];
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
-          uint32_t f[2][4];
+          uint32_t f[M][2][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (w % 2 == 0) {  // two words of 8 codes to a scale
-              const uint32_t two = widen(ks[h][w >> 2]);
-              scale[h] = __byte_perm(two, 0u, D > 64 && (w & 2) ? 0x3232 : 0x1010);
+          for (int u = 0; u < M; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (w % 2 == 0) {  // two words of 8 codes to a scale
+                const uint32_t two = widen(ks[u][h][w >> 2]);
+                scale[u][h] = __byte_perm(two, 0u, D > 64 && (w & 2) ? 0x3232 : 0x1010);
+              }
+              widen8(kw[u][h][w], f[u][h][0], f[u][h][1], f[u][h][2], f[u][h][3]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) f[u][h][y] = mul2(f[u][h][y], scale[u][h]);
             }
-            widen8(kw[h][w], f[h][0], f[h][1], f[h][2], f[h][3]);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) f[h][y] = mul2(f[h][y], scale[h]);
-          }
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t e[4] = {f[0][2 * y], f[1][2 * y], f[0][2 * y + 1], f[1][2 * y + 1]};
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t b[2];
+              if constexpr (C::kQs) read_words<8>(q_at + (nt * KT + 2 * w + y) * 256, b);
+              else b[0] = q[nt][2 * w + y][0], b[1] = q[nt][2 * w + y][1];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<true>(part[y % kSplit][nt], e, q[nt][2 * w + y][0], q[nt][2 * w + y][1]);
-          }
+              for (int u = 0; u < M; ++u) {
+                const uint32_t e[4] = {f[u][0][2 * y], f[u][1][2 * y], f[u][0][2 * y + 1], f[u][1][2 * y + 1]};
+                mma<true>(part[y % kSplit][u][nt], e, b[0], b[1]);
+              }
+            }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < M; ++u)
 #pragma unroll
-          for (int y = 0; y < 4; ++y) sc[nt][y] = (kSplit == 2 ? part[0][nt][y] + part[kSplit - 1][nt][y] : part[0][nt][y]) * in[nt][y & 1];
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              sc[u][nt][y] = (kSplit == 2 ? part[0][u][nt][y] + part[kSplit - 1][u][nt][y] : part[0][u][nt][y]) * in[nt][y & 1];
+      }
+      // the values' words and scales, on their way during the softmax: keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+      uint32_t vw[M][4][kVw], vs[M][2][kVs];  // vs: two keys' scales, a byte each
+#pragma unroll
+      for (int u = 0; u < M; ++u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int pr = 16 * u + 4 * j + t;
+          const uint32_t row = stage + C::kCodes + pr * (D / 2);
+          if constexpr (D == 64) read_words<4>(row + g * 4, vw[u][j]);
+          else if constexpr (D == 128) read_words<8>(row + (((g >> 1) ^ v_turn(pr)) << 4) + (g & 1) * 8, vw[u][j]);
+          else read_words<16>(row + ((g ^ v_turn(pr)) << 4), vw[u][j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t at = stage + 2 * C::kCodes + C::kScales + (16 * u + 2 * t + 8 * j) * (D / 16);
+          if constexpr (D == 256) {
+            const uint32_t x = read_half(at + 2 * g), y = read_half(at + 16 + 2 * g);
+            vs[u][j][0] = __byte_perm(x, y, 0x3340);
+            vs[u][j][1] = __byte_perm(x, y, 0x3351);
+          } else {
+            const int gr = D == 64 ? g >> 1 : g;
+            vs[u][j][0] = read_byte(at + gr) | read_byte(at + D / 16 + gr) << 8;
+          }
+        }
       }
       // ---- scores ---- (element e of an n tile: key half e >> 1, row 2 t + (e & 1))
+      float *const sv = &sc[0][0][0];
+      constexpr int kE = M * NT * 4;
       if (cap > 0.f) {
         if (fast_cap) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = -2.f * cap * rcp(1.f + ex2(sc[nt][e]));
+          for (int y = 0; y < kE; ++y) sv[y] = -2.f * cap * rcp(1.f + ex2(sv[y]));
         } else {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = cap * tanhf(sc[nt][e] / cap);
+          for (int y = 0; y < kE; ++y) sv[y] = cap * tanhf(sv[y] / cap);
         }
       }
-      const bool edge = key0 + 16 > min(c, ke) || key0 < all_see;  // warp-uniform: some row may not see some key
+      const bool edge = key0 + kKeys > min(c, ke) || key0 < all_see;  // warp-uniform: some row may not see some key
       if (biased) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2 * M; ++h) {
           const int key = key0 + g + 8 * h, j = key - c;
           const float place = (float)(edge && j >= 0 && j < s.n ? s_place[j] : key - origin);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float2 sl = *reinterpret_cast<const float2 *>(&s_slope[nt * 8 + 2 * t]);
-            sc[nt][2 * h] = fmaf(sl.x, place, sc[nt][2 * h]);
-            sc[nt][2 * h + 1] = fmaf(sl.y, place, sc[nt][2 * h + 1]);
+            float *x = &sc[h >> 1][nt][2 * (h & 1)];
+            x[0] = fmaf(sl.x, place, x[0]);
+            x[1] = fmaf(sl.y, place, x[1]);
           }
         }
       }
@@ -453,35 +506,42 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
             const uint32_t near = first <= 0 ? ~0u : first >= 32 ? 0u : ~0u << first;
             const uint32_t fresh = base >= 0 ? (base < 64 ? (uint32_t)(mask >> base) : 0u) : (base > -32 ? (uint32_t)mask << -base : 0u);
             const uint32_t seen = ((old & near) | fresh) >> g;
-            if (!(seen & 1u)) sc[nt][e] = -INFINITY;
-            if (!((seen >> 8) & 1u)) sc[nt][e + 2] = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < 2 * M; ++h)
+              if (!((seen >> (8 * h)) & 1u)) sc[h >> 1][nt][2 * (h & 1) + e] = -INFINITY;
           }
         // Values that are NaN must not meet a weight of zero: their scales become zero, and the rows that see their keys
         // get them at the piece's end.
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int u = 0; u < M; ++u)
 #pragma unroll
-          for (int w = 0; w < (D == 256 ? 2 : 1); ++w) {
-            const uint32_t nan = nan_codes(vs[j][w]) & 0xffffu;
-            if (nan != 0u) {
-              vs[j][w] &= ~nan;
-              const int key = key0 + 2 * t + 8 * j;
-              if (((nan & 0xffu) && key >= lo && key < ke) || ((nan >> 8) && key + 1 >= lo && key + 1 < ke)) s_patch = 1;
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int w = 0; w < kVs; ++w) {
+              const uint32_t nan = nan_codes(vs[u][j][w]) & 0xffffu;
+              if (nan != 0u) {
+                vs[u][j][w] &= ~nan;
+                const int key = key0 + 16 * u + 2 * t + 8 * j;
+                if (((nan & 0xffu) && key >= lo && key < ke) || ((nan >> 8) && key + 1 >= lo && key + 1 < ke)) s_patch = 1;
+              }
             }
-          }
       }
       // ---- the running maximum ----
       bool move = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < M; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) move |= sc[nt][e] > m[nt][e & 1] + kMoveAt<true>;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) move |= sc[u][nt][e] > m[nt][e & 1] + kMoveAt<true>;
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(sc[nt][e], sc[nt][e + 2]);
+            float mx = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+#pragma unroll
+            for (int u = 1; u < M; ++u) mx = fmaxf(mx, fmaxf(sc[u][nt][e], sc[u][nt][e + 2]));
 #pragma unroll
             for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
             const float mn = fmaxf(m[nt][e], mx);
@@ -496,36 +556,40 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
           }
       }
       // ---- P^T ----
-      uint32_t pb[NT][2];
+      uint32_t pb[M][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int u = 0; u < M; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] = ex2(sc[nt][e] - m[nt][e & 1]);
-        l[nt][0] += sc[nt][0] + sc[nt][2];
-        l[nt][1] += sc[nt][1] + sc[nt][3];
-        pb[nt][0] = turn8x8(pack2<true>(sc[nt][0], sc[nt][1]));
-        pb[nt][1] = turn8x8(pack2<true>(sc[nt][2], sc[nt][3]));
-      }
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[u][nt][e] = ex2(sc[u][nt][e] - m[nt][e & 1]);
+          l[nt][0] += sc[u][nt][0] + sc[u][nt][2];
+          l[nt][1] += sc[u][nt][1] + sc[u][nt][3];
+          pb[u][nt][0] = turn8x8(pack2<true>(sc[u][nt][0], sc[u][nt][1]));
+          pb[u][nt][1] = turn8x8(pack2<true>(sc[u][nt][2], sc[u][nt][3]));
+        }
       // ---- O^T += V^T P^T: tile mt has values (D / 8) g + 2 mt and the next one, in rows g and g + 8 ----
 #pragma unroll
-      for (int w = 0; w < kVw; ++w) {
-        uint32_t f[2][8];  // pairs of keys; of the even values, of the odd ones
+      for (int w = 0; w < kVw; ++w)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t x = vw[2 * j][w], y = vw[2 * j + 1][w], scale = widen(vs[j][D == 256 ? w >> 1 : 0]);
-          constexpr uint32_t kLow = 0x0f0f0f0fu;
-          widen8((x & kLow) | ((y << 4) & ~kLow), f[j][0], f[j][2], f[j][4], f[j][6]);
-          widen8(((x >> 4) & kLow) | (y & ~kLow), f[j][1], f[j][3], f[j][5], f[j][7]);
+        for (int u = 0; u < M; ++u) {
+          uint32_t f[2][8];  // pairs of keys; of the even values, of the odd ones
 #pragma unroll
-          for (int y2 = 0; y2 < 8; ++y2) f[j][y2] = mul2(f[j][y2], scale);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t x = vw[u][2 * j][w], y = vw[u][2 * j + 1][w], scale = widen(vs[u][j][D == 256 ? w >> 1 : 0]);
+            constexpr uint32_t kLow = 0x0f0f0f0fu;
+            widen8((x & kLow) | ((y << 4) & ~kLow), f[j][0], f[j][2], f[j][4], f[j][6]);
+            widen8(((x >> 4) & kLow) | (y & ~kLow), f[j][1], f[j][3], f[j][5], f[j][7]);
+#pragma unroll
+            for (int y2 = 0; y2 < 8; ++y2) f[j][y2] = mul2(f[j][y2], scale);
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t e[4] = {f[0][2 * y], f[0][2 * y + 1], f[1][2 * y], f[1][2 * y + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<true>(o[4 * w + y][nt], e, pb[u][nt][0], pb[u][nt][1]);
+          }
         }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint32_t e[4] = {f[0][2 * y], f[0][2 * y + 1], f[1][2 * y], f[1][2 * y + 1]};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma<true>(o[4 * w + y][nt], e, pb[nt][0], pb[nt][1]);
-        }
-      }
     }
 
     // ---- the warps' results, merged, 8 rows at a time ----
@@ -610,9 +674,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
         bool nan = false;
 #pragma unroll 1
         for (int key = max(p.kt0 * TK, lo); key < ke && !nan; ++key) {
-          const int key0 = key & ~15, place = key - c;
-          if (!(key0 + 16 > min(c, ke) || key0 < all_see)) {  // on to the next edge step
-            key = (min(c, ke) & ~15) - 1;
+          const int key0 = key & ~(kKeys - 1), place = key - c;
+          if (!(key0 + kKeys > min(c, ke) || key0 < all_see)) {  // on to the next edge step
+            key = (min(c, ke) & ~(kKeys - 1)) - 1;
             continue;
           }
           if (!(place < 0 ? place > s_reach[rl] : (s_mask[rl] >> place) & 1ull)) continue;
@@ -653,16 +717,16 @@ cudaError_t pick4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStre
   const int rows = sa.a.num_q_heads / sa.a.kv.num_kv_heads * sa.a.max_q;
   auto on = [&](auto cfg) { return run4<decltype(cfg)>(sa, workspace, bytes, st, go); };
   if constexpr (D == 64) {
-    if (rows <= 8) return on(Cfg4<D, 1, 4, 8>());
-    if (rows <= 16) return on(Cfg4<D, 2, 4, 8>());
-    return on(Cfg4<D, 4, 2, 12>());
+    if (rows <= 8) return on(Cfg4<D, 1, 2, 4, 4>());
+    if (rows <= 16) return on(Cfg4<D, 2, 2, 3, 5>());
+    return on(Cfg4<D, 4, 2, 2, 6>());
   } else if constexpr (D == 128) {
-    if (rows <= 8) return on(Cfg4<D, 1, 4, 4>());
-    if (rows <= 16) return on(Cfg4<D, 2, 3, 5>());
-    return on(Cfg4<D, 3, 2, 8>());
+    if (rows <= 8) return on(Cfg4<D, 1, 2, 3, 3>());
+    if (rows <= 16) return on(Cfg4<D, 2, 2, 2, 4>());
+    return on(Cfg4<D, 3, 2, 2, 4>());
   } else {
-    if (rows <= 8) return on(Cfg4<D, 1, 2, 4>());
-    return on(Cfg4<D, 2, 2, 4>());
+    if (rows <= 8) return on(Cfg4<D, 1, 1, 2, 4>());
+    return on(Cfg4<D, 2, 1, 2, 4>());
   }
 }
 
