@@ -8,19 +8,17 @@
 // bits stay, and what lies 2^-28 below that value is off by 2^-39 of it at most. No query is too large. Weights are rounded to fp16
 // (2^-11 of themselves, 2^-25 where that is more), their sum is of the unrounded ones.
 //
-// A CTA is two pairs of warps, and a pair works by itself until the end of a piece: it takes 32 of a tile's 64 keys, for all
-// RB = 8 NT rows of the unit. In a step each warp has 16 keys of its own for the scores and half of the head's values for the
-// weighted sum:
+// A CTA is four warps, and each works by itself until the end of a piece: it takes M x 16 of a tile's keys, for all RB = 8
+// NT rows of the unit, through a ring of stages of its own (16 keys' codes and scales: 18 D bytes), filled with 16-byte
+// asynchronous copies that run on into the CTA's next piece. Nothing waits for another warp, so no barrier can run out. In
+// a step
 //   S^T (keys x rows) = K Q^T: a lane's share of a key is a run of D / 4 codes, which one or two reads bring: the order of
-//     the values along the contraction is free, and Q's operands follow it;
-//   weights as in attn_scored.cuh, into shared memory; a barrier of the pair that carries the vote on the running maximum;
-//   O^T (values x rows) += V^T P^T over both warps' keys: a lane's share of a key is a run of D / 16 codes. Two keys'
-//     words become one of pairs by two shifts and two selects, and O's rows follow the order in which they come.
-// (One warp with 16 or 32 keys and all of the values kept 96 sums a thread for 24 rows, two warps a scheduler, and waited:
-// 32 x 6 rows 57 and 51 us.) A pair of codes becomes an operand's word by one conversion and one product with its scale. Codes and scales come
-// through a ring of stages (a warp's 16 keys: 18 D bytes) by 16-byte asynchronous copies that run on into the CTA's next
-// piece; the keys' and values' places in a stage are such that neither kind of read meets a bank twice. Nothing waits for
-// what could fail to come.
+//     the values along the contraction is free, and Q's registers follow it;
+//   weights as in attn_scored.cuh;
+//   O^T (values x rows) += V^T P^T: a lane's share of a key is a run of D / 8 codes. Two keys' words become one of
+//     pairs by two shifts and two selects, and O's rows follow the order in which they come.
+// A pair of codes becomes an operand's word by one conversion and one product with its scale. The keys' and values' places in
+// a stage are such that neither kind of read meets a bank twice.
 #pragma once
 
 #include "attn_scored.cuh"
@@ -29,23 +27,24 @@
 namespace sv {
 namespace scored {
 
-template <int D_, int NT_, int CTAS_, int STAGES_>
+template <int D_, int NT_, int M_, int CTAS_, int STAGES_>
 struct Cfg4 {
   static constexpr int D = D_, NT = NT_, RB = NT_ * 8, kCtasPerSm = CTAS_, kStages = STAGES_;
-  static constexpr int kWarps = 4, kThreads = 128, TK = 64;
-  static constexpr int kAlpha = 4;                  // positions of a unit's lead-in
-  static constexpr int KT = D / 16, MT = D / 32;    // 16-value steps of a head; tiles of a warp's half
-  static constexpr int kCodes = 8 * D, kScales = D;  // bytes of a warp's keys (or values): codes, block scales
+  static constexpr int M = M_, kKeys = 16 * M;  // keys of a step
+  static constexpr int kWarps = 4, kThreads = 128, TK = kWarps * kKeys;
+  static constexpr int kAlpha = M == 1 ? 4 : 2;  // positions of a unit's lead-in
+  static constexpr int KT = D / 16;
+  static constexpr int kCodes = 8 * D * M, kScales = D * M;  // bytes of a step's keys (or values): codes, block scales
   static constexpr int kStage = 2 * (kCodes + kScales);
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kPitch = (NT | 1) * 16;      // bytes of a key's weights: an odd number of 16, for ldmatrix
-  static constexpr int kWeights = 2 * 2 * 32 * kPitch;  // two buffers of each pair
-  static constexpr int kPad = D + 4;                // floats of a row in the merge buffer
-  static constexpr int kMerge = 2 * 8 * kPad * 4;
-  static constexpr bool kQs = NT > 2;               // Q's operands in shared memory, for all warps; else in registers
-  static constexpr int kSmem = kRing + kWeights + kMerge + (kQs ? NT * KT * 256 : 0);
+  static constexpr int kTiles = KT < 8 ? KT : 8;     // 16-value tiles of O that are merged at a time
+  static constexpr int kPad = kTiles * 16 + 4;       // floats of a row in the merge buffer
+  static constexpr int kMerge = kWarps * 8 * kPad * 4;
+  static constexpr bool kQs = NT * KT > 16;  // Q in shared memory: registers are better spent on two chains of products
+  static constexpr int kSmem = kRing + kMerge + (kQs ? NT * KT * 256 : 0);
   static_assert(kCtasPerSm * (kSmem + 3072) <= 227 * 1024, "shared memory of an SM");
 };
+
 // A running maximum moves when a score passes it by this (log2): weights of 2^14 fit fp16, and less moves less often.
 constexpr float kMoveAt4 = 14.f;
 
@@ -56,11 +55,6 @@ __device__ __forceinline__ void copy_all(uint32_t dst, const uint8_t *src) {
 // 16 bytes into shared memory, zeros from byte n on
 __device__ __forceinline__ void copy_some(uint32_t dst, const uint8_t *src, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
 }
 // N bytes of shared memory as words
 template <int N> __device__ __forceinline__ void read_words(uint32_t at, uint32_t *w) {
@@ -90,7 +84,7 @@ template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(const Params P) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
-  constexpr int D = C::D, NT = C::NT, TK = C::TK, RB = C::RB, KT = C::KT, MT = C::MT, ST = C::kStages;
+  constexpr int D = C::D, NT = C::NT, TK = C::TK, RB = C::RB, KT = C::KT, ST = C::kStages, M = C::M, kKeys = C::kKeys;
   constexpr int kThreads = C::kThreads, kWarps = C::kWarps;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t s_mask[RB];         // new keys that a row sees
@@ -176,24 +170,25 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
   }
 
   // ---- the ring: this warp's stages, and its way ahead of what is being used ----
-  const int pair = warp >> 1, half = warp & 1;  // half: which 16 keys of the pair's, and which half of the values
   const uint32_t ring = smem_at(smem) + warp * ST * C::kStage;
   const int bs = kv.block_size, bs_shift = __ffs(bs) - 1;
   // What a lane copies of a stage: kPer times 16 bytes of the keys' codes and as many of the values'; then 16 bytes of scales.
-  // Key r stands in row r; value row p holds key vkey(p), so that the four keys of one read (p = 4 j + t) are
-  // 2 t + (j & 1) + 8 (j >> 1), as a B operand has them.
-  constexpr int kChunks = D / 32, kPer = D / 64;  // 16-byte chunks of a row; of a stage to a lane
-  auto vkey = [](int p) { return 2 * (p & 3) + ((p >> 2) & 1) + 8 * (p >> 3); };
+  // Key r of the step stands in row r; of each 16 value rows row p holds key vkey(p), so that the four keys of one read
+  // (p = 4 j + t) are 2 t + (j & 1) + 8 (j >> 1), as a B operand has them.
+  constexpr int kChunks = D / 32, kPer = M * D / 64;  // 16-byte chunks of a row; of a stage to a lane
+  auto vkey = [](int p) { return (p & 16) + 2 * (p & 3) + ((p >> 2) & 1) + 8 * ((p >> 3) & 1); };
   // (chunk c of row r stands in place c ^ these)
   auto k_turn = [](int r) { return D == 256 ? 4 * (r & 1) : 0; };
   auto v_turn = [](int p) { return D == 256 ? 2 * (p & 3) : D == 128 ? 2 * ((p >> 1) & 1) : 0; };
   // where the warp's copies are: the piece that they belong to, its tiles left, and the next one's first key
-  int ahead_left = 0, ahead_key = 0, ahead_b = 0, ahead_kvh = 0, ahead_ke = 0, ahead_lo = 0, id = -1;
-  auto load_ids = [&] {  // even lanes: of the block with the first 8 of the next tile's keys, odd ones the last; -1: none to be read
-    const int key = ahead_key + 8 * (lane & 1);
+  int ahead_left = 0, ahead_key = 0, id = -1;
+  uint32_t ahead_turn = 0;
+  auto load_ids = [&] {  // lane 2 M k + j: of the block with the j-th 8 of the next tile's keys; -1: none to be read
+    const Turn &y = s_turn[warp][ahead_turn];
+    const int key = ahead_key + 8 * (lane & (2 * M - 1));
     id = -1;
-    if (key < ahead_ke && key + 8 > ahead_lo) {
-      id = kv.block_table[(size_t)ahead_b * kv.max_blocks + (key >> bs_shift)];
+    if (key < y.p.ke && key + 8 > y.p.lo) {
+      id = kv.block_table[(size_t)y.b * kv.max_blocks + (key >> bs_shift)];
       if (id < 0 || id >= kv.num_blocks) {
         record(a.status, SV_ERR_BAD_BLOCK_ID);
         id = -1;
@@ -201,19 +196,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
     }
   };
   auto bring = [&](uint32_t stage) {
-    const int key0 = ahead_key, ke = ahead_ke, lo = ahead_lo;
-    auto row_of = [&](int i8) {  // the pool's row of the i8-th 8 keys, less their place in the step
-      const int x = __shfl_sync(0xffffffffu, id, i8);
-      return (((size_t)max(x, 0) * kv.num_kv_heads + ahead_kvh) << bs_shift) + ((key0 + 8 * i8) & (bs - 1)) - 8 * i8;
-    };
-    const bool all = __all_sync(0xffffffffu, id >= 0) && key0 >= lo && key0 + 16 <= ke;  // every key is there
+    const Turn &y8 = s_turn[warp][ahead_turn];
+    const int key0 = ahead_key, ke = y8.p.ke, lo = y8.p.lo;
+    // this lane's 8 keys: the pool's row (32 bits: the host sees to it) of the first, less its place in the step
+    const int mine8 = lane & (2 * M - 1);
+    const uint32_t mine = ((uint32_t)(max(id, 0) * kv.num_kv_heads + y8.p.kvh) << bs_shift) + ((key0 + 8 * mine8) & (bs - 1)) - 8 * mine8;
+    const bool all = __all_sync(0xffffffffu, id >= 0) && key0 >= lo && key0 + kKeys <= ke;  // every key is there
 #pragma unroll
     for (int y = 0; y < kPer; ++y) {
       const int q = lane + 32 * y, r = q / kChunks, c = q % kChunks, rv = vkey(r), i8 = r >> 3;
-      const size_t row = row_of(i8);
+      const uint32_t row = __shfl_sync(0xffffffffu, mine, i8);
       const uint32_t kd = stage + r * (D / 2) + ((c ^ k_turn(r)) << 4), vd = stage + C::kCodes + r * (D / 2) + ((c ^ v_turn(r)) << 4);
-      const uint8_t *ks = (const uint8_t *)kv.k_pool + (row + r) * (D / 2) + c * 16, *vs = (const uint8_t *)kv.v_pool + (row + rv) * (D / 2) + c * 16;
-      if (all) {
+      const uint8_t *ks = (const uint8_t *)kv.k_pool + (uint64_t)(row + r) * (D / 2) + c * 16, *vs = (const uint8_t *)kv.v_pool + (uint64_t)(row + rv) * (D / 2) + c * 16;
+      if (__builtin_expect(all, 1)) {
         copy_all(kd, ks);
         copy_all(vd, vs);
       } else {
@@ -223,45 +218,32 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
         copy_some(vd, vs, there && vk < ke && vk >= lo ? 16 : 0);
       }
     }
-    const int l = lane & 15, r = l * (256 / D), i8 = (r >> 3) & 1;  // scales: lanes 0 .. 15 the keys', the others the values'
-    const size_t row = row_of(i8);
-    const bool there = __shfl_sync(0xffffffffu, id, i8) >= 0;
-    // those of keys past the end are zeros: what they scale is of no one
-    if (l < D / 16)
-      copy_some(stage + 2 * C::kCodes + (lane >> 4) * C::kScales + l * 16, (lane < 16 ? kv.k_bs : kv.v_bs) + (row + r) * (D / 16),
-                all ? 16 : there ? max(0, min(16, (ke - key0 - r) * (D / 16))) : 0);
+#pragma unroll
+    for (int y = 0; y < (M * D / 16 + 15) / 16; ++y) {  // scales: lanes 0 .. 15 the keys', the others the values'
+      const int l = (lane & 15) + 16 * y, r = l * (256 / D), i8 = (r >> 3) & (2 * M - 1);
+      const uint32_t row = __shfl_sync(0xffffffffu, mine, i8);
+      const bool there = __shfl_sync(0xffffffffu, id, i8) >= 0;
+      // those of keys past the end are zeros: what they scale is of no one
+      if (l < M * D / 16)
+        copy_some(stage + 2 * C::kCodes + (lane >> 4) * C::kScales + l * 16, (lane < 16 ? kv.k_bs : kv.v_bs) + (uint64_t)(row + r) * (D / 16),
+                  all ? 16 : there ? max(0, min(16, (ke - key0 - r) * (D / 16))) : 0);
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   // ---- constants of the launch ----
-  const uint32_t weights = smem_at(smem) + C::kRing + pair * 2 * 32 * C::kPitch;
-  float *merge = reinterpret_cast<float *>(smem + C::kRing + C::kWeights);  // [pair][8][kPad]
-  const uint32_t q_at = smem_at(smem) + C::kRing + C::kWeights + C::kMerge + lane * 8;  // Q's operands, [n tile][16 values][lane]
+  float *merge = reinterpret_cast<float *>(smem + C::kRing);  // [warp][8][kPad]
+  const uint32_t q_at = smem_at(smem) + C::kRing + C::kMerge + lane * 8;  // Q's operands, [n tile][16 values][lane]
   const float cap = P.s.cap;
   const bool fast_cap = cap <= kFastCap * 1.4426950408889634f;
   const int window = P.s.window;
   const bool biased = P.s.slopes != nullptr;
-  auto of_pair = [&] {
-    if (pair == 0) asm volatile("bar.sync 1, 64;" ::: "memory");
-    else asm volatile("bar.sync 2, 64;" ::: "memory");
-  };
-  auto vote = [&](bool one) {  // ... and whether any thread of the pair has one
-    uint32_t any;
-    if (pair == 0)
-      asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-                   : "=r"(any) : "r"((uint32_t)one) : "memory");
-    else
-      asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-                   : "=r"(any) : "r"((uint32_t)one) : "memory");
-    return any != 0u;
-  };
   // what a product is multiplied with, less the row's own factor
   const float factor = (cap > 0.f && fast_cap ? P.cap_in : a.scale_log2) * kv.k_scale;
 
   bool first_piece = true;
-  int filled = 0;             // tiles on their way or there, of which the ring takes one less than it has stages: the other is still read
+  int filled = 0;             // tiles on their way or there
   uint32_t get = 0, put = 0;  // stages
-  uint32_t steps = 0;         // of the pair: the weights' buffers take turns
   auto next = [&](Turn &turn) {
     Place at = s_at[warp];
     Turn x = {};
@@ -278,16 +260,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
   };
   bool has = next(s_turn[warp][0]), ahead_is_next = true;  // the copies have gone on (or go first) to the next piece
   uint32_t turns = 0;
-  auto start_copies = [&](const Turn &y) {
+  auto start_copies = [&](const Turn &y, uint32_t turn) {
     ahead_left = y.p.kt1 - y.p.kt0;
-    ahead_key = y.p.kt0 * TK + warp * 16;
-    ahead_b = y.b;
-    ahead_kvh = y.p.kvh;
-    ahead_ke = y.p.ke;
-    ahead_lo = y.p.lo;
+    ahead_key = y.p.kt0 * TK + warp * kKeys;
+    ahead_turn = turn & 1u;
     load_ids();
   };
-  if (has) start_copies(s_turn[warp][0]);
+  if (has) start_copies(s_turn[warp][0], 0);
   while (has) {
     const Turn &now = s_turn[warp][turns & 1u], &then = s_turn[warp][(turns + 1) & 1u];
     ++turns;
@@ -295,12 +274,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
     const Seq &s = now.s;
     const int &b = now.b;
     has = next(s_turn[warp][turns & 1u]);
-    if (ahead_is_next && ahead_left == 0 && has) start_copies(then);  // the copies had come to the end of what was known
+    if (ahead_is_next && ahead_left == 0 && has) start_copies(then, turns);  // the copies had come to the end of what was known
     else ahead_is_next = false;
     const int n_tiles = p.kt1 - p.kt0;
     const int c = s.c, ke = p.ke, lo = p.lo, kvh = p.kvh, rb = p.rb;
     auto top_up = [&] {
-      while (filled < ST - 1 && ahead_left > 0) {
+      while (filled < ST && ahead_left > 0) {
         bring(ring + put * C::kStage);
         put = put + 1 == ST ? 0 : put + 1;
         ++filled;
@@ -309,7 +288,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
           load_ids();
         } else if (!ahead_is_next && has) {
           ahead_is_next = true;
-          start_copies(then);
+          start_copies(then, turns);
         }
       }
     };
@@ -392,115 +371,148 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
       in[nt][0] = x.x;
       in[nt][1] = x.y;
     }
-    float o[MT][NT][4], m[NT][2], l[NT][2];
+    float o[KT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = kNone;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
+      for (int mt = 0; mt < KT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
     }
 
     for (int tile = 0; tile < n_tiles; ++tile) {
-      if (filled == ST - 1) copies_wait<ST - 2>();
+      __syncwarp();  // every lane is done with the stage that is filled next
+      top_up();
+      if (filled == ST) copies_wait<ST - 1>();
       else copies_wait<0>();
       __syncwarp();
-      const int key0 = (p.kt0 + tile) * TK + pair * 32;  // the pair's first key
-      const uint32_t stage = ring + get * C::kStage, first_stage = stage - half * ST * C::kStage;
+      const int key0 = (p.kt0 + tile) * TK + warp * kKeys;
+      const uint32_t stage = ring + get * C::kStage;
       get = get + 1 == ST ? 0 : get + 1;
       --filled;
-      if (key0 >= ke || key0 + 32 <= lo) {  // the same for the pair: nothing to see here
-        of_pair();                          // both are done with the stage that is filled next
-        top_up();
-        continue;
-      }
+      if (__builtin_expect(key0 >= ke || key0 + kKeys <= lo, 0)) continue;  // warp-uniform: nothing to see here
       // ---- S^T = K Q^T ----
-      constexpr int kWords = D / 32;  // a lane's words of a key's codes
-      uint32_t kw[2][kWords], ks[2][(kWords + 1) / 2];
+      constexpr int kWords = D / 32;  // a lane's words of a key's codes; of a value's half as many
+      constexpr int kVw = kWords / 2, kVs = D == 256 ? 2 : 1;
+      uint32_t kw[M][2][kWords], ks[M][2][(kWords + 1) / 2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = g + 8 * h;
-        const uint32_t row = stage + r * (D / 2), sc = stage + 2 * C::kCodes + r * (D / 16);
-        if constexpr (D == 64) {
-          read_words<8>(row + t * 8, kw[h]);
-          ks[h][0] = read_byte(sc + t);
-        } else if constexpr (D == 128) {
-          read_words<16>(row + t * 16, kw[h]);
-          ks[h][0] = read_half(sc + 2 * t);
-        } else {
-          read_words<16>(row + ((t ^ k_turn(r)) << 4), kw[h]);
-          read_words<16>(row + (((t + 4) ^ k_turn(r)) << 4), kw[h] + 4);
-          ks[h][0] = read_half(sc + 2 * t);
-          ks[h][1] = read_half(sc + 8 + 2 * t);
+      for (int u = 0; u < M; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * u + g + 8 * h;
+          const uint32_t row = stage + r * (D / 2), sc = stage + 2 * C::kCodes + r * (D / 16);
+          if constexpr (D == 64) {
+            read_words<8>(row + t * 8, kw[u][h]);
+            ks[u][h][0] = read_byte(sc + t);
+          } else if constexpr (D == 128) {
+            read_words<16>(row + t * 16, kw[u][h]);
+            ks[u][h][0] = read_half(sc + 2 * t);
+          } else {
+            read_words<16>(row + ((t ^ k_turn(r)) << 4), kw[u][h]);
+            read_words<16>(row + (((t + 4) ^ k_turn(r)) << 4), kw[u][h] + 4);
+            ks[u][h][0] = read_half(sc + 2 * t);
+            ks[u][h][1] = read_half(sc + 8 + 2 * t);
+          }
         }
-      }
-      float sc[NT][4];
+      float sc[M][NT][4];
       {
-        constexpr int kSplit = NT == 1 ? 2 : 1;  // chains of products
-        float part[kSplit][NT][4];
+        constexpr int kSplit = NT * M == 1 ? 2 : 1;  // chains of products
+        float part[kSplit][M][NT][4];
 #pragma unroll
-        for (int y = 0; y < kSplit * NT * 4; ++y) (&part[0][0][0])[y] = 0.f;
-        uint32_t scale[2];
+        for (int y = 0; y < kSplit * M * NT * 4; ++y) (&part[0][0][0][0])[y] = 0.f;
+        uint32_t scale[M][2];
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
-          uint32_t f[2][4];
+          uint32_t f[M][2][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (w % 2 == 0) {  // two words of 8 codes to a scale
-              const uint32_t two = widen(ks[h][w >> 2]);
-              scale[h] = __byte_perm(two, 0u, D > 64 && (w & 2) ? 0x3232 : 0x1010);
+          for (int u = 0; u < M; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (w % 2 == 0) {  // two words of 8 codes to a scale
+                const uint32_t two = widen(ks[u][h][w >> 2]);
+                scale[u][h] = __byte_perm(two, 0u, D > 64 && (w & 2) ? 0x3232 : 0x1010);
+              }
+              widen8(kw[u][h][w], f[u][h][0], f[u][h][1], f[u][h][2], f[u][h][3]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) f[u][h][y] = mul2(f[u][h][y], scale[u][h]);
             }
-            widen8(kw[h][w], f[h][0], f[h][1], f[h][2], f[h][3]);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) f[h][y] = mul2(f[h][y], scale[h]);
-          }
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t e[4] = {f[0][2 * y], f[1][2 * y], f[0][2 * y + 1], f[1][2 * y + 1]};
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               uint32_t b[2];
               if constexpr (C::kQs) read_words<8>(q_at + (nt * KT + 2 * w + y) * 256, b);
               else b[0] = q[nt][2 * w + y][0], b[1] = q[nt][2 * w + y][1];
-              mma<true>(part[y % kSplit][nt], e, b[0], b[1]);
+#pragma unroll
+              for (int u = 0; u < M; ++u) {
+                const uint32_t e[4] = {f[u][0][2 * y], f[u][1][2 * y], f[u][0][2 * y + 1], f[u][1][2 * y + 1]};
+                mma<true>(part[y % kSplit][u][nt], e, b[0], b[1]);
+              }
             }
-          }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < M; ++u)
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            sc[nt][y] = (kSplit == 2 ? part[0][nt][y] + part[kSplit - 1][nt][y] : part[0][nt][y]) * in[nt][y & 1];
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              sc[u][nt][y] = (kSplit == 2 ? part[0][u][nt][y] + part[kSplit - 1][u][nt][y] : part[0][u][nt][y]) * in[nt][y & 1];
+      }
+      // the values' words and scales, on their way during the softmax: keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+      uint32_t vw[M][4][kVw], vs[M][2][kVs];  // vs: two keys' scales, a byte each
+#pragma unroll
+      for (int u = 0; u < M; ++u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int pr = 16 * u + 4 * j + t;
+          const uint32_t row = stage + C::kCodes + pr * (D / 2);
+          if constexpr (D == 64) read_words<4>(row + g * 4, vw[u][j]);
+          else if constexpr (D == 128) read_words<8>(row + (((g >> 1) ^ v_turn(pr)) << 4) + (g & 1) * 8, vw[u][j]);
+          else read_words<16>(row + ((g ^ v_turn(pr)) << 4), vw[u][j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t at = stage + 2 * C::kCodes + C::kScales + (16 * u + 2 * t + 8 * j) * (D / 16);
+          if constexpr (D == 256) {
+            const uint32_t x = read_half(at + 2 * g), y = read_half(at + 16 + 2 * g);
+            vs[u][j][0] = __byte_perm(x, y, 0x3340);
+            vs[u][j][1] = __byte_perm(x, y, 0x3351);
+          } else {
+            const int gr = D == 64 ? g >> 1 : g;
+            vs[u][j][0] = read_byte(at + gr) | read_byte(at + D / 16 + gr) << 8;
+          }
+        }
       }
       // ---- scores ---- (element e of an n tile: key half e >> 1, row 2 t + (e & 1))
-      const int mine = key0 + half * 16;  // this warp's first key
-      float *const sv = &sc[0][0];
+      float *const sv = &sc[0][0][0];
+      constexpr int kE = M * NT * 4;
       if (cap > 0.f) {
         if (fast_cap) {
 #pragma unroll
-          for (int y = 0; y < NT * 4; ++y) sv[y] = -2.f * cap * rcp(1.f + ex2(sv[y]));
+          for (int y = 0; y < kE; ++y) sv[y] = -2.f * cap * rcp(1.f + ex2(sv[y]));
         } else {
 #pragma unroll
-          for (int y = 0; y < NT * 4; ++y) sv[y] = cap * tanhf(sv[y] / cap);
+          for (int y = 0; y < kE; ++y) sv[y] = cap * tanhf(sv[y] / cap);
         }
       }
-      const bool edge = key0 + 32 > min(c, ke) || key0 < all_see;  // the same for the pair: some row may not see some key
-      if (biased) {
+      const bool edge = key0 + kKeys > min(c, ke) || key0 < all_see;  // warp-uniform: some row may not see some key
+      if (__builtin_expect(biased, 0)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = mine + g + 8 * h, j = key - c;
+        for (int h = 0; h < 2 * M; ++h) {
+          const int key = key0 + g + 8 * h, j = key - c;
           const float place = (float)(edge && j >= 0 && j < s.n ? s_place[j] : key - origin);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float2 sl = *reinterpret_cast<const float2 *>(&s_slope[nt * 8 + 2 * t]);
-            sc[nt][2 * h] = fmaf(sl.x, place, sc[nt][2 * h]);
-            sc[nt][2 * h + 1] = fmaf(sl.y, place, sc[nt][2 * h + 1]);
+            float *x = &sc[h >> 1][nt][2 * (h & 1)];
+            x[0] = fmaf(sl.x, place, x[0]);
+            x[1] = fmaf(sl.y, place, x[1]);
           }
         }
       }
-      if (edge) {
-        const int base = mine - c;  // place of the warp's first key
-        // A row's view of the keys as bits: committed keys beyond its reach, and its mask of new ones.
+      if (__builtin_expect(edge, 0)) {
+        const int base = key0 - c;  // place of the step's first key
+        // A row's view of the step's keys as bits: committed keys beyond its reach, and its mask of new ones.
         const uint32_t old = base >= 0 ? 0u : base <= -32 ? ~0u : (1u << -base) - 1u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -511,152 +523,93 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
             const uint32_t near = first <= 0 ? ~0u : first >= 32 ? 0u : ~0u << first;
             const uint32_t fresh = base >= 0 ? (base < 64 ? (uint32_t)(mask >> base) : 0u) : (base > -32 ? (uint32_t)mask << -base : 0u);
             const uint32_t seen = ((old & near) | fresh) >> g;
-            if (!(seen & 1u)) sc[nt][e] = -INFINITY;
-            if (!((seen >> 8) & 1u)) sc[nt][e + 2] = -INFINITY;
-          }
-      }
-      // ---- P^T into shared memory, for both warps ----
-      const uint32_t to = weights + (steps++ & 1u) * 32 * C::kPitch;
-      float sum[NT][2];
-      auto weigh = [&] {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float e0 = ex2(sc[nt][0] - m[nt][0]), e1 = ex2(sc[nt][1] - m[nt][1]);
-          const float e2 = ex2(sc[nt][2] - m[nt][0]), e3 = ex2(sc[nt][3] - m[nt][1]);
-          sum[nt][0] = e0 + e2;
-          sum[nt][1] = e1 + e3;
-          const uint32_t at = to + (half * 16 + g) * C::kPitch + nt * 16 + t * 4;
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack2<true>(e0, e1)) : "memory");
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 8 * C::kPitch), "r"(pack2<true>(e2, e3)) : "memory");
-        }
-      };
-      weigh();
-      // ---- the running maximum, the same for the pair ----
+            for (int h = 0; h < 2 * M; ++h)
+              if (!((seen >> (8 * h)) & 1u)) sc[h >> 1][nt][2 * (h & 1) + e] = -INFINITY;
+          }
+        // Values that are NaN must not meet a weight of zero: their scales become zero, and the rows that see their keys
+        // get them at the piece's end.
+#pragma unroll
+        for (int u = 0; u < M; ++u)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int w = 0; w < kVs; ++w) {
+              const uint32_t nan = nan_codes(vs[u][j][w]) & 0xffffu;
+              if (nan != 0u) {
+                vs[u][j][w] &= ~nan;
+                const int key = key0 + 16 * u + 2 * t + 8 * j;
+                if (((nan & 0xffu) && key >= lo && key < ke) || ((nan >> 8) && key + 1 >= lo && key + 1 < ke)) s_patch = 1;
+              }
+            }
+      }
+      // ---- the running maximum ----
       bool move = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < M; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) move |= sc[nt][e] > m[nt][e & 1] + kMoveAt4;
-      if (vote(move)) {  // (past the barrier the pair is done with the last step's stage, and its copies of this one are there)
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) move |= sc[u][nt][e] > m[nt][e & 1] + kMoveAt4;
+      if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(sc[nt][e], sc[nt][e + 2]);
+            float mx = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+#pragma unroll
+            for (int u = 1; u < M; ++u) mx = fmaxf(mx, fmaxf(sc[u][nt][e], sc[u][nt][e + 2]));
 #pragma unroll
             for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
-            if (g == 0) s_m[warp][nt * 8 + 2 * t + e] = mx;
-          }
-        of_pair();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int rl = nt * 8 + 2 * t + e;
-            const float mn = fmaxf(fmaxf(m[nt][e], s_m[warp][rl]), s_m[warp ^ 1][rl]), f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
+            const float mn = fmaxf(m[nt][e], mx);
+            const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
             m[nt][e] = mn;
             l[nt][e] *= f;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+            for (int mt = 0; mt < KT; ++mt) {
               o[mt][nt][e] *= f;
               o[mt][nt][e + 2] *= f;
             }
           }
-        weigh();
-        of_pair();
       }
+      // ---- P^T ----
+      uint32_t pb[M][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        l[nt][0] += sum[nt][0];
-        l[nt][1] += sum[nt][1];
-      }
-      top_up();
-      // ---- O^T += V^T P^T: tile mt has values (D / 16) g + 2 mt and the next one of the half, in rows g and g + 8 ----
+      for (int u = 0; u < M; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {  // the 16 keys of each warp of the pair
-        const uint32_t slab = first_stage + u * ST * C::kStage;
-        uint32_t pb[NT][2];
-        {
-          const uint32_t from = to + (u * 16 + (lane & 15)) * C::kPitch;
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int nt = 0; nt < NT; nt += 2) {
-            if (nt + 1 < NT) {
-              uint32_t x[4];
-              ldm4t(x, from + (nt + (lane >> 4)) * 16);
-              pb[nt][0] = x[0], pb[nt][1] = x[1], pb[nt + 1][0] = x[2], pb[nt + 1][1] = x[3];
-            } else {
-              asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(pb[nt][0]), "=r"(pb[nt][1]) : "r"(from + nt * 16) : "memory");
-            }
-          }
+          for (int e = 0; e < 4; ++e) sc[u][nt][e] = ex2(sc[u][nt][e] - m[nt][e & 1]);
+          l[nt][0] += sc[u][nt][0] + sc[u][nt][2];
+          l[nt][1] += sc[u][nt][1] + sc[u][nt][3];
+          pb[u][nt][0] = turn8x8(pack2<true>(sc[u][nt][0], sc[u][nt][1]));
+          pb[u][nt][1] = turn8x8(pack2<true>(sc[u][nt][2], sc[u][nt][3]));
         }
-        // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: words of codes, and two keys' scales, a byte each
-        constexpr int kVw = D == 256 ? 2 : 1;
-        uint32_t vw[4][kVw], vs[2];
+      // ---- O^T += V^T P^T: tile mt has values (D / 8) g + 2 mt and the next one, in rows g and g + 8 ----
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int pr = 4 * j + t;
-          const uint32_t row = slab + C::kCodes + pr * (D / 2);
-          if constexpr (D == 64) vw[j][0] = read_half(row + half * 16 + g * 2);
-          else if constexpr (D == 128) read_words<4>(row + (((half * 2 + (g >> 2)) ^ v_turn(pr)) << 4) + (g & 3) * 4, vw[j]);
-          else read_words<8>(row + (((half * 4 + (g >> 1)) ^ v_turn(pr)) << 4) + (g & 1) * 8, vw[j]);
-        }
+      for (int w = 0; w < kVw; ++w)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t at = slab + 2 * C::kCodes + C::kScales + (2 * t + 8 * j) * (D / 16) + half * (D / 32) + (D == 64 ? g >> 2 : D == 128 ? g >> 1 : g);
-          vs[j] = read_byte(at) | read_byte(at + D / 16) << 8;
-        }
-        if (edge) {
-          // Values that are NaN must not meet a weight of zero: their scales become zero, and the rows that see their keys
-          // get them at the piece's end.
+        for (int u = 0; u < M; ++u) {
+          uint32_t f[2][8];  // pairs of keys; of the even values, of the odd ones
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t nan = nan_codes(vs[j]) & 0xffffu;
-            if (nan != 0u) {
-              vs[j] &= ~nan;
-              const int key = key0 + 16 * u + 2 * t + 8 * j;
-              if (((nan & 0xffu) && key >= lo && key < ke) || ((nan >> 8) && key + 1 >= lo && key + 1 < ke)) s_patch = 1;
-            }
+            const uint32_t x = vw[u][2 * j][w], y = vw[u][2 * j + 1][w], scale = widen(vs[u][j][D == 256 ? w >> 1 : 0]);
+            constexpr uint32_t kLow = 0x0f0f0f0fu;
+            widen8((x & kLow) | ((y << 4) & ~kLow), f[j][0], f[j][2], f[j][4], f[j][6]);
+            widen8(((x >> 4) & kLow) | (y & ~kLow), f[j][1], f[j][3], f[j][5], f[j][7]);
+#pragma unroll
+            for (int y2 = 0; y2 < 8; ++y2) f[j][y2] = mul2(f[j][y2], scale);
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t e[4] = {f[0][2 * y], f[0][2 * y + 1], f[1][2 * y], f[1][2 * y + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<true>(o[4 * w + y][nt], e, pb[u][nt][0], pb[u][nt][1]);
           }
         }
-        constexpr uint32_t kLow = 0x0f0f0f0fu;
-        const uint32_t s0 = widen(vs[0]), s1 = widen(vs[1]);
-        if constexpr (D == 64) {
-          // two values' codes a byte, two bytes a key: both pairs of keys in one word
-          const uint32_t x = __byte_perm(vw[0][0], vw[2][0], 0x5410), y = __byte_perm(vw[1][0], vw[3][0], 0x5410);
-          uint32_t even[4], odd[4];  // values 0, 2 of the first two keys, of the last two
-          widen8((x & kLow) | ((y << 4) & ~kLow), even[0], even[1], even[2], even[3]);
-          widen8(((x >> 4) & kLow) | (y & ~kLow), odd[0], odd[1], odd[2], odd[3]);
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            const uint32_t e[4] = {mul2(even[mt], s0), mul2(odd[mt], s0), mul2(even[2 + mt], s1), mul2(odd[2 + mt], s1)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<true>(o[mt][nt], e, pb[nt][0], pb[nt][1]);
-          }
-        } else {
-#pragma unroll
-          for (int w = 0; w < kVw; ++w) {
-            uint32_t f[2][8];  // pairs of keys; of the even values, of the odd ones
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t x = vw[2 * j][w], y = vw[2 * j + 1][w];
-              widen8((x & kLow) | ((y << 4) & ~kLow), f[j][0], f[j][2], f[j][4], f[j][6]);
-              widen8(((x >> 4) & kLow) | (y & ~kLow), f[j][1], f[j][3], f[j][5], f[j][7]);
-#pragma unroll
-              for (int z = 0; z < 8; ++z) f[j][z] = mul2(f[j][z], j == 0 ? s0 : s1);
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t e[4] = {f[0][2 * y], f[0][2 * y + 1], f[1][2 * y], f[1][2 * y + 1]};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<true>(o[4 * w + y][nt], e, pb[nt][0], pb[nt][1]);
-            }
-          }
-        }
-      }
     }
 
-    // ---- the pairs' results, merged, 8 rows at a time ----
-    __syncthreads();  // (s_m has been the pairs' own)
+    // ---- the warps' results, merged, 8 rows at a time ----
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -670,62 +623,65 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
         }
       }
     const size_t slot = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * P.rows_cap;
-    constexpr int kItems = D / 8;  // 8 values of a row each
+    constexpr int MT = C::kTiles, kItems = 2 * MT;  // 8 values of a row each
     bool patch = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float *dst = merge + (pair * 8 + 2 * t + e) * C::kPad + half * (D / 2) + 2 * g;
+      for (int m0 = 0; m0 < KT; m0 += MT) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) *reinterpret_cast<float2 *>(dst + mt * 16) = make_float2(o[mt][nt][e], o[mt][nt][e + 2]);
-      }
-      __syncthreads();
-      if (nt == 0) {  // every warp's weight in a row, over the rows' total
-        patch = s_patch != 0;
-        for (int rl = tid; rl < rows; rl += kThreads) {
-          float mx = s_m[0][rl], tot = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          float *dst = merge + (warp * 8 + 2 * t + e) * C::kPad + 2 * g;
 #pragma unroll
-          for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][rl]);  // finite: kNone at the least
+          for (int mt = 0; mt < MT; ++mt)
+            *reinterpret_cast<float2 *>(dst + mt * 16) = make_float2(o[m0 + mt][nt][e], o[m0 + mt][nt][e + 2]);
+        }
+        __syncthreads();
+        if (nt == 0 && m0 == 0) {  // every warp's weight in a row, over the rows' total
+          patch = s_patch != 0;
+          for (int rl = tid; rl < rows; rl += kThreads) {
+            float mx = s_m[0][rl], tot = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) tot += s_l[w][rl] * ex2(s_m[w][rl] - mx);
-          const float inv = tot == 0.f ? 0.f : kv.v_scale / tot;
-          if (!p.whole) P.part_lse[slot + rl] = tot == 0.f ? -INFINITY : mx + log2f(tot);
+            for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][rl]);  // finite: kNone at the least
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) s_l[w][rl] = ex2(s_m[w][rl] - mx) * inv;
+            for (int w = 0; w < kWarps; ++w) tot += s_l[w][rl] * ex2(s_m[w][rl] - mx);
+            const float inv = tot == 0.f ? 0.f : kv.v_scale / tot;
+            if (!p.whole) P.part_lse[slot + rl] = tot == 0.f ? -INFINITY : mx + log2f(tot);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s_l[w][rl] = ex2(s_m[w][rl] - mx) * inv;
+          }
+          __syncthreads();
+        }
+        for (int x = tid; x < 8 * kItems; x += kThreads) {
+          const int r8 = x / kItems, u = x % kItems, vg = u / (MT / 4), mt0 = u % (MT / 4) * 4, rl = nt * 8 + r8;
+          if (rl >= rows) continue;
+          const int d = vg * (D / 8) + 2 * (m0 + mt0);
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float f = s_l[w][rl];
+            const float *src = merge + (w * 8 + r8) * C::kPad + mt0 * 16 + 2 * vg;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 y = *reinterpret_cast<const float2 *>(src + k * 16);
+              v[2 * k] = fmaf(f, y.x, v[2 * k]);
+              v[2 * k + 1] = fmaf(f, y.y, v[2 * k + 1]);
+            }
+          }
+          if (p.whole) {
+            const int i = s_row[rl], head = kvh * P.G + (rb * RB + rl) - i * P.G;
+            *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + ((size_t)(s.row0 + i) * a.num_q_heads + head) * D + d) =
+                make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(P.part_o + (slot + rl) * D + d);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
         }
         __syncthreads();
       }
-      for (int x = tid; x < 8 * kItems; x += kThreads) {
-        const int r8 = x / kItems, u = x % kItems, rl = nt * 8 + r8;
-        if (rl >= rows) continue;
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.f;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const float f = s_l[2 * w][rl];
-          const float *src = merge + (w * 8 + r8) * C::kPad;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // value pair 4 u + k of the row: of half, lane group and tile
-            const int y = 4 * u + k, z = y % (D / 4);
-            const float2 two = *reinterpret_cast<const float2 *>(src + y / (D / 4) * (D / 2) + z % MT * 16 + z / MT * 2);
-            v[2 * k] = fmaf(f, two.x, v[2 * k]);
-            v[2 * k + 1] = fmaf(f, two.y, v[2 * k + 1]);
-          }
-        }
-        if (p.whole) {
-          const int i = s_row[rl], head = kvh * P.G + (rb * RB + rl) - i * P.G;
-          *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + ((size_t)(s.row0 + i) * a.num_q_heads + head) * D + 8 * u) =
-              make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
-        } else {
-          float4 *dst = reinterpret_cast<float4 *>(P.part_o + (slot + rl) * D + 8 * u);
-          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-      }
-      __syncthreads();
-    }
     if (patch) {
       // The NaN that edge steps took out, for the rows that see their keys, whatever the weight: looked for in the pool again
       // and added to what has been written.
@@ -735,9 +691,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
         bool nan = false;
 #pragma unroll 1
         for (int key = max(p.kt0 * TK, lo); key < ke && !nan; ++key) {
-          const int key0 = key & ~31, place = key - c;
-          if (!(key0 + 32 > min(c, ke) || key0 < all_see)) {  // on to the next edge step
-            key = (min(c, ke) & ~31) - 1;
+          const int key0 = key & ~(kKeys - 1), place = key - c;
+          if (!(key0 + kKeys > min(c, ke) || key0 < all_see)) {  // on to the next edge step
+            key = (min(c, ke) & ~(kKeys - 1)) - 1;
             continue;
           }
           if (!(place < 0 ? place > s_reach[rl] : (s_mask[rl] >> place) & 1ull)) continue;
@@ -778,17 +734,23 @@ cudaError_t pick4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStre
   const int rows = sa.a.num_q_heads / sa.a.kv.num_kv_heads * sa.a.max_q;
   auto on = [&](auto cfg) { return run4<decltype(cfg)>(sa, workspace, bytes, st, go); };
   if constexpr (D == 64) {
-    if (rows <= 8) return on(Cfg4<D, 1, 5, 4>());
-    if (rows <= 16) return on(Cfg4<D, 2, 4, 4>());
-    return on(Cfg4<D, 4, 3, 4>());
+    if (rows <= 8) return on(Cfg4<D, 1, 2, 4, 4>());
+    if (rows <= 16) return on(Cfg4<D, 2, 2, 3, 5>());
+    return on(Cfg4<D, 4, 2, 2, 6>());
   } else if constexpr (D == 128) {
-    if (rows <= 8) return on(Cfg4<D, 1, 5, 3>());
-    if (rows <= 16) return on(Cfg4<D, 2, 4, 3>());
-    if (rows <= 24) return on(Cfg4<D, 3, 4, 3>());
-    return on(Cfg4<D, 5, 3, 3>());
+    if (rows <= 8) return on(Cfg4<D, 1, 2, 3, 3>());
+    if (rows <= 16) return on(Cfg4<D, 2, 2, 2, 4>());
+    if (!wide_fits(sa)) return on(Cfg4<D, 3, 2, 2, 4>());
+    // a cap past the two-instruction tanh stays here; the workspace suits both, and so do the positions
+    size_t most = 0;
+    run_wide(sa, nullptr, &most, st, false);
+    if (go && sa.cap <= kFastCap * 1.4426950408889634f) return run_wide(sa, workspace, bytes, st, go);
+    const cudaError_t e = on(Cfg4<D, 3, 2, 2, 4>());
+    *bytes = *bytes == 0 || most == 0 ? 0 : std::max(*bytes, most);
+    return e;
   } else {
-    if (rows <= 8) return on(Cfg4<D, 1, 2, 4>());
-    return on(Cfg4<D, 2, 2, 4>());
+    if (rows <= 8) return on(Cfg4<D, 1, 1, 2, 4>());
+    return on(Cfg4<D, 2, 1, 2, 4>());
   }
 }
 

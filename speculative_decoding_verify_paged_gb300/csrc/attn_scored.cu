@@ -30,7 +30,7 @@ cudaError_t pick4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStre
 }
 
 // bf16, E4M3 and E2M1 caches with heads of 64, 128 or 256 values in blocks of 8 tokens and more
-// (attn_scored.cuh, attn_e2m1.cuh); a TMA row coordinate is a 32-bit number, and so are a unit's rows.
+// (attn_scored.cuh, attn_e2m1.cuh); a row of a pool is a 32-bit number there, and so are a unit's rows.
 size_t attn_scored_mma_workspace(const ScoredArgs &sa) {
   const KV &kv = sa.a.kv;
   if (kv.elem_bytes == 4 || (kv.head_dim != 64 && kv.head_dim != 128 && kv.head_dim != 256)) return 0;

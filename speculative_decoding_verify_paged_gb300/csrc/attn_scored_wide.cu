@@ -1,5 +1,5 @@
 // Attention with modified scores for wide units (more than kWideRows query rows per KV head and sequence:
-// draft trees, long drafts, wide query groups) on the 5th-generation tensor cores: bf16 caches with
+// draft trees, long drafts, wide query groups) on the 5th-generation tensor cores: bf16 and E2M1 caches with
 // heads of 128 values. The mathematics, the work order, the partials and their merge are those of
 // attn_scored.cuh.
 //
@@ -45,10 +45,20 @@
 // Weights are bf16 for the product with V (2^-8 of themselves at most), and the cap's reciprocals and 2^x the approximate
 // ones (2^-19 of the cap), as in attn_scored.cuh.
 //
+// E2M1 caches (CODES): four converters stand in the producer's place, one a scheduler, two of K and two of V. Each reads 16 bytes
+// of codes and two scales a lane and run of 8 keys, a tile ahead, and writes the fp16 values (exact, e2m1.cuh) where the
+// TMA would have put them. Q becomes fp16 next to a power of two of its row, as in attn_e2m1.cuh, and joins the row's
+// factor; weights are fp16 (2^-11 of themselves, 2^-25 where that is more), so the running maximum stays for capped scores
+// too. Trees as above, not capped: 184 us, 715 TFLOP/s (595 on
+// warp-level instructions). With one block of rows converting bounds it: a tile takes 64 x 256 conversions whether 128 rows meet it or 256.
+// Registers: four warps more, so fewer for each; converters that spilled were the slowest part (trees with 56, 64, 72, 80,
+// 88, 104 registers a converter thread: 267, 221, 215, 190, 186, 178 us; 40 rows 204, 181, 151, 140, 137, 144).
+//
 // All waits are bounded, as in attn_scored.cuh.
 #include <algorithm>
 
 #include "attn_scored.cuh"
+#include "e2m1.cuh"
 
 namespace sv {
 namespace scored {
@@ -60,10 +70,22 @@ struct Wide {  // what the work order and the merge need
   static constexpr int kAlpha = 12;
 };
 constexpr int kSoft = 8;                   // softmax warps
-constexpr int kWideThreads = (kSoft + 4) * 32;  // the last warp does nothing: register shares go by four warps
+// Register shares go by four warps: the producer, two issuers and one that does nothing; with codes the two issuers, two
+// that do nothing, and four converters.
+template <bool CODES>
+constexpr int kOthers = CODES ? 8 : 4;
+template <bool CODES>
+constexpr int kWideThreads = (kSoft + kOthers<CODES>) * 32;
 // Registers of a thread as launched, of the softmax warps and of the others after the split
-constexpr int kWideRegs = 168, kSoftRegs = 216, kOtherRegs = 72;
-static_assert(8 * kSoftRegs + 4 * kOtherRegs == 12 * kWideRegs, "a split above the launch's share would wait forever");
+template <bool CODES>
+constexpr int kWideRegs = CODES ? 128 : 168;
+template <bool CODES>
+constexpr int kSoftRegs = CODES ? 160 : 216;
+template <bool CODES>
+constexpr int kOtherRegs = CODES ? 96 : 72;
+template <bool CODES>
+constexpr bool kSplitFits = kSoft * kSoftRegs<CODES> + kOthers<CODES> * kOtherRegs<CODES> == (kSoft + kOthers<CODES>) * kWideRegs<CODES>;
+static_assert(kSplitFits<false> && kSplitFits<true>, "a split above the launch's share would wait forever");
 constexpr int kTile = Wide::TK;            // keys of a tile
 constexpr int kBlock = 128;                // rows of a block
 constexpr int kHalf = kTile * 256;         // bytes of a tile's K or V
@@ -80,9 +102,14 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lbo, uint32_t 
   return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 | (uint64_t)((sbo >> 4) & 0x3FFF) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// kind::f16, fp32 accumulate, bf16 operands, M 128; N 64 (keys), and N 128 (values) with B's N dimension major
-constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 17) | (8u << 24);
-constexpr uint32_t kIdescV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (16u << 17) | (8u << 24);
+// kind::f16, fp32 accumulate, bf16 operands (fp16 ones of codes), M 128; N 64 (keys), and N 128 (values) with B's N
+// dimension major
+template <bool CODES>
+constexpr uint32_t kTypes = (1u << 4) | (CODES ? 0u : (1u << 7) | (1u << 10));
+template <bool CODES>
+constexpr uint32_t kIdescS = kTypes<CODES> | (8u << 17) | (8u << 24);
+template <bool CODES>
+constexpr uint32_t kIdescV = kTypes<CODES> | (1u << 16) | (16u << 17) | (8u << 24);
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int accumulate) {
   asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
@@ -155,12 +182,17 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
   return (row >> 3) * 2048 + (chunk >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-template <bool ONE>
-__global__ void __launch_bounds__(kWideThreads, 1)
+// The halves of a word that are fp16 infinities or NaN, as a mask
+__device__ __forceinline__ uint32_t nonfinite16(uint32_t x) {
+  return ((x & 0x7c00u) == 0x7c00u ? 0xffffu : 0u) | ((x & 0x7c000000u) == 0x7c000000u ? 0xffff0000u : 0u);
+}
+
+template <bool ONE, bool CODES>
+__global__ void __launch_bounds__(kWideThreads<CODES>, 1)
     attn_scored_wide_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params P) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
-  constexpr int kWarps = kWideThreads / 32, kWideStages = kStages<ONE>;
+  constexpr int kThreads = kWideThreads<CODES>, kWarps = kThreads / 32, kWideStages = kStages<ONE>;
   extern __shared__ uint8_t smem[];
   __shared__ __align__(8) uint64_t s_full[kWideStages], s_free[kWideStages];  // stages
   __shared__ __align__(8) uint64_t s_q[2], s_s[2][2], s_p[2][2], s_o[2][2];  // blocks: Q written; by buffer S there, P written, P V done
@@ -179,7 +211,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   uint8_t *qs = ring + kWideStages * kStage;  // Q of block a, of block b (one block of rows: of both)
   if (tid == 0) {
     for (int k = 0; k < kWideStages; ++k) {
-      bar_init(smem_at(&s_full[k]), 1);
+      bar_init(smem_at(&s_full[k]), CODES ? 4 : 1);
       bar_init(smem_at(&s_free[k]), 2);
     }
     for (int k = 0; k < 2; ++k) {
@@ -229,9 +261,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     return v;
   };
   int v0 = work_of(tid, true), W, incl = scan(v0, &W), run = 0;
-  if (B > kWideThreads) {
+  if (B > kThreads) {
     int more = 0, rest;
-    for (int b = tid + kWideThreads; b < B; b += kWideThreads) more += work_of(b, true);
+    for (int b = tid + kThreads; b < B; b += kThreads) more += work_of(b, true);
     run = W;
     scan(more, &rest);
     W += rest;
@@ -239,7 +271,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   Place at;
   at.pos = range_start(blockIdx.x, W, P.ctas);
   at.end = range_start(blockIdx.x + 1, W, P.ctas);
-  for (int b0 = 0; b0 < B; b0 += kWideThreads) {
+  for (int b0 = 0; b0 < B; b0 += kThreads) {
     const int b = b0 + tid;
     if (b0 > 0) {
       int tot;
@@ -279,8 +311,70 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   auto active = [&](int blk) { return blk == 0 || (ONE ? p.kt1 - p.kt0 > 1 : two_blocks()); };  // has a part in the piece
 
   if (warp >= kSoft) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kSoft) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<CODES>));
+    if (CODES && warp >= kSoft + 4) {
+      // ================= converters: two of K, two of V, half of a tile's keys each =================
+      const bool val = warp >= kSoft + 6;
+      const int half = (warp & 1) * 4;  // the first of its 4 runs of 8 keys
+      const int bs_shift = __ffs(kv.block_size) - 1, r8 = lane & 7, ch = lane >> 3;  // a lane's row of 8, its 32 values
+      const uint8_t *codes = (const uint8_t *)(val ? kv.v_pool : kv.k_pool), *scales = val ? kv.v_bs : kv.k_bs;
+      if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);  // failure-path test: a wait that nothing ends
+      uint4 x[4];
+      uint32_t sc[4];
+      while (!dead && next_piece<Wide>(P, at, p)) {
+        const int32_t *bt = kv.block_table + (size_t)at.b * kv.max_blocks;
+        // lane y's: the block of its y-th 8 keys of a tile (none: -2); later, when the number is there, the pool's row of their first
+        auto id_of = [&](int kt) {
+          const int key = kt * Wide::TK + 8 * (half + (lane & 3));
+          return kt < p.kt1 && key < p.ke && key + 8 > p.lo ? max(bt[key >> bs_shift], -1) : -2;
+        };
+        auto row_of = [&](int id, int kt) {
+          if (id == -2) return -1;
+          if (id < 0 || id >= kv.num_blocks) {
+            record(a.status, SV_ERR_BAD_BLOCK_ID);
+            return -1;
+          }
+          return ((id * kv.num_kv_heads + p.kvh) << bs_shift) + ((kt * Wide::TK + 8 * (half + (lane & 3))) & (kv.block_size - 1));
+        };
+        auto read = [&](int y, int first, int kt) {
+          const int row = __shfl_sync(0xffffffffu, first, y), key = kt * Wide::TK + 8 * (half + y) + r8;
+          x[y] = make_uint4(0, 0, 0, 0);
+          sc[y] = 0u;
+          if (row >= 0 && key >= p.lo && key < p.ke) {  // a place that is no key's is zeros
+            x[y] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)(row + r8) * 64 + ch * 16));
+            sc[y] = __ldg(reinterpret_cast<const uint16_t *>(scales + (size_t)(row + r8) * 8 + ch * 2));
+          }
+        };
+        int first = row_of(id_of(p.kt0), p.kt0);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) read(y, first, p.kt0);
+        int id = id_of(p.kt0 + 1);
+        for (int kt = p.kt0; kt < p.kt1; ++kt, ++tile0) {
+          const uint32_t st = tile0 % kWideStages;
+          first = row_of(id, kt + 1);
+          id = id_of(kt + 2);
+          if (tile0 >= kWideStages) wait(s_free[st], (tile0 / kWideStages - 1) & 1u);
+          if (dead) break;
+          uint8_t *dst = ring + st * kStage + (val ? kHalf : 0) + half * 2048 + r8 * 128 + (ch >> 1) * 1024;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t w[4] = {x[y].x, x[y].y, x[y].z, x[y].w}, two = widen(sc[y]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // (a word's 8 values have one scale; a write's 8 lanes are 8 rows: no bank twice)
+              uint4 f;
+              widen8(w[j], f.x, f.y, f.z, f.w);
+              const uint32_t scale = __byte_perm(two, 0u, j < 2 ? 0x1010 : 0x3232);
+              f = make_uint4(mul2(f.x, scale), mul2(f.y, scale), mul2(f.z, scale), mul2(f.w, scale));
+              *reinterpret_cast<uint4 *>(dst + y * 2048 + ((((ch & 1) * 4 + j) ^ r8) << 4)) = f;
+            }
+            read(y, first, kt + 1);  // (past the piece's last tile nothing is)
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_at(&s_full[st]));
+        }
+      }
+    } else if (!CODES && warp == kSoft) {
       // ================= producer =================
       const int bs_shift = __ffs(kv.block_size) - 1, box = P.box, box_row = (lane >> 1) * box;
       if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);  // failure-path test: a wait that nothing ends
@@ -319,7 +413,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         if (dead) break;
       }
-    } else if (warp <= kSoft + 2) {
+    } else if (warp == kSoft + 1 || warp == kSoft + 2) {
       // ================= issuers =================
       const int blk = warp - kSoft - 1;
       const uint32_t at_s = tmem + blk * 128, at_o = tmem + kColO + blk * 128, at_q = smem_at(qs) + (ONE ? 0 : blk * kQBytes);
@@ -331,7 +425,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 32;
-            mma_ss(at_s + buf * 64, operand(at_q + off, 16, 2048), operand(k + off, 16, 2048), kIdescS, kk > 0);
+            mma_ss(at_s + buf * 64, operand(at_q + off, 16, 2048), operand(k + off, 16, 2048), kIdescS<CODES>, kk > 0);
           }
           commit(smem_at(&s_s[blk][buf]));
         }
@@ -345,7 +439,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (elected()) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ts(at_o, at_s + buf * 64 + kk * 8, operand(v + kk * 4096, 1024, 2048), kIdescV, 1);
+            mma_ts(at_o, at_s + buf * 64 + kk * 8, operand(v + kk * 4096, 1024, 2048), kIdescV<CODES>, 1);
           commit(smem_at(&s_o[blk][buf]));
           commit(smem_at(&s_free[x % kWideStages]));
         }
@@ -392,15 +486,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_at(&s_done), 0, kDrainBudgetNs))) dead = true;
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs<CODES>));
     // ================= softmax: one row per thread =================
     const int blk = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the block
     const uint32_t lane_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t to = lane_at + kColO + blk * 128;
-    const float sl2 = a.scale_log2, cap = P.s.cap, cap_in = P.cap_in;
+    // what scores are multiplied with (codes: times the keys' pool scale, and of each row's power of two, piece by piece)
+    const float sl2_all = CODES ? a.scale_log2 * kv.k_scale : a.scale_log2, cap_in_all = CODES ? P.cap_in * kv.k_scale : P.cap_in;
+    const float cap = P.s.cap;
     const bool biased = P.s.slopes != nullptr;
-    const bool bounded = cap > 0.f && cap <= kBoundedCap && !biased;
-    const bool plain = cap == 0.f && !biased && sl2 >= 0.f;
+    const bool bounded = !CODES && cap > 0.f && cap <= kBoundedCap && !biased;  // (fp16 weights reach less far)
+    const bool plain = cap == 0.f && !biased && sl2_all >= 0.f;
     const int window = P.s.window;
     auto together = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };  // both blocks
     auto of_tile = [&](bool two) {                                            // the threads at a tile
@@ -437,6 +533,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     // A piece's Q into shared memory: this row, or half of it where both blocks have it
     constexpr int kParts = ONE ? 8 : 16;
     uint4 part[kParts];
+    float down = 1.f;  // codes: the power of two that a row's Q has been divided by
     auto get_q = [&](const Place &pl, const Piece &pc) {
       const int r = pc.rb * Wide::RB + (ONE ? 0 : blk * kBlock) + row, i = r / P.G;
       const bool live = r < P.G * pl.s.n;
@@ -445,6 +542,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           (live ? ((size_t)(pl.s.row0 + i) * a.num_q_heads + pc.kvh * P.G + (r - i * P.G)) * 128 : 0));
 #pragma unroll
       for (int c = 0; c < kParts; ++c) part[c] = live ? src[(ONE ? 8 * blk : 0) + c] : make_uint4(0, 0, 0, 0);
+      if constexpr (CODES) {  // fp16 next to a power of two that brings the row's largest value to 2^14 .. 2^15
+        uint32_t most = 0u;  // the largest magnitude's bits, in each half
+        auto look = [&](const uint4 &x) {
+          most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        };
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) look(part[c]);
+        if constexpr (ONE)
+          for (int c = 0; c < 8; ++c) look(live ? src[8 * (blk ^ 1) + c] : make_uint4(0, 0, 0, 0));
+        const int e = max(most & 0xffffu, most >> 16) >> 7, field = e == 255 ? 127 : min(268 - e, 253);  // (infinities and NaN stay what they are)
+        const float up = __int_as_float(field << 23);
+        down = __int_as_float((254 - field) << 23);
+        auto half2_of = [&](uint32_t x) { return pack2<true>(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up); };
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) part[c] = make_uint4(half2_of(part[c].x), half2_of(part[c].y), half2_of(part[c].z), half2_of(part[c].w));
+      }
     };
     auto put_q = [&] {
       uint8_t *dst = qs + (ONE ? 0 : blk * kQBytes);
@@ -463,6 +576,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     while (has) {
       const Seq s = at.s;
       const Piece pc = p;
+      const float sl2 = CODES ? finite(sl2_all * down) : sl2_all, cap_in = CODES ? finite(cap_in_all * down) : cap_in_all;
       const bool two = two_blocks(), mine = ONE || blk == 0 || two;  // a and b have rows; this block has
       has = next_piece<Wide>(P, at, p);                          // at and p: the next piece from here on
       const int c = s.c, ke = pc.ke, rl = (ONE ? 0 : blk * kBlock) + row, r = pc.rb * Wide::RB + rl;
@@ -518,7 +632,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           fence_after();
         };
         auto raise = [&](float mx) {  // the running maximum, if this one passes it by far
-          const bool move = mx > m + kMoveAt<false>;
+          const bool move = mx > m + kMoveAt<CODES>;
           if (!__any_sync(0xffffffffu, move)) return;
           const float f = move ? ex2(m - mx) : 1.f;
           if (move) m = mx;
@@ -546,6 +660,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int key = y >> 4;
             uint4 *w = reinterpret_cast<uint4 *>(vs + chunk_at(key, y & 15));
             if (key0 + key >= ke || key0 + key < pc.lo) *w = make_uint4(0, 0, 0, 0);
+            else if (CODES) odd |= (nonfinite16(w->x) | nonfinite16(w->y) | nonfinite16(w->z) | nonfinite16(w->w)) != 0u;
             else odd |= (nonfinite(w->x) | nonfinite(w->y) | nonfinite(w->z) | nonfinite(w->w)) != 0u;
           }
           fence_async();
@@ -573,8 +688,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                   x[y] = ex2(x[y]);
                   part[y] += x[y];
                 }
-                w[k / 2] = pack2<false>(x[0], x[1]);
-                w[k / 2 + 1] = pack2<false>(x[2], x[3]);
+                w[k / 2] = pack2<CODES>(x[0], x[1]);
+                w[k / 2 + 1] = pack2<CODES>(x[2], x[3]);
               }
             }
             l += (part[0] + part[1]) + (part[2] + part[3]);
@@ -591,7 +706,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               const float x = ex2(fmaf(__uint_as_float(w[k]), sl2, -m)), y = ex2(fmaf(__uint_as_float(w[k + 1]), sl2, -m));
               part[k & 2] += x;
               part[(k & 2) + 1] += y;
-              w[k / 2] = pack2<false>(x, y);
+              w[k / 2] = pack2<CODES>(x, y);
             }
             l += (part[0] + part[1]) + (part[2] + part[3]);
           } else {
@@ -680,7 +795,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                     for (int z = 0; z < 8; ++z) {
                       const uint32_t v = (word[z >> 1] >> (16 * (z & 1))) & 0xffffu;
-                      if ((v & 0x7f80u) == 0x7f80u) o[y * 8 + z] = __float_as_uint(__uint_as_float(o[y * 8 + z]) + __uint_as_float(v << 16));
+                      if (CODES ? (v & 0x7c00u) == 0x7c00u : (v & 0x7f80u) == 0x7f80u)  // (codes: a NaN, in bf16's bits one too)
+                        o[y * 8 + z] = __float_as_uint(__uint_as_float(o[y * 8 + z]) + __uint_as_float(v << 16));
                     }
                   }
                 }
@@ -689,7 +805,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               tmem_put_wait();
             }
 #pragma unroll
-            for (int k = 0; k < kTile / 2; ++k) w[k] = pack2<false>(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+            for (int k = 0; k < kTile / 2; ++k) w[k] = pack2<CODES>(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
           }
           tmem_put(ts, w);
           tmem_put_wait();
@@ -700,8 +816,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             uint32_t *w = reinterpret_cast<uint32_t *>(vs + chunk_at(y >> 4, y & 15));
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-              if ((w[z] & 0x7f80u) == 0x7f80u) w[z] &= 0xffff0000u;
-              if ((w[z] & 0x7f800000u) == 0x7f800000u) w[z] &= 0xffffu;
+              w[z] &= ~(CODES ? nonfinite16(w[z]) : nonfinite(w[z]));
             }
           }
           fence_async();
@@ -742,7 +857,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         fence_after();
       }
       if (warp_live) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l == 0.f ? 0.f : (CODES ? kv.v_scale : 1.f) / l;
         const size_t slot = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * P.rows_cap + rl;
         if (live && !pc.whole && (!ONE || blk == 0)) P.part_lse[slot] = l == 0.f ? -INFINITY : m + log2f(l);
         auto write = [&](int k, const uint32_t (&o)[32], float f) {  // values 32 k and on, times f
@@ -792,30 +907,30 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __syncthreads();
   fence_after();
   // after a wait that gave up: the copies in flight land before the CTA's shared memory is released
-  if (s_dead && warp == kSoft)
+  if (!CODES && s_dead && warp == kSoft)
     for (uint32_t x = tile0 > kWideStages ? tile0 - kWideStages : 0; x < tile0; ++x)
       mbar_wait_bounded(smem_at(&s_full[x % kWideStages]), (x / kWideStages) & 1u, kDrainBudgetNs);
   if (warp == kSoft + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
-template <bool ONE>
+template <bool ONE, bool CODES>
 cudaError_t launch_wide(const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, cudaStream_t st) {
-  auto kernel = attn_scored_wide_kernel<ONE>;
+  auto kernel = attn_scored_wide_kernel<ONE, CODES>;
   static const bool split_fits = [&] {  // the kernel was compiled for the registers that its split shares out
     cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == kWideRegs;
+    return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == kWideRegs<CODES>;
   }();
   if (!split_fits) return cudaErrorInvalidConfiguration;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem<ONE>);
-  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(p.ctas), dim3(kWideThreads), (size_t)kWideSmem<ONE>, st, mk, mv, p);
+  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(p.ctas), dim3(kWideThreads<CODES>), (size_t)kWideSmem<ONE>, st, mk, mv, p);
 }
 
 }  // namespace
 
 bool wide_fits(const ScoredArgs &sa) {
   const KV &kv = sa.a.kv;
-  return !kv.fp8 && kv.elem_bytes == 2 && kv.head_dim == 128 &&
-         sa.a.num_q_heads / kv.num_kv_heads * sa.a.max_q > kWideRows;
+  return (kv.fp4 || (!kv.fp8 && kv.elem_bytes == 2)) && kv.head_dim == 128 &&
+         sa.a.num_q_heads / kv.num_kv_heads * sa.a.max_q > (kv.fp4 ? kWideRows4 : kWideRows);
 }
 
 cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {
@@ -823,11 +938,12 @@ cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaS
   Params p;
   const Layout l = plan<Wide>(sa, workspace, bytes, &p);
   if (!go || *bytes == 0) return cudaSuccess;
-  CUtensorMap mk, mv;
-  if (!make_map<Wide>(&mk, kv.k_pool, kv, p.box) || !make_map<Wide>(&mv, kv.v_pool, kv, p.box)) return cudaErrorInvalidValue;
+  CUtensorMap mk = {}, mv = {};  // (codes are read without)
+  if (!kv.fp4 && (!make_map<Wide>(&mk, kv.k_pool, kv, p.box) || !make_map<Wide>(&mv, kv.v_pool, kv, p.box))) return cudaErrorInvalidValue;
   // One block of rows for all: 32 x 25 rows a head group of 4 over 2K to 4K tokens 170 -> 131 us with both blocks at work
   const bool one = sa.a.num_q_heads / kv.num_kv_heads * sa.a.max_q <= kBlock;
-  const cudaError_t e = one ? launch_wide<true>(mk, mv, p, st) : launch_wide<false>(mk, mv, p, st);
+  const cudaError_t e = kv.fp4 ? (one ? launch_wide<true, true>(mk, mv, p, st) : launch_wide<false, true>(mk, mv, p, st))
+                               : (one ? launch_wide<true, false>(mk, mv, p, st) : launch_wide<false, false>(mk, mv, p, st));
   if (e != cudaSuccess) return e;
   return launch_combine<Wide>(p, l, st);
 }

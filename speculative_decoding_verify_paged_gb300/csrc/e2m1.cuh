@@ -51,6 +51,11 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t &p0, uint32_t &p1, u
       : "=r"(p0), "=r"(p1), "=r"(p2), "=r"(p3)
       : "r"(w));
 }
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
 __device__ __forceinline__ float2 pair_of(uint32_t halves) { return __half22float2(*reinterpret_cast<const __half2 *>(&halves)); }
 
 }  // namespace sv
