@@ -45,14 +45,16 @@
 // Weights are bf16 for the product with V (2^-8 of themselves at most), and the cap's reciprocals and 2^x the approximate
 // ones (2^-19 of the cap), as in attn_scored.cuh.
 //
-// E2M1 caches (CODES): four converters stand in the producer's place, one a scheduler, two of K and two of V. Each reads 16 bytes
-// of codes and two scales a lane and run of 8 keys, a tile ahead, and writes the fp16 values (exact, e2m1.cuh) where the
-// TMA would have put them. Q becomes fp16 next to a power of two of its row, as in attn_e2m1.cuh, and joins the row's
-// factor; weights are fp16 (2^-11 of themselves, 2^-25 where that is more), so the running maximum stays for capped scores
-// too. Trees as above, not capped: 184 us, 715 TFLOP/s (595 on
-// warp-level instructions). With one block of rows converting bounds it: a tile takes 64 x 256 conversions whether 128 rows meet it or 256.
-// Registers: four warps more, so fewer for each; converters that spilled were the slowest part (trees with 56, 64, 72, 80,
-// 88, 104 registers a converter thread: 267, 221, 215, 190, 186, 178 us; 40 rows 204, 181, 151, 140, 137, 144).
+// E2M1 caches (CODES): four converters stand in the producer's place, one a scheduler, two of K and two of V. Each has a ring of
+// its own, three tiles of asynchronous 16-byte copies that run on into the CTA's next piece, and writes the fp16 values (exact,
+// e2m1.cuh) where the TMA would have put them. Q becomes fp16 next to a power of two of its row, as in attn_e2m1.cuh,
+// and joins the row's factor; weights are fp16 (2^-11 of themselves, 2^-25 where that is more), so the running maximum stays for
+// capped scores too. Trees as above, not capped: 174 us, 755 TFLOP/s (595 on warp-level instructions; 184 with the codes
+// a tile ahead in registers). 32 sequences over 2K to 4K tokens: 256 rows a KV head 164, 128 rows 139, 64 rows 123.
+// A tile takes 3000 cycles whether 128 rows meet it or 256: a converter is busy for 1700 of them (800 for the copies' addresses,
+// 850 for its 64 conversions a lane), and a tile's way from there to the end of P V is long.
+// Registers: four warps more, so fewer for each. The others' 80 is where nothing they use in a loop spills (64: 172 us in
+// place of 123 for 64 rows, 188 in place of 174 for the trees); their places in the order are in shared memory for that.
 //
 // All waits are bounded, as in attn_scored.cuh.
 #include <algorithm>
@@ -80,9 +82,9 @@ constexpr int kWideThreads = (kSoft + kOthers<CODES>) * 32;
 template <bool CODES>
 constexpr int kWideRegs = CODES ? 128 : 168;
 template <bool CODES>
-constexpr int kSoftRegs = CODES ? 160 : 216;
+constexpr int kSoftRegs = CODES ? 176 : 216;
 template <bool CODES>
-constexpr int kOtherRegs = CODES ? 96 : 72;
+constexpr int kOtherRegs = CODES ? 80 : 72;
 template <bool CODES>
 constexpr bool kSplitFits = kSoft * kSoftRegs<CODES> + kOthers<CODES> * kOtherRegs<CODES> == (kSoft + kOthers<CODES>) * kWideRegs<CODES>;
 static_assert(kSplitFits<false> && kSplitFits<true>, "a split above the launch's share would wait forever");
@@ -92,10 +94,12 @@ constexpr int kHalf = kTile * 256;         // bytes of a tile's K or V
 constexpr int kStage = 2 * kHalf;
 constexpr int kQBytes = kBlock * 256;      // of a block
 // One block of rows: its Q once, and two stages more (the blocks hold two tiles each)
-template <bool ONE>
-constexpr int kStages = ONE ? 6 : 4;
-template <bool ONE>
-constexpr int kWideSmem = 1024 + kStages<ONE> * kStage + (ONE ? 1 : 2) * kQBytes;
+template <bool ONE, bool CODES>
+constexpr int kStages = !ONE ? 4 : CODES ? 5 : 6;
+constexpr int kRaw = 32 * 72, kAhead = 3;  // codes: bytes of a converter's 32 keys; so many tiles are on their way or there
+template <bool ONE, bool CODES>
+constexpr int kWideSmem = 1024 + kStages<ONE, CODES> * kStage + (ONE ? 1 : 2) * kQBytes + (CODES ? 4 * kAhead * kRaw : 0);
+static_assert(kWideSmem<true, true> + 2048 <= 227 * 1024 && kWideSmem<false, true> + 2048 <= 227 * 1024, "shared memory of an SM");
 constexpr int kColO = 256;                 // S_a 0 (and 64), S_b 128 (and 192), O_a 256, O_b 384
 
 __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lbo, uint32_t sbo) {  // 128-byte swizzle
@@ -192,12 +196,13 @@ __global__ void __launch_bounds__(kWideThreads<CODES>, 1)
     attn_scored_wide_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params P) {
   grid_dependency_wait();  // the earlier kernel on the stream is complete and visible
   grid_dependents_launch();
-  constexpr int kThreads = kWideThreads<CODES>, kWarps = kThreads / 32, kWideStages = kStages<ONE>;
+  constexpr int kThreads = kWideThreads<CODES>, kWarps = kThreads / 32, kWideStages = kStages<ONE, CODES>;
   extern __shared__ uint8_t smem[];
   __shared__ __align__(8) uint64_t s_full[kWideStages], s_free[kWideStages];  // stages
   __shared__ __align__(8) uint64_t s_q[2], s_s[2][2], s_p[2][2], s_o[2][2];  // blocks: Q written; by buffer S there, P written, P V done
   __shared__ __align__(8) uint64_t s_seen;                // one block of rows: the second issuer is past a piece without work
   __shared__ __align__(8) uint64_t s_done;                // every product issued has finished
+  __shared__ Place s_at[CODES ? kOthers<CODES> : 1];  // of the warps with few registers: where they are in the order
   __shared__ int s_dead, s_scan[kWarps], s_first_b, s_first_base;
   __shared__ uint32_t s_tmem;
   __shared__ int s_place[64], s_top[kSoft];
@@ -312,68 +317,92 @@ __global__ void __launch_bounds__(kWideThreads<CODES>, 1)
 
   if (warp >= kSoft) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<CODES>));
+    if (CODES && lane == 0) s_at[warp - kSoft] = at;
+    __syncwarp();
+    auto advance = [&] {
+      if constexpr (!CODES) return next_piece<Wide>(P, at, p);
+      at = s_at[warp - kSoft];
+      __syncwarp();
+      const bool has = next_piece<Wide>(P, at, p);
+      if (lane == 0) s_at[warp - kSoft] = at;
+      __syncwarp();
+      return has;
+    };
     if (CODES && warp >= kSoft + 4) {
       // ================= converters: two of K, two of V, half of a tile's keys each =================
+      const int half = (warp & 1) * 4, bs_shift = __ffs(kv.block_size) - 1;  // the first of its 4 runs of 8 keys
       const bool val = warp >= kSoft + 6;
-      const int half = (warp & 1) * 4;  // the first of its 4 runs of 8 keys
-      const int bs_shift = __ffs(kv.block_size) - 1, r8 = lane & 7, ch = lane >> 3;  // a lane's row of 8, its 32 values
       const uint8_t *codes = (const uint8_t *)(val ? kv.v_pool : kv.k_pool), *scales = val ? kv.v_bs : kv.k_bs;
+      const uint32_t raw = smem_at(qs) + (ONE ? 1 : 2) * kQBytes + (warp & 3) * kAhead * kRaw;
       if (a.stall == SV_STALL_ATTENTION) wait(s_free[0], 0);  // failure-path test: a wait that nothing ends
-      uint4 x[4];
-      uint32_t sc[4];
-      while (!dead && next_piece<Wide>(P, at, p)) {
-        const int32_t *bt = kv.block_table + (size_t)at.b * kv.max_blocks;
-        // lane y's: the block of its y-th 8 keys of a tile (none: -2); later, when the number is there, the pool's row of their first
-        auto id_of = [&](int kt) {
-          const int key = kt * Wide::TK + 8 * (half + (lane & 3));
-          return kt < p.kt1 && key < p.ke && key + 8 > p.lo ? max(bt[key >> bs_shift], -1) : -2;
-        };
-        auto row_of = [&](int id, int kt) {
-          if (id == -2) return -1;
-          if (id < 0 || id >= kv.num_blocks) {
-            record(a.status, SV_ERR_BAD_BLOCK_ID);
-            return -1;
-          }
-          return ((id * kv.num_kv_heads + p.kvh) << bs_shift) + ((kt * Wide::TK + 8 * (half + (lane & 3))) & (kv.block_size - 1));
-        };
-        auto read = [&](int y, int first, int kt) {
-          const int row = __shfl_sync(0xffffffffu, first, y), key = kt * Wide::TK + 8 * (half + y) + r8;
-          x[y] = make_uint4(0, 0, 0, 0);
-          sc[y] = 0u;
-          if (row >= 0 && key >= p.lo && key < p.ke) {  // a place that is no key's is zeros
-            x[y] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)(row + r8) * 64 + ch * 16));
-            sc[y] = __ldg(reinterpret_cast<const uint16_t *>(scales + (size_t)(row + r8) * 8 + ch * 2));
-          }
-        };
-        int first = row_of(id_of(p.kt0), p.kt0);
+      int kt = 0, id = 0, ahead = 0;  // next tile to be asked for; lane y & 3: the block of its y-th run; tiles asked for and not yet written
+      uint32_t put = 0, get = 0;
+      bool more = advance();
+      auto look = [&] {  // which blocks the next tile's keys lie in; the numbers arrive while the last tile is converted
+        const int key = kt * Wide::TK + 8 * (half + (lane & 3));
+        if (key < p.ke && key + 8 > p.lo) id = kv.block_table[(size_t)at.b * kv.max_blocks + (key >> bs_shift)];
+      };
+      auto bring = [&] {
+        const int k0 = kt * Wide::TK + 8 * half;
+        const int first = k0 + 8 * (lane & 3);
+        const bool want = first < p.ke && first + 8 > p.lo, bad = want && (id < 0 || id >= kv.num_blocks);
+        if (bad) record(a.status, SV_ERR_BAD_BLOCK_ID);
+        const int mine = !want || bad ? -1 : ((id * kv.num_kv_heads + p.kvh) << bs_shift) + (first & (kv.block_size - 1));
+        const uint32_t dst = raw + put * kRaw;
+        put = put + 1 == kAhead ? 0 : put + 1;
+        const int r8 = lane >> 2, c = lane & 3;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) read(y, first, p.kt0);
-        int id = id_of(p.kt0 + 1);
-        for (int kt = p.kt0; kt < p.kt1; ++kt, ++tile0) {
-          const uint32_t st = tile0 % kWideStages;
-          first = row_of(id, kt + 1);
-          id = id_of(kt + 2);
-          if (tile0 >= kWideStages) wait(s_free[st], (tile0 / kWideStages - 1) & 1u);
-          if (dead) break;
-          uint8_t *dst = ring + st * kStage + (val ? kHalf : 0) + half * 2048 + r8 * 128 + (ch >> 1) * 1024;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t w[4] = {x[y].x, x[y].y, x[y].z, x[y].w}, two = widen(sc[y]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {  // (a word's 8 values have one scale; a write's 8 lanes are 8 rows: no bank twice)
-              uint4 f;
-              widen8(w[j], f.x, f.y, f.z, f.w);
-              const uint32_t scale = __byte_perm(two, 0u, j < 2 ? 0x1010 : 0x3232);
-              f = make_uint4(mul2(f.x, scale), mul2(f.y, scale), mul2(f.z, scale), mul2(f.w, scale));
-              *reinterpret_cast<uint4 *>(dst + y * 2048 + ((((ch & 1) * 4 + j) ^ r8) << 4)) = f;
-            }
-            read(y, first, kt + 1);  // (past the piece's last tile nothing is)
-          }
-          fence_async();
-          __syncwarp();
-          if (lane == 0) bar_arrive(smem_at(&s_full[st]));
+        for (int y = 0; y < 4; ++y) {
+          const int row = __shfl_sync(0xffffffffu, mine, y), key = k0 + 8 * y + r8;
+          copy_some(dst + (8 * y + r8) * 64 + ((c ^ ((r8 >> 1) & 3)) << 4), codes + (size_t)(max(row, 0) + r8) * 64 + c * 16,
+                    row >= 0 && key >= p.lo && key < p.ke ? 16 : 0);  // a place that is no key's is zeros
         }
+        const int row = __shfl_sync(0xffffffffu, mine, (lane >> 2) & 3), key = k0 + 2 * lane;  // scales: 16 bytes are two keys'
+        if (lane < 16) copy_some(dst + 32 * 64 + lane * 16, scales + (size_t)(max(row, 0) + 2 * c) * 8, row >= 0 ? max(0, min(16, (p.ke - key) * 8)) : 0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++ahead;
+        if (++kt == p.kt1) {
+          more = advance();
+          kt = p.kt0;
+        }
+        if (more) look();
+      };
+      kt = p.kt0;
+      if (more) look();
+      const int r8 = lane & 7, ch = lane >> 3;  // a lane's row of 8, its 32 values
+      while (true) {
+        while (more && ahead < kAhead) bring();
+        if (ahead == 0) break;
+        if (ahead == kAhead) copies_wait<kAhead - 1>();
+        else copies_wait<0>();
+        __syncwarp();
+        const uint32_t st = tile0 % kWideStages;
+        if (tile0 >= kWideStages) wait(s_free[st], (tile0 / kWideStages - 1) & 1u);
+        if (dead) break;
+        const uint32_t src = raw + get * kRaw;
+        uint8_t *dst = ring + st * kStage + (val ? kHalf : 0) + half * 2048 + r8 * 128 + (ch >> 1) * 1024;
+        get = get + 1 == kAhead ? 0 : get + 1;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t w[4];
+          read_words<16>(src + (8 * y + r8) * 64 + ((ch ^ ((r8 >> 1) & 3)) << 4), w);
+          const uint32_t two = widen(read_half(src + 32 * 64 + (8 * y + r8) * 8 + ch * 2));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // (a word's 8 values have one scale; a write's 8 lanes are 8 rows: no bank twice)
+            uint4 f;
+            widen8(w[j], f.x, f.y, f.z, f.w);
+            const uint32_t scale = __byte_perm(two, 0u, j < 2 ? 0x1010 : 0x3232);
+            f = make_uint4(mul2(f.x, scale), mul2(f.y, scale), mul2(f.z, scale), mul2(f.w, scale));
+            *reinterpret_cast<uint4 *>(dst + y * 2048 + ((((ch & 1) * 4 + j) ^ r8) << 4)) = f;
+          }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_at(&s_full[st]));
+        ++tile0;
+        --ahead;
       }
+      copies_wait<0>();
     } else if (!CODES && warp == kSoft) {
       // ================= producer =================
       const int bs_shift = __ffs(kv.block_size) - 1, box = P.box, box_row = (lane >> 1) * box;
@@ -446,7 +475,7 @@ __global__ void __launch_bounds__(kWideThreads<CODES>, 1)
         __syncwarp();
       };
       auto landed = [&](uint32_t x) { wait(s_full[x % kWideStages], (x / kWideStages) & 1u); };
-      while (!dead && next_piece<Wide>(P, at, p)) {
+      while (!dead && advance()) {
         const int n = p.kt1 - p.kt0;
         auto pass = [&](int t) {  // the other block's tile
           landed(tile0 + t);
@@ -921,8 +950,8 @@ cudaError_t launch_wide(const CUtensorMap &mk, const CUtensorMap &mv, const Para
     return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == kWideRegs<CODES>;
   }();
   if (!split_fits) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem<ONE>);
-  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(p.ctas), dim3(kWideThreads<CODES>), (size_t)kWideSmem<ONE>, st, mk, mv, p);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem<ONE, CODES>);
+  return e != cudaSuccess ? e : launch_pdl(kernel, dim3(p.ctas), dim3(kWideThreads<CODES>), (size_t)kWideSmem<ONE, CODES>, st, mk, mv, p);
 }
 
 }  // namespace

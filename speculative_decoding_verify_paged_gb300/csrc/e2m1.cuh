@@ -58,4 +58,30 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ float2 pair_of(uint32_t halves) { return __half22float2(*reinterpret_cast<const __half2 *>(&halves)); }
 
+
+template <int LEFT> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+__device__ __forceinline__ void copy_all(uint32_t dst, const uint8_t *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes into shared memory, zeros from byte n on
+__device__ __forceinline__ void copy_some(uint32_t dst, const uint8_t *src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// N bytes of shared memory as words
+template <int N> __device__ __forceinline__ void read_words(uint32_t at, uint32_t *w) {
+  if constexpr (N == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+  else if constexpr (N == 8) asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+  else asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+}
+__device__ __forceinline__ uint32_t read_byte(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at));
+  return x;
+}
+__device__ __forceinline__ uint32_t read_half(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(at));
+  return x;
+}
+
 }  // namespace sv

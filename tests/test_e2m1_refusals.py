@@ -171,3 +171,19 @@ def test_plain_error_is_bounded():
     v = E.values(*E.quantise(x, 0.75), 0.75)
     top = np.abs(x).reshape(200, -1, 16).max(-1).repeat(16, -1)
     assert np.all(np.abs(v - x) <= top * (1 / 6) * (17 / 16))
+
+
+@pytest.mark.parametrize("d,n,hq,block,tile,lead", [
+    (256, 1, 64, 8, 64, 4), (256, 64, 64, 16, 64, 4), (128, 1, 64, 8, 128, 2), (128, 2, 64, 16, 128, 2), (128, 5, 64, 24, 128, 2),
+    (128, 64, 64, 24, 128, 2), (64, 1, 64, 8, 128, 2), (64, 64, 64, 32, 128, 2)])
+def test_positions_stay_within_32_bits(lib, d, n, hq, block, tile, lead):
+    """A unit (`block` rows of a KV head) has a position for each tile of keys and `lead` more; a call whose positions pass 32
+    bits goes to the CUDA-core kernels, which need no workspace for this many sequences. (Many rows: the kernel for caps past
+    the fast form has the most.)"""
+    def workspace(length):
+        kv = L.sv_paged_kv(num_blocks=1 << 16, block_size=64, max_blocks_per_seq=1 << 17, num_kv_heads=8, head_dim=d, batch=4096, dtype=L.SV_DTYPE_E2M1)
+        return lib.sv_spec_verify_attn_scored_workspace_bytes(ctypes.byref(kv), hq, 1, n, length)
+    units = 4096 * 8 * -(-8 * n // block)
+    most = (2 ** 31 - 1) // units - lead
+    assert most * tile < 1 << 30
+    assert workspace(most * tile) > 0 and workspace(most * tile + 1) == 0 and workspace(1 << 30) == 0
