@@ -698,7 +698,7 @@ sv_status sv_adaptive_k_current(const void *state, int32_t *k);
  *   SV_OPT_STALL_FOR_TEST (SV_STALL_NONE, the default; SV_STALL_ATTENTION;
  *     SV_STALL_SAMPLER): for tests of the failure path only. The producer warp
  *     of the tensor-core attention kernels (sv_spec_verify_attn_scored's
- *     too), or of the sampler's statistics kernel, first waits on a barrier that nothing ever completes, as a
+ *     too; over E2M1 pools the converters), or of the sampler's statistics kernel, first waits on a barrier that nothing ever completes, as a
  *     producer whose data never arrives would; that wait runs out after the
  *     wait budget, the producer issues nothing, and every pipeline wait of its
  *     consumers runs out in turn. The call then records SV_ERR_TIMEOUT and its

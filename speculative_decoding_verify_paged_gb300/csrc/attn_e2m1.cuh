@@ -19,6 +19,18 @@
 //     pairs by two shifts and two selects, and O's rows follow the order in which they come.
 // A pair of codes becomes an operand's word by one conversion and one product with its scale. The keys' and values' places in
 // a stage are such that neither kind of read meets a bank twice.
+//
+// Bound: the issue of instructions, at the rate that few warps of long chains reach. 16 keys of 128 values are 64 conversions and as
+// many products with scales whatever the rows, 48 matrix instructions and some 72 of softmax for 24 rows, 75 for copies and
+// their addresses: about 500 with a piece's share of its set-up and merge, and an issue slot takes one 35 to 41% of
+// the time (two warps a scheduler at 240 registers; fixed latencies first, then instruction fetch). Times, 8 KV heads of 128:
+//   32 sequences of 0.5K to 4K tokens, 24 rows a KV head: 50 us (1.7 TB/s of the cache; 885 on CUDA cores);
+//   4 sequences of 32K tokens, 8 rows: 56 us (2.7 TB/s); 128 of 16 to 8192 tokens, 12 to 36 rows, capped: 160 us.
+// Two steps' worth of keys (M = 2) give the chains something to hide behind: 24 rows 50 us, 61 with 16 keys and three CTAs an
+// SM; 8 rows 56 and 56. Two warps to a step, half of the values each, take 72 us for 24 rows, 75 for 8 and 108 for 40 (123 here,
+// two blocks of 24): the second warp costs scores, copies and weights what it saves in products.
+//
+// More than 48 rows over heads of 128 values go to attn_scored_wide.cu.
 #pragma once
 
 #include "attn_scored.cuh"
@@ -45,7 +57,7 @@ struct Cfg4 {
   static_assert(kCtasPerSm * (kSmem + 3072) <= 227 * 1024, "shared memory of an SM");
 };
 
-// A running maximum moves when a score passes it by this (log2): weights of 2^14 fit fp16, and less moves less often.
+// A running maximum moves when a score passes it by this (log2): weights of 2^14 fit fp16, and a higher bound is passed less often.
 constexpr float kMoveAt4 = 14.f;
 
 // A piece and its sequence. Each warp keeps its place and its turns in shared memory: registers are short, and a piece is long.
@@ -156,27 +168,25 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
   auto k_turn = [](int r) { return D == 256 ? 4 * (r & 1) : 0; };
   auto v_turn = [](int p) { return D == 256 ? 2 * (p & 3) : D == 128 ? 2 * ((p >> 1) & 1) : 0; };
   // where the warp's copies are: the piece that they belong to, its tiles left, and the next one's first key
-  int ahead_left = 0, ahead_key = 0, id = -1;
+  int ahead_left = 0, ahead_key = 0, id = 0;
   uint32_t ahead_turn = 0;
-  auto load_ids = [&] {  // lane 2 M k + j: of the block with the j-th 8 of the next tile's keys; -1: none to be read
+  // Lane 2 M k + j: the block with the j-th 8 of the next tile's keys, if there are some to be read. (Asked for a tile before
+  // the number is looked at: its way here would stand in every step.)
+  auto load_ids = [&] {
     const Turn &y = s_turn[warp][ahead_turn];
     const int key = ahead_key + 8 * (lane & (2 * M - 1));
-    id = -1;
-    if (key < y.p.ke && key + 8 > y.p.lo) {
-      id = kv.block_table[(size_t)y.b * kv.max_blocks + (key >> bs_shift)];
-      if (id < 0 || id >= kv.num_blocks) {
-        record(a.status, SV_ERR_BAD_BLOCK_ID);
-        id = -1;
-      }
-    }
+    if (key < y.p.ke && key + 8 > y.p.lo) id = kv.block_table[(size_t)y.b * kv.max_blocks + (key >> bs_shift)];
   };
   auto bring = [&](uint32_t stage) {
     const Turn &y8 = s_turn[warp][ahead_turn];
     const int key0 = ahead_key, ke = y8.p.ke, lo = y8.p.lo;
-    // this lane's 8 keys: the pool's row (32 bits: the host sees to it) of the first, less its place in the step
-    const int mine8 = lane & (2 * M - 1);
-    const uint32_t mine = ((uint32_t)(max(id, 0) * kv.num_kv_heads + y8.p.kvh) << bs_shift) + ((key0 + 8 * mine8) & (bs - 1)) - 8 * mine8;
-    const bool all = __all_sync(0xffffffffu, id >= 0) && key0 >= lo && key0 + kKeys <= ke;  // every key is there
+    const int mine8 = lane & (2 * M - 1), key8 = key0 + 8 * mine8;  // this lane's 8 keys
+    const bool want = key8 < ke && key8 + 8 > lo, known = (uint32_t)id < (uint32_t)kv.num_blocks;
+    if (want && !known) record(a.status, SV_ERR_BAD_BLOCK_ID);
+    // the pool's row (32 bits: the host sees to it) of the first, less its place in the step
+    const uint32_t mine = ((uint32_t)((known ? id : 0) * kv.num_kv_heads + y8.p.kvh) << bs_shift) + (key8 & (bs - 1)) - 8 * mine8;
+    const uint32_t have = __ballot_sync(0xffffffffu, want && known);
+    const bool all = have == 0xffffffffu && key0 >= lo && key0 + kKeys <= ke;  // every key is there
 #pragma unroll
     for (int y = 0; y < kPer; ++y) {
       const int q = lane + 32 * y, r = q / kChunks, c = q % kChunks, rv = vkey(r), i8 = r >> 3;
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
         copy_all(kd, ks);
         copy_all(vd, vs);
       } else {
-        const bool there = __shfl_sync(0xffffffffu, id, i8) >= 0;
+        const bool there = (have >> i8) & 1u;
         const int kk = key0 + r, vk = key0 + rv;
         copy_some(kd, ks, there && kk < ke && kk >= lo ? 16 : 0);
         copy_some(vd, vs, there && vk < ke && vk >= lo ? 16 : 0);
@@ -197,7 +207,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
     for (int y = 0; y < (M * D / 16 + 15) / 16; ++y) {  // scales: lanes 0 .. 15 the keys', the others the values'
       const int l = (lane & 15) + 16 * y, r = l * (256 / D), i8 = (r >> 3) & (2 * M - 1);
       const uint32_t row = __shfl_sync(0xffffffffu, mine, i8);
-      const bool there = __shfl_sync(0xffffffffu, id, i8) >= 0;
+      const bool there = (have >> i8) & 1u;
       // those of keys past the end are zeros: what they scale is of no one
       if (l < M * D / 16)
         copy_some(stage + 2 * C::kCodes + (lane >> 4) * C::kScales + l * 16, (lane < 16 ? kv.k_bs : kv.v_bs) + (uint64_t)(row + r) * (D / 16),
@@ -706,6 +716,8 @@ cudaError_t run4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStrea
 // The smallest block of query rows that holds a unit's, else blocks of the largest.
 template <int D>
 cudaError_t pick4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {
+  // CTAs an SM and stages: what registers and shared memory leave. 8 rows, 4 long sequences, 32 keys a step: three CTAs with
+  // three stages 55.7 us, four with two 59.2; 16 keys: four with five stages 55.7, three with six 86.
   const int rows = sa.a.num_q_heads / sa.a.kv.num_kv_heads * sa.a.max_q;
   auto on = [&](auto cfg) { return run4<decltype(cfg)>(sa, workspace, bytes, st, go); };
   if constexpr (D == 64) {

@@ -28,7 +28,7 @@
 //
 // bf16, 32 + 8 heads of 128 values: 16384 rows 60.1 us (5.6 TB/s of rows), 4 rows 3.5 us; 640 rows of 64 + 8
 // heads 6.2 us. With the append: 256 x 64 rows 76.8 us (5.2 TB/s), 32 x 6 rows 6.2 us, 1.5K rows into an E4M3
-// pool 15.1 us.
+// pool 15.1 us. With three axes 16384 rows take 60.3 us, 4 rows 4.4 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>

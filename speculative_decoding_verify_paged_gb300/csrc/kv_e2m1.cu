@@ -5,6 +5,9 @@
 // 9/16 out, gather the other way round), so memory bounds long calls and the chain launch -> owner of the row -> length ->
 // block id -> rows short ones. A CTA takes a few consecutive rows: its first warp finds where they stand, then a thread
 // takes 16 values of a row (a group of codes; 16 or 32 bytes of wider types) at a time.
+//
+// 8 heads of 128 values: 256 x 64 rows into the pool 38 us (4.4 TB/s of what it cannot do without), 32 x 6 rows 8.8 us, two
+// launches; 74K rows of 32 sequences out of it 62 us (6.2 TB/s), 4 short sequences' 4.8 us.
 #include <algorithm>
 
 #include "e2m1.cuh"

@@ -3,6 +3,9 @@
 Tolerance: 2^-7 of a query head's row, as over E4M3 pools (test_gpu_scored.py): codes and block scales are operands of
 the products exactly, queries are fp16 with a power of two of their own (2^-39 of the row's largest value at most), each
 weight is rounded to fp16 (2^-11 of itself, 2^-25 where that is more) and the output to bf16 (2^-8)."""
+import os
+import subprocess
+import sys
 import time
 from types import SimpleNamespace
 
@@ -304,6 +307,60 @@ def test_calls_repeat_and_replay(d, hq, n):
                                       stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
+@pytest.mark.parametrize("cap", [150.0, 1000.0, 3.4028234e38])
+def test_large_caps(d, hq, n, cap):
+    """Either side of what the two-instruction tanh takes, and a cap whose product with log2(e) is past fp32's range."""
+    check(*make(73, [200, 33], [n, 2], hq, 2, d, 16, ScoreMod(softcap=cap)))
+
+
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
+@pytest.mark.parametrize("far", [1000, 2000000000])
+def test_a_bias_between_positions_far_past_the_cache(d, hq, n, far):
+    ctx = [200, 37]
+    pos = np.concatenate([c + far + np.arange(n) // 2 for c in ctx])
+    check(*make(74, ctx, [n, n], hq, 2, d, 16, ScoreMod(slopes=T.slopes(hq)), positions=torch.from_numpy(pos.astype(np.int32)).cuda()))
+
+
+FIRST_CALLS_IN_A_CAPTURE = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+from speculative_decoding_verify_paged_gb300 import ScoreMod, _lib as L, step as S, workloads as W
+import _e2m1 as E
+case = W.custom(75, batch=2, ctx_lens=[40, 90], n_q=[{n}, {n}], num_q_heads=8, num_kv_heads=2, head_dim={d}, block_size=16, vocab=16, dtype="bf16", use_bank=False)
+kv, d = E.device_kv(case.state), S.DeviceStep.from_host(case.step, "cuda")
+d.mod = ScoreMod(softcap=20.0, window=30)
+buf = S.StepBuffers.make(kv, d, 90 + {n})
+k, v = torch.empty_like(d.new_k), torch.empty_like(d.new_v)
+table, free, top = kv.block_table.clone(), kv.free_list.clone(), kv.free_top.clone()
+torch.cuda.synchronize()
+def run():
+    S.append(kv, d, buf)
+    S.attention(kv, d, buf, 90 + {n})
+    L.kv_gather(kv, k, v, d.cu_q, buf.status)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+assert int(buf.status.item()) == 0
+first = [x.clone() for x in (buf.attn_out, k, v)]
+kv.block_table.copy_(table), kv.free_list.copy_(free), kv.free_top.copy_(top)
+run()
+torch.cuda.synchronize()
+assert int(buf.status.item()) == 0 and all(torch.equal(x, y) and bool((x != 0).any()) for x, y in zip(first, (buf.attn_out, k, v)))
+"""
+
+
+@pytest.mark.parametrize("d,n", [(64, 3), (128, 3), (128, 20), (128, 40), (96, 3)])
+def test_the_first_calls_of_a_process_may_be_captured(d, n):
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALLS_IN_A_CAPTURE.format(root=os.path.dirname(here), tests=here, d=d, n=n)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("hq,n", [(8, 20), (8, 40)])
