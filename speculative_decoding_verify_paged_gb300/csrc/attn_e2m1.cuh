@@ -22,12 +22,13 @@
 //
 // Bound: the issue of instructions, at the rate that few warps of long chains reach. 16 keys of 128 values are 64 conversions and as
 // many products with scales whatever the rows, 48 matrix instructions and some 72 of softmax for 24 rows, 75 for copies and
-// their addresses: about 500 with a piece's share of its set-up and merge, and an issue slot takes one 35 to 41% of
-// the time (two warps a scheduler at 240 registers; fixed latencies first, then instruction fetch). Times, 8 KV heads of 128:
-//   32 sequences of 0.5K to 4K tokens, 24 rows a KV head: 50 us (1.7 TB/s of the cache; 885 on CUDA cores);
-//   4 sequences of 32K tokens, 8 rows: 56 us (2.7 TB/s); 128 of 16 to 8192 tokens, 12 to 36 rows, capped: 160 us.
+// their addresses: about 500 with a piece's share of its set-up and merge, and an issue slot takes one 39% of
+// the time (two warps a scheduler at 240 registers; fixed latencies first, then instruction fetch; 56% for 8 rows, three warps). Times, 8 KV heads of 128:
+//   32 sequences of 0.5K to 4K tokens, 24 rows a KV head: 47 us (1.8 TB/s of the cache; 885 on CUDA cores);
+//   4 sequences of 32K tokens, 8 rows: 53 us (2.8 TB/s); 128 of 16 to 8192 tokens, 12 to 36 rows, capped: 158 us.
+// (Looking at a block's number as soon as it is asked for costs 5%: 50, 56 and 160.)
 // Two steps' worth of keys (M = 2) give the chains something to hide behind: 24 rows 50 us, 61 with 16 keys and three CTAs an
-// SM; 8 rows 56 and 56. Two warps to a step, half of the values each, take 72 us for 24 rows, 75 for 8 and 108 for 40 (123 here,
+// SM (both before that); 8 rows 56 and 56. Two warps to a step, half of the values each, take 72 us for 24 rows, 75 for 8 and 108 for 40 (123 here,
 // two blocks of 24): the second warp costs scores, copies and weights what it saves in products.
 //
 // More than 48 rows over heads of 128 values go to attn_scored_wide.cu.
@@ -58,6 +59,7 @@ struct Cfg4 {
 };
 
 // A running maximum moves when a score passes it by this (log2): weights of 2^14 fit fp16, and a higher bound is passed less often.
+// (The difference is exact where it counts. The sum of the two may not be: next to 2^28 it would let 16 pass, and fp16 end.)
 constexpr float kMoveAt4 = 14.f;
 
 // A piece and its sequence. Each warp keeps its place and its turns in shared memory: registers are short, and a piece is long.
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) move |= sc[u][nt][e] > m[nt][e & 1] + kMoveAt4;
+          for (int e = 0; e < 4; ++e) move |= sc[u][nt][e] - m[nt][e & 1] > kMoveAt4;
       if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

@@ -49,7 +49,7 @@
 // its own, three tiles of asynchronous 16-byte copies that run on into the CTA's next piece, and writes the fp16 values (exact,
 // e2m1.cuh) where the TMA would have put them. Q becomes fp16 next to a power of two of its row, as in attn_e2m1.cuh,
 // and joins the row's factor; weights are fp16 (2^-11 of themselves, 2^-25 where that is more), so the running maximum stays for
-// capped scores too. Trees as above, not capped: 174 us, 755 TFLOP/s (595 on warp-level instructions; 184 with the codes
+// capped scores too. Trees as above, not capped: 169 us, 780 TFLOP/s (595 on warp-level instructions; 184 with the codes
 // a tile ahead in registers). 32 sequences over 2K to 4K tokens: 256 rows a KV head 164, 128 rows 139, 64 rows 123.
 // A tile takes 3000 cycles whether 128 rows meet it or 256: a converter is busy for 1700 of them (800 for the copies' addresses,
 // 850 for its 64 conversions a lane), and a tile's way from there to the end of P V is long.
@@ -661,7 +661,8 @@ __global__ void __launch_bounds__(kWideThreads<CODES>, 1)
           fence_after();
         };
         auto raise = [&](float mx) {  // the running maximum, if this one passes it by far
-          const bool move = mx > m + kMoveAt<CODES>;
+          // (fp16 weights end soon: what passes is the exact difference, not one to a rounded sum)
+          const bool move = CODES ? mx - m > kMoveAt<CODES> : mx > m + kMoveAt<CODES>;
           if (!__any_sync(0xffffffffu, move)) return;
           const float f = move ? ex2(m - mx) : 1.f;
           if (move) m = mx;
@@ -730,9 +731,16 @@ __global__ void __launch_bounds__(kWideThreads<CODES>, 1)
 #pragma unroll
             for (int k = 0; k < kTile; ++k) mx = fmaxf(mx, __uint_as_float(w[k]));
             raise(mx * sl2);
+            float mul = sl2;
+            if (CODES && __any_sync(0xffffffffu, !(fabsf(mx * sl2) < 0x1p22f))) {
+              // the maximum is a rounded product, and fp16 has no room for what an exact one may have more
+              mul = 1.f;
+#pragma unroll
+              for (int k = 0; k < kTile; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * sl2);
+            }
 #pragma unroll
             for (int k = 0; k < kTile; k += 2) {
-              const float x = ex2(fmaf(__uint_as_float(w[k]), sl2, -m)), y = ex2(fmaf(__uint_as_float(w[k + 1]), sl2, -m));
+              const float x = ex2(fmaf(__uint_as_float(w[k]), mul, -m)), y = ex2(fmaf(__uint_as_float(w[k + 1]), mul, -m));
               part[k & 2] += x;
               part[(k & 2) + 1] += y;
               w[k / 2] = pack2<CODES>(x, y);

@@ -164,6 +164,37 @@ def test_queries_of_any_size(d, hq, n):
     check(kv, step, buf, msl)
 
 
+def gaps(kv, step):
+    """The least distance between a row's two largest scores, over the sum of the sizes of the largest's products."""
+    keys, _ = E.pools(kv)
+    table, lens, cu, q = kv.block_table.cpu().numpy(), kv.seq_lens.tolist(), step.cu_q.tolist(), T.f64(step.q)
+    least = np.inf
+    for b, c in enumerate(lens):
+        for i in range(cu[b + 1] - cu[b]):
+            t = np.arange(c + i + 1)
+            k = keys[table[b, t // 16], :, t % 16]
+            for h in range(q.shape[1]):
+                kh = k[:, h // (q.shape[1] // k.shape[1])]
+                s = kh @ q[cu[b] + i, h]
+                first, second = np.argsort(s)[-1:-3:-1]
+                size = max(np.abs(kh[x] * q[cu[b] + i, h]).sum() for x in (first, second))
+                least = min(least, (s[first] - s[second]) / (2 * size))
+    return least
+
+
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3)])
+def test_scores_of_any_size(d, hq, n):
+    """Scores of up to 2^34 in base 2, where fp32's steps are past 16: the weights stay within fp16, and a row's largest score
+    takes it all. (A sum of 256 products in fp32 is off by 256 2^-24 = 2^-16 of the sum of their sizes at most; the rows here
+    have their two largest scores further apart, which is looked at.)"""
+    for up in (2.0 ** 22, 2.0 ** 26, 2.0 ** 30):
+        kv, step, buf, msl = make(76, [200, 37], [n, 1], hq, 2, d, 16, ScoreMod())
+        assert gaps(kv, step) > 2.0 ** -16
+        step.scale *= up
+        want = reference(kv, step, ScoreMod(), step.scale)
+        T.assert_near(attend(kv, step, buf, msl), want, False)
+
+
 def put(kv, b, t, group=0, code=0x7F, pool="v"):
     """A NaN scale for 16 values of key t of sequence b, every head."""
     getattr(kv, pool + "_block_scales")[int(kv.block_table[b, t // 16]), :, t % 16, group] = code
