@@ -91,6 +91,10 @@ SMALL = {
     "d256-many-rows": (19, [150], [30], 8, 1, 256, 16),
     "mha": (20, [400, 20], [7, 1], 3, 3, 128, 256),
     "no-rows": (45, [400, 20, 70], [0, 3, 0], 4, 2, 128, 16),
+    "one-block-no-rows": (77, [400, 20, 70, 300], [0, 20, 0, 1], 8, 2, 128, 16),
+    "two-blocks-no-rows": (78, [400, 20, 70, 300], [0, 33, 0, 50], 8, 2, 128, 16),
+    "one-block-bs8": (79, [75, 8, 140], [20, 1, 13], 8, 2, 128, 8),
+    "two-blocks-bs8": (80, [75, 0, 140], [40, 1, 33], 8, 2, 128, 8),
 }
 
 
@@ -287,6 +291,37 @@ def test_errors(d, hq, n):
             assert code == 7 or torch.equal(buf.attn_out[rows], want[rows])
         if code == 7:
             assert (buf.attn_out[n:2 * n] == 3.0).all()
+
+
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 8, 6), (128, 8, 20), (128, 8, 40), (96, 4, 5)])
+def test_blocks_past_32_bits(d, hq, n):
+    """Blocks that lie more than 2^31 (heads of 64 and 96 values) or 2^32 bytes (of 128) behind their pool's start."""
+    mod = ScoreMod(softcap=20.0)
+    kv, step, buf, msl = make(81, [300, 37], [n, n], hq, 2, d, 16, mod)
+    want = attend(kv, step, buf, msl)
+    k, v = torch.empty_like(step.new_k), torch.empty_like(step.new_v)
+    L.kv_gather(kv, k, v, step.cu_q, buf.status)
+    few, blocks = kv.k_pool.shape[0], 2200000
+    base = E.device_kv(W.custom(81, batch=2, ctx_lens=[300, 37], n_q=[n, n], num_q_heads=hq, num_kv_heads=2, head_dim=d, block_size=16, vocab=16,
+                                dtype="bf16", use_bank=False).state)
+    far = {}
+    for f in ("k_pool", "v_pool", "k_block_scales", "v_block_scales"):
+        small = getattr(base, f)
+        far[f] = torch.full((blocks, *small.shape[1:]), 0xFF, dtype=torch.uint8, device="cuda")
+        far[f][blocks - few:] = small
+    assert far["k_pool"].numel() > 2 ** (32 if d == 128 else 31)
+    for f, x in far.items():
+        setattr(base, f, x)
+    base.block_table = torch.where(base.block_table >= 0, base.block_table + (blocks - few), base.block_table)
+    free = torch.full((blocks,), -1, dtype=torch.int32, device="cuda")
+    free[:few] = torch.where(base.free_list >= 0, base.free_list + (blocks - few), base.free_list)
+    base.free_list = free
+    far_buf = S.StepBuffers.make(base, step, msl)
+    S.append(base, step, far_buf)
+    assert torch.equal(attend(base, step, far_buf, msl), want)
+    far_k, far_v = torch.empty_like(k), torch.empty_like(v)
+    L.kv_gather(base, far_k, far_v, step.cu_q, far_buf.status)
+    assert status_of(far_buf) == 0 and torch.equal(far_k, k) and torch.equal(far_v, v)
 
 
 def test_rows_behind_the_last_sequence_stay():
