@@ -174,7 +174,7 @@ def test_plain_error_is_bounded():
 
 
 @pytest.mark.parametrize("d,n,hq,block,tile,lead", [
-    (256, 1, 64, 8, 64, 4), (256, 64, 64, 16, 64, 4), (128, 1, 64, 8, 128, 2), (128, 2, 64, 16, 128, 2), (128, 5, 64, 24, 128, 2),
+    (256, 1, 64, 8, 64, 4), (256, 64, 64, 16, 64, 4), (128, 1, 64, 8, 128, 2), (128, 2, 64, 16, 128, 2), (128, 4, 64, 32, 64, 4), (128, 5, 64, 24, 128, 2),
     (128, 64, 64, 24, 128, 2), (64, 1, 64, 8, 128, 2), (64, 64, 64, 32, 128, 2)])
 def test_positions_stay_within_32_bits(lib, d, n, hq, block, tile, lead):
     """A unit (`block` rows of a KV head) has a position for each tile of keys and `lead` more; a call whose positions pass 32

@@ -83,6 +83,8 @@ SMALL = {
     "d32": (38, [130, 31, 5], [2, 4, 1], 6, 2, 32, 4),
     "d160": (44, [100, 31], [9, 3], 8, 2, 160, 16),
     "rows-27": (39, [200, 90, 1000], [9, 7, 9], 6, 2, 128, 16),
+    "rows-28": (82, [200, 90, 1000], [7, 1, 6], 8, 2, 128, 16),
+    "rows-32-bs8": (83, [200, 0, 333], [4, 4, 2], 16, 2, 128, 8),
     "rows-40": (40, [600, 90, 17], [5, 5, 5], 16, 2, 128, 16),
     "wide": (18, [200, 90], [64, 33], 8, 1, 128, 64),
     "wide-bs256": (50, [700, 255], [40, 64], 8, 2, 128, 256),
@@ -127,7 +129,7 @@ def test_trees(d, hq, n, mod):
     check(*make(41, ctx, [n] * 3, hq, 2, d, 16, T.MODS[mod](hq), positions=where, tree_mask=bits))
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 16, 5), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 16, 5), (128, 8, 8), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
 def test_long_contexts(d, hq, n):
     """Many CTAs share a unit; the bound of the lengths is far above them."""
     check(*make(42, [5000, 37, 2900], [n, max(1, n - 2), n], hq, 2, d, 16, None, slack=3000))
@@ -141,7 +143,7 @@ def test_many_sequences(d, hq, n):
     check(*make(44, ctx, rng.randint(1, n + 1, 700).tolist(), hq, 2, d, 16, None))
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 8), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
 def test_plain_call_is_the_scored_one(d, hq, n):
     """spec_verify_attn and its form without a workspace of the caller's: the bits of the scored call with nothing modified."""
     kv, step, buf, msl = make(46, [500, 37, 290], [n, 1, n], hq, 2, d, 16, ScoreMod())
@@ -154,7 +156,7 @@ def test_plain_call_is_the_scored_one(d, hq, n):
     assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 8), (128, 8, 20), (128, 8, 40), (256, 4, 3)])
 def test_queries_of_any_size(d, hq, n):
     """Queries far outside fp16's range, rows of very different sizes, zero rows: nothing is lost or refused."""
     for q_scale in (1e-30, 1e30):
@@ -186,7 +188,7 @@ def gaps(kv, step):
     return least
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 8), (128, 8, 20), (128, 8, 40), (256, 4, 3)])
 def test_scores_of_any_size(d, hq, n):
     """Scores of up to 2^34 in base 2, where fp32's steps are past 16: the weights stay within fp16, and a row's largest score
     takes it all. (A sum of 256 products in fp32 is off by 256 2^-24 = 2^-16 of the sum of their sizes at most; the rows here
@@ -204,7 +206,7 @@ def put(kv, b, t, group=0, code=0x7F, pool="v"):
     getattr(kv, pool + "_block_scales")[int(kv.block_table[b, t // 16]), :, t % 16, group] = code
 
 
-KINDS = [(64, 4), (64, 64), (128, 2), (128, 8), (128, 12), (128, 16), (128, 24), (128, 64), (256, 8), (256, 32), (96, 8)]
+KINDS = [(64, 4), (64, 64), (128, 2), (128, 8), (128, 12), (128, 16), (128, 20), (128, 24), (128, 64), (256, 8), (256, 32), (96, 8)]
 
 
 @pytest.mark.parametrize("d,hq", KINDS)
@@ -260,7 +262,7 @@ def test_slots_of_nobody_reach_nobody(d, hq):
     assert torch.equal(attend(kv, step, buf, msl), want)
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 8), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
 def test_rows_that_see_nothing(d, hq, n):
     """Tree masks without a bit and no committed key: zeros."""
     masks = torch.zeros(2 * n, dtype=torch.int64, device="cuda")
@@ -269,7 +271,7 @@ def test_rows_that_see_nothing(d, hq, n):
     assert (out[:n] == 0).all() and (out[n:] != 0).any()
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 8), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
 def test_errors(d, hq, n):
     """Bad lengths and ids are recorded; the sequences beside them are right."""
     for spoil, code in (("length", 7), ("rows", 7), ("id", 6), ("hole", 6)):
@@ -293,7 +295,7 @@ def test_errors(d, hq, n):
             assert (buf.attn_out[n:2 * n] == 3.0).all()
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 8, 6), (128, 8, 20), (128, 8, 40), (96, 4, 5)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 8, 6), (128, 8, 8), (128, 8, 20), (128, 8, 40), (96, 4, 5)])
 def test_blocks_past_32_bits(d, hq, n):
     """Blocks that lie more than 2^31 (heads of 64 and 96 values) or 2^32 bytes (of 128) behind their pool's start."""
     mod = ScoreMod(softcap=20.0)
@@ -334,7 +336,7 @@ def test_rows_behind_the_last_sequence_stay():
     assert (out[10:] == 3.0).all()
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 4, 1), (128, 8, 6), (128, 8, 8), (128, 8, 20), (128, 8, 40), (256, 4, 3)])
 def test_calls_repeat_and_replay(d, hq, n):
     """The same bits from call to call, from a captured graph (append, attention and gather together) replayed, and from
     two streams at once with workspaces of their own."""
@@ -375,14 +377,14 @@ def test_calls_repeat_and_replay(d, hq, n):
     assert all(torch.equal(o, want) for o in outs)
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 8, 6), (128, 8, 8), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
 @pytest.mark.parametrize("cap", [150.0, 1000.0, 3.4028234e38])
 def test_large_caps(d, hq, n, cap):
     """Either side of what the two-instruction tanh takes, and a cap whose product with log2(e) is past fp32's range."""
     check(*make(73, [200, 33], [n, 2], hq, 2, d, 16, ScoreMod(softcap=cap)))
 
 
-@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 8, 6), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 5), (128, 8, 6), (128, 8, 8), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5)])
 @pytest.mark.parametrize("far", [1000, 2000000000])
 def test_a_bias_between_positions_far_past_the_cache(d, hq, n, far):
     ctx = [200, 37]
