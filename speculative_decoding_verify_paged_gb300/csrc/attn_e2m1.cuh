@@ -55,7 +55,7 @@ struct Cfg4 {
   static constexpr int kMerge = kWarps * 8 * kPad * 4;
   static constexpr bool kQs = NT * KT > 16;  // Q in shared memory: registers are better spent on two chains of products
   static constexpr int kSmem = kRing + kMerge + (kQs ? NT * KT * 256 : 0);
-  static_assert(kCtasPerSm * (kSmem + 3072) <= 227 * 1024, "shared memory of an SM");
+  static_assert(kCtasPerSm * (kSmem + 3840) <= 227 * 1024, "shared memory of an SM");
 };
 
 // A running maximum moves when a score passes it by this (log2): weights of 2^14 fit fp16, and a higher bound is passed less often.
