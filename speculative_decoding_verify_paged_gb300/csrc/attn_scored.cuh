@@ -79,7 +79,8 @@ namespace sv {
 namespace scored {
 
 // The running maximum moves when a score passes it by this (log2): weights in bf16 and sums in fp32 have
-// room for 2^60, weights in fp16 for 2^8 and their sums over the row group's products.
+// room for 2^60, weights in fp16 for 2^8 and their sums over the row group's products. (By the difference, which is exact
+// where it counts: the sum of the maximum and this is rounded, to let 16 pass next to 2^27, and fp16 end.)
 template <bool F16> constexpr float kMoveAt = F16 ? 8.f : 60.f;
 constexpr float kFastCap = 200.f;  // caps up to this take the two-instruction tanh
 // Capped scores lie within [-2 cap, 0] (the constant dropped): up to this cap (log2 units) weights of
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  move |= sc[u][nt][e] > m[nt][e & 1] + kMoveAt<F8>;
+                  move |= sc[u][nt][e] - m[nt][e & 1] > kMoveAt<F8>;
                 }
             if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
