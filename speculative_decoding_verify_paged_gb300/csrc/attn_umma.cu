@@ -716,8 +716,9 @@ __global__ void __launch_bounds__(F8 ? kThreads + kConvWarps * 32 : kThreads, kC
               for (int k = 0; k < w; ++k) t16[k] = fmaxf(t16[k], t16[k + w]);
             mx = t16[0];
           }
-          // move the running maximum only when the tile's exceeds it by the threshold
-          const bool move = mx > m_run + kRescaleThreshold || (m_run == -INFINITY && mx != -INFINITY);
+          // move the running maximum only when the tile's exceeds it by the threshold (the difference, which is exact where it
+          // counts: next to 2^27 the sum would be rounded to let 16 pass, past what an fp16 weight may be)
+          const bool move = mx - m_run > kRescaleThreshold || (m_run == -INFINITY && mx != -INFINITY);
           if (__any_sync(0xffffffffu, move && l_run > 0.f)) {
             // O must be rescaled: wait for P(t-1) V(t-1) (S(t) done means P V up to t-2 is),
             // then scale this lane's row

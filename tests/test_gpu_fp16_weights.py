@@ -37,7 +37,7 @@ def flat_cache(dt, d, ctx, n, batch, hkv=2, bs=16):
     return PagedKV(*pools, table, lens, free, top, k_block_scales=scales[0], v_block_scales=scales[1])
 
 
-@pytest.mark.parametrize("plain", [False], ids=["scored"])
+@pytest.mark.parametrize("plain", [False, True], ids=["scored", "plain"])
 @pytest.mark.parametrize("d,hq,n", [(64, 8, 6), (128, 8, 1), (128, 8, 6), (128, 16, 5), (256, 8, 6), (96, 8, 6)])
 def test_scores_whose_step_is_sixteen(d, hq, n, plain):
     """The same without a bias, for the scored call or the plain one: each key's score is one step above that of the key 64
