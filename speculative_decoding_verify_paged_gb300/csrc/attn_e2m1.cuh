@@ -6,7 +6,7 @@
 // operands without a rounding, and the pool scales join the scores' factor and the outputs' normalisation in fp32.
 // Queries become fp16 next to a power of two of their row that brings its largest value to 2^14 .. 2^15: bf16's 8
 // bits stay, and what lies 2^-28 below that value is off by 2^-39 of it at most. No query is too large. Weights are rounded to fp16
-// (2^-11 of themselves, 2^-25 where that is more), their sum is of the unrounded ones.
+// (2^-11 of themselves, 2^-32 of the row's largest where that is more), their sum is of the unrounded ones.
 //
 // A CTA is four warps, and each works by itself until the end of a piece: it takes M x 16 of a tile's keys, for all RB = 8
 // NT rows of the unit, through a ring of stages of its own (16 keys' codes and scales: 18 D bytes), filled with 16-byte
@@ -57,10 +57,6 @@ struct Cfg4 {
   static constexpr int kSmem = kRing + kMerge + (kQs ? NT * KT * 256 : 0);
   static_assert(kCtasPerSm * (kSmem + 3840) <= 227 * 1024, "shared memory of an SM");
 };
-
-// A running maximum moves when a score passes it by this (log2): weights of 2^14 fit fp16, and a higher bound is passed less often.
-// (The difference is exact where it counts. The sum of the two may not be: next to 2^28 it would let 16 pass, and fp16 end.)
-constexpr float kMoveAt4 = 14.f;
 
 // A piece and its sequence. Each warp keeps its place and its turns in shared memory: registers are short, and a piece is long.
 struct Turn {
@@ -537,7 +533,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) move |= sc[u][nt][e] - m[nt][e & 1] > kMoveAt4;
+          for (int e = 0; e < 4; ++e) move |= sc[u][nt][e] - m[nt][e & 1] > kMoveAt<true>;
       if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -548,7 +544,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
             for (int u = 1; u < M; ++u) mx = fmaxf(mx, fmaxf(sc[u][nt][e], sc[u][nt][e + 2]));
 #pragma unroll
             for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
-            const float mn = fmaxf(m[nt][e], mx);
+            const float mn = fmaxf(m[nt][e], mx - kBelow<true>);
             const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
             m[nt][e] = mn;
             l[nt][e] *= f;

@@ -78,10 +78,13 @@
 namespace sv {
 namespace scored {
 
-// The running maximum moves when a score passes it by this (log2): weights in bf16 and sums in fp32 have
-// room for 2^60, weights in fp16 for 2^8 and their sums over the row group's products. (By the difference, which is exact
-// where it counts: the sum of the maximum and this is rounded, to let 16 pass next to 2^27, and fp16 end.)
-template <bool F16> constexpr float kMoveAt = F16 ? 8.f : 60.f;
+// What weights are relative to (the "running maximum") moves when a score passes it by kMoveAt (log2): weights in bf16 and sums in
+// fp32 have room for 2^60, weights in fp16 for 2^15. (By the difference, which is exact where it counts: the sum of the
+// maximum and this is rounded, to let 16 pass next to 2^27, and fp16 end.) It moves to kBelow under the largest score, so that
+// fp16 weights begin at 2^7 and what their smallest number loses is 2^-32 of the row's largest weight: from 1 on it would be
+// 2^-25, which a million keys far below a large one add up to 3%.
+template <bool F16> constexpr float kMoveAt = F16 ? 15.f : 60.f;
+template <bool F16> constexpr float kBelow = F16 ? 7.f : 0.f;
 constexpr float kFastCap = 200.f;  // caps up to this take the two-instruction tanh
 // Capped scores lie within [-2 cap, 0] (the constant dropped): up to this cap (log2 units) weights of
 // 2^-120 and more keep their precision in bf16 and fp32, and no maximum is needed.
@@ -738,7 +741,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
                   for (int u = 1; u < M; ++u) mx = fmaxf(mx, fmaxf(sc[u][nt][e], sc[u][nt][e + 2]));
 #pragma unroll
                   for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
-                  const float mn = fmaxf(m[nt][e], mx);
+                  const float mn = fmaxf(m[nt][e], mx - kBelow<F8>);
                   const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
                   m[nt][e] = mn;
                   l[nt][e] *= f;

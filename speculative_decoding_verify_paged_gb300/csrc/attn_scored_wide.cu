@@ -48,7 +48,7 @@
 // E2M1 caches (CODES): four converters stand in the producer's place, one a scheduler, two of K and two of V. Each has a ring of
 // its own, three tiles of asynchronous 16-byte copies that run on into the CTA's next piece, and writes the fp16 values (exact,
 // e2m1.cuh) where the TMA would have put them. Q becomes fp16 next to a power of two of its row, as in attn_e2m1.cuh,
-// and joins the row's factor; weights are fp16 (2^-11 of themselves, 2^-25 where that is more), so the running maximum stays for
+// and joins the row's factor; weights are fp16 (as there), so the running maximum stays for
 // capped scores too. Trees as above, not capped: 169 us, 780 TFLOP/s (595 on warp-level instructions; 184 with the codes
 // a tile ahead in registers). 32 sequences over 2K to 4K tokens: 256 rows a KV head 164, 128 rows 139, 64 rows 123.
 // A tile takes 3000 cycles whether 128 rows meet it or 256: a converter is busy for 1700 of them (800 for the copies' addresses,
@@ -664,8 +664,8 @@ __global__ void __launch_bounds__(kWideThreads<CODES>, 1)
           // (fp16 weights end soon: what passes is the exact difference, not one to a rounded sum)
           const bool move = CODES ? mx - m > kMoveAt<CODES> : mx > m + kMoveAt<CODES>;
           if (!__any_sync(0xffffffffu, move)) return;
-          const float f = move ? ex2(m - mx) : 1.f;
-          if (move) m = mx;
+          const float below = mx - kBelow<CODES>, f = move ? ex2(m - below) : 1.f;
+          if (move) m = below;
           l *= f;
           uint32_t o[32];
           o_free();

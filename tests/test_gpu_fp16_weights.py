@@ -63,3 +63,29 @@ def test_scores_whose_step_is_sixteen(d, hq, n, plain):
         L.spec_verify_attn_scored(kv, q, out, cu, mod=ScoreMod(), **args)
     torch.cuda.synchronize()
     assert int(status) == 0 and bool(((out >= 1) & (out <= 2)).all())
+
+
+TAILS = [(dt, d, hq, n) for dt in ("e2m1", "e4m3") for d, hq, n in (
+    (64, 4, 5), (64, 4, 12), (128, 4, 1), (128, 8, 6), (128, 8, 7), (128, 16, 5), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5))]
+
+
+@pytest.mark.parametrize("x", [20.5, 24.5, 27.5])
+@pytest.mark.parametrize("dt,d,hq,n", TAILS)
+def test_a_flat_tail_next_to_one_large_weight(dt, d, hq, n, x):
+    """The first key has weight 1 and a value of 0, all others a weight of 2^-x and values of 1: the output is the tail's share
+    alone. A weight counts to 2^-32 of the row's largest (the smallest fp16 number's half, with the largest weight at 2^7), and
+    to 2^-11 of itself; the output is rounded to bf16 (2^-8), and the sums' own errors are far below. As many units as there
+    are CTAs and more, so that one warp meets the first key and much of the tail."""
+    ctx, batch = 640, 400
+    kv = flat_cache(dt, d, ctx, n, batch)
+    kv.k_pool[0, :, 0], kv.v_pool[0, :, 0] = 0x38 if dt == "e4m3" else 0x22, 0
+    q = torch.ones((batch * n, hq, d), dtype=torch.bfloat16, device="cuda")
+    out, status = torch.full_like(q, float("nan")), torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = torch.arange(0, batch * n + 1, n, dtype=torch.int32, device="cuda")
+    L.spec_verify_attn_scored(kv, q, out, cu, max_q=n, max_seq_len=ctx + n, scale=x * float(np.log(2)) / d, mod=ScoreMod(), status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    others = (ctx + torch.arange(n, dtype=torch.float64, device="cuda")).repeat(batch)[:, None, None]
+    total = 1 + others * 2.0 ** -x
+    want = others * 2.0 ** -x / total
+    assert bool(((out.double() - want).abs() <= want * (2.0 ** -8 + 2.0 ** -11 + 1e-5) + others * 2.0 ** -32 / total).all())
