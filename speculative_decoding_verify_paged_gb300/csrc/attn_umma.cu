@@ -829,8 +829,6 @@ __global__ void __launch_bounds__(F8 ? kThreads + kConvWarps * 32 : kThreads, kC
           x[j] = r < valid ? *reinterpret_cast<const uint4 *>(src + (j / kPer) * kCodeHalf + r * 128 + c * 16)
                            : make_uint4(0, 0, 0, 0);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty[cs]));  // the codes are in registers: the stage can refill
         if (t >= kMS) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&cempty[ms]), ((t / kMS) - 1) & 1, wns));
         if (!ok) break;
         tc_fence_after();
@@ -853,7 +851,12 @@ __global__ void __launch_bounds__(F8 ? kThreads + kConvWarps * 32 : kThreads, kC
         fence_proxy_async();  // the generic-proxy stores, visible to the tensor cores
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&cfull[ms]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&cfull[ms]));
+          // The stage can refill: what was stored came out of it. (Not before: an arrival does not wait for the data of
+          // reads before it, and reads that stood behind a unit's Q and output rows came after the next copy.)
+          mbar_arrive(smem_u32(&empty[cs]));
+        }
       }
     }
   }
