@@ -74,7 +74,11 @@ constexpr int kStageBytes = 4 * kHalfBytes;     // K and V, two halves each
 constexpr int kTmemCols = 256;                  // S0 [0,32) S1 [32,64) O [64,192) Q [192,256)
 constexpr int kColO = 64;
 constexpr int kColQ = 192;
-constexpr float kRescaleThreshold = 8.f;        // log2 units
+// Weights are relative to a running maximum that moves when a score passes it by kMoveAt (log2), to kBelow under that score:
+// fp16 weights (E4M3 pools) begin at 2^7 and end at 2^15, so that what their smallest number loses is 2^-32 of the row's
+// largest weight.
+template <bool F8> constexpr float kMoveAt = F8 ? 15.f : 8.f;
+template <bool F8> constexpr float kBelow = F8 ? 7.f : 0.f;
 constexpr int kCtasPerSm = 2;                   // TMEM: 2 x 256 columns; shared memory: 2 x ~100 KB
 // E4M3 pools: a ring of code stages (K | V codes, 4 KB each) that the TMA fills, two converter
 // warps that widen each stage to fp16 in the operand layout above, and a ring of operand stages
@@ -718,13 +722,14 @@ __global__ void __launch_bounds__(F8 ? kThreads + kConvWarps * 32 : kThreads, kC
           }
           // move the running maximum only when the tile's exceeds it by the threshold (the difference, which is exact where it
           // counts: next to 2^27 the sum would be rounded to let 16 pass, past what an fp16 weight may be)
-          const bool move = mx - m_run > kRescaleThreshold || (m_run == -INFINITY && mx != -INFINITY);
+          const bool move = mx - m_run > kMoveAt<F8> || (m_run == -INFINITY && mx != -INFINITY);
+          const float below = mx - kBelow<F8>;
           if (__any_sync(0xffffffffu, move && l_run > 0.f)) {
             // O must be rescaled: wait for P(t-1) V(t-1) (S(t) done means P V up to t-2 is),
             // then scale this lane's row
             if (!mbar_wait(smem_u32(o_bar), (t - 1) & 1, wns)) ok = false;
             tc_fence_after();
-            const float f = (move && l_run > 0.f) ? exp2f(m_run - mx) : 1.f;
+            const float f = (move && l_run > 0.f) ? exp2f(m_run - below) : 1.f;
 #pragma unroll
             for (int cb = 0; cb < kD / 32; ++cb) {
               uint32_t o[32];
@@ -737,8 +742,8 @@ __global__ void __launch_bounds__(F8 ? kThreads + kConvWarps * 32 : kThreads, kC
             tmem_wait_st();
           }
           if (move) {
-            l_run = (l_run > 0.f) ? l_run * exp2f(m_run - mx) : l_run;
-            m_run = mx;
+            l_run = (l_run > 0.f) ? l_run * exp2f(m_run - below) : l_run;
+            m_run = below;
           }
           const float ref = (m_run == -INFINITY) ? 0.f : m_run;
           uint32_t pr[kTile / 2];

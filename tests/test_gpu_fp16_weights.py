@@ -37,6 +37,17 @@ def flat_cache(dt, d, ctx, n, batch, hkv=2, bs=16):
     return PagedKV(*pools, table, lens, free, top, k_block_scales=scales[0], v_block_scales=scales[1])
 
 
+def attend(kv, q, out, cu, n, ctx, scale, status, plain):
+    """The scored call with nothing modified, or the plain one."""
+    args = dict(max_q=n, max_seq_len=ctx + n, scale=scale, status=status)
+    if plain:
+        need = L.spec_verify_attn_workspace_bytes(kv, q.shape[1], q.shape[0], n, ctx + n)
+        L.spec_verify_attn(kv, q, out, cu, workspace=torch.empty(max(256, need), dtype=torch.uint8, device="cuda"), **args)
+    else:
+        L.spec_verify_attn_scored(kv, q, out, cu, mod=ScoreMod(), **args)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("plain", [False, True], ids=["scored", "plain"])
 @pytest.mark.parametrize("d,hq,n", [(64, 8, 6), (128, 8, 1), (128, 8, 6), (128, 16, 5), (256, 8, 6), (96, 8, 6)])
 def test_scores_whose_step_is_sixteen(d, hq, n, plain):
@@ -55,13 +66,7 @@ def test_scores_whose_step_is_sixteen(d, hq, n, plain):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
     out = torch.full_like(q, float("nan"))
-    args = dict(max_q=n, max_seq_len=ctx + n, scale=16.0 * 2 ** 10 * float(np.log(2)), status=status)
-    if plain:
-        need = L.spec_verify_attn_workspace_bytes(kv, hq, 2 * n, n, ctx + n)
-        L.spec_verify_attn(kv, q, out, cu, workspace=torch.empty(max(256, need), dtype=torch.uint8, device="cuda"), **args)
-    else:
-        L.spec_verify_attn_scored(kv, q, out, cu, mod=ScoreMod(), **args)
-    torch.cuda.synchronize()
+    attend(kv, q, out, cu, n, ctx, 16.0 * 2 ** 10 * float(np.log(2)), status, plain)
     assert int(status) == 0 and bool(((out >= 1) & (out <= 2)).all())
 
 
@@ -69,11 +74,12 @@ TAILS = [(dt, d, hq, n) for dt in ("e2m1", "e4m3") for d, hq, n in (
     (64, 4, 5), (64, 4, 12), (128, 4, 1), (128, 8, 6), (128, 8, 7), (128, 16, 5), (128, 8, 20), (128, 8, 40), (256, 4, 3), (96, 4, 5))]
 
 
+@pytest.mark.parametrize("plain", [False, True], ids=["scored", "plain"])
 @pytest.mark.parametrize("x", [20.5, 24.5, 27.5])
 @pytest.mark.parametrize("dt,d,hq,n", TAILS)
-def test_a_flat_tail_next_to_one_large_weight(dt, d, hq, n, x):
+def test_a_flat_tail_next_to_one_large_weight(dt, d, hq, n, x, plain):
     """The first key has weight 1 and a value of 0, all others a weight of 2^-x and values of 1: the output is the tail's share
-    alone. A weight counts to 2^-32 of the row's largest (the smallest fp16 number's half, with the largest weight at 2^7), and
+    alone. A weight counts to 2^-32 of the row's largest (half of the smallest fp16 number, with the largest weight at 2^7 or more), and
     to 2^-11 of itself; the output is rounded to bf16 (2^-8), and the sums' own errors are far below. As many units as there
     are CTAs and more, so that one warp meets the first key and much of the tail."""
     ctx, batch = 640, 400
@@ -82,8 +88,7 @@ def test_a_flat_tail_next_to_one_large_weight(dt, d, hq, n, x):
     q = torch.ones((batch * n, hq, d), dtype=torch.bfloat16, device="cuda")
     out, status = torch.full_like(q, float("nan")), torch.zeros(1, dtype=torch.int32, device="cuda")
     cu = torch.arange(0, batch * n + 1, n, dtype=torch.int32, device="cuda")
-    L.spec_verify_attn_scored(kv, q, out, cu, max_q=n, max_seq_len=ctx + n, scale=x * float(np.log(2)) / d, mod=ScoreMod(), status=status)
-    torch.cuda.synchronize()
+    attend(kv, q, out, cu, n, ctx, x * float(np.log(2)) / d, status, plain)
     assert int(status) == 0
     others = (ctx + torch.arange(n, dtype=torch.float64, device="cuda")).repeat(batch)[:, None, None]
     total = 1 + others * 2.0 ** -x
