@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) attn_e2m1_kernel(c
       }
       most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-      const int e = most >> 7, field = e == 255 ? 127 : min(268 - e, 253);  // (infinities and NaN stay what they are)
+      const int e = most >> 7, field = min(268 - e, 253);  // (infinities and NaN stay what they are, finite values beside them finite)
       const float up = __int_as_float(field << 23), down = __int_as_float((254 - field) << 23);
 #pragma unroll
       for (int kk = 0; kk < KT; ++kk)

@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kWideThreads<CODES>, 1)
         for (int c = 0; c < kParts; ++c) look(part[c]);
         if constexpr (ONE)
           for (int c = 0; c < 8; ++c) look(live ? src[8 * (blk ^ 1) + c] : make_uint4(0, 0, 0, 0));
-        const int e = max(most & 0xffffu, most >> 16) >> 7, field = e == 255 ? 127 : min(268 - e, 253);  // (infinities and NaN stay what they are)
+        const int e = max(most & 0xffffu, most >> 16) >> 7, field = min(268 - e, 253);  // (as in attn_e2m1.cuh)
         const float up = __int_as_float(field << 23);
         down = __int_as_float((254 - field) << 23);
         auto half2_of = [&](uint32_t x) { return pack2<true>(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up); };
