@@ -255,6 +255,10 @@ def kv_append(kv: PagedKV, new_k: torch.Tensor, new_v: torch.Tensor, cu_q: torch
             raise SVError(rc, "sv_kv_append")
         return
     s = kv.struct()
+    values, size = int(new_k.shape[0]) * s.num_kv_heads * s.head_dim, 4 if s.dtype == SV_DTYPE_F32 else 2
+    for rows in (new_k, new_v):
+        if rows.numel() != values or rows.element_size() != size:
+            raise ValueError("new_k and new_v are [n, num_kv_heads, head_dim] of the cache's row type")
     _check(load().sv_kv_append(ctypes.byref(s), _ptr(new_k), _ptr(new_v), _ptr(cu_q), int(new_k.shape[0]),
                                _ptr(status), _stream(stream)), "sv_kv_append")
 
