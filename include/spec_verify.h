@@ -136,7 +136,8 @@ typedef enum sv_mask_kind { SV_MASK_CAUSAL = 0, SV_MASK_TREE = 1 } sv_mask_kind;
  * in sv_spec_verify_attn_scored one is a NaN to the rows that see its key and
  * nothing to the others. Attention reads code * scale: the CUDA-core
  * kernel in fp32; the tcgen05 kernel (head_dim 128) widens the codes to fp16
- * exactly, rounds the queries and the softmax weights to fp16 and applies the
+ * exactly, rounds the queries and the softmax weights to fp16 (a weight is off by
+ * 2^-11 of itself or 2^-32 of the row's largest, whichever is more) and applies the
  * scales to the scores and the outputs in fp32, so a query element beyond the
  * fp16 range (|q| > 65504) records SV_ERR_NONFINITE there.
  *
@@ -422,13 +423,17 @@ typedef struct sv_score_mod {
  * zeros; what a key holds (NaN and infinities too) reaches the rows that see it
  * and no others.
  * Scores, softmax statistics and sums are fp32, and the output is rounded once.
- * Fewer bits are in two places of the tensor-core kernels (bf16 and E4M3 pools,
- * head_dim 64, 128 or 256, blocks of 8 tokens and more): the weights that V is
- * multiplied with are rounded to bf16 (off by 2^-8 of themselves at most; over an
- * E4M3 pool to fp16, 2^-11), and over an E4M3 pool so are the queries, to fp16:
- * 2^-11, elements below 2^-14 by up to 2^-25, and one beyond 65504 records
- * SV_ERR_NONFINITE. The CUDA-core kernels (the other sizes, and fp32) round
- * neither. A capped score is off by at most 2^-19 of the cap.
+ * Fewer bits are in two places of the tensor-core kernels (bf16, E4M3 and E2M1
+ * pools, head_dim 64, 128 or 256, blocks of 8 tokens and more). The weights that V
+ * is multiplied with are rounded: to bf16 (off by 2^-8 of themselves at most); over
+ * E4M3 and E2M1 pools to fp16, off by 2^-11 of themselves or 2^-32 of the row's
+ * largest weight, whichever is more, while their sum is of the unrounded ones: N
+ * keys far below the largest can lose N 2^-32 of it. And over E4M3 and E2M1 pools
+ * the queries are rounded to fp16. E4M3: off by 2^-11, elements below 2^-14 by up to
+ * 2^-25, and one beyond 65504 records SV_ERR_NONFINITE. E2M1: next to a power of
+ * two of their row, off by 2^-39 of its largest element (by 2^-151 where that is
+ * below 2^-112). The CUDA-core kernels (the other sizes, and fp32) round neither.
+ * A capped score is off by at most 2^-19 of the cap.
  *   positions  int32 [total_q] or NULL; each at least c_b, the first position
  *              after the committed keys (a smaller one sets SV_ERR_BAD_LENGTH
  *              and leaves that sequence's rows undefined)

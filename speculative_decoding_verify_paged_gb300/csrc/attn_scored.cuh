@@ -11,8 +11,8 @@
 // about 2^-22, times the cap is what reaches a score (caps above kFastCap take tanhf).
 //
 // Fewer bits than fp32, and why: the weights are rounded to the type of V's operand, bf16 (off by 2^-8 of themselves at
-// most) or, over E4M3 pools, fp16 (2^-11), since a matrix instruction takes operands of one type; the sum of the weights
-// is of the unrounded ones. Over E4M3 pools the queries are fp16 for the same reason (2^-11; what lies below 2^-14
+// most) or, over E4M3 pools, fp16 (2^-11; see kBelow), since a matrix instruction takes operands of one type; the sum of the
+// weights is of the unrounded ones. Over E4M3 pools the queries are fp16 for the same reason (2^-11; what lies below 2^-14
 // is off by up to 2^-25, beyond 65504 the call records SV_ERR_NONFINITE). The cap's 2^x and reciprocal are the
 // approximate ones: 2^-19 of the cap at most, far below what the rounded weights leave. Against 64 bits a bf16 row is off by
 // 0.0023 of its size, where one rounding of the output alone leaves 0.0017.
