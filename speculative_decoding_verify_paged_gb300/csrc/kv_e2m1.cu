@@ -6,8 +6,9 @@
 // block id -> rows short ones. A CTA takes a few consecutive rows: its first warp finds where they stand, then a thread
 // takes 16 values of a row (a group of codes; 16 or 32 bytes of wider types) at a time.
 //
-// 8 heads of 128 values: 256 x 64 rows into the pool 38 us (4.4 TB/s of what it cannot do without), 32 x 6 rows 8.8 us, two
-// launches; 74K rows of 32 sequences out of it 62 us (6.2 TB/s), 4 short sequences' 4.8 us.
+// 8 heads of 128 values. Rows into the pool (two launches, the allocation's among them): 256 x 64 19.2 us (4.5 TB/s of what it
+// cannot do without, 86 MB), 32 x 6 5.5 us. Rows out of it (one launch): those 256 x 64 18.4 us, 74K rows of 32 sequences
+// 66 us (5.9 TB/s), from E4M3, bf16 and fp32 pools 74, 95 and 186 us (6.2, 6.4 and 6.5 TB/s); 4 short sequences' 4.8 us.
 #include <algorithm>
 
 #include "e2m1.cuh"
@@ -97,7 +98,8 @@ __global__ void __launch_bounds__(kThreads) kv_store_kernel(KV kv, const uint8_t
     read32<W>(new_k + from, k);
     read32<W>(new_v + from, v);
   };
-  // the rows and cu_q are the call's own inputs, read before the wait; what the allocation writes comes after it
+  // the rows are the call's own inputs, read before the wait (the allocation, which lets this kernel start, has waited for the
+  // kernels before it); what the allocation writes comes after it, and cu_q with it
   if ((int)threadIdx.x < items) load(threadIdx.x);
   grid_dependency_wait();
   grid_dependents_launch();
@@ -190,10 +192,16 @@ __global__ void __launch_bounds__(kThreads) kv_gather_narrow_kernel(KV kv, uint4
   }
 }
 
-// Rows of a CTA: as many as leave eight CTAs an SM some, kMostRows at most. (The store's registers let four stay: two waves, the
-// second under the first one's tail. 256 x 64 rows with 4, 5, 6, 8, 12 and 24 an SM: 42.8, 45.1, 42.0, 38.4, 41.0 and 45.3 us;
-// with five or six held by fewer registers 39.8 and 41.0, eight spill: 53.8. The gather is the same with any.)
-int rows_per_cta(int total) { return std::max(1, std::min(kMostRows, ceil_div(total, num_sms() * (2048 / kThreads)))); }
+// Rows of a CTA, with so many CTAs an SM: kMostRows at most.
+int rows_per_cta(int total, int per_sm) { return std::max(1, std::min(kMostRows, ceil_div(total, num_sms() * per_sm))); }
+// The store's registers let four CTAs stay on an SM: one wave while its CTAs have rows enough for that, else two, the second
+// under the first one's tail. (us with 4, 8 and 12 CTAs an SM, 8 heads of 128: 1024 rows 6.2, 8.6, 8.6; 3072 8.2, 9.5,
+// 11.2; 10240 14.5, 16.1, 17.2; 16384 19.2, 20.4, 22.8; 24000, where four are a wave and a quarter, 31.0, 26.1, 28.2; 32768
+// 34.6, 33.6, 35.6; 65536 the same.)
+int store_rows(int total) { return rows_per_cta(total, ceil_div(total, num_sms() * 4) <= kMostRows ? 4 : 8); }
+// The gather's let eight. (The same sizes: 4.6, 4.6, 4.6; 7.2, 6.0, 7.8; 14.8, 12.7, 13.6; 21.5, 18.4, 19.1; 27.7, 24.3, 26.7;
+// 33.4, 32.2, 34.7.)
+int gather_rows(int total) { return rows_per_cta(total, 8); }
 bool aligned32(const void *a, const void *b) { return (((uintptr_t)a | (uintptr_t)b) & 31u) == 0; }
 
 }  // namespace
@@ -204,7 +212,7 @@ cudaError_t launch_kv_store_e2m1(const KV &kv, const void *new_k, const void *ne
     const cudaError_t e = launch_private_copies(kv, cu_q, status, st);
     if (e != cudaSuccess) return e;
   }
-  const int per = rows_per_cta(total_q);
+  const int per = store_rows(total_q);
   auto kernel = aligned32(new_k, new_v) ? kv_store_kernel<true> : kv_store_kernel<false>;
   return launch_pdl(kernel, dim3((unsigned)ceil_div(total_q, per)), dim3(kThreads), 0, st, kv, (const uint8_t *)new_k,
                     (const uint8_t *)new_v, cu_q, total_q, per, 1.f / (6.f * kv.k_scale), 1.f / (6.f * kv.v_scale), status);
@@ -212,7 +220,7 @@ cudaError_t launch_kv_store_e2m1(const KV &kv, const void *new_k, const void *ne
 
 cudaError_t launch_kv_gather(const KV &kv, void *out_k, void *out_v, const int32_t *cu_rows, int total_rows,
                              const int32_t *first, int32_t *status, cudaStream_t st) {
-  const int per = rows_per_cta(total_rows);
+  const int per = gather_rows(total_rows);
   const dim3 grid((unsigned)ceil_div(total_rows, per));
   if (kv.elem_bytes == 2 && kv.head_dim % 16 != 0)
     return launch_pdl(kv_gather_narrow_kernel, grid, dim3(kThreads), 0, st, kv, (uint4 *)out_k, (uint4 *)out_v, cu_rows, total_rows, per,

@@ -1,5 +1,5 @@
-"""4-bit caches where the other tests do not reach: pool scales of any size in attention, infinite queries, and gathered values to
-the bit."""
+"""4-bit caches where the other tests do not reach: pool scales of any size in attention, infinite queries, gathered values to
+the bit, and appends of more rows than one wave of CTAs takes."""
 import numpy as np
 import pytest
 import torch
@@ -69,3 +69,14 @@ def test_gathered_values_to_the_bit(d, scales):
         want = torch.from_numpy(code * step).to(torch.bfloat16)
         nan = torch.isnan(want)
         assert torch.equal(torch.isnan(got.cpu()), nan) and torch.equal(got.cpu()[~nan].view(torch.int16), want[~nan].view(torch.int16))
+
+
+@pytest.mark.parametrize("n", [48, 49, 64])
+def test_append_of_very_many_rows(n):
+    """400 sequences of 48 to 64 rows: just within one wave of CTAs with 32 rows each, just past it, and well past."""
+    _, kv, step, buf = C.make(25, [3 + b % 60 for b in range(400)], [n] * 400, hq=1, hkv=1, d=32, bs=64)
+    before = C.host(kv)
+    L.kv_append(kv, step.new_k, step.new_v, step.cu_q, buf.status)
+    torch.cuda.synchronize()
+    assert int(buf.status) == 0
+    C.assert_stored(kv, before, step.cu_q, step.new_k, step.new_v)
