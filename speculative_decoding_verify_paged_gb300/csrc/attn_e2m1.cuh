@@ -723,7 +723,7 @@ cudaError_t pick4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStre
     if (rows <= 16) return on(Cfg4<D, 2, 2, 3, 5>());
     return on(Cfg4<D, 4, 2, 2, 6>());
   } else if constexpr (D == 128) {
-    if (rows <= 8) return on(Cfg4<D, 1, 2, 3, 3>());
+    if (rows <= 8) return on(Cfg4<D, 1, 2, 4, 2>());
     if (rows <= 16) return on(Cfg4<D, 2, 2, 2, 4>());
     // 25 to 32 rows in one block of 16 keys a step: 32 sequences of 2K to 4K tokens with 28 rows 76 us, in two blocks of 24 rows
     // 102. (Blocks of 40 rows spill: 36 and 40 rows 100 and 102 us in either, and batches of 12 to 36 rows lose a fifth by them.)
