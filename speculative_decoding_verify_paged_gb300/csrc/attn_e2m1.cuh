@@ -22,14 +22,15 @@
 //
 // Bound: the issue of instructions, at the rate that few warps of long chains reach. 16 keys of 128 values are 64 conversions and as
 // many products with scales whatever the rows, 48 matrix instructions and some 72 of softmax for 24 rows, 75 for copies and
-// their addresses: about 500 with a piece's share of its set-up and merge, and an issue slot takes one 39% of
-// the time (two warps a scheduler at 240 registers; fixed latencies first, then instruction fetch; 56% for 8 rows, three warps). Times, 8 KV heads of 128:
+// their addresses: about 500 with a piece's share of its set-up and merge. What a warp waits for is latency more than slots:
+// an issue slot takes an instruction 40% of the time for 24 rows (two warps a scheduler at 244 registers) and 59% for 8 rows (four warps),
+// fixed latencies first, then instruction fetch and the matrix pipe. Times, 8 KV heads of 128:
 //   32 sequences of 0.5K to 4K tokens, 24 rows a KV head: 47 us (1.8 TB/s of the cache; 885 on CUDA cores);
-//   4 sequences of 32K tokens, 8 rows: 53 us (2.8 TB/s); 128 of 16 to 8192 tokens, 12 to 36 rows, capped: 158 us.
-// (Looking at a block's number as soon as it is asked for costs 5%: 50, 56 and 160.)
-// Two steps' worth of keys (M = 2) give the chains something to hide behind: 24 rows 50 us, 61 with 16 keys and three CTAs an
-// SM (both before that); 8 rows 56 and 56. Two warps to a step, half of the values each, take 72 us for 24 rows, 75 for 8 and 108 for 40 (123 here,
-// two blocks of 24): the second warp costs scores, copies and weights what it saves in products.
+//   4 sequences of 32K tokens, 8 rows: 48 us (3.1 TB/s); 128 of 16 to 8192 tokens, 12 to 36 rows, capped: 158 us.
+// (Looking at a block's number as soon as it is asked for cost 5% of each.)
+// Two steps' worth of keys (M = 2) give the chains something to hide behind; see pick4 for both. Two warps to a step, half of the
+// values each, took 72 us for 24 rows, 75 for 8 and 108 for 40 (121 here, two blocks of 24): the second warp costs scores, copies and
+// weights what it saves in products.
 //
 // More than 48 rows over heads of 128 values go to attn_scored_wide.cu.
 #pragma once
@@ -45,7 +46,10 @@ struct Cfg4 {
   static constexpr int D = D_, NT = NT_, RB = NT_ * 8, kCtasPerSm = CTAS_, kStages = STAGES_;
   static constexpr int M = M_, kKeys = 16 * M;  // keys of a step
   static constexpr int kWarps = 4, kThreads = 128, TK = kWarps * kKeys;
-  static constexpr int kAlpha = M == 1 ? 4 : 2;  // positions of a unit's lead-in
+  // Positions of a unit's lead-in. (us with half, with these and with twice as many, the cases of pick4: heads of 128, 24 rows 45.3,
+  // 43.4, 44.4; 32 rows 55.4, 52.8, 56.4; 40 rows of 600 tokens 121, 120, 119. Heads of 256, 24 rows 61.3, 59.3, 64.2; heads
+  // of 64 67.5, 63.0, 59.5.)
+  static constexpr int kAlpha = M == 1 ? 4 : 2;
   static constexpr int KT = D / 16;
   static constexpr int kCodes = 8 * D * M, kScales = D * M;  // bytes of a step's keys (or values): codes, block scales
   static constexpr int kStage = 2 * (kCodes + kScales);
@@ -714,19 +718,26 @@ cudaError_t run4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStrea
 // The smallest block of query rows that holds a unit's, else blocks of the largest.
 template <int D>
 cudaError_t pick4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {
-  // CTAs an SM and stages: what registers and shared memory leave. 8 rows, 4 long sequences, 32 keys a step: three CTAs with
-  // three stages 55.7 us, four with two 59.2; 16 keys: four with five stages 55.7, three with six 86.
+  // CTAs an SM and stages: what registers and shared memory leave. Times in us: of 4 sequences of 32K tokens ("long"), 32 of 0.5K to
+  // 4K, 128 of 512 to 640 ("short"); 16, 8 and 4 KV heads of 64, 128 and 256 values, so that the caches are of one size.
   const int rows = sa.a.num_q_heads / sa.a.kv.num_kv_heads * sa.a.max_q;
   auto on = [&](auto cfg) { return run4<decltype(cfg)>(sa, workspace, bytes, st, go); };
   if constexpr (D == 64) {
+    // 8 rows, long: 53; three CTAs with five stages 63; 16 keys a step, eight stages 67
     if (rows <= 8) return on(Cfg4<D, 1, 2, 4, 4>());
+    // 16 rows: 45 to 54 from run to run; two CTAs with six stages 49; 16 keys a step, eight stages 49 to 55; in a block of 32 63
     if (rows <= 16) return on(Cfg4<D, 2, 2, 3, 5>());
+    // 32 rows: 67; in two blocks of 24 95; 16 keys a step 75. (24 and 40 rows would gain by blocks of 24: 63 and 57, 109 and 98.)
     return on(Cfg4<D, 4, 2, 2, 6>());
   } else if constexpr (D == 128) {
+    // 8 rows, long: 48, and 32 sequences 32.5; three CTAs with three stages 53 and 36.6; 16 keys a step, four CTAs with four stages
+    // 55 and 33.7. (256 sequences of 100 to 600 tokens: 57, 55 and 55.)
     if (rows <= 8) return on(Cfg4<D, 1, 2, 4, 2>());
+    // 16 rows: 39.7; 16 keys a step, eight stages 43.2, three CTAs with five stages 55
     if (rows <= 16) return on(Cfg4<D, 2, 2, 2, 4>());
-    // 25 to 32 rows in one block of 16 keys a step: 32 sequences of 2K to 4K tokens with 28 rows 76 us, in two blocks of 24 rows
-    // 102. (Blocks of 40 rows spill: 36 and 40 rows 100 and 102 us in either, and batches of 12 to 36 rows lose a fifth by them.)
+    // 25 to 32 rows in one block of 16 keys a step: 32 sequences of 2K to 4K tokens with 28 rows 69, in two blocks of 24 rows 93; 64 of
+    // 200 to 300 36 and 48. (Blocks of 40 rows spill, took as long for 36 and 40 rows, and batches of 12 to 36 lost a fifth by them.)
+    // Else blocks of 24: 24 rows 43.4; 16 keys a step, eight stages 47.5, three CTAs with five stages 53.
     if (rows > 24 && rows <= 32) return on(Cfg4<D, 4, 1, 2, 8>());
     if (!wide_fits(sa)) return on(Cfg4<D, 3, 2, 2, 4>());
     // a cap past the two-instruction tanh stays here; the workspace suits both, and so do the positions
@@ -737,7 +748,10 @@ cudaError_t pick4(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStre
     *bytes = *bytes == 0 || most == 0 ? 0 : std::max(*bytes, most);
     return e;
   } else {
+    // 8 rows, long: 49.9, and 128 of 200 to 640 tokens 35.9; three CTAs with two stages 50.9 and 36.6; 32 keys a step, two stages 46.3
+    // and 39.0
     if (rows <= 8) return on(Cfg4<D, 1, 1, 2, 4>());
+    // 16 rows: 39.3; three stages 38.1; in two blocks of 8 49.1
     return on(Cfg4<D, 2, 1, 2, 4>());
   }
 }

@@ -1148,11 +1148,9 @@ cudaError_t run(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream
 }
 
 // Units of more query rows go to attn_scored_wide.cu, where it takes them: with 64 rows a KV head 32 sequences of 2K to
-// 4K tokens take 106 us here and 97 there, 64 of 200 to 300 tokens 64 and 50; with 48 rows 96 and 100.
+// 4K tokens take 106 us here and 97 there, 64 of 200 to 300 tokens 64 and 50; with 48 rows 96 and 100. E2M1 caches: with 64 rows
+// 132 us in attn_e2m1.cuh and 117 there, the short ones 69 and 62; with 48 rows 94 and 116, 50 and 60.
 constexpr int kWideRows = 48;
-// E2M1 caches: with 64 rows 32 such sequences take 148 us in attn_e2m1.cuh and 121 there, with 48 rows 113 and 127; 64 short
-// ones 72 and 66, 55 and 64.
-constexpr int kWideRows4 = 48;
 bool wide_fits(const ScoredArgs &sa);
 cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go);
 

@@ -50,11 +50,12 @@
 // e2m1.cuh) where the TMA would have put them. Q becomes fp16 next to a power of two of its row, as in attn_e2m1.cuh,
 // and joins the row's factor; weights are fp16 (as there), so the running maximum stays for
 // capped scores too. Trees as above, not capped: 169 us, 780 TFLOP/s (595 on warp-level instructions; 184 with the codes
-// a tile ahead in registers). 32 sequences over 2K to 4K tokens: 256 rows a KV head 164, 128 rows 139, 64 rows 123.
+// a tile ahead in registers). 32 sequences over 2K to 4K tokens: 256 rows a KV head 146, 128 rows 124, 64 rows 117.
 // A tile takes 3000 cycles whether 128 rows meet it or 256: a converter is busy for 1700 of them (800 for the copies' addresses,
 // 850 for its 64 conversions a lane), and a tile's way from there to the end of P V is long.
-// Registers: four warps more, so fewer for each. The others' 80 is where nothing they use in a loop spills (64: 172 us in
-// place of 123 for 64 rows, 188 in place of 174 for the trees); their places in the order are in shared memory for that.
+// Registers: four warps more, so fewer for each. The others' 80 is where nothing they use in a loop spills (64 took 40% longer for
+// 64 rows and 8% for the trees); their places in the order are in shared memory for that. The softmax's 176 spill 286 and 434
+// bytes (up to 128 rows): 0.7% of the trees' instructions.
 //
 // All waits are bounded, as in attn_scored.cuh.
 #include <algorithm>
@@ -967,7 +968,7 @@ cudaError_t launch_wide(const CUtensorMap &mk, const CUtensorMap &mv, const Para
 bool wide_fits(const ScoredArgs &sa) {
   const KV &kv = sa.a.kv;
   return (kv.fp4 || (!kv.fp8 && kv.elem_bytes == 2)) && kv.head_dim == 128 &&
-         sa.a.num_q_heads / kv.num_kv_heads * sa.a.max_q > (kv.fp4 ? kWideRows4 : kWideRows);
+         sa.a.num_q_heads / kv.num_kv_heads * sa.a.max_q > kWideRows;
 }
 
 cudaError_t run_wide(const ScoredArgs &sa, void *workspace, size_t *bytes, cudaStream_t st, bool go) {

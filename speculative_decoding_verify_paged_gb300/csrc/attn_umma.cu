@@ -1010,7 +1010,7 @@ bool make_map(CUtensorMap *map, void *pool, const KV &kv, int box_rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 6 stages of 16 KB (E4M3: 4 code stages of 8 KB and 4 operand stages of 16 KB); at most two
+// 6 stages of 16 KB (E4M3: 6 code stages of 8 KB and 3 operand stages of 16 KB); at most two
 // CTAs fit an SM, which is what TMEM allows (2 x 256 columns)
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 32 * 8;
 static_assert(kCodeStages * kCodeStageBytes + kConvStages * kStageBytes <= kStages * kStageBytes,

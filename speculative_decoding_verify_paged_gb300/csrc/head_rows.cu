@@ -27,8 +27,9 @@
 // Short calls are latency: a launch, then the chain of reads that finds a row's place.
 //
 // bf16, 32 + 8 heads of 128 values: 16384 rows 60.1 us (5.6 TB/s of rows), 4 rows 3.5 us; 640 rows of 64 + 8
-// heads 6.2 us. With the append: 256 x 64 rows 76.8 us (5.2 TB/s), 32 x 6 rows 6.2 us, 1.5K rows into an E4M3
-// pool 15.1 us. With three axes 16384 rows take 60.3 us, 4 rows 4.4 us.
+// heads 6.2 us. With the append: 256 x 64 rows 77.3 us (5.2 TB/s), 32 x 6 rows 6.2 us, 1.5K rows into an E4M3
+// pool 15.1 us; 256 x 64 into E4M3 and E2M1 pools 77.8 and 79.3 us, 32 x 6 rows 6.2 and 6.4. With three axes 16384 rows take
+// 60.3 us, 4 rows 4.4 us, 256 x 64 appended 78.8, 79.1 and 80.6 (bf16, E4M3, E2M1); in fp32 16384 rows 105 us (6.4 TB/s), 4 rows 3.0.
 #include <cuda_fp8.h>
 
 #include <algorithm>
