@@ -195,11 +195,11 @@ __global__ void __launch_bounds__(kThreads) kv_gather_narrow_kernel(KV kv, uint4
 // Rows of a CTA, with so many CTAs an SM: kMostRows at most.
 int rows_per_cta(int total, int per_sm) { return std::max(1, std::min(kMostRows, ceil_div(total, num_sms() * per_sm))); }
 // The store's registers let four CTAs stay on an SM: one wave while its CTAs have rows enough for that, else two, the second
-// under the first one's tail. (us with 4, 8 and 12 CTAs an SM, 8 heads of 128: 1024 rows 6.2, 8.6, 8.6; 3072 8.2, 9.5,
-// 11.2; 10240 14.5, 16.1, 17.2; 16384 19.2, 20.4, 22.8; 24000, where four are a wave and a quarter, 31.0, 26.1, 28.2; 32768
+// under the first one's tail. (us with 4, 8 and 12 CTAs an SM, 8 heads of 128: 1024 rows 6.2, 8.6, 8.6; 6144 10.8, 12.4,
+// 13.0; 10240 14.5, 16.1, 17.2; 16384 19.2, 20.4, 22.8; 24000, where four are a wave and a quarter, 31.0, 26.1, 28.2; 32768
 // 34.6, 33.6, 35.6; 65536 the same.)
 int store_rows(int total) { return rows_per_cta(total, ceil_div(total, num_sms() * 4) <= kMostRows ? 4 : 8); }
-// The gather's let eight. (The same sizes: 4.6, 4.6, 4.6; 7.2, 6.0, 7.8; 14.8, 12.7, 13.6; 21.5, 18.4, 19.1; 27.7, 24.3, 26.7;
+// The gather's let eight. (The same sizes: 4.6, 4.6, 4.6; 10.4, 9.4, 9.5; 14.8, 12.7, 13.6; 21.5, 18.4, 19.1; 27.7, 24.3, 26.7;
 // 33.4, 32.2, 34.7.)
 int gather_rows(int total) { return rows_per_cta(total, 8); }
 bool aligned32(const void *a, const void *b) { return (((uintptr_t)a | (uintptr_t)b) & 31u) == 0; }
